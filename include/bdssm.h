@@ -381,6 +381,77 @@ const char *bdssm_status_str(int status);
 /* Library version: major * 10000 + minor * 100 + patch. */
 int bdssm_version(void);
 
+/*
+ * ------------------------------------------------------------------------
+ * The hybrid's other layers.  The pages' hybrid keeps two caches per layer,
+ * the recurrent boundary state and the attention's keys and values [DE-M];
+ * below are a second recurrent mixer (the gated delta rule) with the same
+ * life cycle as the scan above, and the attention side: finished blocks into
+ * a paged 8-bit cache, and the active block's queries over it.  Ownership,
+ * execution and errors as above; all pointers are 16-byte aligned device
+ * memory, all tensors contiguous and token-major.
+ *
+ * The gated delta rule.  Per batch row and value head, with a_t = exp(g_t) and
+ * the state S [d_k, d_v]:
+ *   u_t = beta_t (v_t - (a_t S_{t-1})^T k_t)
+ *   S_t = a_t S_{t-1} + k_t u_t^T,      o_t = scale S_t^T q_t
+ *   q, k    [batch, T, heads_k, d_k]    stream dtype; head h of v uses head
+ *                                       h / (heads_v / heads_k) of q and k
+ *   v, o    [batch, T, heads_v, d_v]    stream dtype
+ *   g, beta [batch, T, heads_v]         fp32; g <= 0 is the log decay, -inf
+ *                                       clears the state (a document starts)
+ *   states  [batch, heads_v, d_k, d_v]  fp32
+ *   lens    NULL, or [batch] int32: tokens at and behind lens[b] are padding
+ *           (values below 0 count as 0, above T as T): they are not read, do
+ *           not touch the state, and o and every gradient are 0 there.
+ * Keys are expected with beta_t |k_t|^2 <= 2 (normalised keys), without which
+ * the recurrence itself diverges.
+ * Limits: d_k and d_v 64 or 128; heads_v a multiple of heads_k, at most 65535.
+ */
+typedef struct {
+    int64_t batch;     /* >= 0, at most 65535 */
+    int64_t heads_k;   /* query / key heads */
+    int64_t heads_v;   /* value heads, a multiple of heads_k */
+    int64_t d_k;       /* 64 or 128 */
+    int64_t d_v;       /* 64 or 128 */
+    int32_t dtype;     /* bdssm_dtype of q, k, v, o */
+} bdssm_delta_shape;
+
+/* Tokens between two of the states that bdssm_delta_scan hands to its backward. */
+#define BDSSM_DELTA_CHUNK 64
+
+/*
+ * The rule over T tokens (prefill, training forward), in chunks of
+ * BDSSM_DELTA_CHUNK.
+ *   h_init   NULL (zero) or the state before token 0.
+ *   o        NULL (states only; q may then be NULL), or out.
+ *   h_final  NULL, or out: the state after the row's last token.  May be
+ *            h_init (in place).
+ *   h_chunks NULL, or [batch, ceil(T / 64), heads_v, d_k, d_v] out: the state
+ *            before each chunk, for the backward.
+ *   ws       ws_bytes >= bdssm_delta_workspace_bytes(shape, T, 0).
+ */
+int bdssm_delta_scan(const bdssm_delta_shape *shape, int64_t T, const void *q, const void *k,
+                     const void *v, const float *g, const float *beta, float scale,
+                     const int32_t *lens, const float *h_init, void *o, float *h_final,
+                     float *h_chunks, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The rule token by token on the active tokens (T of any length, meant for
+ * one token to a block): reads the state once and writes it once.
+ *   h_cache  NULL (zero) or the state before the first token.
+ *   o        NULL (state only; q may then be NULL), or out.
+ *   h_out    NULL (a denoising step: the cache is read only), or out: the state
+ *            after the row's last token.  May be h_cache (a commit in place).
+ */
+int bdssm_delta_step(const bdssm_delta_shape *shape, int64_t T, const float *h_cache, const void *q,
+                     const void *k, const void *v, const float *g, const float *beta, float scale,
+                     const int32_t *lens, void *o, float *h_out, hipStream_t stream);
+
+/* Workspace bytes of the scan over T tokens, or of its backward (bwd
+ * nonzero); (size_t)-1 if the shape is invalid. */
+size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *shape, int64_t T, int bwd);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,7 +40,9 @@ PLAIN = ("bdssm_prefill", "bdssm_block_step", "bdssm_commit", "bdssm_train_scan"
 EXPORTS = PLAIN + tuple(f + "_ex" for f in PLAIN) + (
     "bdssm_prefill_noalloc", "bdssm_train_scan_blocks", "bdssm_train_scan_bwd",
     "bdssm_train_scan_blocks_bwd", "bdssm_workspace_bytes", "bdssm_workspace_bytes_op",
-    "bdssm_status_str", "bdssm_version")
+    "bdssm_status_str", "bdssm_version") + (
+    # the hybrid layer's other operators (hybrid.py)
+    "bdssm_delta_scan", "bdssm_delta_step", "bdssm_delta_workspace_bytes")
 
 
 class BdssmError(RuntimeError):
@@ -95,12 +97,14 @@ def load():
     G = ctypes.POINTER(FusionGrads)
     lib.bdssm_train_scan_bwd.argtypes = [S, I] + [P] * 17 + [Z, F, G, P]
     lib.bdssm_train_scan_blocks_bwd.argtypes = [S, I] + [P] * 16 + [Z, F, G, P]
+    N = ctypes.c_float
+    lib.bdssm_delta_scan.argtypes = [P, I] + [P] * 5 + [N] + [P] * 6 + [Z, P]
+    lib.bdssm_delta_step.argtypes = [P, I] + [P] * 6 + [N] + [P] * 4
+    lib.bdssm_delta_workspace_bytes.argtypes = [P, I, ctypes.c_int]
     for f in EXPORTS:
-        getattr(lib, f).restype = ctypes.c_int
+        getattr(lib, f).restype = ctypes.c_size_t if "workspace" in f else ctypes.c_int
     lib.bdssm_workspace_bytes.argtypes = [S, I]
-    lib.bdssm_workspace_bytes.restype = ctypes.c_size_t
     lib.bdssm_workspace_bytes_op.argtypes = [S, I, ctypes.c_int]
-    lib.bdssm_workspace_bytes_op.restype = ctypes.c_size_t
     lib.bdssm_status_str.argtypes = [ctypes.c_int]
     lib.bdssm_status_str.restype = ctypes.c_char_p
     _lib = lib

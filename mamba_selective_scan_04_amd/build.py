@@ -8,7 +8,8 @@ source tree).
 The kernel launchers live in launch_*.hip; each is compiled twice, once per
 stream type (-DBDSSM_TIN=float and -DBDSSM_TIN=uint16_t, the bf16 bits), so
 that the template instantiations spread over parallel compiler processes.
-bdssm.hip holds the C ABI and the launch plans.  Objects go to _build/.
+bdssm.hip holds the scan's C ABI and launch plans, hybrid.hip those of the
+hybrid layer's other operators.  Objects go to _build/.
 libbdssm_probe.so (csrc/roof_probe.hip) holds the benchmark's
 microbenchmarks; it is not part of the scan library.
 
@@ -27,8 +28,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
-HEADERS = [os.path.join(CSRC, h) for h in ("bdssm_kernels.hpp", "bdssm_bwd_kernels.hpp", "bdssm_launch.hpp")] + [
+HEADERS = [os.path.join(CSRC, h) for h in (
+    "bdssm_kernels.hpp", "bdssm_bwd_kernels.hpp", "bdssm_launch.hpp", "host_checks.hpp")] + [
     os.path.join(ROOT, "include", "bdssm.h")]
+# the hybrid layer's operators include none of the scan's kernels
+HYBRID_HEADERS = [os.path.join(CSRC, h) for h in ("hybrid_common.hpp", "delta_kernels.hpp", "hybrid_launch.hpp",
+                                                  "host_checks.hpp")] + [os.path.join(ROOT, "include", "bdssm.h")]
+HYBRID_UNITS = ("launch_delta",)
 LAUNCH_UNITS = ("launch_chunk", "launch_bidir", "launch_block", "launch_bwd", "launch_bwd_general")
 STREAM_TYPES = (("f32", "float"), ("bf16", "uint16_t"))
 LIB = os.path.join(HERE, "libbdssm.so")
@@ -55,16 +61,21 @@ def hipcc():
 
 def units():
     """(source, object, extra flags) of every translation unit."""
-    out = [(os.path.join(CSRC, "bdssm.hip"), os.path.join(BUILD_DIR, "bdssm.o"), [])]
-    for u in LAUNCH_UNITS:
+    out = [(os.path.join(CSRC, u + ".hip"), os.path.join(BUILD_DIR, u + ".o"), []) for u in ("bdssm", "hybrid")]
+    for u in LAUNCH_UNITS + HYBRID_UNITS:
         for tag, ctype in STREAM_TYPES:
             out.append((os.path.join(CSRC, u + ".hip"), os.path.join(BUILD_DIR, "%s.%s.o" % (u, tag)),
                         ["-DBDSSM_TIN=" + ctype]))
     return out
 
 
+def headers_of(src):
+    name = os.path.splitext(os.path.basename(src))[0]
+    return HYBRID_HEADERS if name in HYBRID_UNITS + ("hybrid",) else HEADERS
+
+
 def sources():
-    return sorted({s for s, _, _ in units()}) + HEADERS + [PROBE_SRC]
+    return sorted({s for s, _, _ in units()} | set(HEADERS) | set(HYBRID_HEADERS)) + [PROBE_SRC]
 
 
 def up_to_date():
@@ -135,7 +146,7 @@ def build(verbose=False, changed_only=False, jobs=None):
     for src, obj, extra in units() + [(PROBE_SRC, PROBE_OBJ, [])]:
         if changed_only and os.path.exists(obj):
             t = os.path.getmtime(obj)
-            if all(os.path.getmtime(d) <= t for d in [src] + HEADERS):
+            if all(os.path.getmtime(d) <= t for d in [src] + headers_of(src)):
                 continue
         todo.append((src, obj, extra))
     jobs = jobs or min(len(todo) or 1, os.cpu_count() or 4, 12)

@@ -28,6 +28,7 @@
 
 #include "bdssm.h"
 #include "bdssm_launch.hpp"
+#include "host_checks.hpp"
 
 using namespace bdssm_host;
 
@@ -36,16 +37,6 @@ namespace {
 constexpr int kVersion = 10700;   // 1.7.0
 
 // ---------------------------------------------------------------- checking
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range { const void *p; size_t n; };
-
-bool overlaps(Range a, Range b) {
-    if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
-}
 
 int check_shape(const bdssm_shape *s) {
     if (s == nullptr) return BDSSM_ERR_NULL;
@@ -130,11 +121,6 @@ int check_fusion(const bdssm_fusion *f, const bdssm_shape *s, int64_t T, bool wi
         for (const Range &i : ins)
             if (overlaps(o, i)) return BDSSM_ERR_ALIAS;
     return BDSSM_OK;
-}
-
-int launch_status() {
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? BDSSM_OK : BDSSM_ERR_HIP;
 }
 
 // dst <- src (or zeros); src may equal dst.

@@ -1,0 +1,38 @@
+// launch_delta.hip -- launchers of the gated delta rule's kernels.
+// Compiled once per stream type (BDSSM_TIN = float, or uint16_t for bf16).
+#include "hybrid_launch.hpp"
+
+#ifndef BDSSM_TIN
+#error "compiled once per stream type: -DBDSSM_TIN=float or -DBDSSM_TIN=uint16_t"
+#endif
+
+namespace bdssm_host {
+
+template <typename T, int kDk>
+void launch_scan_k(const DeltaCall &c, hipStream_t st) {
+    const dim3 gp((unsigned)c.d.chunks, (unsigned)c.d.hk, (unsigned)c.batch);
+    if (c.d.chunks > 0) hipLaunchKernelGGL((delta_prep_kernel<T, kDk>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.k, c.g, c.beta, c.W, c.d);
+    const ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, c.g, c.W, c.h_init, (T *)c.o, c.h_final, c.h_chunks, c.d};
+    const dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
+    if (c.o != nullptr)
+        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, true>), gc, dim3(kDeltaThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, false>), gc, dim3(kDeltaThreads), 0, st, a);
+}
+
+template <>
+void launch_delta_scan<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) {
+    if (c.dk == 64) launch_scan_k<BDSSM_TIN, 64>(c, st);
+    else launch_scan_k<BDSSM_TIN, 128>(c, st);
+}
+
+template <>
+void launch_delta_step<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) {
+    using T = BDSSM_TIN;
+    const StepArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, c.g, c.beta, c.h_init, (T *)c.o, c.h_final, c.d};
+    const dim3 g((unsigned)(c.d.dv / 32), (unsigned)c.d.hv, (unsigned)c.batch);
+    if (c.dk == 64) hipLaunchKernelGGL((delta_step_kernel<T, 64>), g, dim3(64), 0, st, a);
+    else hipLaunchKernelGGL((delta_step_kernel<T, 128>), g, dim3(64), 0, st, a);
+}
+
+}  // namespace bdssm_host

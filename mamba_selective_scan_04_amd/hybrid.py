@@ -1,0 +1,104 @@
+"""ctypes binding of the hybrid layer's other operators (include/bdssm.h), in
+the manner of bdssm.py: argument marshalling only.
+
+The gated delta rule:
+  delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True, want_chunks=False)
+  delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, want_o=True)
+Shapes: q, k [batch, T, heads_k, d_k]; v, o [batch, T, heads_v, d_v]; g (log
+decay), beta [batch, T, heads_v] fp32; states [batch, heads_v, d_k, d_v] fp32;
+lens [batch] int32 or None.  q, k, v, o share fp32 or bf16.  scale None:
+d_k ** -0.5.  All tensors contiguous and on the current CUDA (HIP) device; work
+is enqueued on torch's current stream and nothing synchronises.
+"""
+import ctypes
+
+import torch
+
+from .bdssm import _check, _dtype_code, _p, _raise, _stream, _workspace, load
+
+DELTA_CHUNK = 64        # BDSSM_DELTA_CHUNK
+
+
+class DeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("heads_k", ctypes.c_int64), ("heads_v", ctypes.c_int64),
+                ("d_k", ctypes.c_int64), ("d_v", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+def _delta(q, k, v, g, beta, lens, scale):
+    """Checks of the delta rule's operands -> (shape, T, device, scale)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("k must be [batch, T, heads_k, d_k] and v [batch, T, heads_v, d_v]")
+    _check(k, "k")
+    code = _dtype_code(k)
+    batch, T, hk, dk = k.shape
+    hv, dv = v.shape[2:]
+    _check(v, "v", k.dtype, (batch, T, hv, dv))
+    _check(q, "q", k.dtype, (batch, T, hk, dk))
+    _check(g, "g", torch.float32, (batch, T, hv))
+    _check(beta, "beta", torch.float32, (batch, T, hv))
+    _check(lens, "lens", torch.int32, (batch,))
+    return DeltaShape(batch, hk, hv, dk, dv, code), T, k.device, float(dk ** -0.5 if scale is None else scale)
+
+
+def delta_workspace_bytes(s, T, bwd=False):
+    """Workspace bytes of delta_scan (or of its backward) for a DeltaShape."""
+    n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 1 if bwd else 0)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid shape for workspace query")
+    return n
+
+
+def _state(s):
+    return (s.batch, s.heads_v, s.d_k, s.d_v)
+
+
+def _chunk_states(s, T):
+    return (s.batch, -(-T // DELTA_CHUNK), s.heads_v, s.d_k, s.d_v)
+
+
+def delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True, want_chunks=False, o=None,
+               h_final=None, h_chunks=None, ws=None):
+    """The gated delta rule over whole rows -> (o or None, h_final, h_chunks or
+    None).  h_chunks: the states before every 64th token, for delta_scan_bwd.
+    Tokens at and behind lens[b] are padding.  q may be None with want_o=False."""
+    want_o = want_o or o is not None
+    s, T, dev, scale = _delta(q, k, v, g, beta, lens, scale)
+    if want_o and q is None:
+        raise ValueError("q is needed for o")
+    _check(h_init, "h_init", torch.float32, _state(s))
+    if want_o and o is None:
+        o = torch.empty_like(v)
+    _check(o, "o", k.dtype, tuple(v.shape))
+    if h_final is None:
+        h_final = torch.empty(_state(s), dtype=torch.float32, device=dev)
+    _check(h_final, "h_final", torch.float32, _state(s))
+    if want_chunks and h_chunks is None:
+        h_chunks = torch.empty(_chunk_states(s, T), dtype=torch.float32, device=dev)
+    _check(h_chunks, "h_chunks", torch.float32, _chunk_states(s, T))
+    if ws is None:
+        n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 0)
+        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)   # a bad shape: the call says so
+    rc = load().bdssm_delta_scan(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
+                                 _p(h_init), _p(o), _p(h_final), _p(h_chunks), _p(ws),
+                                 0 if ws is None else ws.numel(), _stream())
+    _raise("bdssm_delta_scan", rc)
+    return o, h_final, h_chunks
+
+
+def delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, want_o=True, o=None):
+    """The gated delta rule token by token on the active tokens -> o or None.
+    h_cache None: zero state.  h_out None: the cache is read only (a denoising
+    step); h_out=h_cache: the state advances in place (a commit)."""
+    want_o = want_o or o is not None
+    s, T, dev, scale = _delta(q, k, v, g, beta, lens, scale)
+    if want_o and q is None:
+        raise ValueError("q is needed for o")
+    _check(h_cache, "h_cache", torch.float32, _state(s))
+    _check(h_out, "h_out", torch.float32, _state(s))
+    if want_o and o is None:
+        o = torch.empty_like(v)
+    _check(o, "o", k.dtype, tuple(v.shape))
+    rc = load().bdssm_delta_step(ctypes.byref(s), T, _p(h_cache), _p(q), _p(k), _p(v), _p(g), _p(beta), scale,
+                                 _p(lens), _p(o), _p(h_out), _stream())
+    _raise("bdssm_delta_step", rc)
+    return o

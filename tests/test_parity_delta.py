@@ -1,0 +1,123 @@
+"""GPU parity of the gated delta rule (chunked, recurrent) against the
+recurrence in 64 bits."""
+import pytest
+import torch
+
+import mamba_selective_scan_04_amd as m
+from delta_util import check, inputs, reference
+
+pytestmark = pytest.mark.gpu
+
+# batch, T, heads_k, heads_v, d_k, d_v: lengths around the chunk, shared heads, both widths
+SIZES = [(1, 1, 1, 1, 64, 64), (1, 63, 1, 1, 64, 64), (2, 64, 2, 2, 128, 128), (1, 65, 1, 3, 128, 64),
+         (2, 130, 2, 4, 64, 128), (3, 200, 1, 2, 128, 128)]
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def args(c):
+    return c["q"], c["k"], c["v"], c["g"], c["beta"]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_scan(dev, size, dtype):
+    c = inputs(*size, dtype, device=dev)
+    o, h, chunks = m.delta_scan(*args(c), h_init=c["h"], want_chunks=True)
+    r = reference(c, h=c["h"])
+    check(o, r["o"], "o")
+    check(h, r["h"], "h")
+    check(chunks, r["chunks"], "chunks")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scan_from_zero_without_output(dev, dtype):
+    c = inputs(2, 150, 2, 4, 128, 128, dtype, seed=1, device=dev)
+    o, h, chunks = m.delta_scan(None, *args(c)[1:], want_o=False)
+    assert o is None and chunks is None
+    check(h, reference(c)["h"], "h")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_padded_rows(dev, dtype):
+    lens = [130, 0, 1, 64, 200, -3]
+    c = inputs(6, 130, 2, 2, 64, 64, dtype, seed=2, device=dev, lens=lens)
+    for b, n in enumerate(lens):   # what padding holds must not matter
+        n = max(0, min(n, 130))
+        for name in ("q", "k", "v", "g", "beta"):
+            c[name][b, n:] = float("nan")
+    o, h, chunks = m.delta_scan(*args(c), h_init=c["h"], lens=c["lens"], want_chunks=True)
+    r = reference(c, h=c["h"])
+    for b, n in enumerate(lens):
+        assert (o[b, max(0, min(n, 130)):] == 0).all()
+    check(o, r["o"], "o")
+    check(h, r["h"], "h")
+    check(chunks, r["chunks"], "chunks")
+    o2 = m.delta_step(c["h"], *args(c), lens=c["lens"], h_out=(h2 := torch.empty_like(h)))
+    check(o2, r["o"], "step o")
+    check(h2, r["h"], "step h")
+
+
+@pytest.mark.parametrize("decay", [-20.0, 3.0, 60.0])
+def test_decays(dev, decay):
+    """No forgetting, forgetting within a token, decays far below the exponent's range."""
+    c = inputs(1, 140, 1, 2, 64, 64, torch.float32, seed=3, device=dev, decay=decay)
+    r = reference(c, h=c["h"])
+    o, h, _ = m.delta_scan(*args(c), h_init=c["h"])
+    check(o, r["o"], "o")
+    check(h, r["h"], "h")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_resets(dev, dtype):
+    """g = -inf clears the state: each document as if alone."""
+    starts = [0, 5, 64, 100, 101]
+    c = inputs(1, 150, 1, 1, 64, 64, dtype, seed=4, device=dev, resets=starts)
+    o, h, _ = m.delta_scan(*args(c), h_init=c["h"])
+    r = reference(c, h=c["h"])
+    check(o, r["o"], "o")
+    check(h, r["h"], "h")
+    alone = [x[:, 101:].clone() for x in args(c)]   # fresh copies: 16-byte bases
+    o1, h1, _ = m.delta_scan(*alone)
+    check(o[:, 101:], o1.cpu().double(), "alone", 2.0)
+    check(h, h1.cpu().double(), "alone", 2.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [(1, 1, 1, 1, 64, 64), (3, 1, 2, 4, 128, 128), (2, 16, 1, 3, 128, 64), (1, 33, 2, 2, 64, 128)])
+def test_step(dev, size, dtype):
+    c = inputs(*size, dtype, seed=5, device=dev)
+    r = reference(c, h=c["h"])
+    h = c["h"].clone()
+    o = m.delta_step(h, *args(c))                   # denoising: the cache stays
+    assert torch.equal(h, c["h"])
+    check(o, r["o"], "o")
+    assert m.delta_step(h, None, *args(c)[1:], h_out=h, want_o=False) is None   # commit in place
+    check(h, r["h"], "h")
+    check(m.delta_step(None, *args(c)), reference(c)["o"], "from zero")
+
+
+def test_prefill_then_steps_is_one_scan(dev):
+    c = inputs(2, 112, 2, 4, 128, 128, torch.bfloat16, seed=6, device=dev)
+    cutp = lambda a, z: [x[:, a:z].clone(memory_format=torch.contiguous_format) for x in args(c)]  # noqa: E731
+    o, h, _ = m.delta_scan(*cutp(0, 64))
+    outs = [o]
+    for t in range(64, 112, 16):
+        outs.append(m.delta_step(h, *cutp(t, t + 16), h_out=h))
+    r = reference(c)
+    check(torch.cat(outs, 1), r["o"], "o")
+    check(h, r["h"], "h")
+
+
+def test_same_bits_again(dev):
+    c = inputs(2, 300, 2, 4, 128, 128, torch.bfloat16, seed=7, device=dev)
+    a = m.delta_scan(*args(c), want_chunks=True)
+    b = m.delta_scan(*args(c), want_chunks=True)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_empty(dev):
+    c = inputs(2, 0, 1, 1, 64, 64, torch.bfloat16, device=dev)
+    o, h, _ = m.delta_scan(*args(c), h_init=c["h"])
+    assert o.shape == (2, 0, 1, 64) and torch.equal(h, c["h"])
+    c = inputs(0, 10, 1, 1, 64, 64, torch.bfloat16, device=dev)
+    assert m.delta_scan(*args(c))[0].shape == (0, 10, 1, 64)
