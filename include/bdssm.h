@@ -448,6 +448,27 @@ int bdssm_delta_step(const bdssm_delta_shape *shape, int64_t T, const float *h_c
                      const void *k, const void *v, const float *g, const float *beta, float scale,
                      const int32_t *lens, void *o, float *h_out, hipStream_t stream);
 
+/*
+ * Gradients of bdssm_delta_scan.
+ *   h_chunks  the states bdssm_delta_scan returned for the same inputs.
+ *   dout      [batch, T, heads_v, d_v] stream dtype: dJ/do.
+ *   dh_final  NULL (zero) or [batch, heads_v, d_k, d_v] fp32: dJ/dh_final.
+ * Outputs, all overwritten:
+ *   dq, dk    [batch, T, heads_k, d_k] stream dtype, summed over the value heads
+ *             that share them;  dv [batch, T, heads_v, d_v] stream dtype;
+ *   dg, dbeta [batch, T, heads_v] fp32;
+ *   dh_init   NULL, or [batch, heads_v, d_k, d_v] fp32: dJ/dh_init (with h_init
+ *             NULL, the gradient at zero).
+ *   ws        ws_bytes >= bdssm_delta_workspace_bytes(shape, T, 1).
+ * Sums are taken in a fixed order: results are bitwise reproducible.
+ */
+int bdssm_delta_scan_bwd(const bdssm_delta_shape *shape, int64_t T, const void *q, const void *k,
+                         const void *v, const float *g, const float *beta, float scale,
+                         const int32_t *lens, const float *h_chunks, const void *dout,
+                         const float *dh_final, void *dq, void *dk, void *dv, float *dg,
+                         float *dbeta, float *dh_init, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+
 /* Workspace bytes of the scan over T tokens, or of its backward (bwd
  * nonzero); (size_t)-1 if the shape is invalid. */
 size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *shape, int64_t T, int bwd);

@@ -42,7 +42,7 @@ EXPORTS = PLAIN + tuple(f + "_ex" for f in PLAIN) + (
     "bdssm_train_scan_blocks_bwd", "bdssm_workspace_bytes", "bdssm_workspace_bytes_op",
     "bdssm_status_str", "bdssm_version") + (
     # the hybrid layer's other operators (hybrid.py)
-    "bdssm_delta_scan", "bdssm_delta_step", "bdssm_delta_workspace_bytes")
+    "bdssm_delta_scan", "bdssm_delta_scan_bwd", "bdssm_delta_step", "bdssm_delta_workspace_bytes")
 
 
 class BdssmError(RuntimeError):
@@ -99,6 +99,7 @@ def load():
     lib.bdssm_train_scan_blocks_bwd.argtypes = [S, I] + [P] * 16 + [Z, F, G, P]
     N = ctypes.c_float
     lib.bdssm_delta_scan.argtypes = [P, I] + [P] * 5 + [N] + [P] * 6 + [Z, P]
+    lib.bdssm_delta_scan_bwd.argtypes = [P, I] + [P] * 5 + [N] + [P] * 11 + [Z, P]
     lib.bdssm_delta_step.argtypes = [P, I] + [P] * 6 + [N] + [P] * 4
     lib.bdssm_delta_workspace_bytes.argtypes = [P, I, ctypes.c_int]
     for f in EXPORTS:

@@ -60,6 +60,10 @@ __device__ __forceinline__ void chunk_decays(const float *g, int64_t stride, int
     }
 }
 
+// beta = 0 counts as 2^-64, which changes nothing in 32 bits and lets the
+// backward divide by it.
+__device__ __forceinline__ float strength(float beta) { return fabsf(beta) < 0x1p-64f ? 0x1p-64f : beta; }
+
 __device__ __forceinline__ float decay(double d) { return __expf((float)d); }
 
 // One [64, dk] tile of a token-major stream on its way to LDS: 16 bytes at a
@@ -107,15 +111,29 @@ __device__ __forceinline__ void transpose_tile(const uint16_t *tile, uint16_t *o
         }
     }
 }
+// fp32 tiles keep no transposed copy: four-byte reads down a column are free of
+// bank conflicts as they are.
 template <int kDk, int kThreads = kDeltaThreads>
-__device__ __forceinline__ void transpose_tile(const float *tile, float *out) {
+__device__ __forceinline__ void transpose_tile(const float *, float *) {}
+
+template <typename T, int kDk>
+constexpr int kTransSize = sizeof(T) == 2 ? kDk * kTransRow<T> : 4;
+
+// Column `c` of a [64][dk] tile, tokens 32 s .. 32 s + 31 in paired order.
+template <int kDk>
+__device__ __forceinline__ Frag<1> load_column(const uint16_t *, const uint16_t *trans, int c, int s, int grp) {
+    return load_paired(trans + c * kTransRow<uint16_t> + s * 32 + grp * 4);
+}
+template <int kDk>
+__device__ __forceinline__ Frag<3> load_column(const float *tile, const float *, int c, int s, int grp) {
     constexpr int kRow = TileLoad<float, kDk>::kRow;
-    for (int at = threadIdx.x; at < 64 * (kDk / 4); at += kThreads) {
-        const int t = at % 64, c = at / 64 * 4;
-        const f32x4 a = *(const f32x4 *)(tile + t * kRow + c);
+    f32x4 a, b;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[(c + i) * kTransRow<float> + t] = a[i];
+    for (int r = 0; r < 4; ++r) {
+        a[r] = tile[(s * 32 + grp * 4 + r) * kRow + c];
+        b[r] = tile[(s * 32 + 16 + grp * 4 + r) * kRow + c];
     }
+    return split_frag<3>(a, b);
 }
 
 // ------------------------------------------------------------------ W
@@ -129,7 +147,8 @@ template <typename T, int kDk>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__restrict__ k,
                                                                   const float *__restrict__ g,
                                                                   const float *__restrict__ beta,
-                                                                  float *__restrict__ W, DeltaDims d) {
+                                                                  float *__restrict__ W, float *__restrict__ Wt,
+                                                                  DeltaDims d) {
     constexpr int kRow = TileLoad<T, kDk>::kRow;
     __shared__ __attribute__((aligned(16))) T kt[kChunk * kRow];
     __shared__ __attribute__((aligned(16))) float gram[kChunk * 68], N[kChunk * 68];
@@ -160,7 +179,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
     for (int hv = h * d.group; hv < (h + 1) * d.group; ++hv) {
         const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv;
         chunk_decays(g + at, d.hv, n, G);
-        if (threadIdx.x < kChunk) bt[threadIdx.x] = (int)threadIdx.x < n ? beta[at + (int64_t)threadIdx.x * d.hv] : 0.f;
+        if (threadIdx.x < kChunk) bt[threadIdx.x] = (int)threadIdx.x < n ? strength(beta[at + (int64_t)threadIdx.x * d.hv]) : 1.f;
         __syncthreads();
         for (int e = threadIdx.x; e < kChunk * kChunk; e += kDeltaThreads) {
             const int i = e / kChunk, j = e % kChunk;
@@ -207,20 +226,27 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
                 X[i] = y;
             }
             float *blk = Wc + (i * (i + 1) / 2 + wave) * 256;
+            f32x4 w;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) blk[(grp * 4 + r) * 16 + col] = X[i][r] * bj;
+            for (int r = 0; r < 4; ++r) w[r] = X[i][r] * bj;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) blk[(grp * 4 + r) * 16 + col] = w[r];
+            if (Wt != nullptr) *(f32x4 *)(Wt + (blk - W) + col * 16 + grp * 4) = w;
         }
         __syncthreads();
     }
 }
 
-// W's blocks from the workspace into three planes of bf16 parts in LDS.
+// W's blocks (kTransposed: W^T's) from the workspace into three planes of bf16
+// parts in LDS.
+template <bool kTransposed, int kThreads = kDeltaThreads>
 struct WLoad {
-    f32x4 r[3];
+    static constexpr int kN = (kWFloats / 4 + kThreads - 1) / kThreads;
+    f32x4 r[kN];
     __device__ void load(const float *W) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int at = threadIdx.x + i * kDeltaThreads;
+        for (int i = 0; i < kN; ++i) {
+            const int at = threadIdx.x + i * kThreads;
             if (at < kWFloats / 4) r[i] = *(const f32x4 *)(W + at * 4);
         }
     }
@@ -228,13 +254,13 @@ struct WLoad {
     __device__ static void place(int at, int *row, int *colm) {
         const int blk = at / 64, e = at % 64;
         const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
-        *row = it * 16 + e / 4;
-        *colm = jt * 16 + e % 4 * 4;
+        *row = (kTransposed ? jt : it) * 16 + e / 4;
+        *colm = (kTransposed ? it : jt) * 16 + e % 4 * 4;
     }
     __device__ void store(uint16_t *lds) const {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int at = threadIdx.x + i * kDeltaThreads;
+        for (int i = 0; i < kN; ++i) {
+            const int at = threadIdx.x + i * kThreads;
             if (at < kWFloats / 4) {
                 int row, c;
                 place(at, &row, &c);
@@ -248,6 +274,44 @@ struct WLoad {
         }
     }
 };
+
+// P_ij = scale exp(G_i - G_j) q_i.k_j (j <= i) in kParts planes: rows i, or rows
+// j if kTransposed.  Each tile is formed with its rows as the product's
+// columns, so that a lane stores four of a row.
+template <typename T, int kDk, bool kTransposed, int kParts, int kThreads = kDeltaThreads>
+__device__ __forceinline__ void form_p(const T *k, const T *q, const double *G, float scale, uint16_t *P) {
+    constexpr int kRow = TileLoad<T, kDk>::kRow;
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+    for (int tile = threadIdx.x >> 6; tile < kWBlocks; tile += kThreads / 64) {
+        const int it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
+        const T *rows = kTransposed ? q + it * 16 * kRow : k + jt * 16 * kRow;
+        const T *cols = kTransposed ? k + jt * 16 * kRow : q + it * 16 * kRow;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kDk / 32; ++s)
+            acc = mma(load_straight(rows + col * kRow + s * 32 + grp * 8), load_straight(cols + col * kRow + s * 32 + grp * 8), acc);
+        const int row = (kTransposed ? jt : it) * 16 + col, c0 = (kTransposed ? it : jt) * 16 + grp * 4;
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = kTransposed ? c0 + r : row, j = kTransposed ? row : c0 + r;
+            p[r] = j <= i ? scale * decay(G[i] - G[j]) * acc[r] : 0.f;
+        }
+        uint32_t w0[kParts], w1[kParts];
+        split_pair<kParts>(p[0], p[1], w0);
+        split_pair<kParts>(p[2], p[3], w1);
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+            *(uint2 *)(P + x * kChunk * kTri + row * kTri + c0) = make_uint2(w0[x], w1[x]);
+    }
+}
+
+// Zero planes: the halves of 32-wide steps beyond W's and P's triangles are
+// read but never written.
+template <int kThreads = kDeltaThreads>
+__device__ __forceinline__ void zero_planes(uint16_t *p, int planes) {
+    for (int i = threadIdx.x; i < planes * kChunk * kTri / 2; i += kThreads) ((uint32_t *)p)[i] = 0;
+}
 
 // --------------------------------------------------------------- forward chain
 
@@ -266,7 +330,7 @@ struct ChainLds {
     static constexpr int kOut = Stream<T>::kOutParts;
     T k[kChunk * TileLoad<T, kDk>::kRow];
     T q[kChunk * TileLoad<T, kDk>::kRow];
-    T kT[kDk * kTransRow<T>];
+    T kT[kTransSize<T, kDk>];
     uint16_t W[3 * kChunk * kTri];
     uint16_t P[kOut * kChunk * kTri];
     double G[2][kChunk];
@@ -276,7 +340,7 @@ struct ChainLds {
 template <typename T, int kDk, bool kWithO>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs<T> a) {
     using L = ChainLds<T, kDk>;
-    constexpr int kRow = TileLoad<T, kDk>::kRow, kTR = kTransRow<T>, kOut = L::kOut;
+    constexpr int kRow = TileLoad<T, kDk>::kRow, kOut = L::kOut;
     constexpr int kTiles = kDk / 16, kSteps = kDk / 32;
     __shared__ __attribute__((aligned(16))) L l;
     const DeltaDims &d = a.d;
@@ -293,9 +357,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
     const float *Wp = a.W + ((int64_t)b * d.hv + hv) * d.chunks * kWFloats;
     const int64_t state = (int64_t)kDk * d.dv;
 
-    // the upper halves of W's and P's 32-wide steps are never written: zero
-    for (int i = threadIdx.x; i < 3 * kChunk * kTri / 2; i += kDeltaThreads) ((uint32_t *)l.W)[i] = 0;
-    for (int i = threadIdx.x; i < kOut * kChunk * kTri / 2; i += kDeltaThreads) ((uint32_t *)l.P)[i] = 0;
+    zero_planes(l.W, 3);
+    zero_planes(l.P, kOut);
 
     f32x4 S[kTiles];
 #pragma unroll
@@ -306,7 +369,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
                                           : a.h_init[((int64_t)b * d.hv + hv) * state + (int64_t)(t * 16 + grp * 4 + r) * d.dv + n];
 
     TileLoad<T, kDk> kl, ql;
-    WLoad wl;
+    WLoad<false> wl;
     float vr[16];
     auto fetch = [&](int c) {
         const int64_t t0 = (int64_t)c * kChunk;
@@ -342,25 +405,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
         if (c + 1 < chunks) fetch(c + 1);
         transpose_tile<kDk>(l.k, l.kT);
         if (kWithO) {
-            // P, formed transposed (rows j, column i) so that a lane stores four of a row
-            for (int tile = wave; tile < kWBlocks; tile += 4) {
-                const int it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    acc = mma(load_straight(l.k + (jt * 16 + col) * kRow + s * 32 + grp * 8),
-                              load_straight(l.q + (it * 16 + col) * kRow + s * 32 + grp * 8), acc);
-                const int i = it * 16 + col, j0 = jt * 16 + grp * 4;
-                float p[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = j0 + r <= i ? d.scale * decay(G[i] - G[j0 + r]) * acc[r] : 0.f;
-                uint32_t w0[kOut], w1[kOut];
-                split_pair<kOut>(p[0], p[1], w0);
-                split_pair<kOut>(p[2], p[3], w1);
-#pragma unroll
-                for (int x = 0; x < kOut; ++x)
-                    *(uint2 *)(l.P + x * kChunk * kTri + i * kTri + j0) = make_uint2(w0[x], w1[x]);
-            }
+            form_p<T, kDk, false, kOut>(l.k, l.q, G, d.scale, l.P);
         }
         if (a.h_chunks != nullptr) {
             float *out = a.h_chunks + (((int64_t)b * d.chunks + c) * d.hv + hv) * state + n;
@@ -441,7 +486,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
             for (int r = 0; r < 4; ++r) S[t][r] *= last;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                S[t] = mma(load_paired(l.kT + (t * 16 + col) * kTR + s * 32 + grp * 4), Up[s], S[t]);
+                S[t] = mma(load_column<kDk>(l.k, l.kT, t * 16 + col, s, grp), Up[s], S[t]);
         }
     }
     if (a.h_final != nullptr) {

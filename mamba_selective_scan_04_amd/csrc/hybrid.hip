@@ -104,8 +104,8 @@ extern "C" {
 
 size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *s, int64_t T, int bwd) {
     if (check_delta(s, T) != BDSSM_OK) return (size_t)-1;
-    (void)bwd;
-    return delta_sizes(s, T).W;
+    const DeltaSizes z = delta_sizes(s, T);
+    return bwd ? 2 * z.W + z.hchunks : z.W;   // W, W^T, the states' adjoints
 }
 
 int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const void *k, const void *v,
@@ -135,6 +135,43 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_scan<uint16_t>(c, st);
     else launch_delta_scan<float>(c, st);
+    return launch_status();
+}
+
+int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, const void *k, const void *v,
+                         const float *g, const float *beta, float scale, const int32_t *lens, const float *h_chunks,
+                         const void *dout, const float *dh_final, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                         float *dh_init, void *ws, size_t ws_bytes, hipStream_t st) {
+    const int rc = check_delta(s, T);
+    if (rc) return rc;
+    if (s->batch == 0) return BDSSM_OK;
+    if (T > 0 && (!q || !k || !v || !g || !beta || !h_chunks || !dout || !dq || !dk || !dv || !dg || !dbeta))
+        return BDSSM_ERR_NULL;
+    if (!all_aligned({q, k, v, g, beta, lens, h_chunks, dout, dh_final, dq, dk, dv, dg, dbeta, dh_init, ws}))
+        return BDSSM_ERR_ALIGN;
+    const DeltaSizes z = delta_sizes(s, T);
+    const size_t need = 2 * z.W + z.hchunks;
+    if (!distinct({{q, z.qk}, {k, z.qk}, {v, z.vo}, {g, z.gate}, {beta, z.gate}, {lens, (size_t)s->batch * 4},
+                   {h_chunks, z.hchunks}, {dout, z.vo}, {dh_final, z.state}},
+                  {{dq, z.qk}, {dk, z.qk}, {dv, z.vo}, {dg, z.gate}, {dbeta, z.gate}, {dh_init, z.state}, {ws, need}}))
+        return BDSSM_ERR_ALIAS;
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return BDSSM_ERR_WORKSPACE;
+    DeltaCall c = delta_call(s, T, q, k, v, g, beta, scale, lens);
+    c.h_chunks = const_cast<float *>(h_chunks);
+    c.dout = dout;
+    c.dh_final = dh_final;
+    c.W = (float *)ws;
+    c.Wt = c.W + z.W / 4;
+    c.dS = c.Wt + z.W / 4;
+    c.dq = dq;
+    c.dk_out = dk;
+    c.dv_out = dv;
+    c.dg = dg;
+    c.dbeta = dbeta;
+    c.dh_init = dh_init;
+    (void)hipGetLastError();
+    if (s->dtype == BDSSM_BF16) launch_delta_bwd<uint16_t>(c, st);
+    else launch_delta_bwd<float>(c, st);
     return launch_status();
 }
 

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "bdssm.h"
+#include "delta_bwd_kernels.hpp"
 #include "delta_kernels.hpp"
 
 namespace bdssm_host {
@@ -19,6 +20,11 @@ struct DeltaCall {
     const float *g, *beta, *h_init;
     void *o;
     float *h_final, *h_chunks, *W;
+    // backward
+    const void *dout;
+    const float *dh_final;
+    float *Wt, *dS, *dh_init, *dg, *dbeta;
+    void *dq, *dk_out, *dv_out;
     int64_t batch;
     int dk;
     DeltaDims d;
@@ -28,6 +34,10 @@ template <typename T>
 void launch_delta_scan(const DeltaCall &c, hipStream_t st);
 template <typename T>
 void launch_delta_step(const DeltaCall &c, hipStream_t st);
+template <typename T>
+void launch_delta_bwd(const DeltaCall &c, hipStream_t st);
+template <> void launch_delta_bwd<float>(const DeltaCall &, hipStream_t);
+template <> void launch_delta_bwd<uint16_t>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_scan<float>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_scan<uint16_t>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_step<float>(const DeltaCall &, hipStream_t);

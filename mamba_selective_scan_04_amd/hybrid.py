@@ -3,6 +3,7 @@ the manner of bdssm.py: argument marshalling only.
 
 The gated delta rule:
   delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True, want_chunks=False)
+  delta_scan_bwd(q, k, v, g, beta, h_chunks, do, scale=None, lens=None, dh_final=None, want_dh_init=False)
   delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, want_o=True)
 Shapes: q, k [batch, T, heads_k, d_k]; v, o [batch, T, heads_v, d_v]; g (log
 decay), beta [batch, T, heads_v] fp32; states [batch, heads_v, d_k, d_v] fp32;
@@ -83,6 +84,30 @@ def delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True
                                  0 if ws is None else ws.numel(), _stream())
     _raise("bdssm_delta_scan", rc)
     return o, h_final, h_chunks
+
+
+def delta_scan_bwd(q, k, v, g, beta, h_chunks, do, scale=None, lens=None, dh_final=None, want_dh_init=False, ws=None):
+    """Gradients of delta_scan given do (and dJ/dh_final) -> dict with dq, dk, dv
+    (stream dtype), dg, dbeta (fp32) and dh_init (fp32 or None).  h_chunks: what
+    delta_scan(..., want_chunks=True) returned for the same inputs."""
+    if q is None:
+        raise ValueError("q is needed for the gradients")
+    s, T, dev, scale = _delta(q, k, v, g, beta, lens, scale)
+    if h_chunks is None or do is None:
+        raise ValueError("h_chunks and do are needed for the gradients")
+    _check(h_chunks, "h_chunks", torch.float32, _chunk_states(s, T))
+    _check(do, "do", k.dtype, tuple(v.shape))
+    _check(dh_final, "dh_final", torch.float32, _state(s))
+    dq, dk, dv, dg, dbeta = (torch.empty_like(x) for x in (q, k, v, g, beta))
+    dh = torch.empty(_state(s), dtype=torch.float32, device=dev) if want_dh_init else None
+    if ws is None:
+        n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 1)
+        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)
+    rc = load().bdssm_delta_scan_bwd(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
+                                     _p(h_chunks), _p(do), _p(dh_final), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta),
+                                     _p(dh), _p(ws), 0 if ws is None else ws.numel(), _stream())
+    _raise("bdssm_delta_scan_bwd", rc)
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dh_init": dh}
 
 
 def delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, want_o=True, o=None):
