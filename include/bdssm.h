@@ -473,6 +473,82 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *shape, int64_t T, const void *
  * nonzero); (size_t)-1 if the shape is invalid. */
 size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *shape, int64_t T, int bwd);
 
+/*
+ * The attention's cache in 8 bits, by pages.  A page holds page_len tokens of
+ * every key/value head, each head with one scale: value = code * scale.
+ *   k_cache [n_pages, heads_kv, page_len, head_dim]  codes, by token
+ *   v_cache [n_pages, heads_kv, head_dim, page_len]  codes, by channel
+ *   k_scale, v_scale [n_pages, heads_kv]             fp32
+ *   page_table [batch, max_pages] int32: the page of each page_len tokens of a
+ *           row.  An entry outside 0..n_pages-1 stands for no page: it is not
+ *           written, and its tokens are not seen.
+ *   ctx_lens [batch] int32: tokens of the row in the cache (a row may have none;
+ *           more than max_pages * page_len count as that many).
+ * Rows may share pages that they only read.
+ * Limits: head_dim 64 or 128; page_len 16, 32, 64 or 128; heads_q a multiple of
+ * heads_kv; batch at most 32767.
+ */
+typedef enum {
+    BDSSM_E4M3 = 0,   /* 8-bit float (4 exponent, 3 mantissa bits, largest 448) */
+    BDSSM_I8 = 1      /* 8-bit integer, -127..127 */
+} bdssm_code;
+
+typedef struct {
+    int64_t batch;
+    int64_t heads_q;
+    int64_t heads_kv;
+    int64_t head_dim;
+    int64_t page_len;
+    int64_t n_pages;
+    int64_t max_pages;
+    int32_t dtype;     /* bdssm_dtype of q, k, v, o */
+    int32_t code;      /* bdssm_code of the cache */
+} bdssm_kv_shape;
+
+/*
+ * Finished blocks into the cache: row b's first floor(lens[b] / page_len) whole
+ * blocks of k, v [batch, T, heads_kv, head_dim] become the pages from position
+ * floor(ctx_lens[b] / page_len) of its table row on.  Tokens behind the last
+ * whole block are left to the caller (they stay active tokens of
+ * bdssm_kv_attn_step); pages and scales not named are left as they are.  lens
+ * NULL: T for every row.  ctx_lens is read, not advanced.  The pages written by
+ * one call must differ (else their content is one of the writers' or a mix).
+ * scale = max(a r, 2^-126) with a the largest finite magnitude of the block and
+ * head and r = 1/448 (e4m3) or 1/127 (int8) rounded to fp32; code = value / scale
+ * (an fp32 division) to nearest even.
+ * Infinities become the largest code, NaN a NaN (e4m3) or 0 (int8).
+ */
+int bdssm_kv_commit(const bdssm_kv_shape *shape, int64_t T, const void *k, const void *v,
+                    const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens,
+                    void *k_cache, float *k_scale, void *v_cache, float *v_scale,
+                    hipStream_t stream);
+
+/*
+ * The active block's attention: queries over the cache and the active tokens'
+ * own keys and values.
+ *   k, v  [batch, L, heads_kv, head_dim] stream dtype: active tokens, row b's
+ *         first lens[b] (NULL: L; values below 0 count as 0, above L as L).
+ *   q, o  [batch, Lq, heads_q, head_dim], Lq <= L: the queries of the row's last
+ *         n = min(Lq, lens[b]) active tokens, query i that of active token
+ *         lens[b] - n + i.  o is 0 for queries from n on, and where nothing is
+ *         seen.
+ *   causal 0: every query sees the whole cached context and all active tokens
+ *         (a denoising step).  Else active token j only where j is not behind
+ *         the query's own.
+ *   scale multiplies the scores.  No mask but these; cached positions from
+ *         ctx_lens[b] on are not seen, whatever their codes.
+ *   ws    ws_bytes >= bdssm_kv_workspace_bytes(shape, Lq).  Need not be cleared.
+ */
+int bdssm_kv_attn_step(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, const void *q,
+                       const void *k, const void *v, const void *k_cache, const float *k_scale,
+                       const void *v_cache, const float *v_scale, const int32_t *page_table,
+                       const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
+                       void *o, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of bdssm_kv_attn_step at Lq queries a row; (size_t)-1 if the
+ * shape is invalid. */
+size_t bdssm_kv_workspace_bytes(const bdssm_kv_shape *shape, int64_t Lq);
+
 #ifdef __cplusplus
 }
 #endif

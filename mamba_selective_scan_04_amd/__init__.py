@@ -13,4 +13,7 @@ from .bdssm import (  # noqa: F401
     OP_PREFILL, OP_TRAIN, OP_FULL, OP_TRAIN_BWD, OP_BLOCKS_BWD, OP_TRAIN_BWD_REV, OP_BLOCKS_BWD_REV,
     F32, BF16, LIB_PATH, EXPORTS,
 )
-from .hybrid import delta_scan, delta_scan_bwd, delta_step, delta_workspace_bytes, DeltaShape, DELTA_CHUNK  # noqa: F401
+from .hybrid import (  # noqa: F401
+    delta_scan, delta_scan_bwd, delta_step, delta_workspace_bytes, DeltaShape, DELTA_CHUNK,
+    kv_cache, kv_commit, kv_attn_step, KvCache, KvShape,
+)

@@ -42,7 +42,8 @@ EXPORTS = PLAIN + tuple(f + "_ex" for f in PLAIN) + (
     "bdssm_train_scan_blocks_bwd", "bdssm_workspace_bytes", "bdssm_workspace_bytes_op",
     "bdssm_status_str", "bdssm_version") + (
     # the hybrid layer's other operators (hybrid.py)
-    "bdssm_delta_scan", "bdssm_delta_scan_bwd", "bdssm_delta_step", "bdssm_delta_workspace_bytes")
+    "bdssm_delta_scan", "bdssm_delta_scan_bwd", "bdssm_delta_step", "bdssm_delta_workspace_bytes",
+    "bdssm_kv_commit", "bdssm_kv_attn_step", "bdssm_kv_workspace_bytes")
 
 
 class BdssmError(RuntimeError):
@@ -102,6 +103,9 @@ def load():
     lib.bdssm_delta_scan_bwd.argtypes = [P, I] + [P] * 5 + [N] + [P] * 11 + [Z, P]
     lib.bdssm_delta_step.argtypes = [P, I] + [P] * 6 + [N] + [P] * 4
     lib.bdssm_delta_workspace_bytes.argtypes = [P, I, ctypes.c_int]
+    lib.bdssm_kv_commit.argtypes = [P, I] + [P] * 10
+    lib.bdssm_kv_attn_step.argtypes = [P, I, I] + [P] * 10 + [ctypes.c_int, N, P, P, Z, P]
+    lib.bdssm_kv_workspace_bytes.argtypes = [P, I]
     for f in EXPORTS:
         getattr(lib, f).restype = ctypes.c_size_t if "workspace" in f else ctypes.c_int
     lib.bdssm_workspace_bytes.argtypes = [S, I]

@@ -32,10 +32,10 @@ HEADERS = [os.path.join(CSRC, h) for h in (
     "bdssm_kernels.hpp", "bdssm_bwd_kernels.hpp", "bdssm_launch.hpp", "host_checks.hpp")] + [
     os.path.join(ROOT, "include", "bdssm.h")]
 # the hybrid layer's operators include none of the scan's kernels
-HYBRID_HEADERS = [os.path.join(CSRC, h) for h in ("hybrid_common.hpp", "delta_kernels.hpp", "delta_bwd_kernels.hpp",
+HYBRID_HEADERS = [os.path.join(CSRC, h) for h in ("hybrid_common.hpp", "delta_kernels.hpp", "delta_bwd_kernels.hpp", "kv_kernels.hpp",
                                                   "hybrid_launch.hpp",
                                                   "host_checks.hpp")] + [os.path.join(ROOT, "include", "bdssm.h")]
-HYBRID_UNITS = ("launch_delta",)
+HYBRID_UNITS = ("launch_delta", "launch_kv")
 LAUNCH_UNITS = ("launch_chunk", "launch_bidir", "launch_block", "launch_bwd", "launch_bwd_general")
 STREAM_TYPES = (("f32", "float"), ("bf16", "uint16_t"))
 LIB = os.path.join(HERE, "libbdssm.so")

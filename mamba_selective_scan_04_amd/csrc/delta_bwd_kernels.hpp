@@ -28,7 +28,8 @@ namespace bdssm_dev {
 template <typename T>
 struct AdjointArgs {
     const T *q, *k, *dout;
-    const float *g, *Wt, *dh_final;   // dh_final null: zero
+    const double *G;
+    const float *Wt, *dh_final;       // dh_final null: zero
     float *dS;                        // [batch, chunks, hv, dk, dv]: dS' of each chunk
     float *dh_init;                   // null: not wanted
     DeltaDims d;
@@ -42,7 +43,7 @@ struct AdjointLds {
     T qT[kTransSize<T, kDk>];
     uint16_t Wt[3 * kChunk * kTri];
     uint16_t Pt[3 * kChunk * kTri];
-    double G[2][kChunk];
+    double G[kChunk];
     float e[kChunk], rest[kChunk];
 };
 
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
     const T *kp = a.k + ((int64_t)b * d.T * d.hk + hk) * kDk;
     const T *qp = a.q + ((int64_t)b * d.T * d.hk + hk) * kDk;
     const T *op = a.dout + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-    const float *gp = a.g + (int64_t)b * d.T * d.hv + hv;
+    const double *Gp = a.G + ((int64_t)b * d.hv + hv) * d.chunks * kChunk;
     const float *Wp = a.Wt + ((int64_t)b * d.hv + hv) * d.chunks * kWFloats;
     zero_planes(l.Wt, 3);
     zero_planes(l.Pt, 3);
@@ -75,7 +76,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
                                             : a.dh_final[((int64_t)b * d.hv + hv) * state + (int64_t)(t * 16 + grp * 4 + r) * d.dv + n];
     TileLoad<T, kDk> kl, ql;
     WLoad<true> wl;
-    float vr[16];
+    T vr[16];
+    double Gr = 0.;
     auto fetch = [&](int c) {
         const int64_t t0 = (int64_t)c * kChunk;
         const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
@@ -85,9 +87,9 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = i / 4 * 16 + grp * 4 + i % 4;
-            vr[i] = t < m ? Stream<T>::load(op + (t0 + t) * vstride) : 0.f;
+            vr[i] = t < m ? op[(t0 + t) * vstride] : T(0);
         }
-        chunk_decays(gp + t0 * d.hv, d.hv, m, l.G[c & 1]);
+        if (threadIdx.x < kChunk) Gr = Gp[(int64_t)c * kChunk + threadIdx.x];
     };
     if (chunks > 0) fetch(chunks - 1);
 
@@ -96,14 +98,15 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
         kl.store(l.k);
         ql.store(l.q);
         wl.store(l.Wt);
-        const double *G = l.G[c & 1];
+        const double *G = l.G;
         if (threadIdx.x < kChunk) {
-            l.e[threadIdx.x] = decay(G[threadIdx.x]);
-            l.rest[threadIdx.x] = decay(G[kChunk - 1] - G[threadIdx.x]);
+            l.G[threadIdx.x] = Gr;
+            l.e[threadIdx.x] = decay(Gr);
+            l.rest[threadIdx.x] = decay(__shfl(Gr, 63, 64) - Gr);
         }
         f32x4 dO[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dO[i / 4][i % 4] = vr[i];
+        for (int i = 0; i < 16; ++i) dO[i / 4][i % 4] = Stream<T>::load(vr + i);
         __syncthreads();
         if (c > 0) fetch(c - 1);
         transpose_tile<kDk>(l.k, l.kT);
@@ -190,7 +193,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
 template <typename T>
 struct GradArgs {
     const T *q, *k, *v, *dout;
-    const float *g, *beta, *W, *Wt, *S, *dS;   // S: h_chunks
+    const double *G;
+    const float *beta, *W, *Wt, *S, *dS;   // S: h_chunks
     T *dq, *dk, *dv;
     float *dg, *dbeta;
     DeltaDims d;
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
         const int n = wave * 16 + col;
         __syncthreads();   // the last head's reads of U and X are done
-        chunk_decays(a.g + at, d.hv, m, l.G);
+        if (threadIdx.x < kChunk) l.G[threadIdx.x] = a.G[(((int64_t)b * d.hv + hv) * d.chunks + c) * kChunk + threadIdx.x];
         if (threadIdx.x < kChunk)
             l.bt[threadIdx.x] = (int)threadIdx.x < m ? strength(a.beta[at + (int64_t)threadIdx.x * d.hv]) : 1.f;
         zero_planes<kThreads>(l.W, 3);

@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
                                                                   const float *__restrict__ g,
                                                                   const float *__restrict__ beta,
                                                                   float *__restrict__ W, float *__restrict__ Wt,
-                                                                  DeltaDims d) {
+                                                                  double *__restrict__ Gs, DeltaDims d) {
     constexpr int kRow = TileLoad<T, kDk>::kRow;
     __shared__ __attribute__((aligned(16))) T kt[kChunk * kRow];
     __shared__ __attribute__((aligned(16))) float gram[kChunk * 68], N[kChunk * 68];
@@ -202,6 +202,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         }
         __syncthreads();
         float *Wc = W + (((int64_t)b * d.hv + hv) * d.chunks + c) * kWFloats;
+        if (threadIdx.x < kChunk) Gs[(((int64_t)b * d.hv + hv) * d.chunks + c) * kChunk + threadIdx.x] = G[threadIdx.x];
         const float bj = bt[r0 + col];
         f32x4 X[4];
 #pragma unroll
@@ -318,7 +319,8 @@ __device__ __forceinline__ void zero_planes(uint16_t *p, int planes) {
 template <typename T>
 struct ChainArgs {
     const T *q, *k, *v;
-    const float *g, *W, *h_init;
+    const double *G;      // the chunks' sums of log decays
+    const float *W, *h_init;
     T *o;                 // null: states only
     float *h_final;       // null: not wanted
     float *h_chunks;      // null, or [batch, chunks, hv, dk, dv]
@@ -333,7 +335,7 @@ struct ChainLds {
     T kT[kTransSize<T, kDk>];
     uint16_t W[3 * kChunk * kTri];
     uint16_t P[kOut * kChunk * kTri];
-    double G[2][kChunk];
+    double G[kChunk];
     float e[kChunk], rest[kChunk];
 };
 
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
     const T *kp = a.k + ((int64_t)b * d.T * d.hk + hk) * kDk;
     const T *qp = a.q + ((int64_t)b * d.T * d.hk + hk) * kDk;
     const T *vp = a.v + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-    const float *gp = a.g + (int64_t)b * d.T * d.hv + hv;
+    const double *Gp = a.G + ((int64_t)b * d.hv + hv) * d.chunks * kChunk;
     const float *Wp = a.W + ((int64_t)b * d.hv + hv) * d.chunks * kWFloats;
     const int64_t state = (int64_t)kDk * d.dv;
 
@@ -370,7 +372,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
 
     TileLoad<T, kDk> kl, ql;
     WLoad<false> wl;
-    float vr[16];
+    T vr[16];         // as stored: nothing may wait for them here
+    double Gr = 0.;   // threads 0..63
     auto fetch = [&](int c) {
         const int64_t t0 = (int64_t)c * kChunk;
         const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
@@ -380,27 +383,28 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = i / 4 * 16 + grp * 4 + i % 4;
-            vr[i] = t < m ? Stream<T>::load(vp + (t0 + t) * vstride) : 0.f;
+            vr[i] = t < m ? vp[(t0 + t) * vstride] : T(0);
         }
-        chunk_decays(gp + t0 * d.hv, d.hv, m, l.G[c & 1]);
+        if (threadIdx.x < kChunk) Gr = Gp[(int64_t)c * kChunk + threadIdx.x];
     };
     if (chunks > 0) fetch(0);
 
     for (int c = 0; c < chunks; ++c) {
         const int64_t t0 = (int64_t)c * kChunk;
         const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
-        __syncthreads();   // the last chunk's reads of LDS are done; G is written
+        __syncthreads();   // the last chunk's reads of LDS are done
         kl.store(l.k);
         if (kWithO) ql.store(l.q);
         wl.store(l.W);
-        const double *G = l.G[c & 1];
-        if (threadIdx.x < kChunk) {
-            l.e[threadIdx.x] = decay(G[threadIdx.x]);
-            l.rest[threadIdx.x] = decay(G[kChunk - 1] - G[threadIdx.x]);
+        const double *G = l.G;
+        if (threadIdx.x < kChunk) {   // one wave: the last token's sum is its last lane's
+            l.G[threadIdx.x] = Gr;
+            l.e[threadIdx.x] = decay(Gr);
+            l.rest[threadIdx.x] = decay(__shfl(Gr, 63, 64) - Gr);
         }
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = vr[i];
+        for (int i = 0; i < 16; ++i) v[i] = Stream<T>::load(vr + i);
         __syncthreads();
         if (c + 1 < chunks) fetch(c + 1);
         transpose_tile<kDk>(l.k, l.kT);

@@ -61,7 +61,9 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 
 struct DeltaSizes {
     int64_t chunks;
-    size_t qk, vo, gate, state, hchunks, W;
+    size_t qk, vo, gate, state, hchunks, W, G;
+    size_t fwd() const { return W + G; }                  // W and the chunks' log decays
+    size_t bwd() const { return 2 * W + G + hchunks; }    // W^T and the states' adjoints too
 };
 
 DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
@@ -74,6 +76,7 @@ DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
     z.state = (size_t)s->batch * s->heads_v * s->d_k * s->d_v * 4;
     z.hchunks = z.state * (size_t)z.chunks;
     z.W = (size_t)s->batch * s->heads_v * z.chunks * kWFloats * 4;
+    z.G = (size_t)s->batch * s->heads_v * z.chunks * kChunk * 8;
     return z;
 }
 
@@ -98,6 +101,88 @@ DeltaCall delta_call(const bdssm_delta_shape *s, int64_t T, const void *q, const
     return c;
 }
 
+// --------------------------------------------------- paged 8-bit cache
+
+int check_kv(const bdssm_kv_shape *s, int64_t L) {
+    if (s == nullptr) return BDSSM_ERR_NULL;
+    if (s->dtype != BDSSM_F32 && s->dtype != BDSSM_BF16) return BDSSM_ERR_DTYPE;
+    if (s->code != BDSSM_E4M3 && s->code != BDSSM_I8) return BDSSM_ERR_DTYPE;
+    if (L < 0 || s->batch < 0 || s->batch > 32767 || s->heads_kv < 1 || s->heads_kv > 32767) return BDSSM_ERR_SHAPE;
+    if (s->heads_q < 1 || s->heads_q > 32767 || s->heads_q % s->heads_kv != 0) return BDSSM_ERR_SHAPE;
+    if (s->head_dim != 64 && s->head_dim != 128) return BDSSM_ERR_SHAPE;
+    if (s->page_len != 16 && s->page_len != 32 && s->page_len != 64 && s->page_len != 128) return BDSSM_ERR_SHAPE;
+    if (s->n_pages < 0 || s->n_pages > 0x7fffffff || s->max_pages < 0 || s->max_pages > 0x7fffffff / s->page_len)
+        return BDSSM_ERR_SHAPE;   // token positions of a row fit 31 bits
+    if (!product_fits({s->n_pages, s->heads_kv, s->page_len, s->head_dim}) || !product_fits({s->batch, s->max_pages}) ||
+        !product_fits({s->batch, L, s->heads_q, s->head_dim}) || L > 0x7fffffff)
+        return BDSSM_ERR_SHAPE;
+    return BDSSM_OK;
+}
+
+struct KvSizes {
+    size_t q, kv, cache, scale, table, row;
+};
+
+KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
+    const size_t e = s->dtype == BDSSM_BF16 ? 2 : 4;
+    KvSizes z;
+    z.q = (size_t)s->batch * Lq * s->heads_q * s->head_dim * e;
+    z.kv = (size_t)s->batch * L * s->heads_kv * s->head_dim * e;
+    z.cache = (size_t)s->n_pages * s->heads_kv * s->page_len * s->head_dim;
+    z.scale = (size_t)s->n_pages * s->heads_kv * 4;
+    z.table = (size_t)s->batch * s->max_pages * 4;
+    z.row = (size_t)s->batch * 4;
+    return z;
+}
+
+// A wave's query tiles: as many as the rows fill, up to four (the accumulators
+// of 64 queries x 128 channels take 128 registers; fp32 streams, whose queries
+// are three parts, two).  Key ranges: until every CU has its workgroups of four
+// waves, but at least one step of 64 keys for each wave of a range.
+KvPlan kv_plan(const bdssm_kv_shape *s, int64_t Lq) {
+    const int64_t rows = Lq * (s->heads_q / s->heads_kv);
+    const int most = s->dtype == BDSSM_F32 && s->head_dim == 128 ? 2 : 4;
+    KvPlan p;
+    p.tiles = rows > 32 && most > 2 ? 4 : rows > 16 ? 2 : 1;
+    const int64_t qtiles = (rows + p.tiles * 16 - 1) / (p.tiles * 16);
+    const int64_t units = s->batch * s->heads_kv * qtiles;
+    const int64_t target = p.tiles == 4 ? 256 : p.tiles == 2 ? 512 : 768;
+    const int64_t ranges = (s->max_pages * s->page_len / 64 + 3) / 4;
+    int64_t n = units > 0 ? (target + units - 1) / units : 1;
+    if (n > ranges) n = ranges;
+    p.qtiles = (int)qtiles;
+    p.splits = (int)(n < 1 ? 1 : n);
+    return p;
+}
+
+size_t kv_workspace(const bdssm_kv_shape *s, const KvPlan &p, size_t *part_o) {
+    if (p.splits <= 1) return 0;
+    const size_t rows = (size_t)s->batch * s->heads_kv * p.qtiles * p.splits * p.tiles * 16;
+    *part_o = rows * s->head_dim * 4;
+    return *part_o + rows * 8;
+}
+
+KvCall kv_call(const bdssm_kv_shape *s, int64_t L, const void *k, const void *v, const int32_t *table, const int32_t *ctx,
+               const int32_t *lens) {
+    KvCall c{};
+    c.k = k;
+    c.v = v;
+    c.batch = s->batch;
+    c.L = L;
+    c.head_dim = (int)s->head_dim;
+    c.code = s->code;
+    c.d.heads_q = (int)s->heads_q;
+    c.d.heads_kv = (int)s->heads_kv;
+    c.d.group = (int)(s->heads_q / s->heads_kv);
+    c.d.page_len = (int)s->page_len;
+    c.d.n_pages = (int)s->n_pages;
+    c.d.max_pages = (int)s->max_pages;
+    c.d.table = table;
+    c.d.ctx = ctx;
+    c.d.lens = lens;
+    return c;
+}
+
 }  // namespace
 
 extern "C" {
@@ -105,7 +190,7 @@ extern "C" {
 size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *s, int64_t T, int bwd) {
     if (check_delta(s, T) != BDSSM_OK) return (size_t)-1;
     const DeltaSizes z = delta_sizes(s, T);
-    return bwd ? 2 * z.W + z.hchunks : z.W;   // W, W^T, the states' adjoints
+    return bwd ? z.bwd() : z.fwd();
 }
 
 int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const void *k, const void *v,
@@ -120,11 +205,11 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     const Range lr{lens, (size_t)s->batch * 4};
     if (!distinct({{o ? q : nullptr, z.qk}, {k, z.qk}, {v, z.vo}, {g, z.gate}, {beta, z.gate}, lr,
                    {h_init == h_final ? nullptr : h_init, z.state}},
-                  {{o, z.vo}, {h_final, z.state}, {h_chunks, z.hchunks}, {ws, z.W}}))
+                  {{o, z.vo}, {h_final, z.state}, {h_chunks, z.hchunks}, {ws, z.fwd()}}))
         return BDSSM_ERR_ALIAS;
-    if (h_init && h_init == h_final && !distinct({{h_init, z.state}}, {{o, z.vo}, {h_chunks, z.hchunks}, {ws, z.W}}))
+    if (h_init && h_init == h_final && !distinct({{h_init, z.state}}, {{o, z.vo}, {h_chunks, z.hchunks}, {ws, z.fwd()}}))
         return BDSSM_ERR_ALIAS;
-    if (z.W > 0 && (ws == nullptr || ws_bytes < z.W)) return BDSSM_ERR_WORKSPACE;
+    if (z.fwd() > 0 && (ws == nullptr || ws_bytes < z.fwd())) return BDSSM_ERR_WORKSPACE;
     if (!o && !h_final && !h_chunks) return BDSSM_OK;
     DeltaCall c = delta_call(s, T, q, k, v, g, beta, scale, lens);
     c.h_init = h_init;
@@ -132,6 +217,7 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     c.h_final = h_final;
     c.h_chunks = h_chunks;
     c.W = (float *)ws;
+    c.G = (double *)(c.W + z.W / 4);
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_scan<uint16_t>(c, st);
     else launch_delta_scan<float>(c, st);
@@ -150,7 +236,7 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, c
     if (!all_aligned({q, k, v, g, beta, lens, h_chunks, dout, dh_final, dq, dk, dv, dg, dbeta, dh_init, ws}))
         return BDSSM_ERR_ALIGN;
     const DeltaSizes z = delta_sizes(s, T);
-    const size_t need = 2 * z.W + z.hchunks;
+    const size_t need = z.bwd();
     if (!distinct({{q, z.qk}, {k, z.qk}, {v, z.vo}, {g, z.gate}, {beta, z.gate}, {lens, (size_t)s->batch * 4},
                    {h_chunks, z.hchunks}, {dout, z.vo}, {dh_final, z.state}},
                   {{dq, z.qk}, {dk, z.qk}, {dv, z.vo}, {dg, z.gate}, {dbeta, z.gate}, {dh_init, z.state}, {ws, need}}))
@@ -162,7 +248,8 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, c
     c.dh_final = dh_final;
     c.W = (float *)ws;
     c.Wt = c.W + z.W / 4;
-    c.dS = c.Wt + z.W / 4;
+    c.G = (double *)(c.Wt + z.W / 4);
+    c.dS = (float *)(c.G + z.G / 8);
     c.dq = dq;
     c.dk_out = dk;
     c.dv_out = dv;
@@ -197,6 +284,76 @@ int bdssm_delta_step(const bdssm_delta_shape *s, int64_t T, const float *h_cache
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_step<uint16_t>(c, st);
     else launch_delta_step<float>(c, st);
+    return launch_status();
+}
+
+int bdssm_kv_commit(const bdssm_kv_shape *s, int64_t T, const void *k, const void *v, const int32_t *page_table,
+                    const int32_t *ctx_lens, const int32_t *lens, void *k_cache, float *k_scale, void *v_cache,
+                    float *v_scale, hipStream_t st) {
+    const int rc = check_kv(s, T);
+    if (rc) return rc;
+    if (s->batch == 0 || T < s->page_len || s->n_pages == 0 || s->max_pages == 0) return BDSSM_OK;
+    if (!k || !v || !page_table || !ctx_lens || !k_cache || !k_scale || !v_cache || !v_scale) return BDSSM_ERR_NULL;
+    if (!all_aligned({k, v, page_table, ctx_lens, lens, k_cache, k_scale, v_cache, v_scale})) return BDSSM_ERR_ALIGN;
+    const KvSizes z = kv_sizes(s, T, 0);
+    if (!distinct({{k, z.kv}, {v, z.kv}, {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row}},
+                  {{k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale}}))
+        return BDSSM_ERR_ALIAS;
+    KvCall c = kv_call(s, T, k, v, page_table, ctx_lens, lens);
+    c.kc = k_cache;
+    c.ks = k_scale;
+    c.vc = v_cache;
+    c.vs = v_scale;
+    (void)hipGetLastError();
+    if (s->dtype == BDSSM_BF16) launch_kv_commit<uint16_t>(c, st);
+    else launch_kv_commit<float>(c, st);
+    return launch_status();
+}
+
+size_t bdssm_kv_workspace_bytes(const bdssm_kv_shape *s, int64_t Lq) {
+    if (check_kv(s, Lq) != BDSSM_OK) return (size_t)-1;
+    size_t part = 0;
+    return kv_workspace(s, kv_plan(s, Lq), &part);
+}
+
+int bdssm_kv_attn_step(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const void *q, const void *k, const void *v,
+                       const void *k_cache, const float *k_scale, const void *v_cache, const float *v_scale,
+                       const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
+                       void *o, void *ws, size_t ws_bytes, hipStream_t st) {
+    const int rc = check_kv(s, L);
+    if (rc) return rc;
+    if (Lq < 0 || Lq > L) return BDSSM_ERR_SHAPE;
+    if (s->batch == 0 || Lq == 0) return BDSSM_OK;
+    const bool cached = s->n_pages > 0 && s->max_pages > 0;
+    if (!q || !k || !v || !o || !ctx_lens || (cached && (!k_cache || !k_scale || !v_cache || !v_scale || !page_table)))
+        return BDSSM_ERR_NULL;
+    if (!all_aligned({q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, o, ws})) return BDSSM_ERR_ALIGN;
+    const KvSizes z = kv_sizes(s, L, Lq);
+    const KvPlan plan = kv_plan(s, Lq);
+    if ((int64_t)plan.qtiles * s->heads_kv > 65535) return BDSSM_ERR_SHAPE;
+    size_t part = 0;
+    const size_t need = kv_workspace(s, plan, &part);
+    if (!distinct({{q, z.q}, {k, z.kv}, {v, z.kv}, {k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale},
+                   {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row}},
+                  {{o, z.q}, {ws, need}}))
+        return BDSSM_ERR_ALIAS;
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return BDSSM_ERR_WORKSPACE;
+    KvCall c = kv_call(s, L, k, v, page_table, ctx_lens, lens);
+    c.q = q;
+    c.kc = const_cast<void *>(k_cache);
+    c.ks = const_cast<float *>(k_scale);
+    c.vc = const_cast<void *>(v_cache);
+    c.vs = const_cast<float *>(v_scale);
+    c.o = o;
+    c.Lq = Lq;
+    c.causal = causal != 0;
+    c.scale = scale;
+    c.plan = plan;
+    c.part_o = (float *)ws;
+    c.part_ml = (float *)((char *)ws + part);
+    (void)hipGetLastError();
+    if (s->dtype == BDSSM_BF16) launch_kv_attn<uint16_t>(c, st);
+    else launch_kv_attn<float>(c, st);
     return launch_status();
 }
 

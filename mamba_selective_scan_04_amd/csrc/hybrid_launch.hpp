@@ -10,6 +10,7 @@
 #include "bdssm.h"
 #include "delta_bwd_kernels.hpp"
 #include "delta_kernels.hpp"
+#include "kv_kernels.hpp"
 
 namespace bdssm_host {
 
@@ -25,6 +26,7 @@ struct DeltaCall {
     const float *dh_final;
     float *Wt, *dS, *dh_init, *dg, *dbeta;
     void *dq, *dk_out, *dv_out;
+    double *G;
     int64_t batch;
     int dk;
     DeltaDims d;
@@ -42,5 +44,31 @@ template <> void launch_delta_scan<float>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_scan<uint16_t>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_step<float>(const DeltaCall &, hipStream_t);
 template <> void launch_delta_step<uint16_t>(const DeltaCall &, hipStream_t);
+
+// How the attention's work is cut: query rows (tokens x heads of a key/value
+// head) in tiles of 16 a wave, keys in `splits` ranges.
+struct KvPlan {
+    int tiles, qtiles, splits;
+};
+
+struct KvCall {
+    const void *q, *k, *v;
+    void *kc, *vc, *o;
+    float *ks, *vs, *part_o, *part_ml;
+    int64_t batch, L, Lq;
+    int head_dim, code, causal;
+    float scale;
+    KvPlan plan;
+    KvDims d;
+};
+
+template <typename T>
+void launch_kv_commit(const KvCall &c, hipStream_t st);
+template <typename T>
+void launch_kv_attn(const KvCall &c, hipStream_t st);
+template <> void launch_kv_commit<float>(const KvCall &, hipStream_t);
+template <> void launch_kv_commit<uint16_t>(const KvCall &, hipStream_t);
+template <> void launch_kv_attn<float>(const KvCall &, hipStream_t);
+template <> void launch_kv_attn<uint16_t>(const KvCall &, hipStream_t);
 
 }  // namespace bdssm_host

@@ -1,0 +1,56 @@
+// launch_kv.hip -- launchers of the paged 8-bit cache's kernels.
+// Compiled once per stream type (BDSSM_TIN = float, or uint16_t for bf16).
+#include "hybrid_launch.hpp"
+
+#ifndef BDSSM_TIN
+#error "compiled once per stream type: -DBDSSM_TIN=float or -DBDSSM_TIN=uint16_t"
+#endif
+
+namespace bdssm_host {
+
+template <typename T, int kCode, int kD>
+void commit_k(const KvCall &c, hipStream_t st) {
+    const CommitArgs<T> a{(const T *)c.k, (const T *)c.v, (uint8_t *)c.kc, (uint8_t *)c.vc, c.ks, c.vs, c.L, c.d};
+    const dim3 g((unsigned)(c.L / c.d.page_len), (unsigned)c.d.heads_kv, (unsigned)(c.batch * 2));
+    switch (c.d.page_len * kD / 256) {
+    case 4: case 8: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 8>), g, dim3(256), 0, st, a); break;
+    case 16: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 16>), g, dim3(256), 0, st, a); break;
+    case 32: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 32>), g, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 64>), g, dim3(256), 0, st, a); break;
+    }
+}
+
+template <typename T, int kCode, int kD>
+void attn_k(const KvCall &c, hipStream_t st) {
+    const AttnArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const uint8_t *)c.kc, (const uint8_t *)c.vc, c.ks, c.vs,
+                        (T *)c.o, c.part_o, c.part_ml, c.L, c.Lq, c.plan.splits, c.plan.qtiles, c.causal,
+                        c.scale * 1.44269504088896341f, c.d};
+    const dim3 g((unsigned)c.plan.splits, (unsigned)(c.d.heads_kv * c.plan.qtiles), (unsigned)c.batch);
+    switch (c.plan.tiles) {
+    case 1: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 2>), g, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 4>), g, dim3(256), 0, st, a); break;
+    }
+    if (c.plan.splits > 1) {
+        const int64_t n = c.Lq * c.d.group * (kD / 4);
+        hipLaunchKernelGGL((kv_join_kernel<T, kD>), dim3((unsigned)((n + 255) / 256), (unsigned)c.d.heads_kv, (unsigned)c.batch),
+                           dim3(256), 0, st, c.part_o, c.part_ml, (T *)c.o, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
+                           c.plan.tiles * 16, c.d);
+    }
+}
+
+template <>
+void launch_kv_commit<BDSSM_TIN>(const KvCall &c, hipStream_t st) {
+    using T = BDSSM_TIN;
+    if (c.head_dim == 64) c.code == kE4m3 ? commit_k<T, kE4m3, 64>(c, st) : commit_k<T, kI8, 64>(c, st);
+    else c.code == kE4m3 ? commit_k<T, kE4m3, 128>(c, st) : commit_k<T, kI8, 128>(c, st);
+}
+
+template <>
+void launch_kv_attn<BDSSM_TIN>(const KvCall &c, hipStream_t st) {
+    using T = BDSSM_TIN;
+    if (c.head_dim == 64) c.code == kE4m3 ? attn_k<T, kE4m3, 64>(c, st) : attn_k<T, kI8, 64>(c, st);
+    else c.code == kE4m3 ? attn_k<T, kE4m3, 128>(c, st) : attn_k<T, kI8, 128>(c, st);
+}
+
+}  // namespace bdssm_host

@@ -8,9 +8,19 @@ The gated delta rule:
 Shapes: q, k [batch, T, heads_k, d_k]; v, o [batch, T, heads_v, d_v]; g (log
 decay), beta [batch, T, heads_v] fp32; states [batch, heads_v, d_k, d_v] fp32;
 lens [batch] int32 or None.  q, k, v, o share fp32 or bf16.  scale None:
-d_k ** -0.5.  All tensors contiguous and on the current CUDA (HIP) device; work
+d_k ** -0.5.
+
+Attention over the paged 8-bit cache:
+  kv_cache(n_pages, heads_kv, head_dim, page_len, code) -> KvCache
+  kv_commit(cache, k, v, page_table, ctx_lens, lens=None)
+  kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None)
+Shapes: k, v [batch, L, heads_kv, head_dim]; q, o [batch, Lq, heads_q,
+head_dim]; page_table [batch, max_pages], ctx_lens, lens [batch] int32.
+
+All tensors contiguous and on the current CUDA (HIP) device; work
 is enqueued on torch's current stream and nothing synchronises.
 """
+import collections
 import ctypes
 
 import torch
@@ -126,4 +136,83 @@ def delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, wan
     rc = load().bdssm_delta_step(ctypes.byref(s), T, _p(h_cache), _p(q), _p(k), _p(v), _p(g), _p(beta), scale,
                                  _p(lens), _p(o), _p(h_out), _stream())
     _raise("bdssm_delta_step", rc)
+    return o
+
+
+CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}     # bdssm_code
+
+# the cache's tensors: codes of keys [n_pages, heads_kv, page_len, head_dim] and
+# values [n_pages, heads_kv, head_dim, page_len] (float8_e4m3fn or int8), their
+# scales [n_pages, heads_kv] fp32
+KvCache = collections.namedtuple("KvCache", "k k_scale v v_scale")
+
+
+class KvShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("heads_q", ctypes.c_int64), ("heads_kv", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("page_len", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("dtype", ctypes.c_int32), ("code", ctypes.c_int32)]
+
+
+def kv_cache(n_pages, heads_kv, head_dim, page_len=16, code=torch.float8_e4m3fn, device="cuda"):
+    """An empty cache (codes and scales zero)."""
+    if code not in CODES:
+        raise TypeError("code must be torch.float8_e4m3fn or torch.int8")
+    z = lambda *s: torch.zeros(*s, dtype=torch.int8, device=device).view(code)  # noqa: E731
+    sc = lambda: torch.zeros(n_pages, heads_kv, dtype=torch.float32, device=device)  # noqa: E731
+    return KvCache(z(n_pages, heads_kv, page_len, head_dim), sc(), z(n_pages, heads_kv, head_dim, page_len), sc())
+
+
+def _kv(cache, k, v, page_table, ctx_lens, lens, heads_q):
+    """Checks of the cache's operands -> (shape, L)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [batch, L, heads_kv, head_dim]")
+    if not isinstance(cache, KvCache) or not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
+        raise ValueError("cache must be a KvCache with k [n_pages, heads_kv, page_len, head_dim]")
+    if cache.k.dtype not in CODES:
+        raise TypeError("the cache's codes must be float8_e4m3fn or int8, got %s" % cache.k.dtype)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    batch, L, hkv, d = k.shape
+    n_pages, page = cache.k.shape[0], cache.k.shape[2]
+    _check(k, "k")
+    _check(v, "v", k.dtype, k.shape)
+    _check(cache.k, "cache.k", cache.k.dtype, (n_pages, hkv, page, d))
+    _check(cache.v, "cache.v", cache.k.dtype, (n_pages, hkv, d, page))
+    _check(cache.k_scale, "cache.k_scale", torch.float32, (n_pages, hkv))
+    _check(cache.v_scale, "cache.v_scale", torch.float32, (n_pages, hkv))
+    _check(page_table, "page_table", torch.int32, (batch, page_table.shape[1]))
+    _check(ctx_lens, "ctx_lens", torch.int32, (batch,))
+    _check(lens, "lens", torch.int32, (batch,))
+    return KvShape(batch, heads_q or hkv, hkv, d, page, n_pages, page_table.shape[1], _dtype_code(k), CODES[cache.k.dtype]), L
+
+
+def kv_commit(cache, k, v, page_table, ctx_lens, lens=None):
+    """The rows' whole blocks of k, v into the pages behind ctx_lens, in place.
+    Tokens behind a row's last whole block are not cached."""
+    s, L = _kv(cache, k, v, page_table, ctx_lens, lens, 0)
+    rc = load().bdssm_kv_commit(ctypes.byref(s), L, _p(k), _p(v), _p(page_table), _p(ctx_lens), _p(lens), _p(cache.k),
+                                _p(cache.k_scale), _p(cache.v), _p(cache.v_scale), _stream())
+    _raise("bdssm_kv_commit", rc)
+
+
+def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None, o=None, ws=None):
+    """Attention of the active tokens' queries over the cache and the active keys
+    and values -> o.  Lq <= L queries a row: those of its last active tokens.
+    causal: among the active tokens; scale None: head_dim ** -0.5."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, Lq, heads_q, head_dim]")
+    s, L = _kv(cache, k, v, page_table, ctx_lens, lens, q.shape[2])
+    Lq = q.shape[1]
+    _check(q, "q", k.dtype, (s.batch, Lq, s.heads_q, s.head_dim))
+    if o is None:
+        o = torch.empty_like(q)
+    _check(o, "o", k.dtype, tuple(q.shape))
+    if ws is None:
+        n = load().bdssm_kv_workspace_bytes(ctypes.byref(s), Lq)
+        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, k.device)   # a bad shape: the call says so
+    rc = load().bdssm_kv_attn_step(ctypes.byref(s), L, Lq, _p(q), _p(k), _p(v), _p(cache.k), _p(cache.k_scale),
+                                   _p(cache.v), _p(cache.v_scale), _p(page_table), _p(ctx_lens), _p(lens),
+                                   1 if causal else 0, float(s.head_dim ** -0.5 if scale is None else scale), _p(o),
+                                   _p(ws), 0 if ws is None else ws.numel(), _stream())
+    _raise("bdssm_kv_attn_step", rc)
     return o
