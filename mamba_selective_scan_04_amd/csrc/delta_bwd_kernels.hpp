@@ -28,98 +28,51 @@ namespace bdssm_dev {
 template <typename T>
 struct AdjointArgs {
     const T *q, *k, *dout;
-    const double *G;
-    const float *Wt, *dh_final;       // dh_final null: zero
+    const Mats<3> *mats;
+    const float *dh_final;            // null: zero
     float *dS;                        // [batch, chunks, hv, dk, dv]: dS' of each chunk
     float *dh_init;                   // null: not wanted
     DeltaDims d;
 };
 
 template <typename T, int kDk>
-struct AdjointLds {
-    T k[kChunk * TileLoad<T, kDk>::kRow];
-    T q[kChunk * TileLoad<T, kDk>::kRow];
-    T kT[kTransSize<T, kDk>];
-    T qT[kTransSize<T, kDk>];
-    uint16_t Wt[3 * kChunk * kTri];
-    uint16_t Pt[3 * kChunk * kTri];
-    double G[kChunk];
-    float e[kChunk], rest[kChunk];
+struct AdjointStage {
+    Tile<T, kDk> k, q;
+    Tile<T, 64> o;
+    Mats<3> m;
 };
 
 template <typename T, int kDk>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(AdjointArgs<T> a) {
-    using L = AdjointLds<T, kDk>;
-    constexpr int kRow = TileLoad<T, kDk>::kRow, kTiles = kDk / 16, kSteps = kDk / 32, kIn = Stream<T>::kParts;
-    __shared__ __attribute__((aligned(16))) L l;
-    const DeltaDims &d = a.d;
-    const int hv = blockIdx.y, b = blockIdx.z, hk = hv / d.group;
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
-    const int n = blockIdx.x * 64 + wave * 16 + col;
-    const int64_t len = row_len(d, b);
-    const int chunks = (int)((len + kChunk - 1) / kChunk);
-    const int64_t kstride = (int64_t)d.hk * kDk, vstride = (int64_t)d.hv * d.dv, state = (int64_t)kDk * d.dv;
-    const T *kp = a.k + ((int64_t)b * d.T * d.hk + hk) * kDk;
-    const T *qp = a.q + ((int64_t)b * d.T * d.hk + hk) * kDk;
-    const T *op = a.dout + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-    const double *Gp = a.G + ((int64_t)b * d.hv + hv) * d.chunks * kChunk;
-    const float *Wp = a.Wt + ((int64_t)b * d.hv + hv) * d.chunks * kWFloats;
-    zero_planes(l.Wt, 3);
-    zero_planes(l.Pt, 3);
-
+struct Adjoint {
+    static constexpr int kTiles = kDk / 16, kSteps = kDk / 32, kIn = Stream<T>::kParts;
+    using Stage = AdjointStage<T, kDk>;
     f32x4 S[kTiles];   // the adjoint of the state
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            S[t][r] = a.dh_final == nullptr ? 0.f
-                                            : a.dh_final[((int64_t)b * d.hv + hv) * state + (int64_t)(t * 16 + grp * 4 + r) * d.dv + n];
-    TileLoad<T, kDk> kl, ql;
-    WLoad<true> wl;
-    T vr[16];
-    double Gr = 0.;
-    auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * kChunk;
-        const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
-        kl.load(kp + t0 * kstride, kstride, m);
-        ql.load(qp + t0 * kstride, kstride, m);
-        wl.load(Wp + (int64_t)c * kWFloats);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = i / 4 * 16 + grp * 4 + i % 4;
-            vr[i] = t < m ? op[(t0 + t) * vstride] : T(0);
-        }
-        if (threadIdx.x < kChunk) Gr = Gp[(int64_t)c * kChunk + threadIdx.x];
-    };
-    if (chunks > 0) fetch(chunks - 1);
+    const AdjointArgs<T> &a;
+    const T *kp, *qp, *op;
+    int64_t kstride, vstride, len;
+    int hv, b, wave, col, grp, n;
 
-    for (int c = chunks - 1; c >= 0; --c) {
-        __syncthreads();
-        kl.store(l.k);
-        ql.store(l.q);
-        wl.store(l.Wt);
-        const double *G = l.G;
-        if (threadIdx.x < kChunk) {
-            l.G[threadIdx.x] = Gr;
-            l.e[threadIdx.x] = decay(Gr);
-            l.rest[threadIdx.x] = decay(__shfl(Gr, 63, 64) - Gr);
-        }
-        f32x4 dO[4];
+    __device__ __forceinline__ int tokens(int c) const {
+        const int64_t left = len - (int64_t)c * kChunk;
+        return left < kChunk ? (int)left : kChunk;
+    }
+    __device__ __forceinline__ void fill(Stage &l, int c) {
+        const int64_t t0 = (int64_t)c * kChunk;
+        const int m = tokens(c);
+        l.k.template fill<4>(kp + t0 * kstride, kstride, m);
+        l.q.template fill<4>(qp + t0 * kstride, kstride, m);
+        l.o.template fill<4>(op + t0 * vstride, vstride, m);
+        fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
+    }
+    __device__ __forceinline__ void store_state(float *out) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dO[i / 4][i % 4] = Stream<T>::load(vr + i);
-        __syncthreads();
-        if (c > 0) fetch(c - 1);
-        transpose_tile<kDk>(l.k, l.kT);
-        transpose_tile<kDk>(l.q, l.qT);
-        form_p<T, kDk, true, 3>(l.k, l.q, G, d.scale, l.Pt);
-        {
-            float *out = a.dS + (((int64_t)b * d.chunks + c) * d.hv + hv) * state + n;
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) out[(int64_t)(t * 16 + grp * 4 + r) * d.dv] = S[t][r];
-        }
-        f32x4 U[4];   // dU
+            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(t, grp, r) * a.d.dv + n] = S[t][r];
+    }
+    __device__ __forceinline__ void step(const Stage &l, int c) {
+        const int m = tokens(c);
+        f32x4 U[4], dO[4];
         {
             Frag<3> Sp[kSteps];
 #pragma unroll
@@ -128,64 +81,112 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
             for (int mt = 0; mt < 4; ++mt) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    acc = mma(load_paired(l.k + (mt * 16 + col) * kRow + s * 32 + grp * 4), Sp[s], acc);
-                const f32x4 e = *(const f32x4 *)(l.rest + mt * 16 + grp * 4);
+                for (int s = 0; s < kSteps; ++s) acc = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], acc);
+                const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
+                dO[mt] = l.o.values(mt, grp, wave * 16, col);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) U[mt][r] = e[r] * acc[r];
+                for (int r = 0; r < 4; ++r) {
+                    U[mt][r] = rest[r] * acc[r];
+                    dO[mt][r] = mt * 16 + grp * 4 + r < m ? dO[mt][r] : 0.f;
+                }
             }
         }
-        __syncthreads();   // the transposes and P^T are written
         {
-            Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
+            const Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int s = mt / 2; s < 2; ++s)
-                    U[mt] = mma(load_planes<3>(l.Pt + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Op[s], U[mt]);
+                for (int s = mt / 2; s < 2; ++s) U[mt] = mma(mat_frag<3>(l.m.P, frag_upper(mt, s)), Op[s], U[mt]);
         }
         f32x4 X[4];
         {
-            Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
+            const Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                X[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = mt / 2; s < 2; ++s)
-                    acc = mma(load_planes<3>(l.Wt + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Up[s], acc);
-                X[mt] = acc;
+                for (int s = mt / 2; s < 2; ++s) X[mt] = mma(mat_frag<3>(l.m.W, frag_upper(mt, s)), Up[s], X[mt]);
             }
         }
-        const float last = l.e[kChunk - 1];
+        const float last = l.m.e[kChunk - 1];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const f32x4 e = *(const f32x4 *)(l.e + mt * 16 + grp * 4);
+            const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 X[mt][r] *= -e[r];
-                dO[mt][r] *= d.scale * e[r];
+                dO[mt][r] *= a.d.scale * e[r];
             }
         }
-        Frag<3> Xp[2] = {split_frag<3>(X[0], X[1]), split_frag<3>(X[2], X[3])};
-        Frag<3> Op[2] = {split_frag<3>(dO[0], dO[1]), split_frag<3>(dO[2], dO[3])};
+        const Frag<3> Xp[2] = {split_frag<3>(X[0], X[1]), split_frag<3>(X[2], X[3])};
+        const Frag<3> Op[2] = {split_frag<3>(dO[0], dO[1]), split_frag<3>(dO[2], dO[3])};
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[t][r] *= last;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                S[t] = mma(load_column<kDk>(l.q, l.qT, t * 16 + col, s, grp), Op[s], S[t]);
-                S[t] = mma(load_column<kDk>(l.k, l.kT, t * 16 + col, s, grp), Xp[s], S[t]);
+                S[t] = mma(l.q.column(t, s, grp, col), Op[s], S[t]);
+                S[t] = mma(l.k.column(t, s, grp, col), Xp[s], S[t]);
             }
         }
     }
-    if (a.dh_init != nullptr) {
-        float *out = a.dh_init + ((int64_t)b * d.hv + hv) * state + n;
+};
+
+template <typename T, int kDk>
+__global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(AdjointArgs<T> a) {
+    using C = Adjoint<T, kDk>;
+    constexpr bool kTwo = sizeof(T) == 2;
+    __shared__ __attribute__((aligned(16))) typename C::Stage l0;
+    __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
+    const DeltaDims &d = a.d;
+    C s{{}, a};
+    s.hv = blockIdx.y;
+    s.b = blockIdx.z;
+    const int hk = s.hv / d.group, lane = lane_id();
+    s.wave = threadIdx.x >> 6;
+    s.col = lane & 15;
+    s.grp = lane >> 4;
+    s.n = blockIdx.x * 64 + s.wave * 16 + s.col;
+    s.len = row_len(d, s.b);
+    s.kstride = (int64_t)d.hk * kDk;
+    s.vstride = (int64_t)d.hv * d.dv;
+    const int64_t tok = (int64_t)s.b * d.T;
+    s.kp = a.k + (tok * d.hk + hk) * kDk;
+    s.qp = a.q + (tok * d.hk + hk) * kDk;
+    s.op = a.dout + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64;
+    const int chunks = (int)((s.len + kChunk - 1) / kChunk);
+    const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[(int64_t)(t * 16 + grp * 4 + r) * d.dv] = S[t][r];
+        for (int r = 0; r < 4; ++r)
+            s.S[t][r] = a.dh_final == nullptr ? 0.f : a.dh_final[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
+    auto keep = [&](int c) { s.store_state(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state); };
+    int c = chunks - 1;
+    if constexpr (kTwo) {
+        if (c >= 0) s.fill(l0, c);
+        for (; c >= 0; c -= 2) {
+            __syncthreads();   // l0 is filled, l1 is read
+            if (c > 0) s.fill(l1, c - 1);
+            keep(c);
+            s.step(l0, c);
+            if (c == 0) break;
+            __syncthreads();
+            if (c > 1) s.fill(l0, c - 2);
+            keep(c - 1);
+            s.step(l1, c - 1);
+        }
+    } else {
+        for (; c >= 0; --c) {
+            __syncthreads();
+            s.fill(l0, c);
+            keep(c);
+            __syncthreads();
+            s.step(l0, c);
+        }
     }
+    if (a.dh_init != nullptr) s.store_state(a.dh_init + head * state);
 }
 
 // ------------------------------------------------------------ chunk gradients
@@ -193,39 +194,36 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
 template <typename T>
 struct GradArgs {
     const T *q, *k, *v, *dout;
+    const Mats<3> *fwd, *bwd;
     const double *G;
-    const float *beta, *W, *Wt, *S, *dS;   // S: h_chunks
+    const float *beta, *S, *dS;   // S: h_chunks
     T *dq, *dk, *dv;
     float *dg, *dbeta;
     DeltaDims d;
 };
 
-// U and X between the two halves of the kernel, [64][dv]: parts in planes for
-// bf16 streams (their results are rounded to bf16: two parts), fp32 else.
+// U and X between the two halves of the kernel, [64][dv] by rows: two parts for
+// bf16 streams (their results are rounded to bf16), fp32 else.
 template <typename T, int kDv>
 struct RowTile;
 template <int kDv>
 struct RowTile<uint16_t, kDv> {
-    static constexpr int kRow = kDv + 8;
-    uint16_t p[2][kChunk * kRow];
-    __device__ void put(int row, int c, float v) {
+    Tile<uint16_t, kDv> p[2];
+    __device__ __forceinline__ void put(int r, int c, float v) {
         const uint32_t h = pk_rne(v, v);
-        p[0][row * kRow + c] = (uint16_t)h;
-        p[1][row * kRow + c] = (uint16_t)pk_rne(v - bf_lo(h), 0.f);
+        const int at = (int)(p[0].piece(r, c / 8) - p[0].e) + c % 8;
+        p[0].e[at] = (uint16_t)h;
+        p[1].e[at] = (uint16_t)pk_rne(v - bf_lo(h), 0.f);
     }
-    __device__ Frag<2> get(int row, int c) const {
-        Frag<2> f;
-        f.p[0] = load_straight(&p[0][row * kRow + c]).p[0];
-        f.p[1] = load_straight(&p[1][row * kRow + c]).p[0];
-        return f;
+    __device__ __forceinline__ Frag<2> get(int r, int s, int grp) const {
+        return Frag<2>{{p[0].row(r, s, grp).p[0], p[1].row(r, s, grp).p[0]}};
     }
 };
 template <int kDv>
 struct RowTile<float, kDv> {
-    static constexpr int kRow = kDv + 4;
-    float p[kChunk * kRow];
-    __device__ void put(int row, int c, float v) { p[row * kRow + c] = v; }
-    __device__ Frag<3> get(int row, int c) const { return load_straight(&p[row * kRow + c]); }
+    Tile<float, kDv> p;
+    __device__ __forceinline__ void put(int r, int c, float v) { p.e[(int)(p.piece(r, c / 4) - p.e) + c % 4] = v; }
+    __device__ __forceinline__ Frag<3> get(int r, int s, int grp) const { return p.row(r, s, grp); }
 };
 
 // eight consecutive fp32 values as parts
@@ -236,17 +234,16 @@ __device__ __forceinline__ Frag<kParts> load_state(const float *p) {
 
 template <typename T, int kDk, int kDv>
 struct GradLds {
-    T k[kChunk * TileLoad<T, kDk>::kRow];
-    T q[kChunk * TileLoad<T, kDk>::kRow];
-    T kT[kTransSize<T, kDk>];
-    T qT[kTransSize<T, kDk>];
+    static constexpr int kOut = Stream<T>::kOutParts;
+    Tile<T, kDk> k, q;
+    typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o;   // dO (fp32 streams: from memory)
     union {
         struct {
-            uint16_t W[3 * kChunk * kTri];   // W, then W^T
-            uint16_t P[3 * kChunk * kTri];   // P, then P^T
+            Mats<3> fwd, bwd;
         };
         struct {
             RowTile<T, kDv> U, X;
+            uint4 pairs[8][kOut][64];   // B fragments of a token by token matrix: (column tile, step)
         };
     };
     double G[kChunk];
@@ -258,17 +255,19 @@ struct GradLds {
 // One workgroup per (chunk, query/key head, batch) and a wave per 16 columns of
 // v: each value head of the group in turn, dQ and dK summed over them in
 // registers.  First by columns as in the chains (U, O, dU, X and the row
-// products), then by rows: wave w takes token tile w % 4 and a share of dk, and
-// forms dQ^T, dK^T as products over dv (S, dS' by rows from memory) and over
-// the chunk's tokens (DP, DA formed as result tiles, which are B operands as
-// they are).
+// products), then by rows: a wave takes 16 of dk (two such, or half the tokens,
+// where waves and dk do not pair up) and forms dQ^T, dK^T as products over dv
+// (rows of S, dS' from memory, each read once) and over the chunk's tokens.  The
+// token by token matrices (DP for dQ, DP and DA + DA^T for dK) are formed in
+// turn, two result tiles to a B fragment as they stand, and shared through LDS.
 template <typename T, int kDk, int kDv>
 __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     using L = GradLds<T, kDk, kDv>;
-    constexpr int kThreads = kDv * 4, kWaves = kDv / 16;
-    constexpr int kRow = TileLoad<T, kDk>::kRow, kSteps = kDk / 32;
+    constexpr int kThreads = kDv * 4, kWaves = kDv / 16, kSteps = kDk / 32, kVSteps = kDv / 32;
     constexpr int kIn = Stream<T>::kParts, kOut = Stream<T>::kOutParts;
-    constexpr int kMine = kDk / 16 / (kWaves / 4);   // dk tiles of a wave
+    constexpr int kDkTiles = kDk / 16;
+    constexpr int kMine = kDkTiles > kWaves ? kDkTiles / kWaves : 1;       // dk tiles of a wave
+    constexpr int kToks = kWaves > kDkTiles ? 4 * kDkTiles / kWaves : 4;   // its token tiles
     __shared__ __attribute__((aligned(16))) L l;
     const DeltaDims &d = a.d;
     const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
@@ -278,161 +277,154 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     const int m = len <= t0 ? 0 : len - t0 < kChunk ? (int)(len - t0) : kChunk;
     const int64_t kstride = (int64_t)d.hk * kDk, vstride = (int64_t)d.hv * kDv, state = (int64_t)kDk * kDv;
     const int64_t kat = (((int64_t)b * d.T + t0) * d.hk + hk) * kDk;
-    const int tok = (wave & 3) * 16 + col, m0 = (wave >> 2) * kMine;   // by rows: this lane's token, first dk tile
+    const int dk0 = wave * kMine % kDkTiles, tk0 = wave * kMine / kDkTiles * kToks;
 
-    f32x4 dQ[kMine], dK[kMine];
+    f32x4 dQ[kMine][kToks], dK[kMine][kToks];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) dQ[i] = dK[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+        for (int j = 0; j < kToks; ++j) dQ[i][j] = dK[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (m > 0) {
-        TileLoad<T, kDk, kThreads> kl, ql;
-        kl.load(a.k + kat, kstride, m);
-        ql.load(a.q + kat, kstride, m);
-        kl.store(l.k);
-        ql.store(l.q);
-        __syncthreads();
-        transpose_tile<kDk, kThreads>(l.k, l.kT);
-        transpose_tile<kDk, kThreads>(l.q, l.qT);
+        l.k.template fill<kWaves>(a.k + kat, kstride, m);
+        l.q.template fill<kWaves>(a.q + kat, kstride, m);
     }
     for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
         const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv;   // of the gates; times dv of v
+        const int64_t unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
         T *dvp = a.dv + at * kDv;
+        const T *dop = a.dout + at * kDv;
         for (int e = threadIdx.x; e < (rows - m) * kDv; e += kThreads)
             Stream<T>::store(dvp + (m + e / kDv) * vstride + e % kDv, 0.f);
         for (int t = m + threadIdx.x; t < rows; t += kThreads) a.dg[at + (int64_t)t * d.hv] = a.dbeta[at + (int64_t)t * d.hv] = 0.f;
         if (m == 0) continue;
         const int64_t chunk_at = (((int64_t)b * d.chunks + c) * d.hv + hv) * state;
-        const int64_t w_at = (((int64_t)b * d.hv + hv) * d.chunks + c) * kWFloats;
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
         const int n = wave * 16 + col;
-        __syncthreads();   // the last head's reads of U and X are done
-        if (threadIdx.x < kChunk) l.G[threadIdx.x] = a.G[(((int64_t)b * d.hv + hv) * d.chunks + c) * kChunk + threadIdx.x];
-        if (threadIdx.x < kChunk)
-            l.bt[threadIdx.x] = (int)threadIdx.x < m ? strength(a.beta[at + (int64_t)threadIdx.x * d.hv]) : 1.f;
-        zero_planes<kThreads>(l.W, 3);
-        zero_planes<kThreads>(l.P, 3);
-        __syncthreads();
-        if (threadIdx.x < kChunk) {
-            l.e[threadIdx.x] = decay(l.G[threadIdx.x]);
-            l.rest[threadIdx.x] = decay(l.G[kChunk - 1] - l.G[threadIdx.x]);
-        }
-        {
-            WLoad<false, kThreads> wl;
-            wl.load(a.W + w_at);
-            wl.store(l.W);
-        }
-        form_p<T, kDk, false, 3, kThreads>(l.k, l.q, l.G, d.scale, l.P);
+        __syncthreads();   // the last head's reads of LDS are done
+        fill_mats<3, kWaves>(a.fwd + unit, &l.fwd);
+        fill_mats<3, kWaves>(a.bwd + unit, &l.bwd);
+        if constexpr (sizeof(T) == 2) l.o.template fill<kWaves>(dop, vstride, m);
         f32x4 v[4], dO[4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = i / 4 * 16 + grp * 4 + i % 4;
-            v[i / 4][i % 4] = t < m ? Stream<T>::load(a.v + at * kDv + t * vstride + n) : 0.f;
-            dO[i / 4][i % 4] = t < m ? Stream<T>::load(a.dout + at * kDv + t * vstride + n) : 0.f;
+            v[i / 4][i % 4] = Stream<T>::load(a.v + at * kDv + (t < m ? t : m - 1) * vstride + n);
+            if constexpr (sizeof(T) == 4) dO[i / 4][i % 4] = dop[(t < m ? t : m - 1) * vstride + n];
+        }
+        if (threadIdx.x < kChunk) {
+            const int t = threadIdx.x;
+            l.G[t] = a.G[unit * kChunk + t];
+            l.bt[t] = t < m ? strength(a.beta[at + (int64_t)t * d.hv]) : 1.f;
         }
         __syncthreads();
-        // by columns: R, O, U
-        f32x4 R[4], O[4], U[4], X[4], Kd[4];
-        float end = 0.f;   // <S, dS'> exp(G_C) + sum of U (K dS') rows
+        if (threadIdx.x < kChunk) {   // these outlast the matrices
+            l.e[threadIdx.x] = l.fwd.e[threadIdx.x];
+            l.rest[threadIdx.x] = l.fwd.rest[threadIdx.x];
+        }
+        // by columns: R, U, O and dO's part of dG
+        f32x4 U[4], X[4], dG[4];
         {
-            Frag<3> Sp[kSteps], Dp[kSteps];
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                f32x4 x[2], y[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int64_t r0 = (int64_t)(s * 32 + i * 16 + grp * 4 + r) * kDv + n;
-                        x[i][r] = Sg[r0];
-                        y[i][r] = dSg[r0];
-                        end = fmaf(x[i][r], y[i][r], end);
-                    }
-                Sp[s] = split_frag<3>(x[0], x[1]);
-                Dp[s] = split_frag<3>(y[0], y[1]);
-            }
-            end *= l.e[kChunk - 1];
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks, kd = ks;
+            f32x4 R[4], O[4];
+            {
+                Frag<3> Sp[kSteps];
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const auto kf = load_paired(l.k + (mt * 16 + col) * kRow + s * 32 + grp * 4);
-                    ks = mma(kf, Sp[s], ks);
-                    kd = mma(kf, Dp[s], kd);
-                    qs = mma(load_paired(l.q + (mt * 16 + col) * kRow + s * 32 + grp * 4), Sp[s], qs);
-                }
-                const f32x4 e = *(const f32x4 *)(l.e + mt * 16 + grp * 4), rest = *(const f32x4 *)(l.rest + mt * 16 + grp * 4);
+                    f32x4 x[2];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    R[mt][r] = fmaf(-e[r], ks[r], v[mt][r]);
-                    O[mt][r] = d.scale * e[r] * qs[r];
-                    Kd[mt][r] = rest[r] * kd[r];
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[i][r] = Sg[(int64_t)state_row(2 * s + i, grp, r) * kDv + n];
+                    Sp[s] = split_frag<3>(x[0], x[1]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        ks = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], ks);
+                        qs = mma(l.q.row(mt * 16 + col, s, grp), Sp[s], qs);
+                    }
+                    const f32x4 e = *(const f32x4 *)(l.fwd.e + mt * 16 + grp * 4);
+                    if constexpr (sizeof(T) == 2) dO[mt] = l.o.values(mt, grp, wave * 16, col);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        R[mt][r] = fmaf(-e[r], ks[r], v[mt][r]);
+                        O[mt][r] = d.scale * e[r] * qs[r];
+                        dO[mt][r] = mt * 16 + grp * 4 + r < m ? dO[mt][r] : 0.f;
+                    }
                 }
             }
-        }
-        {
-            Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
+            const Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                U[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s <= mt / 2; ++s)
-                    acc = mma(load_planes<3>(l.W + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Rp[s], acc);
-                U[mt] = acc;
+                for (int s = 0; s <= mt / 2; ++s) U[mt] = mma(mat_frag<3>(l.fwd.W, frag_lower(mt, s)), Rp[s], U[mt]);
             }
-            Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
+            const Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                for (int s = 0; s <= mt / 2; ++s) O[mt] = mma(mat_frag<3>(l.fwd.P, frag_lower(mt, s)), Up[s], O[mt]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[mt][r] * O[mt][r];
+            }
+        }
+        float end = 0.f;   // <S, dS'> exp(G_C) (by rows, below) + sum of U (K dS') rows
+        {
+            f32x4 dU[4];
+            {
+                Frag<3> Sp[kSteps];
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    f32x4 x[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[i][r] = dSg[(int64_t)state_row(2 * s + i, grp, r) * kDv + n];
+                    Sp[s] = split_frag<3>(x[0], x[1]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    f32x4 kd = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) kd = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], kd);
+                    const f32x4 rest = *(const f32x4 *)(l.bwd.rest + mt * 16 + grp * 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        dU[mt][r] = rest[r] * kd[r];
+                        end = fmaf(U[mt][r], dU[mt][r], end);
+                    }
+                }
+            }
+            const Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int s = 0; s <= mt / 2; ++s)
-                    O[mt] = mma(load_planes<3>(l.P + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Up[s], O[mt]);
-        }
-        __syncthreads();   // W and P are read: their transposes take their place
-        zero_planes<kThreads>(l.W, 3);
-        zero_planes<kThreads>(l.P, 3);
-        __syncthreads();
-        {
-            WLoad<true, kThreads> wl;
-            wl.load(a.Wt + w_at);
-            wl.store(l.W);
-        }
-        form_p<T, kDk, true, 3, kThreads>(l.k, l.q, l.G, d.scale, l.P);
-        __syncthreads();
-        {
-            f32x4 dU[4];
-            Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
+                for (int s = mt / 2; s < 2; ++s) dU[mt] = mma(mat_frag<3>(l.bwd.P, frag_upper(mt, s)), Op[s], dU[mt]);
+            const Frag<3> Dp[2] = {split_frag<3>(dU[0], dU[1]), split_frag<3>(dU[2], dU[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                dU[mt] = Kd[mt];
+                X[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = mt / 2; s < 2; ++s)
-                    dU[mt] = mma(load_planes<3>(l.P + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Op[s], dU[mt]);
-            }
-            Frag<3> Dp[2] = {split_frag<3>(dU[0], dU[1]), split_frag<3>(dU[2], dU[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = mt / 2; s < 2; ++s)
-                    acc = mma(load_planes<3>(l.W + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Dp[s], acc);
-                X[mt] = acc;
+                for (int s = mt / 2; s < 2; ++s) X[mt] = mma(mat_frag<3>(l.bwd.W, frag_upper(mt, s)), Dp[s], X[mt]);
             }
         }
-        __syncthreads();   // W^T and P^T are read: U and X take their place
+        __syncthreads();   // the matrices are read: U and X take their place
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = mt * 16 + grp * 4 + r;
                 const float u = U[mt][r], x = X[mt][r], ib = 1.f / l.bt[t], y = u * ib, z = x * ib;
-                end = fmaf(u, Kd[mt][r], end);
-                float dG = dO[mt][r] * O[mt][r] - x * (v[mt][r] - y) - u * z, db = y * z;
+                float s = dG[mt][r] - x * (v[mt][r] - y) - u * z, db = y * z;
 #pragma unroll
-                for (int s = 1; s < 16; s <<= 1) {
-                    dG += __shfl_xor(dG, s, 64);
-                    db += __shfl_xor(db, s, 64);
+                for (int w = 1; w < 16; w <<= 1) {
+                    s += __shfl_xor(s, w, 64);
+                    db += __shfl_xor(db, w, 64);
                 }
                 if (col == 0) {
-                    l.dG[wave][t] = dG;
+                    l.dG[wave][t] = s;
                     l.db[wave][t] = db;
                 }
                 l.U.put(t, n, u);
@@ -440,106 +432,147 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 if (t < m) Stream<T>::store(dvp + t * vstride + n, x);
             }
         }
+        __syncthreads();
+        // by rows: products over dv
+        const auto dout_row = [&](int r, int s) {
+            if constexpr (sizeof(T) == 2) return l.o.row(r, s, grp);
+            else return load_straight(dop + (r < m ? r : m - 1) * vstride + s * 32 + grp * 8);
+        };
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = dk0 + i;
+            const int64_t r0 = (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * kDv + grp * 8;
+            f32x4 so[kToks], sx[kToks], du[kToks];
+#pragma unroll
+            for (int j = 0; j < kToks; ++j) so[j] = sx[j] = du[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kVSteps; ++s) {
+                f32x4 x[2], y[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    x[h] = *(const f32x4 *)(Sg + r0 + s * 32 + h * 4);
+                    y[h] = *(const f32x4 *)(dSg + r0 + s * 32 + h * 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dot = fmaf(x[h][r], y[h][r], dot);
+                }
+                const Frag<kOut> sf = split_frag<kOut>(x[0], x[1]), df = split_frag<kOut>(y[0], y[1]);
+#pragma unroll
+                for (int j = 0; j < kToks; ++j) {
+                    const int t = (tk0 + j) * 16 + col;
+                    so[j] = mma(sf, dout_row(t, s), so[j]);
+                    sx[j] = mma(sf, l.X.get(t, s, grp), sx[j]);
+                    du[j] = mma(df, l.U.get(t, s, grp), du[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kToks; ++j) {
+                const float et = l.e[(tk0 + j) * 16 + col], rt = l.rest[(tk0 + j) * 16 + col];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dQ[i][j][r] = fmaf(d.scale * et, so[j][r], dQ[i][j][r]);
+                    dK[i][j][r] += rt * du[j][r] - et * sx[j][r];
+                }
+            }
+        }
+        if (tk0 == 0) end = fmaf(l.e[kChunk - 1], dot, end);   // each row of dk once
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) end += __shfl_xor(end, s, 64);
         if (lane == 0) l.ends[wave] = end;
-        __syncthreads();
+        // products over the chunk's tokens.  kind 0: DP^T (rows j, columns i) for
+        // dQ; 1: DP (rows i, columns j), 2: DA + DA^T, for dK.
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind) {
+            const int frags = kind == 2 ? 8 : kFrags;
+            for (int f = wave; f < frags; f += kWaves) {
+                // column tile and step of the fragment
+                const int ct = kind == 2 ? f / 2 : kind == 0 ? (f < 2 ? f : f / 2 + 1) : (f < 4 ? f / 2 : f - 2);
+                const int st = kind == 2 ? f & 1 : kind == 0 ? (f < 2 ? 0 : f & 1) : (f < 4 ? f & 1 : 1);
+                const int t = ct * 16 + col;
+                f32x4 tile[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rt = st * 2 + i;
+                    f32x4 below = {0.f, 0.f, 0.f, 0.f}, above = below;   // rows before / behind the column's token
+                    if (rt <= ct && kind != 1) {
+#pragma unroll
+                        for (int s = 0; s < kVSteps; ++s) {
+                            if (kind == 0) below = mma(l.U.get(rt * 16 + col, s, grp), dout_row(t, s), below);
+                            else below = mma(l.U.get(rt * 16 + col, s, grp), l.X.get(t, s, grp), below);
+                        }
+                    }
+                    if (rt >= ct && kind != 0) {
+#pragma unroll
+                        for (int s = 0; s < kVSteps; ++s) {
+                            if (kind == 1) above = mma(dout_row(rt * 16 + col, s), l.U.get(t, s, grp), above);
+                            else above = mma(l.X.get(rt * 16 + col, s, grp), l.U.get(t, s, grp), above);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = rt * 16 + grp * 4 + r;
+                        const float D = decay(j <= t ? l.G[t] - l.G[j] : l.G[j] - l.G[t]);
+                        const bool in = j < m && t < m;   // repeated rows count for nothing
+                        if (kind == 0) tile[i][r] = j <= t && in ? d.scale * D * below[r] : 0.f;
+                        else if (kind == 1) tile[i][r] = j >= t && in ? d.scale * D * above[r] : 0.f;
+                        else tile[i][r] = j == t || !in ? 0.f : -D * (j < t ? below[r] : above[r]);
+                    }
+                }
+                const Frag<kOut> x = split_frag<kOut>(tile[0], tile[1]);
+#pragma unroll
+                for (int p = 0; p < kOut; ++p) l.pairs[f][p][lane] = __builtin_bit_cast(uint4, x.p[p]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const auto x = kind == 1 ? l.q.column(dk0 + i, s, grp, col) : l.k.column(dk0 + i, s, grp, col);
+#pragma unroll
+                    for (int j = 0; j < kToks; ++j) {
+                        const int ct = tk0 + j;
+                        if (kind == 0 ? s > ct / 2 : kind == 1 ? s < ct / 2 : false) continue;
+                        const int f = kind == 2 ? ct * 2 + s : kind == 0 ? frag_lower(ct, s) : frag_upper(ct, s);
+                        Frag<kOut> y;
+#pragma unroll
+                        for (int p = 0; p < kOut; ++p) y.p[p] = __builtin_bit_cast(bf16x8, l.pairs[f][p][lane]);
+                        if (kind == 0) dQ[i][j] = mma(x, y, dQ[i][j]);
+                        else dK[i][j] = mma(x, y, dK[i][j]);
+                    }
+                }
+            __syncthreads();
+        }
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
-            float dG = 0.f, db = 0.f, ends = 0.f;
+            float s = 0.f, db = 0.f, ends = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                dG += l.dG[w][t];
+                s += l.dG[w][t];
                 db += l.db[w][t];
                 ends += l.ends[w];
             }
-            if (t == kChunk - 1) dG += ends;
+            if (t == kChunk - 1) s += ends;
 #pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const float up = __shfl_down(dG, s, 64);
-                if (t + s < 64) dG += up;
+            for (int w = 1; w < 64; w <<= 1) {
+                const float up = __shfl_down(s, w, 64);
+                if (t + w < 64) s += up;
             }
             if (t < m) {
-                a.dg[at + (int64_t)t * d.hv] = dG;
+                a.dg[at + (int64_t)t * d.hv] = s;
                 a.dbeta[at + (int64_t)t * d.hv] = db;
             }
         }
-        // by rows: products over dv
-        const T *dop = a.dout + at * kDv;
-        auto dout_frag = [&](int row, int c0) {
-            if (row < m) return load_straight(dop + row * vstride + c0);
-            Frag<kIn> z{};
-            return z;
-        };
-        const float et = l.e[tok], rt = l.rest[tok];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            f32x4 so = {0.f, 0.f, 0.f, 0.f}, sx = so, du = so;
-            const int64_t r0 = (int64_t)((m0 + i) * 16 + col) * kDv;
-#pragma unroll
-            for (int s = 0; s < kDv / 32; ++s) {
-                const int c0 = s * 32 + grp * 8;
-                const Frag<kOut> sf = load_state<kOut>(Sg + r0 + c0), df = load_state<kOut>(dSg + r0 + c0);
-                so = mma(sf, dout_frag(tok, c0), so);
-                sx = mma(sf, l.X.get(tok, c0), sx);
-                du = mma(df, l.U.get(tok, c0), du);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dQ[i][r] = fmaf(d.scale * et, so[r], dQ[i][r]);
-                dK[i][r] += rt * du[r] - et * sx[r];
-            }
-        }
-        // products over the chunk's tokens: tiles rows `jt`, column this lane's token
-        const double Gt = l.G[tok];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            f32x4 tq[2], tp[2], ta[2];   // DP^T (for dQ), DP and DA + DA^T (for dK)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int jt = s * 2 + i;
-                f32x4 uo = {0.f, 0.f, 0.f, 0.f}, ou = uo, xu = uo, ux = uo;
-#pragma unroll
-                for (int x = 0; x < kDv / 32; ++x) {
-                    const int c0 = x * 32 + grp * 8;
-                    const auto uj = l.U.get(jt * 16 + col, c0), ut = l.U.get(tok, c0);
-                    if (jt <= (wave & 3)) {
-                        uo = mma(uj, dout_frag(tok, c0), uo);           // U_j.dO_t
-                        ux = mma(uj, l.X.get(tok, c0), ux);             // U_j.X_t
-                    }
-                    if (jt >= (wave & 3)) {
-                        ou = mma(dout_frag(jt * 16 + col, c0), ut, ou);   // dO_j.U_t
-                        xu = mma(l.X.get(jt * 16 + col, c0), ut, xu);     // X_j.U_t
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = jt * 16 + grp * 4 + r;
-                    const float below = j <= tok ? decay(Gt - l.G[j]) : 0.f, above = j >= tok ? decay(l.G[j] - Gt) : 0.f;
-                    tq[i][r] = j <= tok ? d.scale * below * uo[r] : 0.f;
-                    tp[i][r] = j >= tok ? d.scale * above * ou[r] : 0.f;
-                    ta[i][r] = j < tok ? -below * ux[r] : j > tok ? -above * xu[r] : 0.f;
-                }
-            }
-            const auto fq = split_frag<kOut>(tq[0], tq[1]), fp = split_frag<kOut>(tp[0], tp[1]), fa = split_frag<kOut>(ta[0], ta[1]);
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const auto kc = load_column<kDk>(l.k, l.kT, (m0 + i) * 16 + col, s, grp);
-                dQ[i] = mma(kc, fq, dQ[i]);
-                dK[i] = mma(load_column<kDk>(l.q, l.qT, (m0 + i) * 16 + col, s, grp), fp, dK[i]);
-                dK[i] = mma(kc, fa, dK[i]);
-            }
-        }
     }
-    if (tok < rows) {   // padding: m leaves zeros
-        T *dqp = a.dq + kat + tok * kstride, *dkp = a.dk + kat + tok * kstride;
-        const bool pad = tok >= m;
+#pragma unroll
+    for (int j = 0; j < kToks; ++j) {
+        const int t = (tk0 + j) * 16 + col;
+        if (t >= rows) continue;
+        T *dqp = a.dq + kat + t * kstride, *dkp = a.dk + kat + t * kstride;
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};   // padding
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int at = (m0 + i) * 16 + grp * 4;
-            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-            store4(dqp + at, pad ? z : dQ[i]);
-            store4(dkp + at, pad ? z : dK[i]);
+            store4(dqp + state_row(dk0 + i, grp, 0), t < m ? dQ[i][j] : z);
+            store4(dkp + state_row(dk0 + i, grp, 0), t < m ? dK[i][j] : z);
         }
     }
 }

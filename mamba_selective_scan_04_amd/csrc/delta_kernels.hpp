@@ -21,15 +21,17 @@
 // differences of the tokens behind it keep their precision.
 #pragma once
 
+#include <type_traits>
+
 #include "hybrid_common.hpp"
 
 namespace bdssm_dev {
 
 constexpr int kChunk = 64;                 // BDSSM_DELTA_CHUNK
 constexpr int kDeltaThreads = 256;
-constexpr int kWBlocks = 10;               // 16x16 blocks on and below W's diagonal
-constexpr int kWFloats = kWBlocks * 256;   // W of one chunk and head in the workspace
-constexpr int kTri = kChunk + 8;           // row length of the 64x64 tiles' planes in LDS
+constexpr int kBlocks = 10;                // 16x16 blocks on and below the diagonal of a chunk's matrix
+constexpr int kFrags = 6;                  // A fragments (16 x 32) that hold them
+constexpr int kFragBytes = 1024;           // of one part: 16 bytes a lane
 
 struct DeltaDims {
     int64_t T;
@@ -66,93 +68,170 @@ __device__ __forceinline__ float strength(float beta) { return fabsf(beta) < 0x1
 
 __device__ __forceinline__ float decay(double d) { return __expf((float)d); }
 
-// One [64, dk] tile of a token-major stream on its way to LDS: 16 bytes at a
-// time in registers (issued a chunk ahead), zeros behind the row's length.
-template <typename T, int kDk, int kThreads = kDeltaThreads>
-struct TileLoad {
-    static constexpr int kVec = 16 / sizeof(T);
-    static constexpr int kPerRow = kDk / kVec;
-    static constexpr int kN = kChunk * kPerRow / kThreads;
-    static constexpr int kRow = kDk + (sizeof(T) == 2 ? 8 : 4);   // LDS row length
-    uint4 r[kN];
-    __device__ void load(const T *src, int64_t stride, int n) {
+// ------------------------------------------------------------------- tiles
+//
+// A [64][kCols] tile of a token-major stream in LDS, filled by 16-byte loads
+// straight from memory (no registers, any number in flight).  Such a load
+// writes a wave's 64 pieces one after another, so rows cannot be padded;
+// instead piece p of row r lies at place p ^ turn(r), which spreads the same
+// piece of 16 rows over all banks.  Rows behind the chunk's last token repeat
+// it: what they feed is multiplied by zero or not stored.
+typedef __attribute__((address_space(3))) void lds_ptr;
+typedef const __attribute__((address_space(1))) void glb_ptr;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// one wave's 64 x 16 bytes: lane l's piece to base + 16 l
+__device__ __forceinline__ void load_lds(const void *src, void *base) {
+    __builtin_amdgcn_global_load_lds((glb_ptr *)src, (lds_ptr *)base, 16, 0, 0);
+}
+
+template <typename T, int kCols>
+struct Tile {
+    static constexpr int kVec = 16 / sizeof(T);            // elements of a piece
+    static constexpr int kPieces = kCols / kVec;           // of a row
+    static constexpr int kBytes = kChunk * kCols * (int)sizeof(T);
+    T e[kChunk * kCols];
+
+    __device__ static int turn(int r) {
+        return kPieces >= 16 ? r & 15 : r / (16 / kPieces) & (kPieces - 1);
+    }
+    __device__ __forceinline__ const T *piece(int r, int p) const { return e + r * kCols + (p ^ turn(r)) * kVec; }
+
+    // by kWaves waves; m: tokens of the chunk (at least 1)
+    template <int kWaves>
+    __device__ __forceinline__ void fill(const T *src, int64_t stride, int m) {
+        constexpr int kLoads = kBytes / 1024 / kWaves;
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = threadIdx.x + i * kThreads, row = at / kPerRow, c = at % kPerRow;
-            r[i] = row < n ? *(const uint4 *)(src + row * stride + c * kVec) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = (wave * kLoads + i) * 64 + lane, r = at / kPieces, p = at % kPieces ^ turn(r);
+            load_lds(src + (r < m ? r : m - 1) * stride + p * kVec, (char *)e + (wave * kLoads + i) * 1024);
         }
     }
-    __device__ void store(T *lds) const {
+    // eight consecutive elements of a row: columns 32 s + 8 grp ..
+    __device__ __forceinline__ auto row(int r, int s, int grp) const {
+        if constexpr (sizeof(T) == 2) {
+            return load_straight(piece(r, s * 4 + grp));
+        } else {
+            return split_frag<3>(*(const f32x4 *)piece(r, s * 8 + grp * 2), *(const f32x4 *)piece(r, s * 8 + grp * 2 + 1));
+        }
+    }
+    // four tokens t0 .. t0 + 3 of column c0 + 8 (col / 4) + col % 4 (by lane; the
+    // 16 lanes of a group share t0).  bf16: the transposing read gives lane i of
+    // a group column i of what the group's lanes address, 4 rows of 4 x 8 bytes.
+    __device__ __forceinline__ uint2 quad(int t0, int c0, int col) const {
+        static_assert(sizeof(T) == 2, "");
+        const int r = t0 + col / 4, c = c0 + col % 4 * 8;
+        const T *p = piece(r, c / kVec) + c % kVec;
+        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+    }
+    // the same of 16 consecutive columns c0 + col
+    __device__ __forceinline__ uint2 quad16(int t0, int c0, int col) const {
+        const int r = t0 + col / 4, c = c0 + col % 4 * 4;
+        const T *p = piece(r, c / kVec) + c % kVec;
+        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+    }
+    __device__ __forceinline__ float at(int r, int c) const { return Stream<T>::load(piece(r, c / kVec) + c % kVec); }
+
+    // A fragment of the tile's transpose: row `col` of state tile `tile`, tokens
+    // 32 s .. in paired order.  State tiles come in pairs of 32 dk: row m of the
+    // first is dk 8 (m / 4) + m % 4 of the 32, of the second 4 more, so that
+    // lane group g's rows of a pair are dk 8g..8g+7.
+    __device__ __forceinline__ auto column(int tile, int s, int grp, int col) const {
+        const int c0 = tile / 2 * 32 + (tile & 1) * 4;
+        if constexpr (sizeof(T) == 2) {
+            const uint2 a = quad(s * 32 + grp * 4, c0, col), b = quad(s * 32 + 16 + grp * 4, c0, col);
+            return Frag<1>{{frag_of(a.x, a.y, b.x, b.y)}};
+        } else {
+            const int c = c0 + col / 4 * 8 + col % 4;
+            f32x4 a, b;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = threadIdx.x + i * kThreads, row = at / kPerRow, c = at % kPerRow;
-            *(uint4 *)(lds + row * kRow + c * kVec) = r[i];
+            for (int r = 0; r < 4; ++r) {
+                a[r] = at(s * 32 + grp * 4 + r, c);
+                b[r] = at(s * 32 + 16 + grp * 4 + r, c);
+            }
+            return split_frag<3>(a, b);
+        }
+    }
+    // a result tile's registers (rows 16 mt + 4 grp + r, column c0 + col)
+    __device__ __forceinline__ f32x4 values(int mt, int grp, int c0, int col) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 w = quad16(mt * 16 + grp * 4, c0, col);
+            return f32x4{bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
+        } else {
+            f32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = at(mt * 16 + grp * 4 + r, c0 + col);
+            return v;
         }
     }
 };
 
-// LDS tile [64][dk] -> its transpose [dk][64] (row lengths TileLoad::kRow and
-// kTransRow), bf16 by token pairs.
-template <typename T>
-constexpr int kTransRow = kChunk + (sizeof(T) == 2 ? 8 : 4);
+// dk of register r of state tile `tile` (see Tile::column)
+__device__ __forceinline__ int state_row(int tile, int grp, int r) { return tile / 2 * 32 + grp * 8 + (tile & 1) * 4 + r; }
 
-template <int kDk, int kThreads = kDeltaThreads>
-__device__ __forceinline__ void transpose_tile(const uint16_t *tile, uint16_t *out) {
-    constexpr int kRow = TileLoad<uint16_t, kDk>::kRow;
-    for (int at = threadIdx.x; at < 32 * (kDk / 8); at += kThreads) {
-        const int tp = at % 32, c = at / 32 * 8;
-        const uint4 a = *(const uint4 *)(tile + (2 * tp) * kRow + c);
-        const uint4 b = *(const uint4 *)(tile + (2 * tp + 1) * kRow + c);
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *(uint32_t *)(out + (c + 2 * i) * kTransRow<uint16_t> + 2 * tp) = __builtin_amdgcn_perm(bv[i], av[i], 0x05040100u);
-            *(uint32_t *)(out + (c + 2 * i + 1) * kTransRow<uint16_t> + 2 * tp) = __builtin_amdgcn_perm(bv[i], av[i], 0x07060302u);
-        }
-    }
-}
-// fp32 tiles keep no transposed copy: four-byte reads down a column are free of
-// bank conflicts as they are.
-template <int kDk, int kThreads = kDeltaThreads>
-__device__ __forceinline__ void transpose_tile(const float *, float *) {}
-
-template <typename T, int kDk>
-constexpr int kTransSize = sizeof(T) == 2 ? kDk * kTransRow<T> : 4;
-
-// Column `c` of a [64][dk] tile, tokens 32 s .. 32 s + 31 in paired order.
-template <int kDk>
-__device__ __forceinline__ Frag<1> load_column(const uint16_t *, const uint16_t *trans, int c, int s, int grp) {
-    return load_paired(trans + c * kTransRow<uint16_t> + s * 32 + grp * 4);
-}
-template <int kDk>
-__device__ __forceinline__ Frag<3> load_column(const float *tile, const float *, int c, int s, int grp) {
-    constexpr int kRow = TileLoad<float, kDk>::kRow;
-    f32x4 a, b;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        a[r] = tile[(s * 32 + grp * 4 + r) * kRow + c];
-        b[r] = tile[(s * 32 + 16 + grp * 4 + r) * kRow + c];
-    }
-    return split_frag<3>(a, b);
-}
-
-// ------------------------------------------------------------------ W
+// ------------------------------------------------------------- chunk matrices
 //
-// One workgroup per (chunk, query/key head, batch); K K^T once, then each
-// value head of the group.  N = -diag(beta) A is strictly lower; (I - N)^-1 by
-// 16x16 blocks: wave j inverts diagonal block j by substitution (a lane per
+// What the chains need of a chunk besides its tokens, laid out by
+// delta_prep_kernel as they read it: the 64x64 matrices as A fragments in
+// paired order (W in three parts, P in as many as its result needs), then
+// exp(G_i) and exp(G_C - G_i), 0 behind the last token.
+//   forward:  W  (row tile mt, steps s <= mt / 2)   P
+//   backward: W^T (row tile mt, steps s >= mt / 2)  P^T in three parts
+template <int kPParts>
+struct Mats {
+    static constexpr int kP = kPParts;
+    uint4 W[3][kFrags][64];
+    uint4 P[kPParts][kFrags][64];
+    float e[kChunk], rest[kChunk];
+    float pad[128];   // whole kilobytes
+};
+__device__ __forceinline__ int frag_lower(int mt, int s) { return mt < 2 ? mt : mt * 2 - 2 + s; }
+__device__ __forceinline__ int frag_upper(int mt, int s) { return mt < 2 ? mt * 2 + s : mt + 2; }
+
+template <int kParts>
+__device__ __forceinline__ Frag<kParts> mat_frag(const uint4 (*m)[kFrags][64], int f) {
+    Frag<kParts> x;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) x.p[i] = __builtin_bit_cast(bf16x8, m[i][f][threadIdx.x & 63]);
+    return x;
+}
+// four of a row into half h of its lane's 16 bytes
+template <int kParts>
+__device__ __forceinline__ void put_quad(uint4 (*m)[kFrags][64], int f, int lane, int h, const float *v) {
+    uint32_t a[kParts], b[kParts];
+    split_pair<kParts>(v[0], v[1], a);
+    split_pair<kParts>(v[2], v[3], b);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) ((uint2 *)&m[i][f][lane])[h] = make_uint2(a[i], b[i]);
+}
+
+__device__ __forceinline__ void block_of(int tile, int *it, int *jt) {
+    *it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0;
+    *jt = tile - *it * (*it + 1) / 2;
+}
+
+// One workgroup per (chunk, query/key head, batch): K K^T and Q K^T once, then
+// each value head of the group.  N = -diag(beta) A is strictly lower; (I - N)^-1
+// by 16x16 blocks: wave j inverts diagonal block j by substitution (a lane per
 // column), then runs down block column j: X_i = inv_ii sum_k N_ik X_k, in fp32
 // matrix instructions, X_k staying in registers.
-template <typename T, int kDk>
-__global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__restrict__ k,
+template <typename T, int kDk, int kPF, bool kBwd>
+__global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__restrict__ q, const T *__restrict__ k,
                                                                   const float *__restrict__ g,
-                                                                  const float *__restrict__ beta,
-                                                                  float *__restrict__ W, float *__restrict__ Wt,
-                                                                  double *__restrict__ Gs, DeltaDims d) {
-    constexpr int kRow = TileLoad<T, kDk>::kRow;
-    __shared__ __attribute__((aligned(16))) T kt[kChunk * kRow];
-    __shared__ __attribute__((aligned(16))) float gram[kChunk * 68], N[kChunk * 68];
-    __shared__ __attribute__((aligned(16))) float inv[4 * 16 * 20];   // diagonal blocks' inverses
+                                                                  const float *__restrict__ beta, Mats<kPF> *__restrict__ fwd,
+                                                                  Mats<3> *__restrict__ bwd, double *__restrict__ Gs,
+                                                                  DeltaDims d) {
+    constexpr int kN = 68;
+    __shared__ __attribute__((aligned(16))) union {
+        struct {
+            Tile<T, kDk> k, q;
+        };
+        struct {
+            float N[kChunk * kN], inv[kChunk * 20];   // inv: the diagonal blocks' inverses
+        };
+    } l;
     __shared__ double G[kChunk];
     __shared__ float bt[kChunk];
     const int c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -161,29 +240,73 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
     const int n = len - t0 < kChunk ? (int)(len - t0) : kChunk;
     const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
     {
-        TileLoad<T, kDk> kl;
-        kl.load(k + (((int64_t)b * d.T + t0) * d.hk + h) * kDk, (int64_t)d.hk * kDk, n);
-        kl.store(kt);
+        const int64_t at = (((int64_t)b * d.T + t0) * d.hk + h) * kDk;
+        l.k.template fill<4>(k + at, (int64_t)d.hk * kDk, n);
+        if (q != nullptr) l.q.template fill<4>(q + at, (int64_t)d.hk * kDk, n);
     }
     __syncthreads();
-    for (int tile = wave; tile < kWBlocks; tile += 4) {
-        const int it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 kk[3], kq[3], qk[3];   // this wave's tiles: K K^T; Q K^T by rows j (columns i) and by rows i
 #pragma unroll
-        for (int s = 0; s < kDk / 32; ++s)
-            acc = mma(load_straight(kt + (it * 16 + col) * kRow + s * 32 + grp * 8),
-                      load_straight(kt + (jt * 16 + col) * kRow + s * 32 + grp * 8), acc);
+    for (int x = 0; x < 3; ++x) {
+        int it, jt;
+        block_of(wave + 4 * x < kBlocks ? wave + 4 * x : 0, &it, &jt);
+        kk[x] = kq[x] = qk[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) gram[(it * 16 + grp * 4 + r) * 68 + jt * 16 + col] = acc[r];
+        for (int s = 0; s < kDk / 32; ++s) {
+            const auto ki = l.k.row(it * 16 + col, s, grp), kj = l.k.row(jt * 16 + col, s, grp);
+            kk[x] = mma(ki, kj, kk[x]);
+            if (q != nullptr) {
+                const auto qi = l.q.row(it * 16 + col, s, grp);
+                kq[x] = mma(kj, qi, kq[x]);
+                if (kBwd) qk[x] = mma(qi, kj, qk[x]);
+            }
+        }
     }
+    __syncthreads();   // the tiles are read: N takes their place
     for (int hv = h * d.group; hv < (h + 1) * d.group; ++hv) {
-        const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv;
+        const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv, unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
         chunk_decays(g + at, d.hv, n, G);
         if (threadIdx.x < kChunk) bt[threadIdx.x] = (int)threadIdx.x < n ? strength(beta[at + (int64_t)threadIdx.x * d.hv]) : 1.f;
         __syncthreads();
-        for (int e = threadIdx.x; e < kChunk * kChunk; e += kDeltaThreads) {
-            const int i = e / kChunk, j = e % kChunk;
-            N[i * 68 + j] = j < i ? -bt[i] * (decay(G[i] - G[j]) * gram[i * 68 + j]) : 0.f;
+        if (threadIdx.x < kChunk) {
+            const int t = threadIdx.x;
+            const float e = decay(G[t]), rest = t < n ? decay(G[kChunk - 1] - G[t]) : 0.f;
+            fwd[unit].e[t] = e;
+            fwd[unit].rest[t] = rest;
+            if (kBwd) {
+                bwd[unit].e[t] = e;
+                bwd[unit].rest[t] = rest;
+                Gs[unit * kChunk + t] = G[t];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            if (wave + 4 * x >= kBlocks) continue;
+            int it, jt;
+            block_of(wave + 4 * x, &it, &jt);
+            float pt[4], pq[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = it * 16 + grp * 4 + r, j = jt * 16 + col;   // a result tile's rows and columns
+                const bool in = i < n && j < n;                            // repeated rows count for nothing
+                const float D = decay(G[i] - G[j]);
+                l.N[i * kN + j] = j < i && in ? -bt[i] * (D * kk[x][r]) : 0.f;
+                pq[r] = j <= i && in ? d.scale * D * qk[x][r] : 0.f;
+                const int i2 = it * 16 + col, j2 = jt * 16 + grp * 4 + r;
+                pt[r] = j2 <= i2 && i2 < n ? d.scale * decay(G[i2] - G[j2]) * kq[x][r] : 0.f;
+            }
+            if (q != nullptr) put_quad<kPF>(fwd[unit].P, frag_lower(it, jt / 2), lane, jt & 1, pt);
+            if (kBwd) put_quad<3>(bwd[unit].P, frag_upper(jt, it / 2), lane, it & 1, pq);
+        }
+        // halves of the 32-wide steps beyond the triangle
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        if (wave < 2) {
+            put_quad<3>(fwd[unit].W, frag_lower(wave * 2, wave), lane, 1, zero);
+            if (q != nullptr) put_quad<kPF>(fwd[unit].P, frag_lower(wave * 2, wave), lane, 1, zero);
+        } else if (kBwd) {
+            const int x = wave - 2;
+            put_quad<3>(bwd[unit].W, frag_upper(x * 2 + 1, x), lane, 0, zero);
+            put_quad<3>(bwd[unit].P, frag_upper(x * 2 + 1, x), lane, 0, zero);
         }
         __syncthreads();
         // diagonal block `wave`, column `col` of its inverse
@@ -193,16 +316,19 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         for (int i = 0; i < 16; ++i) {
             float s = i == col ? 1.f : 0.f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) s = fmaf(N[(r0 + i) * 68 + r0 + j], x[j], s);
+            for (int j = 0; j < i; j += 4) {
+                const f32x4 w = *(const f32x4 *)&l.N[(r0 + i) * kN + r0 + j];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (j + y < i) s = fmaf(w[y], x[j + y], s);
+            }
             x[i] = s;
         }
         if (grp == 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) inv[(r0 + i) * 20 + col] = x[i];
+            for (int i = 0; i < 16; ++i) l.inv[(r0 + i) * 20 + col] = x[i];
         }
         __syncthreads();
-        float *Wc = W + (((int64_t)b * d.hv + hv) * d.chunks + c) * kWFloats;
-        if (threadIdx.x < kChunk) Gs[(((int64_t)b * d.hv + hv) * d.chunks + c) * kChunk + threadIdx.x] = G[threadIdx.x];
         const float bj = bt[r0 + col];
         f32x4 X[4];
 #pragma unroll
@@ -210,108 +336,56 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
             if (i < wave) continue;
             if (i == wave) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) X[i][r] = inv[(r0 + grp * 4 + r) * 20 + col];
+                for (int r = 0; r < 4; ++r) X[i][r] = l.inv[(r0 + grp * 4 + r) * 20 + col];
             } else {
                 f32x4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kb = 0; kb < i; ++kb) {
                     if (kb < wave) continue;
-                    const f32x4 a = *(const f32x4 *)&N[(i * 16 + col) * 68 + kb * 16 + grp * 4];
+                    const f32x4 a = *(const f32x4 *)&l.N[(i * 16 + col) * kN + kb * 16 + grp * 4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) t = mfma32(a[r], X[kb][r], t);
                 }
                 f32x4 y = {0.f, 0.f, 0.f, 0.f};
-                const f32x4 a = *(const f32x4 *)&inv[(i * 16 + col) * 20 + grp * 4];
+                const f32x4 a = *(const f32x4 *)&l.inv[(i * 16 + col) * 20 + grp * 4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y = mfma32(a[r], t[r], y);
                 X[i] = y;
             }
-            float *blk = Wc + (i * (i + 1) / 2 + wave) * 256;
-            f32x4 w;
+        }
+        __syncthreads();   // N is read: W takes its place
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i < wave) continue;
+            float w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) w[r] = X[i][r] * bj;
+            if (kBwd) put_quad<3>(bwd[unit].W, frag_upper(wave, i / 2), lane, i & 1, w);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) blk[(grp * 4 + r) * 16 + col] = w[r];
-            if (Wt != nullptr) *(f32x4 *)(Wt + (blk - W) + col * 16 + grp * 4) = w;
+            for (int r = 0; r < 4; ++r) l.N[(i * 16 + grp * 4 + r) * kN + wave * 16 + col] = w[r];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+            if (wave + 4 * y >= kBlocks) continue;
+            int it, jt;
+            block_of(wave + 4 * y, &it, &jt);
+            const f32x4 w = *(const f32x4 *)&l.N[(it * 16 + col) * kN + jt * 16 + grp * 4];
+            const float v[4] = {w[0], w[1], w[2], w[3]};
+            put_quad<3>(fwd[unit].W, frag_lower(it, jt / 2), lane, jt & 1, v);
         }
         __syncthreads();
     }
 }
 
-// W's blocks (kTransposed: W^T's) from the workspace into three planes of bf16
-// parts in LDS.
-template <bool kTransposed, int kThreads = kDeltaThreads>
-struct WLoad {
-    static constexpr int kN = (kWFloats / 4 + kThreads - 1) / kThreads;
-    f32x4 r[kN];
-    __device__ void load(const float *W) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = threadIdx.x + i * kThreads;
-            if (at < kWFloats / 4) r[i] = *(const f32x4 *)(W + at * 4);
-        }
-    }
-    // row of the block at `at` and its column: element (row, col..col+3)
-    __device__ static void place(int at, int *row, int *colm) {
-        const int blk = at / 64, e = at % 64;
-        const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
-        *row = (kTransposed ? jt : it) * 16 + e / 4;
-        *colm = (kTransposed ? it : jt) * 16 + e % 4 * 4;
-    }
-    __device__ void store(uint16_t *lds) const {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = threadIdx.x + i * kThreads;
-            if (at < kWFloats / 4) {
-                int row, c;
-                place(at, &row, &c);
-                uint32_t a[3], b[3];
-                split_pair<3>(r[i][0], r[i][1], a);
-                split_pair<3>(r[i][2], r[i][3], b);
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    *(uint2 *)(lds + p * kChunk * kTri + row * kTri + c) = make_uint2(a[p], b[p]);
-            }
-        }
-    }
-};
-
-// P_ij = scale exp(G_i - G_j) q_i.k_j (j <= i) in kParts planes: rows i, or rows
-// j if kTransposed.  Each tile is formed with its rows as the product's
-// columns, so that a lane stores four of a row.
-template <typename T, int kDk, bool kTransposed, int kParts, int kThreads = kDeltaThreads>
-__device__ __forceinline__ void form_p(const T *k, const T *q, const double *G, float scale, uint16_t *P) {
-    constexpr int kRow = TileLoad<T, kDk>::kRow;
-    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
-    for (int tile = threadIdx.x >> 6; tile < kWBlocks; tile += kThreads / 64) {
-        const int it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, jt = tile - it * (it + 1) / 2;
-        const T *rows = kTransposed ? q + it * 16 * kRow : k + jt * 16 * kRow;
-        const T *cols = kTransposed ? k + jt * 16 * kRow : q + it * 16 * kRow;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < kDk / 32; ++s)
-            acc = mma(load_straight(rows + col * kRow + s * 32 + grp * 8), load_straight(cols + col * kRow + s * 32 + grp * 8), acc);
-        const int row = (kTransposed ? jt : it) * 16 + col, c0 = (kTransposed ? it : jt) * 16 + grp * 4;
-        float p[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = kTransposed ? c0 + r : row, j = kTransposed ? row : c0 + r;
-            p[r] = j <= i ? scale * decay(G[i] - G[j]) * acc[r] : 0.f;
-        }
-        uint32_t w0[kParts], w1[kParts];
-        split_pair<kParts>(p[0], p[1], w0);
-        split_pair<kParts>(p[2], p[3], w1);
-#pragma unroll
-        for (int x = 0; x < kParts; ++x)
-            *(uint2 *)(P + x * kChunk * kTri + row * kTri + c0) = make_uint2(w0[x], w1[x]);
-    }
-}
-
-// Zero planes: the halves of 32-wide steps beyond W's and P's triangles are
-// read but never written.
-template <int kThreads = kDeltaThreads>
-__device__ __forceinline__ void zero_planes(uint16_t *p, int planes) {
-    for (int i = threadIdx.x; i < planes * kChunk * kTri / 2; i += kThreads) ((uint32_t *)p)[i] = 0;
+// A chunk's matrices into LDS.
+template <int kParts, int kWaves = 4>
+__device__ __forceinline__ void fill_mats(const Mats<kParts> *src, Mats<kParts> *dst) {
+    constexpr int kLoads = (int)sizeof(Mats<kParts>) / 1024;
+    static_assert(sizeof(Mats<kParts>) % 1024 == 0, "");
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = wave; i < kLoads; i += kWaves)
+        load_lds((const char *)src + i * 1024 + lane * 16, (char *)dst + i * 1024);
 }
 
 // --------------------------------------------------------------- forward chain
@@ -319,105 +393,55 @@ __device__ __forceinline__ void zero_planes(uint16_t *p, int planes) {
 template <typename T>
 struct ChainArgs {
     const T *q, *k, *v;
-    const double *G;      // the chunks' sums of log decays
-    const float *W, *h_init;
+    const Mats<Stream<T>::kOutParts> *mats;
+    const float *h_init;
     T *o;                 // null: states only
     float *h_final;       // null: not wanted
     float *h_chunks;      // null, or [batch, chunks, hv, dk, dv]
     DeltaDims d;
 };
 
-template <typename T, int kDk>
-struct ChainLds {
-    static constexpr int kOut = Stream<T>::kOutParts;
-    T k[kChunk * TileLoad<T, kDk>::kRow];
-    T q[kChunk * TileLoad<T, kDk>::kRow];
-    T kT[kTransSize<T, kDk>];
-    uint16_t W[3 * kChunk * kTri];
-    uint16_t P[kOut * kChunk * kTri];
-    double G[kChunk];
-    float e[kChunk], rest[kChunk];
+// What a step of the chain reads, filled while the step before it computes
+// (bf16; fp32 streams have room for one set only).
+template <typename T, int kDk, bool kWithO>
+struct ChainStage {
+    Tile<T, kDk> k;
+    Tile<T, kWithO ? kDk : 64> q;
+    Tile<T, 64> v;
+    Mats<Stream<T>::kOutParts> m;
 };
 
 template <typename T, int kDk, bool kWithO>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs<T> a) {
-    using L = ChainLds<T, kDk>;
-    constexpr int kRow = TileLoad<T, kDk>::kRow, kOut = L::kOut;
-    constexpr int kTiles = kDk / 16, kSteps = kDk / 32;
-    __shared__ __attribute__((aligned(16))) L l;
-    const DeltaDims &d = a.d;
-    const int hv = blockIdx.y, b = blockIdx.z, hk = hv / d.group;
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
-    const int n = blockIdx.x * 64 + wave * 16 + col;   // this lane's state column
-    const int64_t len = row_len(d, b);
-    const int chunks = (int)((len + kChunk - 1) / kChunk);
-    const int64_t kstride = (int64_t)d.hk * kDk, vstride = (int64_t)d.hv * d.dv;
-    const T *kp = a.k + ((int64_t)b * d.T * d.hk + hk) * kDk;
-    const T *qp = a.q + ((int64_t)b * d.T * d.hk + hk) * kDk;
-    const T *vp = a.v + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-    const double *Gp = a.G + ((int64_t)b * d.hv + hv) * d.chunks * kChunk;
-    const float *Wp = a.W + ((int64_t)b * d.hv + hv) * d.chunks * kWFloats;
-    const int64_t state = (int64_t)kDk * d.dv;
-
-    zero_planes(l.W, 3);
-    zero_planes(l.P, kOut);
-
+struct Chain {
+    static constexpr int kOut = Stream<T>::kOutParts, kTiles = kDk / 16, kSteps = kDk / 32;
+    using Stage = ChainStage<T, kDk, kWithO>;
     f32x4 S[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            S[t][r] = a.h_init == nullptr ? 0.f
-                                          : a.h_init[((int64_t)b * d.hv + hv) * state + (int64_t)(t * 16 + grp * 4 + r) * d.dv + n];
+    const ChainArgs<T> &a;
+    const T *kp, *qp, *vp;
+    T *op;
+    int64_t kstride, vstride, len;
+    int hv, b, lane, wave, col, grp, n;
 
-    TileLoad<T, kDk> kl, ql;
-    WLoad<false> wl;
-    T vr[16];         // as stored: nothing may wait for them here
-    double Gr = 0.;   // threads 0..63
-    auto fetch = [&](int c) {
+    __device__ __forceinline__ void fill(Stage &l, int c) {
         const int64_t t0 = (int64_t)c * kChunk;
         const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
-        kl.load(kp + t0 * kstride, kstride, m);
-        if (kWithO) ql.load(qp + t0 * kstride, kstride, m);
-        wl.load(Wp + (int64_t)c * kWFloats);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = i / 4 * 16 + grp * 4 + i % 4;
-            vr[i] = t < m ? vp[(t0 + t) * vstride] : T(0);
-        }
-        if (threadIdx.x < kChunk) Gr = Gp[(int64_t)c * kChunk + threadIdx.x];
-    };
-    if (chunks > 0) fetch(0);
+        l.k.template fill<4>(kp + t0 * kstride, kstride, m);
+        if (kWithO) l.q.template fill<4>(qp + t0 * kstride, kstride, m);
+        l.v.template fill<4>(vp + t0 * vstride, vstride, m);
+        fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
+    }
 
-    for (int c = 0; c < chunks; ++c) {
+    __device__ __forceinline__ void store_state(float *out) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(t, grp, r) * a.d.dv + n] = S[t][r];
+    }
+
+    __device__ __forceinline__ void step(const Stage &l, int c) {
+        const DeltaDims &d = a.d;
         const int64_t t0 = (int64_t)c * kChunk;
         const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
-        __syncthreads();   // the last chunk's reads of LDS are done
-        kl.store(l.k);
-        if (kWithO) ql.store(l.q);
-        wl.store(l.W);
-        const double *G = l.G;
-        if (threadIdx.x < kChunk) {   // one wave: the last token's sum is its last lane's
-            l.G[threadIdx.x] = Gr;
-            l.e[threadIdx.x] = decay(Gr);
-            l.rest[threadIdx.x] = decay(__shfl(Gr, 63, 64) - Gr);
-        }
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = Stream<T>::load(vr + i);
-        __syncthreads();
-        if (c + 1 < chunks) fetch(c + 1);
-        transpose_tile<kDk>(l.k, l.kT);
-        if (kWithO) {
-            form_p<T, kDk, false, kOut>(l.k, l.q, G, d.scale, l.P);
-        }
-        if (a.h_chunks != nullptr) {
-            float *out = a.h_chunks + (((int64_t)b * d.chunks + c) * d.hv + hv) * state + n;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) out[(int64_t)(t * 16 + grp * 4 + r) * d.dv] = S[t][r];
-        }
         // R = V - E K S and the state's part of O
         f32x4 R[4], O[4];
         {
@@ -426,93 +450,138 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
             for (int s = 0; s < kSteps; ++s) Sp[s] = split_frag<3>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    acc = mma(load_paired(l.k + (mt * 16 + col) * kRow + s * 32 + grp * 4), Sp[s], acc);
-                const f32x4 e = *(const f32x4 *)(l.e + mt * 16 + grp * 4);
+                for (int s = 0; s < kSteps; ++s) ks = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], ks);
+                const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = l.v.values(mt, grp, wave * 16, col);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) R[mt][r] = fmaf(-e[r], acc[r], v[mt * 4 + r]);
-                if (kWithO) {
-                    f32x4 qs = {0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < 4; ++r) R[mt][r] = fmaf(-e[r], ks[r], v[r]);
+                if constexpr (kWithO) {
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s) {
                         Frag<kOut> So;
 #pragma unroll
                         for (int x = 0; x < kOut; ++x) So.p[x] = Sp[s].p[x];
-                        qs = mma(load_paired(l.q + (mt * 16 + col) * kRow + s * 32 + grp * 4), So, qs);
+                        qs = mma(l.q.row(mt * 16 + col, s, grp), So, qs);
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[mt][r] = d.scale * e[r] * qs[r];
                 }
             }
         }
-        __syncthreads();   // kT and P are written
         f32x4 U[4];
         {
-            Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
+            const Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                U[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s <= mt / 2; ++s)
-                    acc = mma(load_planes<3>(l.W + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Rp[s], acc);
-                U[mt] = acc;
-            }
-        }
-        if (kWithO) {
-            Frag<kOut> Up[2] = {split_frag<kOut>(U[0], U[1]), split_frag<kOut>(U[2], U[3])};
-            T *op = a.o + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                for (int s = 0; s <= mt / 2; ++s)
-                    O[mt] = mma(load_planes<kOut>(l.P + (mt * 16 + col) * kTri + s * 32 + grp * 4, kChunk * kTri), Up[s], O[mt]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = mt * 16 + grp * 4 + r;
-                    if (t < m) Stream<T>::store(op + (t0 + t) * vstride, O[mt][r]);
-                }
+                for (int s = 0; s <= mt / 2; ++s) U[mt] = mma(mat_frag<3>(l.m.W, frag_lower(mt, s)), Rp[s], U[mt]);
             }
         }
         // the next state
-        const float last = l.e[kChunk - 1];
+        {
+            const float last = l.m.e[kChunk - 1];
+            f32x4 Ur[4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            const f32x4 e = *(const f32x4 *)(l.rest + mt * 16 + grp * 4);
+            for (int mt = 0; mt < 4; ++mt) {
+                const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) U[mt][r] *= e[r];
+                for (int r = 0; r < 4; ++r) Ur[mt][r] = rest[r] * U[mt][r];
+            }
+            const Frag<3> Up[2] = {split_frag<3>(Ur[0], Ur[1]), split_frag<3>(Ur[2], Ur[3])};
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[t][r] *= last;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) S[t] = mma(l.k.column(t, s, grp, col), Up[s], S[t]);
+            }
         }
-        Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
+        if constexpr (kWithO) {
+            const Frag<kOut> Up[2] = {split_frag<kOut>(U[0], U[1]), split_frag<kOut>(U[2], U[3])};
+            T *out = op + t0 * vstride;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+            for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] *= last;
+                for (int s = 0; s <= mt / 2; ++s) O[mt] = mma(mat_frag<kOut>(l.m.P, frag_lower(mt, s)), Up[s], O[mt]);
+            }
+            if (m == kChunk) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                S[t] = mma(load_column<kDk>(l.k, l.kT, t * 16 + col, s, grp), Up[s], S[t]);
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) Stream<T>::store(out + (mt * 16 + grp * 4 + r) * vstride, O[mt][r]);
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (mt * 16 + grp * 4 + r < m) Stream<T>::store(out + (mt * 16 + grp * 4 + r) * vstride, O[mt][r]);
+            }
         }
     }
-    if (a.h_final != nullptr) {
-        float *out = a.h_final + ((int64_t)b * d.hv + hv) * state + n;
+};
+
+template <typename T, int kDk, bool kWithO>
+__global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs<T> a) {
+    using C = Chain<T, kDk, kWithO>;
+    constexpr bool kTwo = sizeof(T) == 2;
+    __shared__ __attribute__((aligned(16))) typename C::Stage l0;
+    __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
+    const DeltaDims &d = a.d;
+    C s{{}, a};
+    s.hv = blockIdx.y;
+    s.b = blockIdx.z;
+    const int hk = s.hv / d.group;
+    s.lane = lane_id();
+    s.wave = threadIdx.x >> 6;
+    s.col = s.lane & 15;
+    s.grp = s.lane >> 4;
+    s.n = blockIdx.x * 64 + s.wave * 16 + s.col;   // this lane's state column
+    s.len = row_len(d, s.b);
+    s.kstride = (int64_t)d.hk * kDk;
+    s.vstride = (int64_t)d.hv * d.dv;
+    const int64_t tok = (int64_t)s.b * d.T;
+    s.kp = a.k + (tok * d.hk + hk) * kDk;
+    s.qp = kWithO ? a.q + (tok * d.hk + hk) * kDk : nullptr;
+    s.vp = a.v + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64;
+    s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + s.n : nullptr;
+    const int chunks = (int)((s.len + kChunk - 1) / kChunk);
+    const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[(int64_t)(t * 16 + grp * 4 + r) * d.dv] = S[t][r];
-    }
-    if (a.h_chunks != nullptr) {   // chunks of padding alone: the state stays
-        for (int c = chunks; c < d.chunks; ++c) {
-            float *out = a.h_chunks + (((int64_t)b * d.chunks + c) * d.hv + hv) * state + n;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) out[(int64_t)(t * 16 + grp * 4 + r) * d.dv] = S[t][r];
+        for (int r = 0; r < 4; ++r)
+            s.S[t][r] = a.h_init == nullptr ? 0.f : a.h_init[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
+    auto keep = [&](int c) {
+        if (a.h_chunks != nullptr) s.store_state(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
+    };
+    if constexpr (kTwo) {
+        if (chunks > 0) s.fill(l0, 0);
+        for (int c = 0; c < chunks; c += 2) {
+            __syncthreads();   // l0 is filled, l1 is read
+            if (c + 1 < chunks) s.fill(l1, c + 1);
+            keep(c);
+            s.step(l0, c);
+            if (c + 1 >= chunks) break;
+            __syncthreads();
+            if (c + 2 < chunks) s.fill(l0, c + 2);
+            keep(c + 1);
+            s.step(l1, c + 1);
+        }
+    } else {
+        for (int c = 0; c < chunks; ++c) {
+            __syncthreads();
+            s.fill(l0, c);
+            keep(c);
+            __syncthreads();
+            s.step(l0, c);
         }
     }
-    if (kWithO) {   // padding: zeros
-        T *op = a.o + ((int64_t)b * d.T * d.hv + hv) * d.dv + n;
-        for (int64_t t = len + grp; t < d.T; t += 4) Stream<T>::store(op + t * vstride, 0.f);
-    }
+    if (a.h_final != nullptr) s.store_state(a.h_final + head * state);
+    for (int c = chunks; c < d.chunks; ++c) keep(c);   // chunks of padding alone: the state stays
+    if (kWithO)   // padding: zeros
+        for (int64_t t = s.len + s.grp; t < d.T; t += 4) Stream<T>::store(s.op + t * s.vstride, 0.f);
 }
 
 // ---------------------------------------------------------------- recurrent

@@ -60,23 +60,27 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 }
 
 struct DeltaSizes {
-    int64_t chunks;
-    size_t qk, vo, gate, state, hchunks, W, G;
-    size_t fwd() const { return W + G; }                  // W and the chunks' log decays
-    size_t bwd() const { return 2 * W + G + hchunks; }    // W^T and the states' adjoints too
+    size_t qk, vo, gate, state, hchunks, units;
+    bool bf16;
+    // the workspace: the chunks' matrices; for the backward those of both
+    // directions, the summed log decays and the states' adjoints
+    size_t fwd() const { return units * (bf16 ? sizeof(Mats<2>) : sizeof(Mats<3>)); }
+    size_t mats3() const { return units * sizeof(Mats<3>); }
+    size_t sums() const { return units * kChunk * 8; }
+    size_t bwd() const { return 2 * mats3() + sums() + hchunks; }
 };
 
 DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
     const size_t e = s->dtype == BDSSM_BF16 ? 2 : 4;
+    const size_t chunks = (size_t)(T + kChunk - 1) / kChunk;
     DeltaSizes z;
-    z.chunks = (T + kChunk - 1) / kChunk;
     z.qk = (size_t)s->batch * T * s->heads_k * s->d_k * e;
     z.vo = (size_t)s->batch * T * s->heads_v * s->d_v * e;
     z.gate = (size_t)s->batch * T * s->heads_v * 4;
     z.state = (size_t)s->batch * s->heads_v * s->d_k * s->d_v * 4;
-    z.hchunks = z.state * (size_t)z.chunks;
-    z.W = (size_t)s->batch * s->heads_v * z.chunks * kWFloats * 4;
-    z.G = (size_t)s->batch * s->heads_v * z.chunks * kChunk * 8;
+    z.hchunks = z.state * chunks;
+    z.units = (size_t)s->batch * s->heads_v * chunks;
+    z.bf16 = s->dtype == BDSSM_BF16;
     return z;
 }
 
@@ -216,8 +220,7 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     c.o = o;
     c.h_final = h_final;
     c.h_chunks = h_chunks;
-    c.W = (float *)ws;
-    c.G = (double *)(c.W + z.W / 4);
+    c.fwd = ws;
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_scan<uint16_t>(c, st);
     else launch_delta_scan<float>(c, st);
@@ -246,10 +249,11 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, c
     c.h_chunks = const_cast<float *>(h_chunks);
     c.dout = dout;
     c.dh_final = dh_final;
-    c.W = (float *)ws;
-    c.Wt = c.W + z.W / 4;
-    c.G = (double *)(c.Wt + z.W / 4);
-    c.dS = (float *)(c.G + z.G / 8);
+    char *w = (char *)ws;
+    c.fwd = w;
+    c.bwd = w + z.mats3();
+    c.G = (double *)(w + 2 * z.mats3());
+    c.dS = (float *)(w + 2 * z.mats3() + z.sums());
     c.dq = dq;
     c.dk_out = dk;
     c.dv_out = dv;

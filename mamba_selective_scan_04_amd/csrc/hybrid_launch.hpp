@@ -20,11 +20,13 @@ struct DeltaCall {
     const void *q, *k, *v;
     const float *g, *beta, *h_init;
     void *o;
-    float *h_final, *h_chunks, *W;
+    float *h_final, *h_chunks;
+    void *fwd;   // the chunks' matrices (Mats)
     // backward
     const void *dout;
     const float *dh_final;
-    float *Wt, *dS, *dh_init, *dg, *dbeta;
+    void *bwd;
+    float *dS, *dh_init, *dg, *dbeta;
     void *dq, *dk_out, *dv_out;
     double *G;
     int64_t batch;

@@ -10,9 +10,13 @@ namespace bdssm_host {
 
 template <typename T, int kDk>
 void launch_scan_k(const DeltaCall &c, hipStream_t st) {
+    constexpr int kOut = Stream<T>::kOutParts;
     const dim3 gp((unsigned)c.d.chunks, (unsigned)c.d.hk, (unsigned)c.batch);
-    if (c.d.chunks > 0) hipLaunchKernelGGL((delta_prep_kernel<T, kDk>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.k, c.g, c.beta, c.W, (float *)nullptr, c.G, c.d);
-    const ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, c.G, c.W, c.h_init, (T *)c.o, c.h_final, c.h_chunks, c.d};
+    if (c.d.chunks > 0)
+        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, kOut, false>), gp, dim3(kDeltaThreads), 0, st,
+                           c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.fwd,
+                           (Mats<3> *)nullptr, (double *)nullptr, c.d);
+    const ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.fwd, c.h_init, (T *)c.o, c.h_final, c.h_chunks, c.d};
     const dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
     if (c.o != nullptr)
         hipLaunchKernelGGL((delta_chain_kernel<T, kDk, true>), gc, dim3(kDeltaThreads), 0, st, a);
@@ -24,13 +28,14 @@ template <typename T, int kDk>
 void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
     const dim3 gp((unsigned)c.d.chunks, (unsigned)c.d.hk, (unsigned)c.batch);
     if (c.d.chunks > 0)
-        hipLaunchKernelGGL((delta_prep_kernel<T, kDk>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.k, c.g, c.beta, c.W, c.Wt, c.G, c.d);
-    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, c.G, c.Wt, c.dh_final, c.dS, c.dh_init, c.d};
+        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, 3, true>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.q, (const T *)c.k, c.g, c.beta,
+                           (Mats<3> *)c.fwd, (Mats<3> *)c.bwd, c.G, c.d);
+    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.bwd, c.dh_final, c.dS, c.dh_init, c.d};
     const dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
     hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk>), gc, dim3(kDeltaThreads), 0, st, a);
     if (c.d.chunks == 0) return;
-    const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, c.G, c.beta, c.W, c.Wt, c.h_chunks,
-                         c.dS, (T *)c.dq, (T *)c.dk_out, (T *)c.dv_out, c.dg, c.dbeta, c.d};
+    const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.fwd, (const Mats<3> *)c.bwd,
+                         c.G, c.beta, c.h_chunks, c.dS, (T *)c.dq, (T *)c.dk_out, (T *)c.dv_out, c.dg, c.dbeta, c.d};
     if (c.d.dv == 64) hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 64>), gp, dim3(256), 0, st, ga);
     else hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 128>), gp, dim3(512), 0, st, ga);
 }
