@@ -74,40 +74,30 @@ struct Adjoint {
         const int m = tokens(c);
         f32x4 U[4], dO[4];
         {
-            Frag<3> Sp[kSteps];
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) Sp[s] = split_frag<3>(S[2 * s], S[2 * s + 1]);
+            for (int mt = 0; mt < 4; ++mt) U[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const Frag<3> Sp = split_frag<3>(S[2 * s], S[2 * s + 1]);
+                Frag<kIn> kf[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) kf[mt] = l.k.row(mt * 16 + col, s, grp);
+                mma_n<4>(kf, Sp, U);
+            }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) acc = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], acc);
                 const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
                 dO[mt] = l.o.values(mt, grp, wave * 16, col);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    U[mt][r] = rest[r] * acc[r];
+                    U[mt][r] *= rest[r];
                     dO[mt][r] = mt * 16 + grp * 4 + r < m ? dO[mt][r] : 0.f;
                 }
             }
         }
-        {
-            const Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int s = mt / 2; s < 2; ++s) U[mt] = mma(mat_frag<3>(l.m.P, frag_upper(mt, s)), Op[s], U[mt]);
-        }
+        upper_product<3, false, kIn>(l.m.P, dO, U);
         f32x4 X[4];
-        {
-            const Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                X[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = mt / 2; s < 2; ++s) X[mt] = mma(mat_frag<3>(l.m.W, frag_upper(mt, s)), Up[s], X[mt]);
-            }
-        }
+        upper_product<3>(l.m.W, U, X);
         const float last = l.m.e[kChunk - 1];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
@@ -118,18 +108,12 @@ struct Adjoint {
                 dO[mt][r] *= a.d.scale * e[r];
             }
         }
-        const Frag<3> Xp[2] = {split_frag<3>(X[0], X[1]), split_frag<3>(X[2], X[3])};
-        const Frag<3> Op[2] = {split_frag<3>(dO[0], dO[1]), split_frag<3>(dO[2], dO[3])};
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[t][r] *= last;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                S[t] = mma(l.q.column(t, s, grp, col), Op[s], S[t]);
-                S[t] = mma(l.k.column(t, s, grp, col), Xp[s], S[t]);
-            }
-        }
+        add_columns(l.q, dO, S);
+        add_columns(l.k, X, S);
     }
 };
 
@@ -232,6 +216,17 @@ __device__ __forceinline__ Frag<kParts> load_state(const float *p) {
     return split_frag<kParts>(*(const f32x4 *)p, *(const f32x4 *)(p + 4));
 }
 
+// B fragment (rows of state tiles 2 s, 2 s + 1) of a state's column at p
+template <int kDv>
+__device__ __forceinline__ Frag<3> state_columns(const float *p, int s, int grp) {
+    f32x4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][r] = p[state_row(2 * s + i, grp, r) * kDv];
+    return split_frag<3>(x[0], x[1]);
+}
+
 template <typename T, int kDk, int kDv>
 struct GradLds {
     static constexpr int kOut = Stream<T>::kOutParts;
@@ -326,89 +321,71 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         {
             f32x4 R[4], O[4];
             {
-                Frag<3> Sp[kSteps];
+                f32x4 ks[4], qs[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) ks[mt] = qs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    f32x4 x[2];
+                    const Frag<3> Sp = state_columns<kDv>(Sg + n, s, grp);
+                    Frag<kIn> kf[4], qf[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) x[i][r] = Sg[(int64_t)state_row(2 * s + i, grp, r) * kDv + n];
-                    Sp[s] = split_frag<3>(x[0], x[1]);
+                    for (int mt = 0; mt < 4; ++mt) {
+                        kf[mt] = l.k.row(mt * 16 + col, s, grp);
+                        qf[mt] = l.q.row(mt * 16 + col, s, grp);
+                    }
+                    mma_n<4>(kf, Sp, ks);
+                    mma_n<4>(qf, Sp, qs);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
-                    f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        ks = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], ks);
-                        qs = mma(l.q.row(mt * 16 + col, s, grp), Sp[s], qs);
-                    }
                     const f32x4 e = *(const f32x4 *)(l.fwd.e + mt * 16 + grp * 4);
                     if constexpr (sizeof(T) == 2) dO[mt] = l.o.values(mt, grp, wave * 16, col);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        R[mt][r] = fmaf(-e[r], ks[r], v[mt][r]);
-                        O[mt][r] = d.scale * e[r] * qs[r];
+                        R[mt][r] = fmaf(-e[r], ks[mt][r], v[mt][r]);
+                        O[mt][r] = d.scale * e[r] * qs[mt][r];
                         dO[mt][r] = mt * 16 + grp * 4 + r < m ? dO[mt][r] : 0.f;
                     }
                 }
             }
-            const Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                U[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s <= mt / 2; ++s) U[mt] = mma(mat_frag<3>(l.fwd.W, frag_lower(mt, s)), Rp[s], U[mt]);
-            }
-            const Frag<3> Up[2] = {split_frag<3>(U[0], U[1]), split_frag<3>(U[2], U[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                for (int s = 0; s <= mt / 2; ++s) O[mt] = mma(mat_frag<3>(l.fwd.P, frag_lower(mt, s)), Up[s], O[mt]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[mt][r] * O[mt][r];
-            }
-        }
-        float end = 0.f;   // <S, dS'> exp(G_C) (by rows, below) + sum of U (K dS') rows
-        {
-            f32x4 dU[4];
-            {
-                Frag<3> Sp[kSteps];
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    f32x4 x[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) x[i][r] = dSg[(int64_t)state_row(2 * s + i, grp, r) * kDv + n];
-                    Sp[s] = split_frag<3>(x[0], x[1]);
-                }
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    f32x4 kd = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) kd = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], kd);
-                    const f32x4 rest = *(const f32x4 *)(l.bwd.rest + mt * 16 + grp * 4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        dU[mt][r] = rest[r] * kd[r];
-                        end = fmaf(U[mt][r], dU[mt][r], end);
-                    }
-                }
-            }
-            const Frag<kIn> Op[2] = {split_frag<kIn>(dO[0], dO[1]), split_frag<kIn>(dO[2], dO[3])};
+            __builtin_amdgcn_sched_barrier(0);
+            lower_product<3>(l.fwd.W, R, U);
+            __builtin_amdgcn_sched_barrier(0);
+            lower_product<3, false>(l.fwd.P, U, O);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int s = mt / 2; s < 2; ++s) dU[mt] = mma(mat_frag<3>(l.bwd.P, frag_upper(mt, s)), Op[s], dU[mt]);
-            const Frag<3> Dp[2] = {split_frag<3>(dU[0], dU[1]), split_frag<3>(dU[2], dU[3])};
+                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[mt][r] * O[mt][r];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float end = 0.f;   // <S, dS'> exp(G_C) (by rows, below) + sum of U (K dS') rows
+        {
+            f32x4 dU[4];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) dU[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const Frag<3> Sp = state_columns<kDv>(dSg + n, s, grp);
+                Frag<kIn> kf[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) kf[mt] = l.k.row(mt * 16 + col, s, grp);
+                mma_n<4>(kf, Sp, dU);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                X[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                const f32x4 rest = *(const f32x4 *)(l.bwd.rest + mt * 16 + grp * 4);
 #pragma unroll
-                for (int s = mt / 2; s < 2; ++s) X[mt] = mma(mat_frag<3>(l.bwd.W, frag_upper(mt, s)), Dp[s], X[mt]);
+                for (int r = 0; r < 4; ++r) {
+                    dU[mt][r] *= rest[r];
+                    end = fmaf(U[mt][r], dU[mt][r], end);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            upper_product<3, false, kIn>(l.bwd.P, dO, dU);
+            __builtin_amdgcn_sched_barrier(0);
+            upper_product<3>(l.bwd.W, dU, X);
         }
         __syncthreads();   // the matrices are read: U and X take their place
 #pragma unroll
@@ -464,6 +441,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                     sx[j] = mma(sf, l.X.get(t, s, grp), sx[j]);
                     du[j] = mma(df, l.U.get(t, s, grp), du[j]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int j = 0; j < kToks; ++j) {

@@ -388,6 +388,58 @@ __device__ __forceinline__ void fill_mats(const Mats<kParts> *src, Mats<kParts> 
         load_lds((const char *)src + i * 1024 + lane * 16, (char *)dst + i * 1024);
 }
 
+// out (+)= M x for a lower (kLower) or upper triangular matrix in kParts parts
+// and a [64 x 16] column slice x in result tiles.
+template <int kParts, bool kZero = true, bool kLower = true, int kXParts = kParts>
+__device__ __forceinline__ void tri_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
+    if (kZero) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) out[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const Frag<kXParts> xp = split_frag<kXParts>(x[2 * s], x[2 * s + 1]);
+        if ((s == 0) == kLower) {   // all four row tiles
+            const Frag<kParts> f[4] = {mat_frag<kParts>(m, kLower ? frag_lower(0, s) : frag_upper(0, s)),
+                                       mat_frag<kParts>(m, kLower ? frag_lower(1, s) : frag_upper(1, s)),
+                                       mat_frag<kParts>(m, kLower ? frag_lower(2, s) : frag_upper(2, s)),
+                                       mat_frag<kParts>(m, kLower ? frag_lower(3, s) : frag_upper(3, s))};
+            mma_n<4>(f, xp, out);
+        } else {                    // the two at the far side
+            constexpr int k0 = kLower ? 2 : 0;
+            const Frag<kParts> f[2] = {mat_frag<kParts>(m, kLower ? frag_lower(k0, s) : frag_upper(k0, s)),
+                                       mat_frag<kParts>(m, kLower ? frag_lower(k0 + 1, s) : frag_upper(k0 + 1, s))};
+            mma_n<2>(f, xp, out + k0);
+        }
+    }
+}
+template <int kParts, bool kZero = true>
+__device__ __forceinline__ void lower_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
+    tri_product<kParts, kZero, true>(m, x, out);
+}
+template <int kParts, bool kZero = true, int kXParts = kParts>
+__device__ __forceinline__ void upper_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
+    tri_product<kParts, kZero, false, kXParts>(m, x, out);
+}
+
+// S += tile^T x (rows dk, summed over the chunk's tokens), x in three parts
+template <typename T, int kDk>
+__device__ __forceinline__ void add_columns(const Tile<T, kDk> &tile, const f32x4 *x, f32x4 *S) {
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+    constexpr int kTiles = kDk / 16;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const Frag<3> xp = split_frag<3>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+        for (int h = 0; h < kTiles; h += 4) {
+            Frag<Stream<T>::kParts> f[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) f[t] = tile.column(h + t, s, grp, col);
+            mma_n<4>(f, xp, S + h);
+        }
+    }
+}
+
 // --------------------------------------------------------------- forward chain
 
 template <typename T>
@@ -415,6 +467,7 @@ template <typename T, int kDk, bool kWithO>
 struct Chain {
     static constexpr int kOut = Stream<T>::kOutParts, kTiles = kDk / 16, kSteps = kDk / 32;
     using Stage = ChainStage<T, kDk, kWithO>;
+    using In = Frag<Stream<T>::kParts>;
     f32x4 S[kTiles];
     const ChainArgs<T> &a;
     const T *kp, *qp, *vp;
@@ -445,40 +498,33 @@ struct Chain {
         // R = V - E K S and the state's part of O
         f32x4 R[4], O[4];
         {
-            Frag<3> Sp[kSteps];
+            f32x4 ks[4], qs[4];
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) Sp[s] = split_frag<3>(S[2 * s], S[2 * s + 1]);
+            for (int mt = 0; mt < 4; ++mt) ks[mt] = qs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const Frag<3> Sp = split_frag<3>(S[2 * s], S[2 * s + 1]);
+                In kf[4], qf[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    kf[mt] = l.k.row(mt * 16 + col, s, grp);
+                    if constexpr (kWithO) qf[mt] = l.q.row(mt * 16 + col, s, grp);
+                }
+                mma_n<4>(kf, Sp, ks);
+                if constexpr (kWithO) mma_n<4>(qf, first_parts<kOut>(Sp), qs);
+            }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) ks = mma(l.k.row(mt * 16 + col, s, grp), Sp[s], ks);
                 const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = l.v.values(mt, grp, wave * 16, col);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) R[mt][r] = fmaf(-e[r], ks[r], v[r]);
-                if constexpr (kWithO) {
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        Frag<kOut> So;
-#pragma unroll
-                        for (int x = 0; x < kOut; ++x) So.p[x] = Sp[s].p[x];
-                        qs = mma(l.q.row(mt * 16 + col, s, grp), So, qs);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) O[mt][r] = d.scale * e[r] * qs[r];
+                for (int r = 0; r < 4; ++r) {
+                    R[mt][r] = fmaf(-e[r], ks[mt][r], v[r]);
+                    O[mt][r] = d.scale * e[r] * qs[mt][r];
                 }
             }
         }
         f32x4 U[4];
-        {
-            const Frag<3> Rp[2] = {split_frag<3>(R[0], R[1]), split_frag<3>(R[2], R[3])};
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                U[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s <= mt / 2; ++s) U[mt] = mma(mat_frag<3>(l.m.W, frag_lower(mt, s)), Rp[s], U[mt]);
-            }
-        }
+        lower_product<3>(l.m.W, R, U);
         // the next state
         {
             const float last = l.m.e[kChunk - 1];
@@ -489,23 +535,15 @@ struct Chain {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) Ur[mt][r] = rest[r] * U[mt][r];
             }
-            const Frag<3> Up[2] = {split_frag<3>(Ur[0], Ur[1]), split_frag<3>(Ur[2], Ur[3])};
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
+            for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[t][r] *= last;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) S[t] = mma(l.k.column(t, s, grp, col), Up[s], S[t]);
-            }
+            add_columns(l.k, Ur, S);
         }
         if constexpr (kWithO) {
-            const Frag<kOut> Up[2] = {split_frag<kOut>(U[0], U[1]), split_frag<kOut>(U[2], U[3])};
             T *out = op + t0 * vstride;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                for (int s = 0; s <= mt / 2; ++s) O[mt] = mma(mat_frag<kOut>(l.m.P, frag_lower(mt, s)), Up[s], O[mt]);
-            }
+            lower_product<kOut, false>(l.m.P, U, O);
             if (m == kChunk) {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)

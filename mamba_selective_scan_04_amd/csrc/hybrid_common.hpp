@@ -113,6 +113,32 @@ __device__ __forceinline__ f32x4 mma(const Frag<kA> &a, const Frag<kB> &b, f32x4
     return acc;
 }
 
+// The same for kN results at once, acc[i] += A_i B: consecutive instructions are
+// independent, where one result's own chain would wait for each.
+template <int kN, int kA, int kB>
+__device__ __forceinline__ void mma_n(const Frag<kA> *a, const Frag<kB> &b, f32x4 *acc) {
+    constexpr int kOrder = kA > kB ? kA : kB;
+#pragma unroll
+    for (int s = kOrder - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < kA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < kB) {
+#pragma unroll
+                for (int x = 0; x < kN; ++x) acc[x] = mfma(a[x].p[i], b.p[j], acc[x]);
+            }
+        }
+}
+
+// the first kTo parts
+template <int kTo, int kFrom>
+__device__ __forceinline__ Frag<kTo> first_parts(const Frag<kFrom> &f) {
+    Frag<kTo> g;
+#pragma unroll
+    for (int i = 0; i < kTo; ++i) g.p[i] = f.p[i];
+    return g;
+}
+
 // How a stream type (uint16_t: bf16 bits; float) enters products.
 template <typename T>
 struct Stream;
