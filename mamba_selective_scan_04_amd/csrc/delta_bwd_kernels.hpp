@@ -56,19 +56,22 @@ struct Adjoint {
         const int64_t left = len - (int64_t)c * kChunk;
         return left < kChunk ? (int)left : kChunk;
     }
+    typename Tile<T, kDk>::template Offsets<4> koff;
+    typename Tile<T, 64>::template Offsets<4> voff;
+
     __device__ __forceinline__ void fill(Stage &l, int c) {
         const int64_t t0 = (int64_t)c * kChunk;
-        const int m = tokens(c);
-        l.k.template fill<4>(kp + t0 * kstride, kstride, m);
-        l.q.template fill<4>(qp + t0 * kstride, kstride, m);
-        l.o.template fill<4>(op + t0 * vstride, vstride, m);
+        l.k.template fill<4>(kp + t0 * kstride, koff);
+        l.q.template fill<4>(qp + t0 * kstride, koff);
+        l.o.template fill<4>(op + t0 * vstride, voff);
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
     }
     __device__ __forceinline__ void store_state(float *out) {
+        const uint32_t lane_off = (uint32_t)(grp * 8 * a.d.dv + n);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(t, grp, r) * a.d.dv + n] = S[t][r];
+            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * a.d.dv)[lane_off] = S[t][r];
     }
     __device__ __forceinline__ void step(const Stage &l, int c) {
         const int m = tokens(c);
@@ -148,8 +151,12 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
             s.S[t][r] = a.dh_final == nullptr ? 0.f : a.dh_final[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
     auto keep = [&](int c) { s.store_state(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state); };
     int c = chunks - 1;
+    s.koff.set(s.kstride, c >= 0 ? s.tokens(c) : kChunk);   // the last chunk's; the others are full
+    s.voff.set(s.vstride, c >= 0 ? s.tokens(c) : kChunk);
     if constexpr (kTwo) {
         if (c >= 0) s.fill(l0, c);
+        s.koff.set(s.kstride, kChunk);
+        s.voff.set(s.vstride, kChunk);
         for (; c >= 0; c -= 2) {
             __syncthreads();   // l0 is filled, l1 is read
             if (c > 0) s.fill(l1, c - 1);
@@ -165,6 +172,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
         for (; c >= 0; --c) {
             __syncthreads();
             s.fill(l0, c);
+            s.koff.set(s.kstride, kChunk);
+            s.voff.set(s.vstride, kChunk);
             keep(c);
             __syncthreads();
             s.step(l0, c);
@@ -216,22 +225,11 @@ __device__ __forceinline__ Frag<kParts> load_state(const float *p) {
     return split_frag<kParts>(*(const f32x4 *)p, *(const f32x4 *)(p + 4));
 }
 
-// B fragment (rows of state tiles 2 s, 2 s + 1) of a state's column at p
-template <int kDv>
-__device__ __forceinline__ Frag<3> state_columns(const float *p, int s, int grp) {
-    f32x4 x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][r] = p[state_row(2 * s + i, grp, r) * kDv];
-    return split_frag<3>(x[0], x[1]);
-}
-
 template <typename T, int kDk, int kDv>
 struct GradLds {
     static constexpr int kOut = Stream<T>::kOutParts;
     Tile<T, kDk> k, q;
-    typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o;   // dO (fp32 streams: from memory)
+    typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o, v;   // dO, V (fp32 streams: from memory)
     union {
         struct {
             Mats<3> fwd, bwd;
@@ -255,9 +253,10 @@ struct GradLds {
 // (rows of S, dS' from memory, each read once) and over the chunk's tokens.  The
 // token by token matrices (DP for dQ, DP and DA + DA^T for dK) are formed in
 // turn, two result tiles to a B fragment as they stand, and shared through LDS.
-template <typename T, int kDk, int kDv>
+template <typename T, int kDk, int kDv, bool kShared>
 __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     using L = GradLds<T, kDk, kDv>;
+    constexpr bool kBf16 = sizeof(T) == 2;
     constexpr int kThreads = kDv * 4, kWaves = kDv / 16, kSteps = kDk / 32, kVSteps = kDv / 32;
     constexpr int kIn = Stream<T>::kParts, kOut = Stream<T>::kOutParts;
     constexpr int kDkTiles = kDk / 16;
@@ -266,51 +265,82 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     __shared__ __attribute__((aligned(16))) L l;
     const DeltaDims &d = a.d;
     const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
     const int64_t len = row_len(d, b), t0 = (int64_t)c * kChunk;
     const int rows = d.T - t0 < kChunk ? (int)(d.T - t0) : kChunk;
     const int m = len <= t0 ? 0 : len - t0 < kChunk ? (int)(len - t0) : kChunk;
     const int64_t kstride = (int64_t)d.hk * kDk, vstride = (int64_t)d.hv * kDv, state = (int64_t)kDk * kDv;
     const int64_t kat = (((int64_t)b * d.T + t0) * d.hk + hk) * kDk;
-    const int dk0 = wave * kMine % kDkTiles, tk0 = wave * kMine / kDkTiles * kToks;
+    const int dk0 = wave * kMine % kDkTiles, tk0 = kToks == 4 ? 0 : wave * kMine / kDkTiles * kToks;
+    const int n = wave * 16 + col;
 
     f32x4 dQ[kMine][kToks], dK[kMine][kToks];
+    if (kShared || m == 0) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
+        for (int i = 0; i < kMine; ++i)
 #pragma unroll
-        for (int j = 0; j < kToks; ++j) dQ[i][j] = dK[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < kToks; ++j) dQ[i][j] = dK[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     if (m > 0) {
         l.k.template fill<kWaves>(a.k + kat, kstride, m);
         l.q.template fill<kWaves>(a.q + kat, kstride, m);
     }
-    for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
+    for (int hv = hk * d.group; hv < (kShared ? (hk + 1) * d.group : hk + 1); ++hv) {
         const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv;   // of the gates; times dv of v
         const int64_t unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
         T *dvp = a.dv + at * kDv;
-        const T *dop = a.dout + at * kDv;
+        const T *dop = a.dout + at * kDv, *vp = a.v + at * kDv;
         for (int e = threadIdx.x; e < (rows - m) * kDv; e += kThreads)
             Stream<T>::store(dvp + (m + e / kDv) * vstride + e % kDv, 0.f);
         for (int t = m + threadIdx.x; t < rows; t += kThreads) a.dg[at + (int64_t)t * d.hv] = a.dbeta[at + (int64_t)t * d.hv] = 0.f;
         if (m == 0) continue;
         const int64_t chunk_at = (((int64_t)b * d.chunks + c) * d.hv + hv) * state;
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
-        const int n = wave * 16 + col;
+        const uint32_t col_off = (uint32_t)(grp * 8 * kDv + n);
         __syncthreads();   // the last head's reads of LDS are done
         fill_mats<3, kWaves>(a.fwd + unit, &l.fwd);
         fill_mats<3, kWaves>(a.bwd + unit, &l.bwd);
-        if constexpr (sizeof(T) == 2) l.o.template fill<kWaves>(dop, vstride, m);
-        f32x4 v[4], dO[4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = i / 4 * 16 + grp * 4 + i % 4;
-            v[i / 4][i % 4] = Stream<T>::load(a.v + at * kDv + (t < m ? t : m - 1) * vstride + n);
-            if constexpr (sizeof(T) == 4) dO[i / 4][i % 4] = dop[(t < m ? t : m - 1) * vstride + n];
+        if constexpr (kBf16) {
+            l.o.template fill<kWaves>(dop, vstride, m);
+            l.v.template fill<kWaves>(vp, vstride, m);
         }
+        f32x4 raw[2 * kSteps];   // the state's columns, then its adjoint's, on their way
+        const auto load_columns = [&](const float *p) {
+#pragma unroll
+            for (int t = 0; t < 2 * kSteps; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) raw[t][r] = (p + state_row(t, 0, r) * kDv)[col_off];
+        };
+        load_columns(Sg);
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
             l.G[t] = a.G[unit * kChunk + t];
             l.bt[t] = t < m ? strength(a.beta[at + (int64_t)t * d.hv]) : 1.f;
         }
+        const auto value_tile = [&](int mt) {
+            if constexpr (kBf16) {
+                return l.v.values(mt, grp, wave * 16, col);
+            } else {
+                f32x4 x;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = mt * 16 + grp * 4 + r;
+                    x[r] = vp[(t < m ? t : m - 1) * vstride + n];
+                }
+                return x;
+            }
+        };
+        const auto dout_tile = [&](int mt) {
+            f32x4 x;
+            if constexpr (kBf16) x = l.o.values(mt, grp, wave * 16, col);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = mt * 16 + grp * 4 + r;
+                if constexpr (!kBf16) x[r] = dop[(t < m ? t : m - 1) * vstride + n];
+                x[r] = t < m ? x[r] : 0.f;
+            }
+            return x;
+        };
         __syncthreads();
         if (threadIdx.x < kChunk) {   // these outlast the matrices
             l.e[threadIdx.x] = l.fwd.e[threadIdx.x];
@@ -326,26 +356,24 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 for (int mt = 0; mt < 4; ++mt) ks[mt] = qs[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const Frag<3> Sp = state_columns<kDv>(Sg + n, s, grp);
-                    Frag<kIn> kf[4], qf[4];
+                    const Frag<3> Sp = split_frag<3>(raw[2 * s], raw[2 * s + 1]);
+                    Frag<kIn> f[4];
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) {
-                        kf[mt] = l.k.row(mt * 16 + col, s, grp);
-                        qf[mt] = l.q.row(mt * 16 + col, s, grp);
-                    }
-                    mma_n<4>(kf, Sp, ks);
-                    mma_n<4>(qf, Sp, qs);
+                    for (int mt = 0; mt < 4; ++mt) f[mt] = l.k.row(mt * 16 + col, s, grp);
+                    mma_n<4>(f, Sp, ks);
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) f[mt] = l.q.row(mt * 16 + col, s, grp);
+                    mma_n<4>(f, Sp, qs);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                load_columns(dSg);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
-                    const f32x4 e = *(const f32x4 *)(l.fwd.e + mt * 16 + grp * 4);
-                    if constexpr (sizeof(T) == 2) dO[mt] = l.o.values(mt, grp, wave * 16, col);
+                    const f32x4 e = *(const f32x4 *)(l.fwd.e + mt * 16 + grp * 4), v = value_tile(mt);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        R[mt][r] = fmaf(-e[r], ks[mt][r], v[mt][r]);
+                        R[mt][r] = fmaf(-e[r], ks[mt][r], v[r]);
                         O[mt][r] = d.scale * e[r] * qs[mt][r];
-                        dO[mt][r] = mt * 16 + grp * 4 + r < m ? dO[mt][r] : 0.f;
                     }
                 }
             }
@@ -354,9 +382,11 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             __builtin_amdgcn_sched_barrier(0);
             lower_product<3, false>(l.fwd.P, U, O);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < 4; ++mt) {
+                const f32x4 dO = dout_tile(mt);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[mt][r] * O[mt][r];
+                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[r] * O[mt][r];
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
         float end = 0.f;   // <S, dS'> exp(G_C) (by rows, below) + sum of U (K dS') rows
@@ -366,7 +396,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             for (int mt = 0; mt < 4; ++mt) dU[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const Frag<3> Sp = state_columns<kDv>(dSg + n, s, grp);
+                const Frag<3> Sp = split_frag<3>(raw[2 * s], raw[2 * s + 1]);
                 Frag<kIn> kf[4];
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) kf[mt] = l.k.row(mt * 16 + col, s, grp);
@@ -383,57 +413,86 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            upper_product<3, false, kIn>(l.bwd.P, dO, dU);
+            {
+                f32x4 dO[4];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) dO[mt] = dout_tile(mt);
+                upper_product<3, false, kIn>(l.bwd.P, dO, dU);
+            }
             __builtin_amdgcn_sched_barrier(0);
             upper_product<3>(l.bwd.W, dU, X);
         }
         __syncthreads();   // the matrices are read: U and X take their place
+        float sdG[4], sdb[4];   // row sums over this wave's columns, lane r = col of each result row set
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
+            const f32x4 v = value_tile(mt);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = mt * 16 + grp * 4 + r;
                 const float u = U[mt][r], x = X[mt][r], ib = 1.f / l.bt[t], y = u * ib, z = x * ib;
-                float s = dG[mt][r] - x * (v[mt][r] - y) - u * z, db = y * z;
-#pragma unroll
-                for (int w = 1; w < 16; w <<= 1) {
-                    s += __shfl_xor(s, w, 64);
-                    db += __shfl_xor(db, w, 64);
-                }
-                if (col == 0) {
-                    l.dG[wave][t] = s;
-                    l.db[wave][t] = db;
-                }
+                sdG[r] = dG[mt][r] - x * (v[r] - y) - u * z;
+                sdb[r] = y * z;
                 l.U.put(t, n, u);
                 l.X.put(t, n, x);
                 if (t < m) Stream<T>::store(dvp + t * vstride + n, x);
             }
+            // four sums over 16 lanes together: halve the values as the lanes
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                sdG[r] += __shfl_xor(sdG[r], 1, 64);
+                sdb[r] += __shfl_xor(sdb[r], 1, 64);
+            }
+            const bool odd = col & 1, two = col & 2;
+            float g0 = odd ? sdG[1] : sdG[0], g1 = odd ? sdG[3] : sdG[2], b0 = odd ? sdb[1] : sdb[0], b1 = odd ? sdb[3] : sdb[2];
+            g0 += __shfl_xor(g0, 2, 64);
+            g1 += __shfl_xor(g1, 2, 64);
+            b0 += __shfl_xor(b0, 2, 64);
+            b1 += __shfl_xor(b1, 2, 64);
+            float g = two ? g1 : g0, db = two ? b1 : b0;
+            g += __shfl_xor(g, 4, 64);
+            db += __shfl_xor(db, 4, 64);
+            g += __shfl_xor(g, 8, 64);
+            db += __shfl_xor(db, 8, 64);
+            if (col < 4) {   // lane col holds row 2 (col / 2) + col % 2
+                l.dG[wave][mt * 16 + grp * 4 + col] = g;
+                l.db[wave][mt * 16 + grp * 4 + col] = db;
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
         // by rows: products over dv
         const auto dout_row = [&](int r, int s) {
-            if constexpr (sizeof(T) == 2) return l.o.row(r, s, grp);
+            if constexpr (kBf16) return l.o.row(r, s, grp);
             else return load_straight(dop + (r < m ? r : m - 1) * vstride + s * 32 + grp * 8);
         };
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int tile = dk0 + i;
-            const int64_t r0 = (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * kDv + grp * 8;
-            f32x4 so[kToks], sx[kToks], du[kToks];
+            const uint32_t r0 = (uint32_t)((tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * kDv + grp * 8);
+            f32x4 so[kToks], sx[kToks], du[kToks], x[2], y[2];
 #pragma unroll
             for (int j = 0; j < kToks; ++j) so[j] = sx[j] = du[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < kVSteps; ++s) {
-                f32x4 x[2], y[2];
+            for (int h = 0; h < 2; ++h) {
+                x[h] = *(const f32x4 *)(Sg + r0 + h * 4);
+                y[h] = *(const f32x4 *)(dSg + r0 + h * 4);
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    x[h] = *(const f32x4 *)(Sg + r0 + s * 32 + h * 4);
-                    y[h] = *(const f32x4 *)(dSg + r0 + s * 32 + h * 4);
+            for (int s = 0; s < kVSteps; ++s) {
+                const Frag<kOut> sf = split_frag<kOut>(x[0], x[1]), df = split_frag<kOut>(y[0], y[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dot = fmaf(x[h][r], y[h][r], dot);
+                if (s + 1 < kVSteps) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[h] = *(const f32x4 *)(Sg + r0 + (s + 1) * 32 + h * 4);
+                        y[h] = *(const f32x4 *)(dSg + r0 + (s + 1) * 32 + h * 4);
+                    }
                 }
-                const Frag<kOut> sf = split_frag<kOut>(x[0], x[1]), df = split_frag<kOut>(y[0], y[1]);
 #pragma unroll
                 for (int j = 0; j < kToks; ++j) {
                     const int t = (tk0 + j) * 16 + col;
@@ -448,8 +507,9 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 const float et = l.e[(tk0 + j) * 16 + col], rt = l.rest[(tk0 + j) * 16 + col];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    dQ[i][j][r] = fmaf(d.scale * et, so[j][r], dQ[i][j][r]);
-                    dK[i][j][r] += rt * du[j][r] - et * sx[j][r];
+                    const float q = d.scale * et * so[j][r], k = rt * du[j][r] - et * sx[j][r];
+                    dQ[i][j][r] = kShared ? dQ[i][j][r] + q : q;
+                    dK[i][j][r] = kShared ? dK[i][j][r] + k : k;
                 }
             }
         }
@@ -459,9 +519,9 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         if (lane == 0) l.ends[wave] = end;
         // products over the chunk's tokens.  kind 0: DP^T (rows j, columns i) for
         // dQ; 1: DP (rows i, columns j), 2: DA + DA^T, for dK.
-#pragma unroll
-        for (int kind = 0; kind < 3; ++kind) {
-            const int frags = kind == 2 ? 8 : kFrags;
+        const auto pass = [&](auto which) {
+            constexpr int kind = decltype(which)::value, frags = kind == 2 ? 8 : kFrags;
+#pragma unroll 1
             for (int f = wave; f < frags; f += kWaves) {
                 // column tile and step of the fragment
                 const int ct = kind == 2 ? f / 2 : kind == 0 ? (f < 2 ? f : f / 2 + 1) : (f < 4 ? f / 2 : f - 2);
@@ -502,24 +562,31 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             }
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
+            for (int s = 0; s < 2; ++s) {
+                Frag<kIn> x[kMine];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const auto x = kind == 1 ? l.q.column(dk0 + i, s, grp, col) : l.k.column(dk0 + i, s, grp, col);
+                for (int i = 0; i < kMine; ++i) x[i] = kind == 1 ? l.q.column(dk0 + i, s, grp, col) : l.k.column(dk0 + i, s, grp, col);
 #pragma unroll
-                    for (int j = 0; j < kToks; ++j) {
-                        const int ct = tk0 + j;
-                        if (kind == 0 ? s > ct / 2 : kind == 1 ? s < ct / 2 : false) continue;
-                        const int f = kind == 2 ? ct * 2 + s : kind == 0 ? frag_lower(ct, s) : frag_upper(ct, s);
-                        Frag<kOut> y;
+                for (int j = 0; j < kToks; ++j) {
+                    // beyond the triangle: no fragment (with two token tiles a wave, both or none)
+                    const int half = kToks == 4 ? j / 2 : tk0 / 2;
+                    if (kind == 0 ? s > half : kind == 1 ? s < half : false) continue;
+                    const int ct = tk0 + j, f = kind == 2 ? ct * 2 + s : kind == 0 ? frag_lower(ct, s) : frag_upper(ct, s);
+                    Frag<kOut> y;
 #pragma unroll
-                        for (int p = 0; p < kOut; ++p) y.p[p] = __builtin_bit_cast(bf16x8, l.pairs[f][p][lane]);
-                        if (kind == 0) dQ[i][j] = mma(x, y, dQ[i][j]);
-                        else dK[i][j] = mma(x, y, dK[i][j]);
+                    for (int p = 0; p < kOut; ++p) y.p[p] = __builtin_bit_cast(bf16x8, l.pairs[f][p][lane]);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        if constexpr (kind == 0) dQ[i][j] = mma(x[i], y, dQ[i][j]);
+                        else dK[i][j] = mma(x[i], y, dK[i][j]);
                     }
                 }
+            }
             __syncthreads();
-        }
+        };
+        pass(std::integral_constant<int, 0>{});
+        pass(std::integral_constant<int, 1>{});
+        pass(std::integral_constant<int, 2>{});
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
             float s = 0.f, db = 0.f, ends = 0.f;

@@ -81,9 +81,10 @@ typedef const __attribute__((address_space(1))) void glb_ptr;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// one wave's 64 x 16 bytes: lane l's piece to base + 16 l
-__device__ __forceinline__ void load_lds(const void *src, void *base) {
-    __builtin_amdgcn_global_load_lds((glb_ptr *)src, (lds_ptr *)base, 16, 0, 0);
+// one wave's 64 x 16 bytes: lane l's piece, `off` bytes behind the uniform src, to
+// base + 16 l
+__device__ __forceinline__ void load_lds(const void *src, uint32_t off, void *base) {
+    __builtin_amdgcn_global_load_lds((glb_ptr *)((const char *)src + off), (lds_ptr *)base, 16, 0, 0);
 }
 
 template <typename T, int kCols>
@@ -98,16 +99,34 @@ struct Tile {
     }
     __device__ __forceinline__ const T *piece(int r, int p) const { return e + r * kCols + (p ^ turn(r)) * kVec; }
 
-    // by kWaves waves; m: tokens of the chunk (at least 1)
+    // Filled by kWaves waves.  A lane's offsets into the rows (stride elements
+    // apart, of which m, at least 1, are tokens) do not change from one full
+    // chunk to the next.
+    template <int kWaves>
+    struct Offsets {
+        static constexpr int kLoads = kBytes / 1024 / kWaves;
+        uint32_t off[kLoads];
+        __device__ __forceinline__ void set(int64_t stride, int m) {
+            const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int at = (wave * kLoads + i) * 64 + lane, r = at / kPieces, p = at % kPieces ^ turn(r);
+                off[i] = ((uint32_t)(r < m ? r : m - 1) * (uint32_t)stride + (uint32_t)(p * kVec)) * (uint32_t)sizeof(T);
+            }
+        }
+    };
+    template <int kWaves>
+    __device__ __forceinline__ void fill(const T *src, const Offsets<kWaves> &o) {
+        constexpr int kLoads = Offsets<kWaves>::kLoads;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load_lds(src, o.off[i], (char *)e + (wave * kLoads + i) * 1024);
+    }
     template <int kWaves>
     __device__ __forceinline__ void fill(const T *src, int64_t stride, int m) {
-        constexpr int kLoads = kBytes / 1024 / kWaves;
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = (wave * kLoads + i) * 64 + lane, r = at / kPieces, p = at % kPieces ^ turn(r);
-            load_lds(src + (r < m ? r : m - 1) * stride + p * kVec, (char *)e + (wave * kLoads + i) * 1024);
-        }
+        Offsets<kWaves> o;
+        o.set(stride, m);
+        fill(src, o);
     }
     // eight consecutive elements of a row: columns 32 s + 8 grp ..
     __device__ __forceinline__ auto row(int r, int s, int grp) const {
@@ -383,9 +402,10 @@ template <int kParts, int kWaves = 4>
 __device__ __forceinline__ void fill_mats(const Mats<kParts> *src, Mats<kParts> *dst) {
     constexpr int kLoads = (int)sizeof(Mats<kParts>) / 1024;
     static_assert(sizeof(Mats<kParts>) % 1024 == 0, "");
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lane = threadIdx.x & 63;
     for (int i = wave; i < kLoads; i += kWaves)
-        load_lds((const char *)src + i * 1024 + lane * 16, (char *)dst + i * 1024);
+        load_lds((const char *)src + i * 1024, lane * 16, (char *)dst + i * 1024);
 }
 
 // out (+)= M x for a lower (kLower) or upper triangular matrix in kParts parts
@@ -474,21 +494,29 @@ struct Chain {
     T *op;
     int64_t kstride, vstride, len;
     int hv, b, lane, wave, col, grp, n;
+    uint32_t ooff;   // of this lane's outputs within a chunk's rows
+
+    typename Tile<T, kDk>::template Offsets<4> koff;
+    typename Tile<T, 64>::template Offsets<4> voff;
 
     __device__ __forceinline__ void fill(Stage &l, int c) {
         const int64_t t0 = (int64_t)c * kChunk;
-        const int m = len - t0 < kChunk ? (int)(len - t0) : kChunk;
-        l.k.template fill<4>(kp + t0 * kstride, kstride, m);
-        if (kWithO) l.q.template fill<4>(qp + t0 * kstride, kstride, m);
-        l.v.template fill<4>(vp + t0 * vstride, vstride, m);
+        if (len - t0 < kChunk) {
+            koff.set(kstride, (int)(len - t0));
+            voff.set(vstride, (int)(len - t0));
+        }
+        l.k.template fill<4>(kp + t0 * kstride, koff);
+        if constexpr (kWithO) l.q.template fill<4>(qp + t0 * kstride, koff);
+        l.v.template fill<4>(vp + t0 * vstride, voff);
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
     }
 
     __device__ __forceinline__ void store_state(float *out) {
+        const uint32_t lane_off = (uint32_t)(grp * 8 * a.d.dv + n);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(t, grp, r) * a.d.dv + n] = S[t][r];
+            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * a.d.dv)[lane_off] = S[t][r];
     }
 
     __device__ __forceinline__ void step(const Stage &l, int c) {
@@ -544,17 +572,17 @@ struct Chain {
         if constexpr (kWithO) {
             T *out = op + t0 * vstride;
             lower_product<kOut, false>(l.m.P, U, O);
-            if (m == kChunk) {
+            if (m == kChunk) {   // uniform rows and a lane's own offset
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) Stream<T>::store(out + (mt * 16 + grp * 4 + r) * vstride, O[mt][r]);
+                    for (int r = 0; r < 4; ++r) Stream<T>::store(out + (mt * 16 + r) * vstride + ooff, O[mt][r]);
             } else {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (mt * 16 + grp * 4 + r < m) Stream<T>::store(out + (mt * 16 + grp * 4 + r) * vstride, O[mt][r]);
+                        if (mt * 16 + grp * 4 + r < m) Stream<T>::store(out + (mt * 16 + r) * vstride + ooff, O[mt][r]);
             }
         }
     }
@@ -583,7 +611,10 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
     s.kp = a.k + (tok * d.hk + hk) * kDk;
     s.qp = kWithO ? a.q + (tok * d.hk + hk) * kDk : nullptr;
     s.vp = a.v + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64;
-    s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + s.n : nullptr;
+    s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64 : nullptr;
+    s.ooff = (uint32_t)(s.grp * 4 * s.vstride) + s.wave * 16 + s.col;
+    s.koff.set(s.kstride, kChunk);
+    s.voff.set(s.vstride, kChunk);
     const int chunks = (int)((s.len + kChunk - 1) / kChunk);
     const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
 #pragma unroll
@@ -619,7 +650,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
     if (a.h_final != nullptr) s.store_state(a.h_final + head * state);
     for (int c = chunks; c < d.chunks; ++c) keep(c);   // chunks of padding alone: the state stays
     if (kWithO)   // padding: zeros
-        for (int64_t t = s.len + s.grp; t < d.T; t += 4) Stream<T>::store(s.op + t * s.vstride, 0.f);
+        for (int64_t t = s.len + s.grp; t < d.T; t += 4) Stream<T>::store(s.op + t * s.vstride + s.wave * 16 + s.col, 0.f);
 }
 
 // ---------------------------------------------------------------- recurrent

@@ -36,8 +36,14 @@ void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
     if (c.d.chunks == 0) return;
     const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.fwd, (const Mats<3> *)c.bwd,
                          c.G, c.beta, c.h_chunks, c.dS, (T *)c.dq, (T *)c.dk_out, (T *)c.dv_out, c.dg, c.dbeta, c.d};
-    if (c.d.dv == 64) hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 64>), gp, dim3(256), 0, st, ga);
-    else hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 128>), gp, dim3(512), 0, st, ga);
+    const bool shared = c.d.group > 1;
+    if (c.d.dv == 64) {
+        if (shared) hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 64, true>), gp, dim3(256), 0, st, ga);
+        else hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 64, false>), gp, dim3(256), 0, st, ga);
+    } else {
+        if (shared) hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 128, true>), gp, dim3(512), 0, st, ga);
+        else hipLaunchKernelGGL((delta_grad_kernel<T, kDk, 128, false>), gp, dim3(512), 0, st, ga);
+    }
 }
 
 template <>
