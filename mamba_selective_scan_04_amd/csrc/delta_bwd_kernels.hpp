@@ -265,14 +265,13 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     __shared__ __attribute__((aligned(16))) L l;
     const DeltaDims &d = a.d;
     const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t len = row_len(d, b), t0 = (int64_t)c * kChunk;
     const int rows = d.T - t0 < kChunk ? (int)(d.T - t0) : kChunk;
     const int m = len <= t0 ? 0 : len - t0 < kChunk ? (int)(len - t0) : kChunk;
     const int64_t kstride = (int64_t)d.hk * kDk, vstride = (int64_t)d.hv * kDv, state = (int64_t)kDk * kDv;
     const int64_t kat = (((int64_t)b * d.T + t0) * d.hk + hk) * kDk;
     const int dk0 = wave * kMine % kDkTiles, tk0 = kToks == 4 ? 0 : wave * kMine / kDkTiles * kToks;
-    const int n = wave * 16 + col;
 
     f32x4 dQ[kMine][kToks], dK[kMine][kToks];
     if (kShared || m == 0) {
@@ -286,6 +285,11 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         l.q.template fill<kWaves>(a.q + kat, kstride, m);
     }
     for (int hv = hk * d.group; hv < (kShared ? (hk + 1) * d.group : hk + 1); ++hv) {
+        // opaque to the compiler: it would keep some 200 lane addresses of the
+        // loop's body in registers (and spill them) rather than form them again
+        int lane = lane_id();
+        asm volatile("" : "+v"(lane));
+        const int col = lane & 15, grp = lane >> 4, n = wave * 16 + col;
         const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv;   // of the gates; times dv of v
         const int64_t unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
         T *dvp = a.dv + at * kDv;
@@ -608,6 +612,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             }
         }
     }
+    const int col = lane_id() & 15, grp = lane_id() >> 4;
 #pragma unroll
     for (int j = 0; j < kToks; ++j) {
         const int t = (tk0 + j) * 16 + col;

@@ -588,6 +588,14 @@ struct Chain {
     }
 };
 
+// A barrier behind which every wave's loads into LDS have arrived; the kLater
+// youngest memory operations of a wave (stores that it issued after them) may
+// still be under way.
+template <int kLater>
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLater) : "memory");
+}
+
 template <typename T, int kDk, bool kWithO>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs<T> a) {
     using C = Chain<T, kDk, kWithO>;
@@ -628,12 +636,15 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
     if constexpr (kTwo) {
         if (chunks > 0) s.fill(l0, 0);
         for (int c = 0; c < chunks; c += 2) {
-            __syncthreads();   // l0 is filled, l1 is read
+            // l0 is filled, l1 is read.  A full chunk's step ends with 16 stores of
+            // its outputs; only the last is not full.
+            if (kWithO && c > 0) stage_barrier<16>();
+            else __syncthreads();
             if (c + 1 < chunks) s.fill(l1, c + 1);
             keep(c);
             s.step(l0, c);
             if (c + 1 >= chunks) break;
-            __syncthreads();
+            stage_barrier<kWithO ? 16 : 0>();
             if (c + 2 < chunks) s.fill(l0, c + 2);
             keep(c + 1);
             s.step(l1, c + 1);
