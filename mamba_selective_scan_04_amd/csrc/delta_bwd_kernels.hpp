@@ -302,8 +302,8 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
         const uint32_t col_off = (uint32_t)(grp * 8 * kDv + n);
         __syncthreads();   // the last head's reads of LDS are done
-        fill_mats<3, kWaves>(a.fwd + unit, &l.fwd);
-        fill_mats<3, kWaves>(a.bwd + unit, &l.bwd);
+        fill_mats<kWaves>(a.fwd + unit, &l.fwd);
+        fill_mats<kWaves>(a.bwd + unit, &l.bwd);
         if constexpr (kBf16) {
             l.o.template fill<kWaves>(dop, vstride, m);
             l.v.template fill<kWaves>(vp, vstride, m);

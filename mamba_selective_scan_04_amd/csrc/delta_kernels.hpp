@@ -200,11 +200,10 @@ __device__ __forceinline__ int state_row(int tile, int grp, int r) { return tile
 //   backward: W^T (row tile mt, steps s >= mt / 2)  P^T in three parts
 template <int kPParts>
 struct Mats {
-    static constexpr int kP = kPParts;
     uint4 W[3][kFrags][64];
-    uint4 P[kPParts][kFrags][64];
     float e[kChunk], rest[kChunk];
-    float pad[128];   // whole kilobytes
+    float pad[128];               // whole kilobytes
+    uint4 P[kPParts][kFrags][64]; // last: a chain without outputs stops here
 };
 __device__ __forceinline__ int frag_lower(int mt, int s) { return mt < 2 ? mt : mt * 2 - 2 + s; }
 __device__ __forceinline__ int frag_upper(int mt, int s) { return mt < 2 ? mt * 2 + s : mt + 2; }
@@ -397,11 +396,21 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
     }
 }
 
-// A chunk's matrices into LDS.
-template <int kParts, int kWaves = 4>
-__device__ __forceinline__ void fill_mats(const Mats<kParts> *src, Mats<kParts> *dst) {
-    constexpr int kLoads = (int)sizeof(Mats<kParts>) / 1024;
-    static_assert(sizeof(Mats<kParts>) % 1024 == 0, "");
+// A chunk's matrices into LDS (kParts 0: all but P).
+template <int kParts>
+struct MatsUsed { using type = Mats<kParts>; };
+template <>
+struct MatsUsed<0> {
+    struct type {
+        uint4 W[3][kFrags][64];
+        float e[kChunk], rest[kChunk];
+        float pad[128];
+    };
+};
+template <int kWaves = 4, typename M>
+__device__ __forceinline__ void fill_mats(const void *src, M *dst) {
+    constexpr int kLoads = (int)sizeof(M) / 1024;
+    static_assert(sizeof(M) % 1024 == 0, "");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = threadIdx.x & 63;
     for (int i = wave; i < kLoads; i += kWaves)
@@ -461,32 +470,41 @@ __device__ __forceinline__ void add_columns(const Tile<T, kDk> &tile, const f32x
 }
 
 // --------------------------------------------------------------- forward chain
+//
+// Where batch, heads and columns are too few to fill the chip, the chunks are
+// cut into segments that run at once.  A segment maps the state before it to
+// the state behind it by S' = M S + N, the same for every column; the chain
+// run from zero gives N, and run from the identity without V gives M
+// (kAggregate).  delta_join_kernel goes through the segments once, and the
+// chain proper starts each segment from the state it finds there.
+enum ChainMode { kStates, kOutputs, kAggregate };
 
 template <typename T>
 struct ChainArgs {
     const T *q, *k, *v;
     const Mats<Stream<T>::kOutParts> *mats;
-    const float *h_init;
-    T *o;                 // null: states only
+    const float *h_init;  // null: zero; with segments [batch, hv, segs, dk, dv]
+    T *o;                 // kOutputs
     float *h_final;       // null: not wanted
     float *h_chunks;      // null, or [batch, chunks, hv, dk, dv]
+    float *agg;           // kAggregate: [batch, hv, segs, dk, dv + dk]
+    int segs, per;        // segments, and chunks of each
     DeltaDims d;
 };
 
-// What a step of the chain reads, filled while the step before it computes
-// (bf16; fp32 streams have room for one set only).
-template <typename T, int kDk, bool kWithO>
+template <typename T, int kDk, int kMode>
 struct ChainStage {
     Tile<T, kDk> k;
-    Tile<T, kWithO ? kDk : 64> q;
+    typename std::conditional<kMode == kOutputs, Tile<T, kDk>, char>::type q;
     Tile<T, 64> v;
-    Mats<Stream<T>::kOutParts> m;
+    typename MatsUsed<kMode == kOutputs ? Stream<T>::kOutParts : 0>::type m;
 };
 
-template <typename T, int kDk, bool kWithO>
+template <typename T, int kDk, int kMode>
 struct Chain {
+    static constexpr bool kWithO = kMode == kOutputs;
     static constexpr int kOut = Stream<T>::kOutParts, kTiles = kDk / 16, kSteps = kDk / 32;
-    using Stage = ChainStage<T, kDk, kWithO>;
+    using Stage = ChainStage<T, kDk, kMode>;
     using In = Frag<Stream<T>::kParts>;
     f32x4 S[kTiles];
     const ChainArgs<T> &a;
@@ -494,8 +512,8 @@ struct Chain {
     T *op;
     int64_t kstride, vstride, len;
     int hv, b, lane, wave, col, grp, n;
+    bool has_v;      // kAggregate: not the identity's columns
     uint32_t ooff;   // of this lane's outputs within a chunk's rows
-
     typename Tile<T, kDk>::template Offsets<4> koff;
     typename Tile<T, 64>::template Offsets<4> voff;
 
@@ -507,16 +525,17 @@ struct Chain {
         }
         l.k.template fill<4>(kp + t0 * kstride, koff);
         if constexpr (kWithO) l.q.template fill<4>(qp + t0 * kstride, koff);
-        l.v.template fill<4>(vp + t0 * vstride, voff);
+        if (kMode != kAggregate || has_v) l.v.template fill<4>(vp + t0 * vstride, voff);
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
     }
 
-    __device__ __forceinline__ void store_state(float *out) {
-        const uint32_t lane_off = (uint32_t)(grp * 8 * a.d.dv + n);
+    // rows `ld` apart
+    __device__ __forceinline__ void store_state(float *out, int ld) {
+        const uint32_t lane_off = (uint32_t)(grp * 8 * ld + n);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * a.d.dv)[lane_off] = S[t][r];
+            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * ld)[lane_off] = S[t][r];
     }
 
     __device__ __forceinline__ void step(const Stage &l, int c) {
@@ -543,7 +562,9 @@ struct Chain {
             }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = l.v.values(mt, grp, wave * 16, col);
+                const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4);
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                if (kMode != kAggregate || has_v) v = l.v.values(mt, grp, wave * 16, col);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     R[mt][r] = fmaf(-e[r], ks[mt][r], v[r]);
@@ -596,61 +617,70 @@ __device__ __forceinline__ void stage_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLater) : "memory");
 }
 
-template <typename T, int kDk, bool kWithO>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs<T> a) {
-    using C = Chain<T, kDk, kWithO>;
-    constexpr bool kTwo = sizeof(T) == 2;
+// kTwo: a second set of tiles in LDS, filled while a step computes: one
+// workgroup a CU.  Else one set, and two workgroups a CU cover each other's
+// waits: the faster of the two wherever there are enough workgroups.
+template <typename T, int kDk, int kMode, bool kTwo>
+__global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void delta_chain_kernel(ChainArgs<T> a) {
+    using C = Chain<T, kDk, kMode>;
+    constexpr bool kWithO = kMode == kOutputs;
     __shared__ __attribute__((aligned(16))) typename C::Stage l0;
     __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
     const DeltaDims &d = a.d;
     C s{{}, a};
     s.hv = blockIdx.y;
-    s.b = blockIdx.z;
-    const int hk = s.hv / d.group;
+    s.b = blockIdx.z / a.segs;
+    const int seg = blockIdx.z % a.segs, hk = s.hv / d.group;
     s.lane = lane_id();
     s.wave = threadIdx.x >> 6;
     s.col = s.lane & 15;
     s.grp = s.lane >> 4;
     s.n = blockIdx.x * 64 + s.wave * 16 + s.col;   // this lane's state column
+    s.has_v = kMode != kAggregate || (int)blockIdx.x * 64 < d.dv;
     s.len = row_len(d, s.b);
     s.kstride = (int64_t)d.hk * kDk;
     s.vstride = (int64_t)d.hv * d.dv;
     const int64_t tok = (int64_t)s.b * d.T;
     s.kp = a.k + (tok * d.hk + hk) * kDk;
     s.qp = kWithO ? a.q + (tok * d.hk + hk) * kDk : nullptr;
-    s.vp = a.v + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64;
+    s.vp = a.v + (tok * d.hv + s.hv) * d.dv + (s.has_v ? blockIdx.x * 64 : 0);
     s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64 : nullptr;
     s.ooff = (uint32_t)(s.grp * 4 * s.vstride) + s.wave * 16 + s.col;
     s.koff.set(s.kstride, kChunk);
     s.voff.set(s.vstride, kChunk);
-    const int chunks = (int)((s.len + kChunk - 1) / kChunk);
+    const int chunks = (int)((s.len + kChunk - 1) / kChunk);   // the row's, of all segments
+    const int c0 = seg * a.per, c1 = c0 + a.per < chunks ? c0 + a.per : chunks;
     const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
 #pragma unroll
     for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s.S[t][r] = a.h_init == nullptr ? 0.f : a.h_init[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
+        for (int r = 0; r < 4; ++r) {
+            const int row = state_row(t, s.grp, r);
+            if (kMode == kAggregate) s.S[t][r] = s.n - d.dv == row ? 1.f : 0.f;
+            else s.S[t][r] = a.h_init == nullptr ? 0.f : a.h_init[(head * a.segs + seg) * state + (int64_t)row * d.dv + s.n];
+        }
     auto keep = [&](int c) {
-        if (a.h_chunks != nullptr) s.store_state(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
+        if (kMode != kAggregate && a.h_chunks != nullptr)
+            s.store_state(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state, d.dv);
     };
     if constexpr (kTwo) {
-        if (chunks > 0) s.fill(l0, 0);
-        for (int c = 0; c < chunks; c += 2) {
+        if (c0 < c1) s.fill(l0, c0);
+        for (int c = c0; c < c1; c += 2) {
             // l0 is filled, l1 is read.  A full chunk's step ends with 16 stores of
             // its outputs; only the last is not full.
-            if (kWithO && c > 0) stage_barrier<16>();
+            if (kWithO && c > c0) stage_barrier<16>();
             else __syncthreads();
-            if (c + 1 < chunks) s.fill(l1, c + 1);
+            if (c + 1 < c1) s.fill(l1, c + 1);
             keep(c);
             s.step(l0, c);
-            if (c + 1 >= chunks) break;
+            if (c + 1 >= c1) break;
             stage_barrier<kWithO ? 16 : 0>();
-            if (c + 2 < chunks) s.fill(l0, c + 2);
+            if (c + 2 < c1) s.fill(l0, c + 2);
             keep(c + 1);
             s.step(l1, c + 1);
         }
     } else {
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = c0; c < c1; ++c) {
             __syncthreads();
             s.fill(l0, c);
             keep(c);
@@ -658,10 +688,84 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_chain_kernel(ChainArgs
             s.step(l0, c);
         }
     }
-    if (a.h_final != nullptr) s.store_state(a.h_final + head * state);
-    for (int c = chunks; c < d.chunks; ++c) keep(c);   // chunks of padding alone: the state stays
-    if (kWithO)   // padding: zeros
-        for (int64_t t = s.len + s.grp; t < d.T; t += 4) Stream<T>::store(s.op + t * s.vstride + s.wave * 16 + s.col, 0.f);
+    if (kMode == kAggregate) {
+        s.store_state(a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk), d.dv + kDk);
+        return;
+    }
+    if (a.h_final != nullptr && seg == a.segs - 1) s.store_state(a.h_final + head * state, d.dv);
+    // chunks of padding alone: the state stays
+    const int end = c0 + a.per < d.chunks ? c0 + a.per : d.chunks;
+    for (int c = c1 > c0 ? c1 : c0; c < end; ++c) keep(c);
+    if (kWithO) {   // padding: zeros
+        const int64_t t0 = s.len > (int64_t)c0 * kChunk ? s.len : (int64_t)c0 * kChunk;
+        const int64_t t1 = (int64_t)end * kChunk < d.T ? (int64_t)end * kChunk : d.T;
+        for (int64_t t = t0 + s.grp; t < t1; t += 4) Stream<T>::store(s.op + t * s.vstride + s.wave * 16 + s.col, 0.f);
+    }
+}
+
+// Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s.  One workgroup per
+// 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave per
+// kDk / 4 of the rows of M, read once by rows from memory.
+struct JoinArgs {
+    const float *agg, *h_init;   // h_init null: zero
+    float *h_seg;                // [batch, hv, segs, dk, dv] out, or null
+    float *h_final;              // behind the last segment, or null
+    int segs, dv;
+};
+
+template <int kDk>
+__global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
+    constexpr int kTiles = kDk / 16, kMine = kTiles / 4, kSteps = kDk / 32;
+    __shared__ uint4 part[kSteps][3][64];
+    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4, n = blockIdx.x * 16 + col;
+    const int64_t head = blockIdx.y, state = (int64_t)kDk * a.dv;
+    const int ld = a.dv + kDk;
+    f32x4 h[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            h[i][r] = a.h_init == nullptr ? 0.f : a.h_init[head * state + (int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n];
+    const auto store = [&](float *out) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n] = h[i][r];
+    };
+    for (int s = 0; s < a.segs; ++s) {
+        if (a.h_seg != nullptr) store(a.h_seg + (head * a.segs + s) * state);
+        if (s + 1 == a.segs && a.h_final == nullptr) break;
+        const float *m = a.agg + (head * a.segs + s) * kDk * ld;
+        // a state tile holds half of a 32-row step's slots (kMine 1 at dk 64, 2 at 128)
+        __syncthreads();   // the parts of the segment before are read
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = wave * kMine + i;
+            uint32_t lo[3], hi[3];
+            split_pair<3>(h[i][0], h[i][1], lo);
+            split_pair<3>(h[i][2], h[i][3], hi);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) ((uint2 *)&part[tile / 2][p][lane])[tile & 1] = make_uint2(lo[p], hi[p]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = wave * kMine + i;
+            f32x4 acc;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = m[(int64_t)state_row(tile, grp, r) * ld + n];
+            const float *row = m + (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * ld + a.dv + grp * 8;
+#pragma unroll
+            for (int x = 0; x < kSteps; ++x) {
+                Frag<3> y;
+#pragma unroll
+                for (int p = 0; p < 3; ++p) y.p[p] = __builtin_bit_cast(bf16x8, part[x][p][lane]);
+                acc = mma(load_straight(row + x * 32), y, acc);
+            }
+            h[i] = acc;
+        }
+    }
+    if (a.h_final != nullptr) store(a.h_final + head * state);
 }
 
 // ---------------------------------------------------------------- recurrent

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <initializer_list>
 
@@ -15,6 +16,7 @@ using namespace bdssm_host;
 
 namespace {
 
+constexpr int64_t kDeltaTarget = 256;         // workgroups of a chain that fill the chip
 constexpr int64_t kMost = (int64_t)1 << 40;   // elements of one tensor
 
 bool product_fits(std::initializer_list<int64_t> f) {
@@ -59,12 +61,30 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
     return BDSSM_OK;
 }
 
+// Segments of a row's chunks (1: none).  A chain's step is a chunk's, whatever
+// the batch; cutting the row costs the aggregate pass over d_v + d_k columns
+// besides the chain's own d_v, so it pays from about three segments on, each of
+// 8 chunks at least.  BDSSM_DELTA_SEGMENTS forces a count (tests).
+int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
+    const int64_t groups = s->batch * s->heads_v * (s->d_v / 64);
+    int64_t n = groups > 0 ? kDeltaTarget / groups : 1;
+    if (n > chunks / 8) n = chunks / 8;
+    if (n < 3) n = 1;
+    const char *e = getenv("BDSSM_DELTA_SEGMENTS");
+    if (e != nullptr && *e != 0) n = atoi(e);
+    if (n > chunks) n = chunks;
+    if (n * s->batch > 65535) n = 65535 / (s->batch > 0 ? s->batch : 1);
+    return n < 1 ? 1 : (int)n;
+}
+
 struct DeltaSizes {
-    size_t qk, vo, gate, state, hchunks, units;
+    size_t qk, vo, gate, state, hchunks, units, agg;
     bool bf16;
+    int segs;
     // the workspace: the chunks' matrices; for the backward those of both
     // directions, the summed log decays and the states' adjoints
-    size_t fwd() const { return units * (bf16 ? sizeof(Mats<2>) : sizeof(Mats<3>)); }
+    size_t mats() const { return units * (bf16 ? sizeof(Mats<2>) : sizeof(Mats<3>)); }
+    size_t fwd() const { return mats() + (segs > 1 ? agg + state * segs : 0); }
     size_t mats3() const { return units * sizeof(Mats<3>); }
     size_t sums() const { return units * kChunk * 8; }
     size_t bwd() const { return 2 * mats3() + sums() + hchunks; }
@@ -81,6 +101,8 @@ DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
     z.hchunks = z.state * chunks;
     z.units = (size_t)s->batch * s->heads_v * chunks;
     z.bf16 = s->dtype == BDSSM_BF16;
+    z.segs = delta_segments(s, (int64_t)chunks);
+    z.agg = (size_t)s->batch * s->heads_v * z.segs * s->d_k * (s->d_v + s->d_k) * 4;
     return z;
 }
 
@@ -221,6 +243,9 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     c.h_final = h_final;
     c.h_chunks = h_chunks;
     c.fwd = ws;
+    c.segs = z.segs;
+    c.agg = (float *)((char *)ws + z.mats());
+    c.h_seg = (float *)((char *)ws + z.mats() + z.agg);
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_scan<uint16_t>(c, st);
     else launch_delta_scan<float>(c, st);

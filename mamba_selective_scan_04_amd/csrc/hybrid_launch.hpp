@@ -22,6 +22,8 @@ struct DeltaCall {
     void *o;
     float *h_final, *h_chunks;
     void *fwd;   // the chunks' matrices (Mats)
+    float *agg, *h_seg;   // the segments' maps and first states
+    int segs;
     // backward
     const void *dout;
     const float *dh_final;

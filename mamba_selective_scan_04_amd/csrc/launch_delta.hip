@@ -16,12 +16,33 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
         hipLaunchKernelGGL((delta_prep_kernel<T, kDk, kOut, false>), gp, dim3(kDeltaThreads), 0, st,
                            c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.fwd,
                            (Mats<3> *)nullptr, (double *)nullptr, c.d);
-    const ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.fwd, c.h_init, (T *)c.o, c.h_final, c.h_chunks, c.d};
-    const dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
-    if (c.o != nullptr)
-        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, true>), gc, dim3(kDeltaThreads), 0, st, a);
-    else
-        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, false>), gc, dim3(kDeltaThreads), 0, st, a);
+    ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.fwd, c.h_init, (T *)c.o, c.h_final, c.h_chunks,
+                   c.agg, 1, c.d.chunks, c.d};
+    dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
+    if (c.segs > 1) {
+        a.segs = c.segs;
+        a.per = (c.d.chunks + c.segs - 1) / c.segs;
+        gc.z = (unsigned)(c.batch * c.segs);
+        const dim3 ga((unsigned)((c.d.dv + kDk) / 64), gc.y, gc.z);
+        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), ga, dim3(kDeltaThreads), 0, st, a);
+        // states alone: the join has the last
+        const bool chain = c.o != nullptr || c.h_chunks != nullptr;
+        const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv};
+        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
+        if (!chain) return;
+        a.h_init = c.h_seg;
+    }
+    const bool two = sizeof(T) == 2 && (int64_t)gc.x * gc.y * gc.z <= 256;
+    if (c.o != nullptr) {
+        if constexpr (sizeof(T) == 2) {
+            if (two) hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kOutputs, true>), gc, dim3(kDeltaThreads), 0, st, a);
+            else hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kOutputs, false>), gc, dim3(kDeltaThreads), 0, st, a);
+        } else {
+            hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kOutputs, false>), gc, dim3(kDeltaThreads), 0, st, a);
+        }
+    } else {
+        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kStates, false>), gc, dim3(kDeltaThreads), 0, st, a);
+    }
 }
 
 template <typename T, int kDk>

@@ -121,3 +121,29 @@ def test_empty(dev):
     assert o.shape == (2, 0, 1, 64) and torch.equal(h, c["h"])
     c = inputs(0, 10, 1, 1, 64, 64, torch.bfloat16, device=dev)
     assert m.delta_scan(*args(c))[0].shape == (0, 10, 1, 64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segs", [2, 3, 5])
+def test_segments(dev, segs, dtype, monkeypatch):
+    """A row's chunks in segments that run at once, joined by their maps."""
+    monkeypatch.setenv("BDSSM_DELTA_SEGMENTS", str(segs))
+    c = inputs(3, 330, 1, 2, 64, 128, dtype, seed=8, device=dev, resets=[100, 200], lens=[330, 65, 0])
+    r = reference(c, h=c["h"])
+    o, h, chunks = m.delta_scan(*args(c), h_init=c["h"], lens=c["lens"], want_chunks=True)
+    check(o, r["o"], "o", 2.0)          # each segment's map once more on the state
+    check(h, r["h"], "h", 2.0)
+    check(chunks, r["chunks"], "chunks", 2.0)
+    _, h, _ = m.delta_scan(None, *args(c)[1:], h_init=c["h"], lens=c["lens"], want_o=False)
+    check(h, r["h"], "state alone", 2.0)
+    h0 = c["h"].clone()
+    m.delta_scan(*args(c), h_init=h0, h_final=h0, lens=c["lens"])
+    check(h0, r["h"], "in place", 2.0)
+
+
+def test_long_row_is_segmented(dev):
+    c = inputs(1, 2100, 1, 1, 128, 64, torch.bfloat16, seed=9, device=dev)
+    r = reference(c, h=c["h"])
+    o, h, _ = m.delta_scan(*args(c), h_init=c["h"])
+    check(o, r["o"], "o", 2.0)
+    check(h, r["h"], "h", 2.0)
