@@ -16,7 +16,7 @@ using namespace bdssm_host;
 
 namespace {
 
-constexpr int64_t kDeltaTarget = 256;         // workgroups of a chain that fill the chip
+constexpr int64_t kDeltaTarget = 448;         // workgroups of a chain that fill the chip, near two a CU
 constexpr int64_t kMost = (int64_t)1 << 40;   // elements of one tensor
 
 bool product_fits(std::initializer_list<int64_t> f) {
@@ -63,13 +63,15 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 
 // Segments of a row's chunks (1: none).  A chain's step is a chunk's, whatever
 // the batch; cutting the row costs the aggregate pass over d_v + d_k columns
-// besides the chain's own d_v, so it pays from about three segments on, each of
-// 8 chunks at least.  BDSSM_DELTA_SEGMENTS forces a count (tests).
+// besides the chain's own d_v, so it pays from about four segments on, each of
+// 8 chunks at least.  65,536 tokens of 12 heads (24 groups): 4.7 ms whole, 1.14
+// ms in 10 segments, 1.06 in 16, 1.15 in 40; 192 groups of 64 chunks: 2% slower
+// in two segments than whole.  BDSSM_DELTA_SEGMENTS forces a count (tests).
 int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
     const int64_t groups = s->batch * s->heads_v * (s->d_v / 64);
     int64_t n = groups > 0 ? kDeltaTarget / groups : 1;
     if (n > chunks / 8) n = chunks / 8;
-    if (n < 3) n = 1;
+    if (n < 4) n = 1;
     const char *e = getenv("BDSSM_DELTA_SEGMENTS");
     if (e != nullptr && *e != 0) n = atoi(e);
     if (n > chunks) n = chunks;

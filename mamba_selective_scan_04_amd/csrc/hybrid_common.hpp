@@ -55,7 +55,21 @@ __device__ __forceinline__ uint32_t pk_rne(float a, float b) {
 __device__ __forceinline__ uint32_t pk_cut(float a, float b) {
     return __builtin_amdgcn_perm(as_u(b), as_u(a), 0x07060302u);
 }
-__device__ __forceinline__ float cut(float a) { return as_f(as_u(a) & 0xffff0000u); }
+
+// a less the low (b less the high) bf16 of a pair, in one instruction: the dot
+// product with (-1, 0) or (0, -1) on top of a.  Exact where the pair was cut from
+// (a, b).  The factors are kept in scalar registers: as inline constants of
+// this instruction they came out as other values.
+__device__ __forceinline__ float less_low(float a, uint32_t pair) {
+    uint32_t f = 0x0000bf80u;
+    asm("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, f), a, false);
+}
+__device__ __forceinline__ float less_high(float b, uint32_t pair) {
+    uint32_t f = 0xbf800000u;
+    asm("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, f), b, false);
+}
 
 // (a, b) as kParts packed bf16 pairs whose sum is the pair: one part rounds to
 // nearest; two: the second rounds what the first leaves; three are exact.
@@ -65,12 +79,12 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t *out) {
         out[0] = pk_rne(a, b);
     } else if constexpr (kParts == 2) {
         out[0] = pk_rne(a, b);
-        out[1] = pk_rne(a - bf_lo(out[0]), b - bf_hi(out[0]));
+        out[1] = pk_rne(less_low(a, out[0]), less_high(b, out[0]));
     } else {
         out[0] = pk_cut(a, b);
-        const float ra = a - cut(a), rb = b - cut(b);
+        const float ra = less_low(a, out[0]), rb = less_high(b, out[0]);
         out[1] = pk_cut(ra, rb);
-        out[2] = pk_cut(ra - cut(ra), rb - cut(rb));
+        out[2] = pk_cut(less_low(ra, out[1]), less_high(rb, out[1]));
     }
 }
 
