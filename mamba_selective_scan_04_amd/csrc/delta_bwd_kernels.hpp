@@ -32,6 +32,7 @@ struct AdjointArgs {
     const float *dh_final;            // null: zero
     float *dS;                        // [batch, chunks, hv, dk, dv]: dS' of each chunk
     float *dh_init;                   // null: not wanted
+    int groups;                       // batch * hv
     DeltaDims d;
 };
 
@@ -127,21 +128,23 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
     __shared__ __attribute__((aligned(16))) typename C::Stage l0;
     __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
     const DeltaDims &d = a.d;
+    const ChainPlace at = chain_place(d.dv / 64);
+    if (at.group >= a.groups) return;
     C s{{}, a};
-    s.hv = blockIdx.y;
-    s.b = blockIdx.z;
+    s.hv = at.group % d.hv;
+    s.b = at.group / d.hv;
     const int hk = s.hv / d.group, lane = lane_id();
     s.wave = threadIdx.x >> 6;
     s.col = lane & 15;
     s.grp = lane >> 4;
-    s.n = blockIdx.x * 64 + s.wave * 16 + s.col;
+    s.n = at.col * 64 + s.wave * 16 + s.col;
     s.len = row_len(d, s.b);
     s.kstride = (int64_t)d.hk * kDk;
     s.vstride = (int64_t)d.hv * d.dv;
     const int64_t tok = (int64_t)s.b * d.T;
     s.kp = a.k + (tok * d.hk + hk) * kDk;
     s.qp = a.q + (tok * d.hk + hk) * kDk;
-    s.op = a.dout + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64;
+    s.op = a.dout + (tok * d.hv + s.hv) * d.dv + at.col * 64;
     const int chunks = (int)((s.len + kChunk - 1) / kChunk);
     const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
 #pragma unroll

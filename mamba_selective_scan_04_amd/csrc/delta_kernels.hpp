@@ -489,6 +489,7 @@ struct ChainArgs {
     float *h_chunks;      // null, or [batch, chunks, hv, dk, dv]
     float *agg;           // kAggregate: [batch, hv, segs, dk, dv + dk]
     int segs, per;        // segments, and chunks of each
+    int groups;           // batch * segs * hv
     DeltaDims d;
 };
 
@@ -609,6 +610,17 @@ struct Chain {
     }
 };
 
+// A chain's workgroups in one dimension.  Consecutive workgroups go to the eight
+// XCDs in turn; the column blocks of one head read the same keys and matrices
+// and share an XCD's L2, so they take every eighth place.
+struct ChainPlace {
+    int col, group;   // column block; (row, segment, head), head fastest
+};
+__device__ __forceinline__ ChainPlace chain_place(int cols) {
+    const int x = blockIdx.x % 8, r = blockIdx.x / 8;
+    return ChainPlace{r % cols, r / cols * 8 + x};
+}
+
 // A barrier behind which every wave's loads into LDS have arrived; the kLater
 // youngest memory operations of a wave (stores that it issued after them) may
 // still be under way.
@@ -627,24 +639,26 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
     __shared__ __attribute__((aligned(16))) typename C::Stage l0;
     __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
     const DeltaDims &d = a.d;
+    const ChainPlace at = chain_place((d.dv + (kMode == kAggregate ? kDk : 0)) / 64);
+    if (at.group >= a.groups) return;
     C s{{}, a};
-    s.hv = blockIdx.y;
-    s.b = blockIdx.z / a.segs;
-    const int seg = blockIdx.z % a.segs, hk = s.hv / d.group;
+    s.hv = at.group % d.hv;
+    s.b = at.group / d.hv / a.segs;
+    const int seg = at.group / d.hv % a.segs, hk = s.hv / d.group;
     s.lane = lane_id();
     s.wave = threadIdx.x >> 6;
     s.col = s.lane & 15;
     s.grp = s.lane >> 4;
-    s.n = blockIdx.x * 64 + s.wave * 16 + s.col;   // this lane's state column
-    s.has_v = kMode != kAggregate || (int)blockIdx.x * 64 < d.dv;
+    s.n = at.col * 64 + s.wave * 16 + s.col;   // this lane's state column
+    s.has_v = kMode != kAggregate || at.col * 64 < d.dv;
     s.len = row_len(d, s.b);
     s.kstride = (int64_t)d.hk * kDk;
     s.vstride = (int64_t)d.hv * d.dv;
     const int64_t tok = (int64_t)s.b * d.T;
     s.kp = a.k + (tok * d.hk + hk) * kDk;
     s.qp = kWithO ? a.q + (tok * d.hk + hk) * kDk : nullptr;
-    s.vp = a.v + (tok * d.hv + s.hv) * d.dv + (s.has_v ? blockIdx.x * 64 : 0);
-    s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + blockIdx.x * 64 : nullptr;
+    s.vp = a.v + (tok * d.hv + s.hv) * d.dv + (s.has_v ? at.col * 64 : 0);
+    s.op = kWithO ? a.o + (tok * d.hv + s.hv) * d.dv + at.col * 64 : nullptr;
     s.ooff = (uint32_t)(s.grp * 4 * s.vstride) + s.wave * 16 + s.col;
     s.koff.set(s.kstride, kChunk);
     s.voff.set(s.vstride, kChunk);

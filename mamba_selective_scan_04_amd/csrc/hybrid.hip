@@ -55,6 +55,8 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
         return BDSSM_ERR_SHAPE;
     if (s->heads_v % s->heads_k != 0) return BDSSM_ERR_SHAPE;
     if ((s->d_k != 64 && s->d_k != 128) || (s->d_v != 64 && s->d_v != 128)) return BDSSM_ERR_SHAPE;
+    // a chain's workgroups are counted in 31 bits, segments included
+    if (s->batch * s->heads_v > ((int64_t)1 << 24)) return BDSSM_ERR_SHAPE;
     // 2^31 - 1 chunks at most in a launch, and every tensor's elements countable
     if (T > kMost || (T + 63) / 64 >= ((int64_t)1 << 31)) return BDSSM_ERR_SHAPE;
     if (!product_fits({s->batch, (T + 63) / 64, s->heads_v, s->d_k, s->d_v})) return BDSSM_ERR_SHAPE;

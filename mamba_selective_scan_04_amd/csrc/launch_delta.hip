@@ -17,14 +17,13 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
                            c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.fwd,
                            (Mats<3> *)nullptr, (double *)nullptr, c.d);
     ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.fwd, c.h_init, (T *)c.o, c.h_final, c.h_chunks,
-                   c.agg, 1, c.d.chunks, c.d};
-    dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
+                   c.agg, 1, c.d.chunks, (int)(c.batch * c.d.hv), c.d};
+    const auto grid = [&](int columns) { return dim3((unsigned)((a.groups + 7) / 8 * 8 * (columns / 64))); };
     if (c.segs > 1) {
         a.segs = c.segs;
         a.per = (c.d.chunks + c.segs - 1) / c.segs;
-        gc.z = (unsigned)(c.batch * c.segs);
-        const dim3 ga((unsigned)((c.d.dv + kDk) / 64), gc.y, gc.z);
-        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), ga, dim3(kDeltaThreads), 0, st, a);
+        a.groups *= c.segs;
+        hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
         // states alone: the join has the last
         const bool chain = c.o != nullptr || c.h_chunks != nullptr;
         const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv};
@@ -32,7 +31,8 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
         if (!chain) return;
         a.h_init = c.h_seg;
     }
-    const bool two = sizeof(T) == 2 && (int64_t)gc.x * gc.y * gc.z <= 256;
+    const dim3 gc = grid(c.d.dv);
+    const bool two = sizeof(T) == 2 && (int64_t)a.groups * (c.d.dv / 64) <= 256;
     if (c.o != nullptr) {
         if constexpr (sizeof(T) == 2) {
             if (two) hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kOutputs, true>), gc, dim3(kDeltaThreads), 0, st, a);
@@ -51,8 +51,8 @@ void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
     if (c.d.chunks > 0)
         hipLaunchKernelGGL((delta_prep_kernel<T, kDk, 3, true>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.q, (const T *)c.k, c.g, c.beta,
                            (Mats<3> *)c.fwd, (Mats<3> *)c.bwd, c.G, c.d);
-    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.bwd, c.dh_final, c.dS, c.dh_init, c.d};
-    const dim3 gc((unsigned)(c.d.dv / 64), (unsigned)c.d.hv, (unsigned)c.batch);
+    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.bwd, c.dh_final, c.dS, c.dh_init, (int)(c.batch * c.d.hv), c.d};
+    const dim3 gc((unsigned)((a.groups + 7) / 8 * 8 * (c.d.dv / 64)));
     hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk>), gc, dim3(kDeltaThreads), 0, st, a);
     if (c.d.chunks == 0) return;
     const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.fwd, (const Mats<3> *)c.bwd,
