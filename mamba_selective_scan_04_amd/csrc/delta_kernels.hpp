@@ -76,16 +76,8 @@ __device__ __forceinline__ float decay(double d) { return __expf((float)d); }
 // instead piece p of row r lies at place p ^ turn(r), which spreads the same
 // piece of 16 rows over all banks.  Rows behind the chunk's last token repeat
 // it: what they feed is multiplied by zero or not stored.
-typedef __attribute__((address_space(3))) void lds_ptr;
-typedef const __attribute__((address_space(1))) void glb_ptr;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// one wave's 64 x 16 bytes: lane l's piece, `off` bytes behind the uniform src, to
-// base + 16 l
-__device__ __forceinline__ void load_lds(const void *src, uint32_t off, void *base) {
-    __builtin_amdgcn_global_load_lds((glb_ptr *)((const char *)src + off), (lds_ptr *)base, 16, 0, 0);
-}
 
 template <typename T, int kCols>
 struct Tile {

@@ -149,6 +149,8 @@ int check_kv(const bdssm_kv_shape *s, int64_t L) {
     return BDSSM_OK;
 }
 
+int64_t kv_group(const bdssm_kv_shape *s) { return s->heads_q / s->heads_kv; }
+
 struct KvSizes {
     size_t q, kv, cache, scale, table, row;
 };
@@ -165,21 +167,27 @@ KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
     return z;
 }
 
-// A wave's query tiles: as many as the rows fill, up to four (the accumulators
-// of 64 queries x 128 channels take 128 registers; fp32 streams, whose queries
-// are three parts, two).  Key ranges: until every CU has its workgroups of four
-// waves, but at least one step of 64 keys for each wave of a range.
+// A wave's query tiles: two where there are more than 16 rows (64 accumulators at
+// 128 channels; four tiles' 128 made the compiler spill, and ran at half the
+// speed).  Key ranges: until every CU has its workgroups of four waves, but at
+// least one step of 32 keys for each wave of a range; beyond that up to three
+// times as many, of at least 2,048 keys, so that rows of different lengths (which
+// only the GPU knows) even out.
 KvPlan kv_plan(const bdssm_kv_shape *s, int64_t Lq) {
-    const int64_t rows = Lq * (s->heads_q / s->heads_kv);
-    const int most = s->dtype == BDSSM_F32 && s->head_dim == 128 ? 2 : 4;
+    const int64_t rows = Lq * kv_group(s);
     KvPlan p;
-    p.tiles = rows > 32 && most > 2 ? 4 : rows > 16 ? 2 : 1;
+    p.tiles = rows > 16 ? 2 : 1;
     const int64_t qtiles = (rows + p.tiles * 16 - 1) / (p.tiles * 16);
     const int64_t units = s->batch * s->heads_kv * qtiles;
-    const int64_t target = p.tiles == 4 ? 256 : p.tiles == 2 ? 512 : 768;
-    const int64_t ranges = (s->max_pages * s->page_len / 64 + 3) / 4;
-    int64_t n = units > 0 ? (target + units - 1) / units : 1;
-    if (n > ranges) n = ranges;
+    const int64_t fill = 512;   // resident at once
+    const int64_t steps = (s->max_pages * s->page_len + 31) / 32;
+    int64_t n = units > 0 ? (fill + units - 1) / units : 1;
+    int64_t even = units > 0 ? (3 * fill + units - 1) / units : 1;
+    if (even > steps / 64) even = steps / 64;
+    if (n < even) n = even;
+    if (n > (steps + 3) / 4) n = (steps + 3) / 4;
+    const char *e = getenv("BDSSM_KV_SPLITS");   // forces a count (tests)
+    if (e != nullptr && *e != 0) n = atoi(e);
     p.qtiles = (int)qtiles;
     p.splits = (int)(n < 1 ? 1 : n);
     return p;
@@ -203,7 +211,7 @@ KvCall kv_call(const bdssm_kv_shape *s, int64_t L, const void *k, const void *v,
     c.code = s->code;
     c.d.heads_q = (int)s->heads_q;
     c.d.heads_kv = (int)s->heads_kv;
-    c.d.group = (int)(s->heads_q / s->heads_kv);
+    c.d.group = (int)kv_group(s);
     c.d.page_len = (int)s->page_len;
     c.d.n_pages = (int)s->n_pages;
     c.d.max_pages = (int)s->max_pages;
@@ -363,7 +371,10 @@ int bdssm_kv_attn_step(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const voi
     if (!all_aligned({q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, o, ws})) return BDSSM_ERR_ALIGN;
     const KvSizes z = kv_sizes(s, L, Lq);
     const KvPlan plan = kv_plan(s, Lq);
-    if ((int64_t)plan.qtiles * s->heads_kv > 65535) return BDSSM_ERR_SHAPE;
+    // workgroups are counted in 31 bits
+    if (!product_fits({s->batch, s->heads_kv, plan.splits, plan.qtiles}) ||
+        s->batch * s->heads_kv * plan.splits * plan.qtiles > 0x70000000 || Lq * kv_group(s) > 0x7fffffff)
+        return BDSSM_ERR_SHAPE;
     size_t part = 0;
     const size_t need = kv_workspace(s, plan, &part);
     if (!distinct({{q, z.q}, {k, z.kv}, {v, z.kv}, {k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale},

@@ -199,6 +199,18 @@ __device__ __forceinline__ Frag<3> load_straight(const float *p) {
     return split_frag<3>(*(const f32x4 *)p, *(const f32x4 *)(p + 4));
 }
 
+// one wave's 64 x 16 bytes from memory straight into LDS: each lane's piece, to
+// base + 16 * lane
+typedef __attribute__((address_space(3))) void lds_ptr;
+typedef const __attribute__((address_space(1))) void glb_ptr;
+__device__ __forceinline__ void load_lds(const void *src, void *base) {
+    __builtin_amdgcn_global_load_lds((glb_ptr *)src, (lds_ptr *)base, 16, 0, 0);
+}
+// ... `off` bytes behind a uniform src
+__device__ __forceinline__ void load_lds(const void *src, uint32_t off, void *base) {
+    load_lds((const char *)src + off, base);
+}
+
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
 }  // namespace bdssm_dev

@@ -142,15 +142,16 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 
 // --------------------------------------------------------------- attention
 //
-// A wave takes 64 keys at a time and kTiles * 16 queries: the rows of one
+// A wave takes 32 keys at a time and kTiles * 16 queries: the rows of one
 // key/value head's query heads and all query tokens, so that a key is read once
 // for all of them.  Scores are formed as S^T = K Q^T (rows keys, columns
 // queries), which makes each lane the owner of one query per tile (its maximum
 // and sum need no exchange but over the four lane groups) and the probabilities
 // the B operand of O^T = V^T P^T as they stand.  Score row 4 g + r of tile t
-// is key 16 g + 4 t + r of the 64: lane group g then holds 16 consecutive keys,
-// which lie in one page (one scale a lane) and are 16 consecutive codes of a
-// channel's row.
+// is key 8 g + 4 t + r of the 32: lane group g then holds 8 consecutive keys,
+// which lie in one page (one scale a lane) and are 8 consecutive codes of a
+// channel's row.  32 keys are two pages at most, the same for the whole wave:
+// their numbers and scales come by scalar loads.
 //
 // Probabilities enter their product as bf16 (two parts for fp32 streams: three)
 // after the page's value scale is multiplied in; scores, maxima, sums and
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // 2^8: probabilities stay below 2^8 and the outputs are seldom rescaled.
 //
 // The keys of a row are cut into `splits` ranges (workgroups) and each range's
-// 64-key steps go round its four waves; the waves join through LDS, the ranges
+// 32-key steps go round its four waves; the waves join through LDS, the ranges
 // through the workspace and kv_join_kernel.
 template <typename T>
 struct AttnArgs {
@@ -170,6 +171,7 @@ struct AttnArgs {
     int64_t L, Lq;
     int splits, qtiles, causal;
     float scale;               // times log2(e)
+    int64_t jobs;              // batch * heads_kv * splits
     KvDims d;
 };
 
@@ -205,17 +207,17 @@ struct AttnState {
     float m[kTiles], l[kTiles];
     Frag<kIn> Q[kD / 32][kTiles];
 
-    // scores S[t][nt] (already times scale, masked to -inf) of 64 keys; V(mt, u)
+    // scores S[t][nt] (already times scale, masked to -inf) of 32 keys; V(mt)
     // gives the values' fragment, vs their scale
     template <typename VFrag>
-    __device__ __forceinline__ void step(f32x4 (&S)[4][kTiles], float vs, VFrag &&V) {
+    __device__ __forceinline__ void step(f32x4 (&S)[2][kTiles], float vs, VFrag &&V) {
         float top[kTiles];
         bool raise = false;
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
             float x = S[0][nt][0];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x = fmaxf(x, S[t][nt][r]);
             top[nt] = x;
@@ -236,49 +238,72 @@ struct AttnState {
                     for (int r = 0; r < 4; ++r) O[mt][nt][r] *= f;
             }
         }
-        Frag<kProbParts<T>> P[2][kTiles];
+        Frag<kProbParts<T>> P[kTiles];
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float p = __builtin_amdgcn_exp2f(S[t][nt][r] - m[nt]);
                     l[nt] += p;
                     S[t][nt][r] = p * vs;
                 }
-            P[0][nt] = split_frag<kProbParts<T>>(S[0][nt], S[1][nt]);
-            P[1][nt] = split_frag<kProbParts<T>>(S[2][nt], S[3][nt]);
+            P[nt] = split_frag<kProbParts<T>>(S[0][nt], S[1][nt]);
         }
 #pragma unroll
-        for (int mt = 0; mt < kD / 16; ++mt)
+        for (int mt = 0; mt < kD / 16; ++mt) {
+            const auto vf = V(mt);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const auto vf = V(mt, u);
-#pragma unroll
-                for (int nt = 0; nt < kTiles; ++nt) O[mt][nt] = mma(vf, P[u][nt], O[mt][nt]);
-            }
+            for (int nt = 0; nt < kTiles; ++nt) O[mt][nt] = mma(vf, P[nt], O[mt][nt]);
+        }
     }
 };
 
+// A wave-uniform value that no kernel writes meanwhile, by a scalar load (a vector
+// load would count among the loads into LDS that the waits below count).
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T *p) {
+    return *(const __attribute__((address_space(4))) T *)p;
+}
+
 template <typename T, int kCode, int kD, int kTiles>
-__global__ __launch_bounds__(256) void kv_attn_kernel(AttnArgs<T> a) {
+__global__ __launch_bounds__(256, kTiles == 2 && kD == 128 ? 2 : 3) void kv_attn_kernel(AttnArgs<T> a) {
     constexpr int kIn = Stream<T>::kParts, kRows = kTiles * 16, kChan = kD / 16, kORow = kD + 4;
     const KvDims &d = a.d;
-    const int split = blockIdx.x, h = blockIdx.y / a.qtiles, qt = blockIdx.y % a.qtiles, b = blockIdx.z;
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
-    const int64_t unit = (int64_t)b * gridDim.y + blockIdx.y;
+    // the query tiles of one range of keys on one XCD, as the chains' column
+    // blocks: the second finds the codes in its L2
+    const int64_t place = blockIdx.x, job = place / 8 / a.qtiles * 8 + place % 8;
+    if (job >= a.jobs) return;
+    const int qt = (int)(place / 8 % a.qtiles), split = (int)(job % a.splits), h = (int)(job / a.splits % d.heads_kv);
+    const int b = (int)(job / a.splits / d.heads_kv);
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const int64_t unit = ((int64_t)b * d.heads_kv + h) * a.qtiles + qt;
     int64_t n = a.L;
     if (d.lens != nullptr) n = d.lens[b] < 0 ? 0 : d.lens[b] < n ? d.lens[b] : n;
     const int64_t nq = n < a.Lq ? n : a.Lq, rows = nq * d.group;   // the row's live queries
     int64_t ctx = d.ctx[b] < 0 ? 0 : d.ctx[b];
     const int64_t most = d.n_pages > 0 ? (int64_t)d.max_pages * d.page_len : 0;
     ctx = ctx < most ? ctx : most;
-    const int64_t steps = (ctx + 63) / 64, per = (steps + a.splits - 1) / a.splits;
+    const int64_t steps = (ctx + 31) / 32, per = (steps + a.splits - 1) / a.splits;
     const int64_t s0 = split * per, s1 = s0 + per < steps ? s0 + per : steps;
     const bool live = (int64_t)qt * kRows < rows, has_active = split == a.splits - 1;
 
-    __shared__ __attribute__((aligned(16))) float Ol[kRows * kORow];
+    // Each wave's codes of two steps: of two key tiles 16 bytes a lane, as its
+    // lanes use them, then the channels' rows of 32 keys.  Loaded straight from
+    // memory a step ahead; a wave reads only what it loaded, so nothing but its
+    // own wait is needed.  The waves' outputs take the room afterwards.
+    constexpr int kKeyLoads = 2 * (kD / 64), kLoads = kKeyLoads + kD / 32;
+    struct Codes {
+        uint4 p[4][kLoads][64];
+    };
+    union Room {
+        Codes c;
+        float O[kRows * kORow];
+    };
+    __shared__ __attribute__((aligned(16))) Room r0;
+    __shared__ __attribute__((aligned(16))) Codes r1;
+    float *Ol = r0.O;
     __shared__ float ml[4][kRows][2];
     AttnState<T, kD, kTiles> st;
 #pragma unroll
@@ -292,104 +317,130 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(AttnArgs<T> a) {
         // queries: k slot (step 2 t + x, group g, j) is channel 64 t + 16 g + 8 x + j
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
-            const int64_t row = (int64_t)qt * kRows + nt * 16 + col;
+            const int64_t at = (int64_t)qt * kRows + nt * 16 + col, row = at < rows ? at : rows - 1;   // not stored
             const T *qp = a.q + (((int64_t)b * a.Lq + row / d.group) * d.heads_q + h * d.group + row % d.group) * kD;
 #pragma unroll
-            for (int s = 0; s < kD / 32; ++s) {
-                if (row < rows) st.Q[s][nt] = load_straight(qp + s / 2 * 64 + grp * 16 + (s & 1) * 8);
-                else st.Q[s][nt] = Frag<kIn>{};
-            }
+            for (int s = 0; s < kD / 32; ++s) st.Q[s][nt] = load_straight(qp + s / 2 * 64 + grp * 16 + (s & 1) * 8);
         }
         const int32_t *table = d.table + (int64_t)b * d.max_pages;
-        // what a step needs of memory: codes of keys and values, and scales
-        struct Step {
-            uint4 k[4][kD / 64], v[kChan];
-            float ks, vs;
-            int valid;   // of the lane's 16 keys (its values and scores)
-        };
         const int shift = 31 - __builtin_clz(d.page_len);
-        auto page_of = [&](int64_t key, bool *ok) {
-            const int64_t p = key >> shift;
-            int id = -1;
-            if (key < ctx) id = table[p];
-            *ok = id >= 0 && id < d.n_pages;
-            return *ok ? id : 0;
+        // A step's two halves of 16 keys: their pages (-1: none) and scales.
+        struct Pages {
+            int id[2];
         };
-        auto fetch = [&](Step &f, int64_t step) {
-            bool ok;
-            const int64_t key0 = step * 64 + grp * 16;
-            const int64_t u = (int64_t)page_of(key0, &ok) * d.heads_kv + h;
-            f.valid = !ok ? 0 : ctx - key0 < 16 ? (int)(ctx - key0) : 16;
-            f.ks = a.ks[u];
-            f.vs = ok ? a.vs[u] : 0.f;
-            const uint8_t *vp = a.vc + u * (kD * d.page_len) + (key0 & (d.page_len - 1));
-#pragma unroll
-            for (int mt = 0; mt < kChan; ++mt) f.v[mt] = *(const uint4 *)(vp + (mt * 16 + col) * d.page_len);
-            // score rows: lane row `col` of tile t is key 16 (col / 4) + 4 t + col % 4
-            const int64_t kk = step * 64 + (col >> 2) * 16;
-            bool okk;
-            const int64_t uk = (int64_t)page_of(kk, &okk) * d.heads_kv + h;
-            const uint8_t *kp = a.kc + uk * (kD * d.page_len) + ((kk & (d.page_len - 1)) + (col & 3)) * kD + grp * 16;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int s = 0; s < kD / 64; ++s) f.k[t][s] = *(const uint4 *)(kp + t * 4 * kD + s * 64);
+        struct Scales {
+            float k[2], v[2];
         };
-        auto use = [&](Step &f) {
-            f32x4 S[4][kTiles];
-            const float ks = f.ks * a.scale;
+        auto find = [&](int64_t step) {
+            Pages p;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int i = 0; i < 2; ++i) {
+                const int64_t key = step * 32 + i * 16;
+                p.id[i] = key < ctx ? uniform_load(table + (key >> shift)) : -1;
+                if (p.id[i] >= d.n_pages) p.id[i] = -1;
+            }
+            return p;
+        };
+        auto unit_of = [&](int id) { return (int64_t)(id < 0 ? 0 : id) * d.heads_kv + h; };
+        auto scales = [&](Pages p) {
+            const int64_t u0 = unit_of(p.id[0]), u1 = unit_of(p.id[1]);
+            return Scales{{uniform_load(a.ks + u0), uniform_load(a.ks + u1)}, {uniform_load(a.vs + u0), uniform_load(a.vs + u1)}};
+        };
+        const int64_t page_bytes = (int64_t)kD * d.page_len;
+        // a lane's offsets in a half's page: key row of its score row, channel row
+        const bool khalf = col >= 8, vhalf = lane & 1;
+        const uint32_t koff = ((col >> 2 & 1) * 8 + (col & 3)) * kD + grp * 16, voff = (lane >> 1) * d.page_len;
+        auto fetch = [&](Codes &buf, int64_t step, Pages p) {
+            const uint8_t *k0 = a.kc + unit_of(p.id[0]) * page_bytes, *k1 = a.kc + unit_of(p.id[1]) * page_bytes;
+            const uint8_t *v0 = a.vc + unit_of(p.id[0]) * page_bytes, *v1 = a.vc + unit_of(p.id[1]) * page_bytes;
+            const int in0 = (int)(step * 32 & (d.page_len - 1)), in1 = (int)((step * 32 + 16) & (d.page_len - 1));
+            const uint8_t *kp = (khalf ? k1 + in1 * kD : k0 + in0 * kD) + koff, *vp = (vhalf ? v1 + in1 : v0 + in0) + voff;
+            uint4(*to)[64] = buf.p[wave];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int s = 0; s < kD / 64; ++s) load_lds(kp + t * 4 * kD + s * 64, to[t * (kD / 64) + s]);
+#pragma unroll
+            for (int i = 0; i < kD / 32; ++i) load_lds(vp + i * 32 * d.page_len, to[kKeyLoads + i]);
+        };
+        auto use = [&](Codes &buf, int64_t step, Pages p, Scales sc) {
+            uint4(*from)[64] = buf.p[wave];
+            uint2 *vals = (uint2 *)from[kKeyLoads];   // of channel c, lane group g: 4 c + g
+            const bool upper = grp >= 2;
+            const float ks = (upper ? sc.k[1] : sc.k[0]) * a.scale;
+            float vs = upper ? sc.v[1] : sc.v[0];
+            f32x4 S[2][kTiles];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
                 for (int nt = 0; nt < kTiles; ++nt) S[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < kD / 64; ++s) {
-                    const uint4 w = f.k[t][s];
+                    const uint4 w = from[t * (kD / 64) + s][lane];
                     const Frag<1> k0{{widen<kCode>(w.x, w.y)}}, k1{{widen<kCode>(w.z, w.w)}};
 #pragma unroll
-                    for (int nt = 0; nt < kTiles; ++nt) {
-                        S[t][nt] = mma(k0, st.Q[2 * s][nt], S[t][nt]);
-                        S[t][nt] = mma(k1, st.Q[2 * s + 1][nt], S[t][nt]);
-                    }
+                    for (int nt = 0; nt < kTiles; ++nt) S[t][nt] = mma(k0, st.Q[2 * s][nt], S[t][nt]);
+#pragma unroll
+                    for (int nt = 0; nt < kTiles; ++nt) S[t][nt] = mma(k1, st.Q[2 * s + 1][nt], S[t][nt]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) S[t][nt][r] *= ks;
             }
-            if (__any(f.valid < 16)) {   // the context's end, or a page that is not there
+            if (step * 32 + 32 > ctx || p.id[0] < 0 || p.id[1] < 0) {   // the context's end, or a page that is not there
+                const int64_t left = ctx - (step * 32 + grp * 8);
+                const int valid = (upper ? p.id[1] : p.id[0]) < 0 ? 0 : left < 8 ? (int)left : 8;   // of the lane's keys
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (4 * t + r >= f.valid) {
+                        if (4 * t + r >= valid) {
 #pragma unroll
                             for (int nt = 0; nt < kTiles; ++nt) S[t][nt][r] = -__builtin_inff();
                         }
-                // codes behind the end may be anything (a NaN times 0 is a NaN)
-                uint32_t keep[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int left = f.valid - 4 * i;
-                    keep[i] = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1u;
-                }
-#pragma unroll
+                // codes and scales behind the end may be anything (a NaN times 0 is a NaN)
+                if (valid <= 0) vs = 0.f;
+                const uint32_t k0 = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << 8 * valid) - 1u;
+                const uint32_t k1 = valid >= 8 ? ~0u : valid <= 4 ? 0u : (1u << 8 * (valid - 4)) - 1u;
+#pragma unroll 1
                 for (int mt = 0; mt < kChan; ++mt) {
-                    f.v[mt].x &= keep[0];
-                    f.v[mt].y &= keep[1];
-                    f.v[mt].z &= keep[2];
-                    f.v[mt].w &= keep[3];
+                    uint2 &w = vals[(mt * 16 + col) * 4 + grp];
+                    w = make_uint2(w.x & k0, w.y & k1);
                 }
             }
-            st.step(S, f.vs, [&](int mt, int u) {
-                const uint4 w = f.v[mt];
-                return u == 0 ? Frag<1>{{widen<kCode>(w.x, w.y)}} : Frag<1>{{widen<kCode>(w.z, w.w)}};
+            st.step(S, vs, [&](int mt) {
+                const uint2 w = vals[(mt * 16 + col) * 4 + grp];
+                return Frag<1>{{widen<kCode>(w.x, w.y)}};
             });
         };
-        Step f;
-        for (int64_t s = s0 + wave; s < s1; s += 4) {
-            fetch(f, s);
-            use(f);
+        if (s0 + wave < s1) {
+            int64_t s = s0 + wave;
+            Pages p0 = find(s), p1 = find(s + 4);
+            Scales c0 = scales(p0);
+            fetch(r0.c, s, p0);
+            // One turn: the next step's codes on their way (none behind the range:
+            // then page 0's or the row's own, never used), then a wait until nothing
+            // but those is: they are the wave's youngest kLoads memory operations.
+            const auto turn = [&](Codes &now, Codes &next) {
+                fetch(next, s + 4, p1);
+                const Scales c1 = scales(p1);
+                const Pages p2 = find(s + 8);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                use(now, s, p0, c0);
+                p0 = p1;
+                c0 = c1;
+                p1 = p2;
+                s += 4;
+            };
+            for (;;) {
+                turn(r0.c, r1);
+                if (s >= s1) break;
+                turn(r1, r0.c);
+                if (s >= s1) break;
+            }
+            // what is still on its way lands before the room is used again
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
         if (has_active) {   // the active tokens' own keys and values
             const T *kb = a.k + ((int64_t)b * a.L * d.heads_kv + h) * kD, *vb = a.v + ((int64_t)b * a.L * d.heads_kv + h) * kD;
@@ -400,17 +451,17 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(AttnArgs<T> a) {
                 const int64_t row = (int64_t)qt * kRows + nt * 16 + col;
                 pos[nt] = a.causal ? n - nq + row / d.group : n - 1;
             }
-            for (int64_t s = wave; s * 64 < n; s += 4) {
-                f32x4 S[4][kTiles];
-                const int64_t kk = s * 64 + (col >> 2) * 16 + (col & 3), key0 = s * 64 + grp * 16;
+            for (int64_t s = wave; s * 32 < n; s += 4) {
+                f32x4 S[2][kTiles];
+                const int64_t kk = s * 32 + (col >> 2) * 8 + (col & 3), key0 = s * 32 + grp * 8;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
+                for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int nt = 0; nt < kTiles; ++nt) S[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int x = 0; x < kD / 32; ++x) {
-                        Frag<kIn> kf{};
-                        if (kk + 4 * t < n) kf = load_straight(kb + (kk + 4 * t) * stride + x / 2 * 64 + grp * 16 + (x & 1) * 8);
+                        const int64_t key = kk + 4 * t < n ? kk + 4 * t : n - 1;   // repeated tokens are masked
+                        const auto kf = load_straight(kb + key * stride + x / 2 * 64 + grp * 16 + (x & 1) * 8);
 #pragma unroll
                         for (int nt = 0; nt < kTiles; ++nt) S[t][nt] = mma(kf, st.Q[x][nt], S[t][nt]);
                     }
@@ -422,19 +473,24 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(AttnArgs<T> a) {
                             S[t][nt][r] = key < n && key <= pos[nt] ? S[t][nt][r] * a.scale : -__builtin_inff();
                         }
                 }
-                st.step(S, 1.f, [&](int mt, int u) {
+                T vals[kChan][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const T *row = vb + (key0 + j < n ? key0 + j : n - 1) * stride + col;
+#pragma unroll
+                    for (int mt = 0; mt < kChan; ++mt) vals[mt][j] = row[mt * 16];
+                }
+                st.step(S, 1.f, [&](int mt) {
                     f32x4 x[2];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int64_t key = key0 + u * 8 + j;
-                        x[j / 4][j % 4] = key < n ? Stream<T>::load(vb + key * stride + mt * 16 + col) : 0.f;
-                    }
+                    for (int j = 0; j < 8; ++j) x[j / 4][j % 4] = Stream<T>::load(&vals[mt][j]);
                     return split_frag<kIn>(x[0], x[1]);
                 });
             }
         }
     }
-    // the four waves' outputs: to the largest maximum, then added in order
+    // the four waves' outputs: to the largest maximum, then added in order (the
+    // barrier behind the sums also ends every wave's use of the codes)
 #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
         float l = st.l[nt];
@@ -514,39 +570,77 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(AttnArgs<T> a) {
     }
 }
 
-// Joins the splits: a thread per four channels of a query row.
+// Joins the ranges of one query row: a workgroup each.  The ranges' weights in LDS
+// (kMaxSplits at a time), then eight groups of threads go round the ranges, four
+// channels a thread.
+constexpr int kMaxSplits = 1024;
+
 template <typename T, int kD>
-__global__ __launch_bounds__(256) void kv_join_kernel(const float *part_o, const float *part_ml, T *o, int64_t L, int64_t Lq,
-                                                      int splits, int qtiles, int kRows, KvDims d) {
+__global__ __launch_bounds__(kD * 2) void kv_join_kernel(const float *part_o, const float *part_ml, T *o, int64_t L, int64_t Lq,
+                                                         int splits, int qtiles, int kRows, KvDims d) {
+    constexpr int kThreads = kD * 2, kLanes = kD / 4, kGroups = kThreads / kLanes;
+    __shared__ float w[kMaxSplits];
+    __shared__ float red[kThreads / 64][2];
+    __shared__ __attribute__((aligned(16))) float acc[kGroups][kD];
     const int b = blockIdx.z, h = blockIdx.y;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, row = e / (kD / 4);
-    const int c = (int)(e % (kD / 4)) * 4;
-    if (row >= Lq * d.group) return;
+    const int64_t row = blockIdx.x;
     int64_t n = L;
     if (d.lens != nullptr) n = d.lens[b] < 0 ? 0 : d.lens[b] < n ? d.lens[b] : n;
     const int64_t nq = n < Lq ? n : Lq;
+    T *op = o + (((int64_t)b * Lq + row / d.group) * d.heads_q + h * d.group + row % d.group) * kD;
+    const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes, c = lane * 4;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
     if (row < nq * d.group) {
         const int64_t unit = ((int64_t)b * d.heads_kv + h) * qtiles + row / kRows;
         const int64_t at = unit * splits * kRows + row % kRows;
-        float top = kNone, sum = 0.f;
-        for (int s = 0; s < splits; ++s) top = fmaxf(top, part_ml[(at + (int64_t)s * kRows) * 2]);
-        for (int s = 0; s < splits; ++s) {
-            const float *p = part_ml + (at + (int64_t)s * kRows) * 2;
-            if (p[1] == 0.f) continue;   // no key in this range
-            const float f = __builtin_amdgcn_exp2f(p[0] - top);
-            sum = fmaf(p[1], f, sum);
-            const f32x4 x = *(const f32x4 *)(part_o + (at + (int64_t)s * kRows) * kD + c);
+        float top = kNone;
+        for (int s = threadIdx.x; s < splits; s += kThreads) top = fmaxf(top, part_ml[(at + (int64_t)s * kRows) * 2]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = fmaf(x[i], f, y[i]);
+        for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][0] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 64; ++i) top = fmaxf(top, red[i][0]);
+        for (int s0 = 0; s0 < splits; s0 += kMaxSplits) {
+            const int m = splits - s0 < kMaxSplits ? splits - s0 : kMaxSplits;
+            __syncthreads();
+            for (int s = threadIdx.x; s < m; s += kThreads) {
+                const float *p = part_ml + (at + (int64_t)(s0 + s) * kRows) * 2;
+                const float f = p[1] != 0.f ? __builtin_amdgcn_exp2f(p[0] - top) : 0.f;
+                w[s] = f;
+                if (f != 0.f) sum = fmaf(p[1], f, sum);
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int s = grp; s < m; s += kGroups) {
+                const float f = w[s];   // 0: no key in this range, and nothing written
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                if (f != 0.f) x = *(const f32x4 *)(part_o + (at + (int64_t)(s0 + s) * kRows) * kD + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = fmaf(x[i], f, y[i]);
+            }
         }
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = inv != 0.f ? y[i] * inv : 0.f;
     }
-    T *op = o + (((int64_t)b * Lq + row / d.group) * d.heads_q + h * d.group + row % d.group) * kD + c;
-    if constexpr (sizeof(T) == 2) *(uint2 *)op = make_uint2(pk_rne(y[0], y[1]), pk_rne(y[2], y[3]));
-    else *(f32x4 *)op = y;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][1] = sum;
+    *(f32x4 *)&acc[grp][c] = y;
+    __syncthreads();
+    if (grp > 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) sum += red[i][1];
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = 0.f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) v += acc[g][c + i];
+        y[i] = inv != 0.f ? v * inv : 0.f;
+    }
+    if constexpr (sizeof(T) == 2) *(uint2 *)(op + c) = make_uint2(pk_rne(y[0], y[1]), pk_rne(y[2], y[3]));
+    else *(f32x4 *)(op + c) = y;
 }
 
 }  // namespace bdssm_dev

@@ -24,17 +24,13 @@ template <typename T, int kCode, int kD>
 void attn_k(const KvCall &c, hipStream_t st) {
     const AttnArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const uint8_t *)c.kc, (const uint8_t *)c.vc, c.ks, c.vs,
                         (T *)c.o, c.part_o, c.part_ml, c.L, c.Lq, c.plan.splits, c.plan.qtiles, c.causal,
-                        c.scale * 1.44269504088896341f, c.d};
-    const dim3 g((unsigned)c.plan.splits, (unsigned)(c.d.heads_kv * c.plan.qtiles), (unsigned)c.batch);
-    switch (c.plan.tiles) {
-    case 1: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a); break;
-    case 2: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 2>), g, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 4>), g, dim3(256), 0, st, a); break;
-    }
+                        c.scale * 1.44269504088896341f, c.batch * c.d.heads_kv * c.plan.splits, c.d};
+    const dim3 g((unsigned)((a.jobs + 7) / 8 * 8 * c.plan.qtiles));
+    if (c.plan.tiles == 1) hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 2>), g, dim3(256), 0, st, a);
     if (c.plan.splits > 1) {
-        const int64_t n = c.Lq * c.d.group * (kD / 4);
-        hipLaunchKernelGGL((kv_join_kernel<T, kD>), dim3((unsigned)((n + 255) / 256), (unsigned)c.d.heads_kv, (unsigned)c.batch),
-                           dim3(256), 0, st, c.part_o, c.part_ml, (T *)c.o, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
+        hipLaunchKernelGGL((kv_join_kernel<T, kD>), dim3((unsigned)(c.Lq * c.d.group), (unsigned)c.d.heads_kv, (unsigned)c.batch),
+                           dim3(kD * 2), 0, st, c.part_o, c.part_ml, (T *)c.o, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
                            c.plan.tiles * 16, c.d);
     }
 }
