@@ -161,11 +161,15 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
         s.koff.set(s.kstride, kChunk);
         s.voff.set(s.vstride, kChunk);
         for (; c >= 0; c -= 2) {
-            __syncthreads();   // l0 is filled, l1 is read
+            // l0 is filled, l1 is read; the state's stores came after the loads
+            if (c < chunks - 1) loads_done<C::kTiles * 4>();
+            else loads_done<0>();
+            __syncthreads();
             if (c > 0) s.fill(l1, c - 1);
             keep(c);
             s.step(l0, c);
             if (c == 0) break;
+            loads_done<C::kTiles * 4>();
             __syncthreads();
             if (c > 1) s.fill(l0, c - 2);
             keep(c - 1);
@@ -178,6 +182,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
             s.koff.set(s.kstride, kChunk);
             s.voff.set(s.vstride, kChunk);
             keep(c);
+            loads_done<0>();
             __syncthreads();
             s.step(l0, c);
         }
@@ -348,6 +353,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             }
             return x;
         };
+        loads_done<0>();
         __syncthreads();
         if (threadIdx.x < kChunk) {   // these outlast the matrices
             l.e[threadIdx.x] = l.fwd.e[threadIdx.x];

@@ -253,6 +253,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         const int64_t at = (((int64_t)b * d.T + t0) * d.hk + h) * kDk;
         l.k.template fill<4>(k + at, (int64_t)d.hk * kDk, n);
         if (q != nullptr) l.q.template fill<4>(q + at, (int64_t)d.hk * kDk, n);
+        loads_done<0>();
     }
     __syncthreads();
     f32x4 kk[3], kq[3], qk[3];   // this wave's tiles: K K^T; Q K^T by rows j (columns i) and by rows i
@@ -613,14 +614,6 @@ __device__ __forceinline__ ChainPlace chain_place(int cols) {
     return ChainPlace{r % cols, r / cols * 8 + x};
 }
 
-// A barrier behind which every wave's loads into LDS have arrived; the kLater
-// youngest memory operations of a wave (stores that it issued after them) may
-// still be under way.
-template <int kLater>
-__device__ __forceinline__ void stage_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLater) : "memory");
-}
-
 // kTwo: a second set of tiles in LDS, filled while a step computes: one
 // workgroup a CU.  Else one set, and two workgroups a CU cover each other's
 // waits: the faster of the two wherever there are enough workgroups.
@@ -674,13 +667,15 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
         for (int c = c0; c < c1; c += 2) {
             // l0 is filled, l1 is read.  A full chunk's step ends with 16 stores of
             // its outputs; only the last is not full.
-            if (kWithO && c > c0) stage_barrier<16>();
-            else __syncthreads();
+            if (kWithO && c > c0) loads_done<16>();
+            else loads_done<0>();
+            __syncthreads();
             if (c + 1 < c1) s.fill(l1, c + 1);
             keep(c);
             s.step(l0, c);
             if (c + 1 >= c1) break;
-            stage_barrier<kWithO ? 16 : 0>();
+            loads_done<kWithO ? 16 : 0>();
+            __syncthreads();
             if (c + 2 < c1) s.fill(l0, c + 2);
             keep(c + 1);
             s.step(l1, c + 1);
@@ -690,6 +685,7 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
             __syncthreads();
             s.fill(l0, c);
             keep(c);
+            loads_done<0>();
             __syncthreads();
             s.step(l0, c);
         }

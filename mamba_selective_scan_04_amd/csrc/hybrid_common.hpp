@@ -199,16 +199,26 @@ __device__ __forceinline__ Frag<3> load_straight(const float *p) {
     return split_frag<3>(*(const f32x4 *)p, *(const f32x4 *)(p + 4));
 }
 
-// one wave's 64 x 16 bytes from memory straight into LDS: each lane's piece, to
-// base + 16 * lane
+// One wave's 64 x 16 bytes from memory straight into LDS: each lane's piece,
+// `off` bytes behind the uniform src, to base + 16 * lane (base uniform).  By
+// hand, for the compiler's own form made it wait for all such loads before the
+// next read of LDS, whichever buffer that was from.  It writes no register; who
+// reads the data waits by loads_done first.
 typedef __attribute__((address_space(3))) void lds_ptr;
-typedef const __attribute__((address_space(1))) void glb_ptr;
-__device__ __forceinline__ void load_lds(const void *src, void *base) {
-    __builtin_amdgcn_global_load_lds((glb_ptr *)src, (lds_ptr *)base, 16, 0, 0);
-}
-// ... `off` bytes behind a uniform src
 __device__ __forceinline__ void load_lds(const void *src, uint32_t off, void *base) {
-    load_lds((const char *)src + off, base);
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr *)base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(src), "s"(at) : "memory");
+}
+// ... from a lane's own address
+__device__ __forceinline__ void load_lds(const void *src, void *base) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr *)base);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(at) : "memory");
+}
+// Until no more than the kLater youngest memory operations of the wave are under
+// way (they finish in order).
+template <int kLater>
+__device__ __forceinline__ void loads_done() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
 }
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
