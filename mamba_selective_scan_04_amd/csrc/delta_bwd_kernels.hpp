@@ -248,7 +248,7 @@ struct GradLds {
         };
     };
     double G[kChunk];
-    float e[kChunk], rest[kChunk], bt[kChunk];
+    float e[kChunk], rest[kChunk], ib[kChunk];   // ib: 1 / beta
     float dG[kDv / 16][kChunk], db[kDv / 16][kChunk];
     float ends[kDv / 16];
 };
@@ -289,8 +289,10 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             for (int j = 0; j < kToks; ++j) dQ[i][j] = dK[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (m > 0) {
-        l.k.template fill<kWaves>(a.k + kat, kstride, m);
-        l.q.template fill<kWaves>(a.q + kat, kstride, m);
+        typename Tile<T, kDk>::template Offsets<kWaves> off;
+        off.set(kstride, m);
+        l.k.template fill<kWaves>(a.k + kat, off);
+        l.q.template fill<kWaves>(a.q + kat, off);
     }
     for (int hv = hk * d.group; hv < (kShared ? (hk + 1) * d.group : hk + 1); ++hv) {
         // opaque to the compiler: it would keep some 200 lane addresses of the
@@ -313,8 +315,10 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         fill_mats<kWaves>(a.fwd + unit, &l.fwd);
         fill_mats<kWaves>(a.bwd + unit, &l.bwd);
         if constexpr (kBf16) {
-            l.o.template fill<kWaves>(dop, vstride, m);
-            l.v.template fill<kWaves>(vp, vstride, m);
+            typename Tile<T, kDv>::template Offsets<kWaves> off;
+            off.set(vstride, m);
+            l.o.template fill<kWaves>(dop, off);
+            l.v.template fill<kWaves>(vp, off);
         }
         f32x4 raw[2 * kSteps];   // the state's columns, then its adjoint's, on their way
         const auto load_columns = [&](const float *p) {
@@ -327,7 +331,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
             l.G[t] = a.G[unit * kChunk + t];
-            l.bt[t] = t < m ? strength(a.beta[at + (int64_t)t * d.hv]) : 1.f;
+            l.ib[t] = t < m ? 1.f / strength(a.beta[at + (int64_t)t * d.hv]) : 1.f;
         }
         const auto value_tile = [&](int mt) {
             if constexpr (kBf16) {
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = mt * 16 + grp * 4 + r;
-                const float u = U[mt][r], x = X[mt][r], ib = 1.f / l.bt[t], y = u * ib, z = x * ib;
+                const float u = U[mt][r], x = X[mt][r], ib = l.ib[t], y = u * ib, z = x * ib;
                 sdG[r] = dG[mt][r] - x * (v[r] - y) - u * z;
                 sdb[r] = y * z;
                 l.U.put(t, n, u);

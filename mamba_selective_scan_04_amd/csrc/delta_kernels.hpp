@@ -48,11 +48,12 @@ __device__ __forceinline__ int64_t row_len(const DeltaDims &d, int b) {
     return n < 0 ? 0 : (n < d.T ? n : d.T);
 }
 
-// Inclusive sums of the chunk's log decays, by the first wave.
-__device__ __forceinline__ void chunk_decays(const float *g, int64_t stride, int n, double *G) {
+// Inclusive sums of the chunk's log decays, by the first wave (g: the lane's
+// own, 0 behind the last token).
+__device__ __forceinline__ void chunk_decays(float g, double *G) {
     if (threadIdx.x < 64) {
         const int t = threadIdx.x;
-        double x = t < n ? (double)fmaxf(g[t * stride], -1e4f) : 0.0;
+        double x = (double)fmaxf(g, -1e4f);
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) {
             const double up = __shfl_up(x, s, 64);
@@ -253,8 +254,18 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         const int64_t at = (((int64_t)b * d.T + t0) * d.hk + h) * kDk;
         l.k.template fill<4>(k + at, (int64_t)d.hk * kDk, n);
         if (q != nullptr) l.q.template fill<4>(q + at, (int64_t)d.hk * kDk, n);
-        loads_done<0>();
     }
+    // a head's gates, loaded a head ahead
+    float gv = 0.f, bv = 1.f;
+    const auto gates = [&](int hv) {
+        const int64_t at = ((int64_t)b * d.T + t0 + threadIdx.x) * d.hv + hv;
+        if ((int)threadIdx.x < n) {
+            gv = g[at];
+            bv = strength(beta[at]);
+        }
+    };
+    gates(h * d.group);
+    loads_done<0>();
     __syncthreads();
     f32x4 kk[3], kq[3], qk[3];   // this wave's tiles: K K^T; Q K^T by rows j (columns i) and by rows i
 #pragma unroll
@@ -275,10 +286,11 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
     }
     __syncthreads();   // the tiles are read: N takes their place
     for (int hv = h * d.group; hv < (h + 1) * d.group; ++hv) {
-        const int64_t at = ((int64_t)b * d.T + t0) * d.hv + hv, unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
-        chunk_decays(g + at, d.hv, n, G);
-        if (threadIdx.x < kChunk) bt[threadIdx.x] = (int)threadIdx.x < n ? strength(beta[at + (int64_t)threadIdx.x * d.hv]) : 1.f;
+        const int64_t unit = ((int64_t)b * d.hv + hv) * d.chunks + c;
+        chunk_decays(gv, G);
+        if (threadIdx.x < kChunk) bt[threadIdx.x] = bv;
         __syncthreads();
+        if (hv + 1 < (h + 1) * d.group) gates(hv + 1);
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
             const float e = decay(G[t]), rest = t < n ? decay(G[kChunk - 1] - G[t]) : 0.f;
@@ -734,11 +746,28 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) out[(int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n] = h[i][r];
     };
+    // a segment's N and rows of M, loaded a segment ahead
+    f32x4 N[kMine], M[kMine][kSteps][2];
+    const auto fetch = [&](int s) {
+        const float *m = a.agg + (head * a.segs + s) * kDk * ld;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = wave * kMine + i;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) N[i][r] = m[(int64_t)state_row(tile, grp, r) * ld + n];
+            const float *row = m + (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * ld + a.dv + grp * 8;
+#pragma unroll
+            for (int x = 0; x < kSteps; ++x) {
+                M[i][x][0] = *(const f32x4 *)(row + x * 32);
+                M[i][x][1] = *(const f32x4 *)(row + x * 32 + 4);
+            }
+        }
+    };
+    const int last = a.h_final != nullptr ? a.segs : a.segs - 1;   // maps that are needed
+    if (last > 0) fetch(0);
     for (int s = 0; s < a.segs; ++s) {
         if (a.h_seg != nullptr) store(a.h_seg + (head * a.segs + s) * state);
-        if (s + 1 == a.segs && a.h_final == nullptr) break;
-        const float *m = a.agg + (head * a.segs + s) * kDk * ld;
-        // a state tile holds half of a 32-row step's slots (kMine 1 at dk 64, 2 at 128)
+        if (s >= last) break;
         __syncthreads();   // the parts of the segment before are read
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -749,22 +778,22 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
 #pragma unroll
             for (int p = 0; p < 3; ++p) ((uint2 *)&part[tile / 2][p][lane])[tile & 1] = make_uint2(lo[p], hi[p]);
         }
-        __syncthreads();
+        Frag<3> mf[kMine][kSteps];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int tile = wave * kMine + i;
-            f32x4 acc;
+            h[i] = N[i];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = m[(int64_t)state_row(tile, grp, r) * ld + n];
-            const float *row = m + (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * ld + a.dv + grp * 8;
+            for (int x = 0; x < kSteps; ++x) mf[i][x] = split_frag<3>(M[i][x][0], M[i][x][1]);
+        }
+        if (s + 1 < last) fetch(s + 1);
+        __syncthreads();
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x) {
-                Frag<3> y;
+        for (int x = 0; x < kSteps; ++x) {
+            Frag<3> y;
 #pragma unroll
-                for (int p = 0; p < 3; ++p) y.p[p] = __builtin_bit_cast(bf16x8, part[x][p][lane]);
-                acc = mma(load_straight(row + x * 32), y, acc);
-            }
-            h[i] = acc;
+            for (int p = 0; p < 3; ++p) y.p[p] = __builtin_bit_cast(bf16x8, part[x][p][lane]);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) h[i] = mma(mf[i][x], y, h[i]);
         }
     }
     if (a.h_final != nullptr) store(a.h_final + head * state);
