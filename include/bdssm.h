@@ -427,8 +427,9 @@ typedef struct {
  *   o        NULL (states only; q may then be NULL), or out.
  *   h_final  NULL, or out: the state after the row's last token.  May be
  *            h_init (in place).
- *   h_chunks NULL, or [batch, ceil(T / 64), heads_v, d_k, d_v] out: the state
- *            before each chunk, for the backward.
+ *   h_chunks NULL, or [batch, ceil(T / 64), heads_v, d_v, d_k] out: the state
+ *            before each chunk (transposed: each column in a row), for the
+ *            backward.
  *   ws       ws_bytes >= bdssm_delta_workspace_bytes(shape, T, 0).
  */
 int bdssm_delta_scan(const bdssm_delta_shape *shape, int64_t T, const void *q, const void *k,

@@ -30,7 +30,7 @@ struct AdjointArgs {
     const T *q, *k, *dout;
     const Mats<3> *mats;
     const float *dh_final;            // null: zero
-    float *dS;                        // [batch, chunks, hv, dk, dv]: dS' of each chunk
+    float *dS;                        // [batch, chunks, hv, dv, dk]: dS' of each chunk
     float *dh_init;                   // null: not wanted
     int groups;                       // batch * hv
     DeltaDims d;
@@ -66,6 +66,11 @@ struct Adjoint {
         l.q.template fill<4>(qp + t0 * kstride, koff);
         l.o.template fill<4>(op + t0 * vstride, voff);
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
+    }
+    __device__ __forceinline__ void store_columns(float *out) {
+        const uint32_t lane_off = (uint32_t)(n * kDk + grp * 8);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) *(f32x4 *)(out + state_row(t, 0, 0) + lane_off) = S[t];
     }
     __device__ __forceinline__ void store_state(float *out) {
         const uint32_t lane_off = (uint32_t)(grp * 8 * a.d.dv + n);
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             s.S[t][r] = a.dh_final == nullptr ? 0.f : a.dh_final[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
-    auto keep = [&](int c) { s.store_state(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state); };
+    auto keep = [&](int c) { s.store_columns(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state); };
     int c = chunks - 1;
     s.koff.set(s.kstride, c >= 0 ? s.tokens(c) : kChunk);   // the last chunk's; the others are full
     s.voff.set(s.vstride, c >= 0 ? s.tokens(c) : kChunk);
@@ -162,14 +167,14 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
         s.voff.set(s.vstride, kChunk);
         for (; c >= 0; c -= 2) {
             // l0 is filled, l1 is read; the state's stores came after the loads
-            if (c < chunks - 1) loads_done<C::kTiles * 4>();
+            if (c < chunks - 1) loads_done<C::kTiles>();
             else loads_done<0>();
             __syncthreads();
             if (c > 0) s.fill(l1, c - 1);
             keep(c);
             s.step(l0, c);
             if (c == 0) break;
-            loads_done<C::kTiles * 4>();
+            loads_done<C::kTiles>();
             __syncthreads();
             if (c > 1) s.fill(l0, c - 2);
             keep(c - 1);
@@ -195,7 +200,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
 template <typename T>
 struct GradArgs {
     const T *q, *k, *v, *dout;
-    const Mats<3> *fwd, *bwd;
+    const Mats<3> *mats;
     const double *G;
     const float *beta, *S, *dS;   // S: h_chunks
     T *dq, *dk, *dv;
@@ -239,9 +244,7 @@ struct GradLds {
     Tile<T, kDk> k, q;
     typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o, v;   // dO, V (fp32 streams: from memory)
     union {
-        struct {
-            Mats<3> fwd, bwd;
-        };
+        Mats<3> m;
         struct {
             RowTile<T, kDv> U, X;
             uint4 pairs[8][kOut][64];   // B fragments of a token by token matrix: (column tile, step)
@@ -310,10 +313,9 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         if (m == 0) continue;
         const int64_t chunk_at = (((int64_t)b * d.chunks + c) * d.hv + hv) * state;
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
-        const uint32_t col_off = (uint32_t)(grp * 8 * kDv + n);
+        const uint32_t col_off = (uint32_t)(n * kDk + grp * 8);
         __syncthreads();   // the last head's reads of LDS are done
-        fill_mats<kWaves>(a.fwd + unit, &l.fwd);
-        fill_mats<kWaves>(a.bwd + unit, &l.bwd);
+        fill_mats<kWaves>(a.mats + unit, &l.m);
         if constexpr (kBf16) {
             typename Tile<T, kDv>::template Offsets<kWaves> off;
             off.set(vstride, m);
@@ -323,9 +325,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         f32x4 raw[2 * kSteps];   // the state's columns, then its adjoint's, on their way
         const auto load_columns = [&](const float *p) {
 #pragma unroll
-            for (int t = 0; t < 2 * kSteps; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) raw[t][r] = (p + state_row(t, 0, r) * kDv)[col_off];
+            for (int t = 0; t < 2 * kSteps; ++t) raw[t] = *(const f32x4 *)(p + state_row(t, 0, 0) + col_off);
         };
         load_columns(Sg);
         if (threadIdx.x < kChunk) {
@@ -360,8 +360,8 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         loads_done<0>();
         __syncthreads();
         if (threadIdx.x < kChunk) {   // these outlast the matrices
-            l.e[threadIdx.x] = l.fwd.e[threadIdx.x];
-            l.rest[threadIdx.x] = l.fwd.rest[threadIdx.x];
+            l.e[threadIdx.x] = l.m.e[threadIdx.x];
+            l.rest[threadIdx.x] = l.m.rest[threadIdx.x];
         }
         // by columns: R, U, O and dO's part of dG
         f32x4 U[4], X[4], dG[4];
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 load_columns(dSg);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
-                    const f32x4 e = *(const f32x4 *)(l.fwd.e + mt * 16 + grp * 4), v = value_tile(mt);
+                    const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = value_tile(mt);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         R[mt][r] = fmaf(-e[r], ks[mt][r], v[r]);
@@ -395,9 +395,9 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            lower_product<3>(l.fwd.W, R, U);
+            lower_product<3>(l.m.W, R, U);
             __builtin_amdgcn_sched_barrier(0);
-            lower_product<3, false>(l.fwd.P, U, O);
+            lower_product<3, false>(l.m.P, U, O);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 const f32x4 dO = dout_tile(mt);
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const f32x4 rest = *(const f32x4 *)(l.bwd.rest + mt * 16 + grp * 4);
+                const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     dU[mt][r] *= rest[r];
@@ -434,10 +434,10 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 f32x4 dO[4];
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) dO[mt] = dout_tile(mt);
-                upper_product<3, false, kIn>(l.bwd.P, dO, dU);
+                upper_product<3, false, kIn>(l.m.P, dO, dU);
             }
             __builtin_amdgcn_sched_barrier(0);
-            upper_product<3>(l.bwd.W, dU, X);
+            upper_product<3>(l.m.W, dU, X);
         }
         __syncthreads();   // the matrices are read: U and X take their place
         float sdG[4], sdb[4];   // row sums over this wave's columns, lane r = col of each result row set
@@ -487,15 +487,21 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int tile = dk0 + i;
-            const uint32_t r0 = (uint32_t)((tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * kDv + grp * 8);
+            // row of dk in [dv][dk]: eight dv apart by rows
+            const uint32_t r0 = (uint32_t)(grp * 8 * kDk + tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4);
             f32x4 so[kToks], sx[kToks], du[kToks], x[2], y[2];
 #pragma unroll
             for (int j = 0; j < kToks; ++j) so[j] = sx[j] = du[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const auto load_rows = [&](int s) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                x[h] = *(const f32x4 *)(Sg + r0 + h * 4);
-                y[h] = *(const f32x4 *)(dSg + r0 + h * 4);
-            }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        x[h][r] = (Sg + (s * 32 + h * 4 + r) * kDk)[r0];
+                        y[h][r] = (dSg + (s * 32 + h * 4 + r) * kDk)[r0];
+                    }
+            };
+            load_rows(0);
 #pragma unroll
             for (int s = 0; s < kVSteps; ++s) {
                 const Frag<kOut> sf = split_frag<kOut>(x[0], x[1]), df = split_frag<kOut>(y[0], y[1]);
@@ -503,13 +509,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dot = fmaf(x[h][r], y[h][r], dot);
-                if (s + 1 < kVSteps) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        x[h] = *(const f32x4 *)(Sg + r0 + (s + 1) * 32 + h * 4);
-                        y[h] = *(const f32x4 *)(dSg + r0 + (s + 1) * 32 + h * 4);
-                    }
-                }
+                if (s + 1 < kVSteps) load_rows(s + 1);
 #pragma unroll
                 for (int j = 0; j < kToks; ++j) {
                     const int t = (tk0 + j) * 16 + col;
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                     // beyond the triangle: no fragment (with two token tiles a wave, both or none)
                     const int half = kToks == 4 ? j / 2 : tk0 / 2;
                     if (kind == 0 ? s > half : kind == 1 ? s < half : false) continue;
-                    const int ct = tk0 + j, f = kind == 2 ? ct * 2 + s : kind == 0 ? frag_lower(ct, s) : frag_upper(ct, s);
+                    const int ct = tk0 + j, f = kind == 2 ? ct * 2 + s : kind == 0 ? frag_lower(ct, s) : ct < 2 ? ct * 2 + s : ct + 2;
                     Frag<kOut> y;
 #pragma unroll
                     for (int p = 0; p < kOut; ++p) y.p[p] = __builtin_bit_cast(bf16x8, l.pairs[f][p][lane]);

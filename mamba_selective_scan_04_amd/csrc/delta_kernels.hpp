@@ -186,11 +186,10 @@ __device__ __forceinline__ int state_row(int tile, int grp, int r) { return tile
 // ------------------------------------------------------------- chunk matrices
 //
 // What the chains need of a chunk besides its tokens, laid out by
-// delta_prep_kernel as they read it: the 64x64 matrices as A fragments in
-// paired order (W in three parts, P in as many as its result needs), then
-// exp(G_i) and exp(G_C - G_i), 0 behind the last token.
-//   forward:  W  (row tile mt, steps s <= mt / 2)   P
-//   backward: W^T (row tile mt, steps s >= mt / 2)  P^T in three parts
+// delta_prep_kernel as they read it: W (in three parts) and P (in as many as its
+// result needs) as A fragments in paired order, row tile mt, steps s <= mt / 2;
+// then exp(G_i) and exp(G_C - G_i), 0 behind the last token.  The backward reads
+// W^T and P^T out of the same fragments by transposing LDS reads.
 template <int kPParts>
 struct Mats {
     uint4 W[3][kFrags][64];
@@ -199,13 +198,30 @@ struct Mats {
     uint4 P[kPParts][kFrags][64]; // last: a chain without outputs stops here
 };
 __device__ __forceinline__ int frag_lower(int mt, int s) { return mt < 2 ? mt : mt * 2 - 2 + s; }
-__device__ __forceinline__ int frag_upper(int mt, int s) { return mt < 2 ? mt * 2 + s : mt + 2; }
 
 template <int kParts>
 __device__ __forceinline__ Frag<kParts> mat_frag(const uint4 (*m)[kFrags][64], int f) {
     Frag<kParts> x;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) x.p[i] = __builtin_bit_cast(bf16x8, m[i][f][threadIdx.x & 63]);
+    return x;
+}
+// Fragment of the transpose: row tile mt, step s >= mt / 2.  Block (it, mt) of the
+// matrix holds four columns of a row in each lane's 8 bytes.
+template <int kParts>
+__device__ __forceinline__ Frag<kParts> mat_frag_t(const uint4 (*m)[kFrags][64], int mt, int s, int col, int grp) {
+    const int at = (col & 3) * 16 + grp * 4 + (col >> 2);
+    Frag<kParts> x;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        uint2 h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint2 *p = (const uint2 *)&m[i][frag_lower(2 * s + j, mt / 2)][at] + (mt & 1);
+            h[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+        }
+        x.p[i] = frag_of(h[0].x, h[0].y, h[1].x, h[1].y);
+    }
     return x;
 }
 // four of a row into half h of its lane's 16 bytes
@@ -228,12 +244,11 @@ __device__ __forceinline__ void block_of(int tile, int *it, int *jt) {
 // by 16x16 blocks: wave j inverts diagonal block j by substitution (a lane per
 // column), then runs down block column j: X_i = inv_ii sum_k N_ik X_k, in fp32
 // matrix instructions, X_k staying in registers.
-template <typename T, int kDk, int kPF, bool kBwd>
+template <typename T, int kDk, int kPF>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__restrict__ q, const T *__restrict__ k,
                                                                   const float *__restrict__ g,
-                                                                  const float *__restrict__ beta, Mats<kPF> *__restrict__ fwd,
-                                                                  Mats<3> *__restrict__ bwd, double *__restrict__ Gs,
-                                                                  DeltaDims d) {
+                                                                  const float *__restrict__ beta, Mats<kPF> *__restrict__ mats,
+                                                                  double *__restrict__ Gs, DeltaDims d) {
     constexpr int kN = 68;
     __shared__ __attribute__((aligned(16))) union {
         struct {
@@ -267,21 +282,17 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
     gates(h * d.group);
     loads_done<0>();
     __syncthreads();
-    f32x4 kk[3], kq[3], qk[3];   // this wave's tiles: K K^T; Q K^T by rows j (columns i) and by rows i
+    f32x4 kk[3], kq[3];   // this wave's tiles: K K^T; K Q^T (rows j, columns i)
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         int it, jt;
         block_of(wave + 4 * x < kBlocks ? wave + 4 * x : 0, &it, &jt);
-        kk[x] = kq[x] = qk[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        kk[x] = kq[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < kDk / 32; ++s) {
             const auto ki = l.k.row(it * 16 + col, s, grp), kj = l.k.row(jt * 16 + col, s, grp);
             kk[x] = mma(ki, kj, kk[x]);
-            if (q != nullptr) {
-                const auto qi = l.q.row(it * 16 + col, s, grp);
-                kq[x] = mma(kj, qi, kq[x]);
-                if (kBwd) qk[x] = mma(qi, kj, qk[x]);
-            }
+            if (q != nullptr) kq[x] = mma(kj, l.q.row(it * 16 + col, s, grp), kq[x]);
         }
     }
     __syncthreads();   // the tiles are read: N takes their place
@@ -294,42 +305,32 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
             const float e = decay(G[t]), rest = t < n ? decay(G[kChunk - 1] - G[t]) : 0.f;
-            fwd[unit].e[t] = e;
-            fwd[unit].rest[t] = rest;
-            if (kBwd) {
-                bwd[unit].e[t] = e;
-                bwd[unit].rest[t] = rest;
-                Gs[unit * kChunk + t] = G[t];
-            }
+            mats[unit].e[t] = e;
+            mats[unit].rest[t] = rest;
+            if (Gs != nullptr) Gs[unit * kChunk + t] = G[t];
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             if (wave + 4 * x >= kBlocks) continue;
             int it, jt;
             block_of(wave + 4 * x, &it, &jt);
-            float pt[4], pq[4];
+            float pt[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = it * 16 + grp * 4 + r, j = jt * 16 + col;   // a result tile's rows and columns
                 const bool in = i < n && j < n;                            // repeated rows count for nothing
                 const float D = decay(G[i] - G[j]);
                 l.N[i * kN + j] = j < i && in ? -bt[i] * (D * kk[x][r]) : 0.f;
-                pq[r] = j <= i && in ? d.scale * D * qk[x][r] : 0.f;
                 const int i2 = it * 16 + col, j2 = jt * 16 + grp * 4 + r;
                 pt[r] = j2 <= i2 && i2 < n ? d.scale * decay(G[i2] - G[j2]) * kq[x][r] : 0.f;
             }
-            if (q != nullptr) put_quad<kPF>(fwd[unit].P, frag_lower(it, jt / 2), lane, jt & 1, pt);
-            if (kBwd) put_quad<3>(bwd[unit].P, frag_upper(jt, it / 2), lane, it & 1, pq);
+            if (q != nullptr) put_quad<kPF>(mats[unit].P, frag_lower(it, jt / 2), lane, jt & 1, pt);
         }
         // halves of the 32-wide steps beyond the triangle
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
         if (wave < 2) {
-            put_quad<3>(fwd[unit].W, frag_lower(wave * 2, wave), lane, 1, zero);
-            if (q != nullptr) put_quad<kPF>(fwd[unit].P, frag_lower(wave * 2, wave), lane, 1, zero);
-        } else if (kBwd) {
-            const int x = wave - 2;
-            put_quad<3>(bwd[unit].W, frag_upper(x * 2 + 1, x), lane, 0, zero);
-            put_quad<3>(bwd[unit].P, frag_upper(x * 2 + 1, x), lane, 0, zero);
+            put_quad<3>(mats[unit].W, frag_lower(wave * 2, wave), lane, 1, zero);
+            if (q != nullptr) put_quad<kPF>(mats[unit].P, frag_lower(wave * 2, wave), lane, 1, zero);
         }
         __syncthreads();
         // diagonal block `wave`, column `col` of its inverse
@@ -383,7 +384,6 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
             float w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) w[r] = X[i][r] * bj;
-            if (kBwd) put_quad<3>(bwd[unit].W, frag_upper(wave, i / 2), lane, i & 1, w);
 #pragma unroll
             for (int r = 0; r < 4; ++r) l.N[(i * 16 + grp * 4 + r) * kN + wave * 16 + col] = w[r];
         }
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
             block_of(wave + 4 * y, &it, &jt);
             const f32x4 w = *(const f32x4 *)&l.N[(it * 16 + col) * kN + jt * 16 + grp * 4];
             const float v[4] = {w[0], w[1], w[2], w[3]};
-            put_quad<3>(fwd[unit].W, frag_lower(it, jt / 2), lane, jt & 1, v);
+            put_quad<3>(mats[unit].W, frag_lower(it, jt / 2), lane, jt & 1, v);
         }
         __syncthreads();
     }
@@ -422,10 +422,15 @@ __device__ __forceinline__ void fill_mats(const void *src, M *dst) {
         load_lds((const char *)src + i * 1024, lane * 16, (char *)dst + i * 1024);
 }
 
-// out (+)= M x for a lower (kLower) or upper triangular matrix in kParts parts
-// and a [64 x 16] column slice x in result tiles.
-template <int kParts, bool kZero = true, bool kLower = true, int kXParts = kParts>
+// out (+)= M x, or M^T x (kTransposed), for a chunk's lower triangular matrix in
+// kParts parts and a [64 x 16] column slice x in result tiles.
+template <int kParts, bool kZero, bool kTransposed, int kXParts>
 __device__ __forceinline__ void tri_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
+    const int col = lane_id() & 15, grp = lane_id() >> 4;
+    const auto frag = [&](int mt, int s) {
+        if constexpr (kTransposed) return mat_frag_t<kParts>(m, mt, s, col, grp);
+        else return mat_frag<kParts>(m, frag_lower(mt, s));
+    };
     if (kZero) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) out[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -433,27 +438,23 @@ __device__ __forceinline__ void tri_product(const uint4 (*m)[kFrags][64], const 
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const Frag<kXParts> xp = split_frag<kXParts>(x[2 * s], x[2 * s + 1]);
-        if ((s == 0) == kLower) {   // all four row tiles
-            const Frag<kParts> f[4] = {mat_frag<kParts>(m, kLower ? frag_lower(0, s) : frag_upper(0, s)),
-                                       mat_frag<kParts>(m, kLower ? frag_lower(1, s) : frag_upper(1, s)),
-                                       mat_frag<kParts>(m, kLower ? frag_lower(2, s) : frag_upper(2, s)),
-                                       mat_frag<kParts>(m, kLower ? frag_lower(3, s) : frag_upper(3, s))};
+        if ((s == 0) != kTransposed) {   // all four row tiles
+            const Frag<kParts> f[4] = {frag(0, s), frag(1, s), frag(2, s), frag(3, s)};
             mma_n<4>(f, xp, out);
-        } else {                    // the two at the far side
-            constexpr int k0 = kLower ? 2 : 0;
-            const Frag<kParts> f[2] = {mat_frag<kParts>(m, kLower ? frag_lower(k0, s) : frag_upper(k0, s)),
-                                       mat_frag<kParts>(m, kLower ? frag_lower(k0 + 1, s) : frag_upper(k0 + 1, s))};
+        } else {                         // the two at the far side
+            constexpr int k0 = kTransposed ? 0 : 2;
+            const Frag<kParts> f[2] = {frag(k0, s), frag(k0 + 1, s)};
             mma_n<2>(f, xp, out + k0);
         }
     }
 }
 template <int kParts, bool kZero = true>
 __device__ __forceinline__ void lower_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
-    tri_product<kParts, kZero, true>(m, x, out);
+    tri_product<kParts, kZero, false, kParts>(m, x, out);
 }
 template <int kParts, bool kZero = true, int kXParts = kParts>
 __device__ __forceinline__ void upper_product(const uint4 (*m)[kFrags][64], const f32x4 *x, f32x4 *out) {
-    tri_product<kParts, kZero, false, kXParts>(m, x, out);
+    tri_product<kParts, kZero, true, kXParts>(m, x, out);
 }
 
 // S += tile^T x (rows dk, summed over the chunk's tokens), x in three parts
@@ -491,7 +492,7 @@ struct ChainArgs {
     const float *h_init;  // null: zero; with segments [batch, hv, segs, dk, dv]
     T *o;                 // kOutputs
     float *h_final;       // null: not wanted
-    float *h_chunks;      // null, or [batch, chunks, hv, dk, dv]
+    float *h_chunks;      // null, or [batch, chunks, hv, dv, dk]
     float *agg;           // kAggregate: [batch, hv, segs, dk, dv + dk]
     int segs, per;        // segments, and chunks of each
     int groups;           // batch * segs * hv
@@ -535,6 +536,12 @@ struct Chain {
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
     }
 
+    // the chunk states' layout, [dv][dk]: 16 bytes a lane and tile
+    __device__ __forceinline__ void store_columns(float *out) {
+        const uint32_t lane_off = (uint32_t)(n * kDk + grp * 8);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) *(f32x4 *)(out + state_row(t, 0, 0) + lane_off) = S[t];
+    }
     // rows `ld` apart
     __device__ __forceinline__ void store_state(float *out, int ld) {
         const uint32_t lane_off = (uint32_t)(grp * 8 * ld + n);
@@ -672,7 +679,7 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
         }
     auto keep = [&](int c) {
         if (kMode != kAggregate && a.h_chunks != nullptr)
-            s.store_state(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state, d.dv);
+            s.store_columns(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
     };
     if constexpr (kTwo) {
         if (c0 < c1) s.fill(l0, c0);

@@ -85,13 +85,13 @@ struct DeltaSizes {
     size_t qk, vo, gate, state, hchunks, units, agg;
     bool bf16;
     int segs;
-    // the workspace: the chunks' matrices; for the backward those of both
-    // directions, the summed log decays and the states' adjoints
+    // the workspace: the chunks' matrices and the segments' maps; for the backward
+    // the matrices, the summed log decays and the states' adjoints
     size_t mats() const { return units * (bf16 ? sizeof(Mats<2>) : sizeof(Mats<3>)); }
     size_t fwd() const { return mats() + (segs > 1 ? agg + state * segs : 0); }
     size_t mats3() const { return units * sizeof(Mats<3>); }
     size_t sums() const { return units * kChunk * 8; }
-    size_t bwd() const { return 2 * mats3() + sums() + hchunks; }
+    size_t bwd() const { return mats3() + sums() + hchunks; }
 };
 
 DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
@@ -254,7 +254,7 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     c.o = o;
     c.h_final = h_final;
     c.h_chunks = h_chunks;
-    c.fwd = ws;
+    c.mats = ws;
     c.segs = z.segs;
     c.agg = (float *)((char *)ws + z.mats());
     c.h_seg = (float *)((char *)ws + z.mats() + z.agg);
@@ -287,10 +287,9 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, c
     c.dout = dout;
     c.dh_final = dh_final;
     char *w = (char *)ws;
-    c.fwd = w;
-    c.bwd = w + z.mats3();
-    c.G = (double *)(w + 2 * z.mats3());
-    c.dS = (float *)(w + 2 * z.mats3() + z.sums());
+    c.mats = w;
+    c.G = (double *)(w + z.mats3());
+    c.dS = (float *)(w + z.mats3() + z.sums());
     c.dq = dq;
     c.dk_out = dk;
     c.dv_out = dv;

@@ -21,13 +21,12 @@ struct DeltaCall {
     const float *g, *beta, *h_init;
     void *o;
     float *h_final, *h_chunks;
-    void *fwd;   // the chunks' matrices (Mats)
+    void *mats;   // the chunks' matrices (Mats)
     float *agg, *h_seg;   // the segments' maps and first states
     int segs;
     // backward
     const void *dout;
     const float *dh_final;
-    void *bwd;
     float *dS, *dh_init, *dg, *dbeta;
     void *dq, *dk_out, *dv_out;
     double *G;

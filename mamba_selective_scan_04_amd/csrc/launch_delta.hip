@@ -13,10 +13,10 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
     constexpr int kOut = Stream<T>::kOutParts;
     const dim3 gp((unsigned)c.d.chunks, (unsigned)c.d.hk, (unsigned)c.batch);
     if (c.d.chunks > 0)
-        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, kOut, false>), gp, dim3(kDeltaThreads), 0, st,
-                           c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.fwd,
-                           (Mats<3> *)nullptr, (double *)nullptr, c.d);
-    ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.fwd, c.h_init, (T *)c.o, c.h_final, c.h_chunks,
+        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, kOut>), gp, dim3(kDeltaThreads), 0, st,
+                           c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.mats,
+                           (double *)nullptr, c.d);
+    ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.mats, c.h_init, (T *)c.o, c.h_final, c.h_chunks,
                    c.agg, 1, c.d.chunks, (int)(c.batch * c.d.hv), c.d};
     const auto grid = [&](int columns) { return dim3((unsigned)((a.groups + 7) / 8 * 8 * (columns / 64))); };
     if (c.segs > 1) {
@@ -49,13 +49,13 @@ template <typename T, int kDk>
 void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
     const dim3 gp((unsigned)c.d.chunks, (unsigned)c.d.hk, (unsigned)c.batch);
     if (c.d.chunks > 0)
-        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, 3, true>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.q, (const T *)c.k, c.g, c.beta,
-                           (Mats<3> *)c.fwd, (Mats<3> *)c.bwd, c.G, c.d);
-    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.bwd, c.dh_final, c.dS, c.dh_init, (int)(c.batch * c.d.hv), c.d};
+        hipLaunchKernelGGL((delta_prep_kernel<T, kDk, 3>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.q, (const T *)c.k, c.g, c.beta,
+                           (Mats<3> *)c.mats, c.G, c.d);
+    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.mats, c.dh_final, c.dS, c.dh_init, (int)(c.batch * c.d.hv), c.d};
     const dim3 gc((unsigned)((a.groups + 7) / 8 * 8 * (c.d.dv / 64)));
     hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk>), gc, dim3(kDeltaThreads), 0, st, a);
     if (c.d.chunks == 0) return;
-    const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.fwd, (const Mats<3> *)c.bwd,
+    const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.mats,
                          c.G, c.beta, c.h_chunks, c.dS, (T *)c.dq, (T *)c.dk_out, (T *)c.dv_out, c.dg, c.dbeta, c.d};
     const bool shared = c.d.group > 1;
     if (c.d.dv == 64) {

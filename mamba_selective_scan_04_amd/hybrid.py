@@ -64,13 +64,14 @@ def _state(s):
 
 
 def _chunk_states(s, T):
-    return (s.batch, -(-T // DELTA_CHUNK), s.heads_v, s.d_k, s.d_v)
+    return (s.batch, -(-T // DELTA_CHUNK), s.heads_v, s.d_v, s.d_k)
 
 
 def delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True, want_chunks=False, o=None,
                h_final=None, h_chunks=None, ws=None):
     """The gated delta rule over whole rows -> (o or None, h_final, h_chunks or
-    None).  h_chunks: the states before every 64th token, for delta_scan_bwd.
+    None).  h_chunks [batch, ceil(T / 64), heads_v, d_v, d_k]: the (transposed)
+    states before every 64th token, for delta_scan_bwd.
     Tokens at and behind lens[b] are padding.  q may be None with want_o=False."""
     want_o = want_o or o is not None
     s, T, dev, scale = _delta(q, k, v, g, beta, lens, scale)

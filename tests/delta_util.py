@@ -40,7 +40,7 @@ def inputs(batch, T, hk, hv, dk, dv, dtype, seed=0, device="cpu", decay=-4.0, re
 
 
 def reference(c, scale=None, h=None, want_grads=False):
-    """-> dict(o, h, chunks [batch, n, hv, dk, dv]) and, if asked, the gradients
+    """-> dict(o, h, chunks [batch, n, hv, dv, dk]) and, if asked, the gradients
     given c['do'], c['dh'] (their padding ignored), all fp64 on the CPU."""
     q, k, v, g, beta, do = (c[n].detach().cpu().double() for n in ("q", "k", "v", "g", "beta", "do"))
     batch, T, hk, dk = k.shape
@@ -49,7 +49,7 @@ def reference(c, scale=None, h=None, want_grads=False):
     rep = hv // hk
     n = [T] * batch if c["lens"] is None else c["lens"].cpu().clamp(0, T).tolist()
     out = dict(o=torch.zeros(batch, T, hv, dv, dtype=torch.float64), h=torch.zeros(batch, hv, dk, dv, dtype=torch.float64),
-               chunks=torch.zeros(batch, -(-T // 64), hv, dk, dv, dtype=torch.float64))
+               chunks=torch.zeros(batch, -(-T // 64), hv, dv, dk, dtype=torch.float64))
     for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
         out[name] = torch.zeros_like(like)
     out["dh_init"] = torch.zeros_like(out["h"])
@@ -59,7 +59,7 @@ def reference(c, scale=None, h=None, want_grads=False):
         before, err = [], []
         for t in range(-(-T // 64) * 64):
             if t % 64 == 0:
-                out["chunks"][b, t // 64] = S
+                out["chunks"][b, t // 64] = S.transpose(-1, -2)
             if t >= n[b]:
                 continue
             before.append(S)
