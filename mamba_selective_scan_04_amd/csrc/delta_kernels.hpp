@@ -822,41 +822,67 @@ struct StepArgs {
     DeltaDims d;
 };
 
+// kN consecutive stream elements as they lie in memory, and as fp32
 template <typename T, int kN>
-__device__ __forceinline__ void load_run(const T *p, float *out) {
-    if constexpr (sizeof(T) == 2) {
+struct Run {
+    static constexpr int kWords = kN * (int)sizeof(T) / 16;
+    uint4 w[kWords];
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < kN / 8; ++i) {
-            const uint4 w = *(const uint4 *)(p + i * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < kWords; ++i) w[i] = ((const uint4 *)p)[i];
+    }
+    __device__ __forceinline__ void values(float *out) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                out[i * 8 + 2 * j] = bf_lo(u[j]);
-                out[i * 8 + 2 * j + 1] = bf_hi(u[j]);
+                if constexpr (sizeof(T) == 2) {
+                    out[i * 8 + 2 * j] = bf_lo(u[j]);
+                    out[i * 8 + 2 * j + 1] = bf_hi(u[j]);
+                } else {
+                    out[i * 4 + j] = as_f(u[j]);
+                }
             }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN / 4; ++i) *(f32x4 *)(out + i * 4) = *(const f32x4 *)(p + i * 4);
     }
-}
+};
 
-__device__ __forceinline__ f32x4 load4(const uint16_t *p) {
-    const uint2 w = *(const uint2 *)p;
-    return f32x4{bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
-}
-__device__ __forceinline__ f32x4 load4(const float *p) { return *(const f32x4 *)p; }
+template <typename T>
+struct Four;
+template <>
+struct Four<uint16_t> {
+    uint2 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *(const uint2 *)p; }
+    __device__ __forceinline__ f32x4 values() const { return f32x4{bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)}; }
+};
+template <>
+struct Four<float> {
+    f32x4 w;
+    __device__ __forceinline__ void load(const float *p) { w = *(const f32x4 *)p; }
+    __device__ __forceinline__ f32x4 values() const { return w; }
+};
 __device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
     *(uint2 *)p = make_uint2(pk_rne(v[0], v[1]), pk_rne(v[2], v[3]));
 }
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *(f32x4 *)p = v; }
 
-// sum over the 8 row groups (lanes 8 apart), in every lane
+// sum over the 8 row groups (lanes 8 apart), in every lane: by 8 within rows of
+// 16 lanes, then by exchanging halves of 32 and of 64
 __device__ __forceinline__ float row_sum(float x) {
-    x += __shfl_xor(x, 8, 64);
-    x += __shfl_xor(x, 16, 64);
-    x += __shfl_xor(x, 32, 64);
-    return x;
+    x += as_f(__builtin_amdgcn_update_dpp(0, as_u(x), 0x128, 0xf, 0xf, false));   // row_ror:8
+    const auto h = __builtin_amdgcn_permlane16_swap(as_u(x), as_u(x), false, false);
+    x = as_f(h[0]) + as_f(h[1]);
+    const auto w = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(x), false, false);
+    return as_f(w[0]) + as_f(w[1]);
+}
+
+template <int kR>
+__device__ __forceinline__ void scale_state(f32x4 (&S)[kR], float c) {
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) S[i][x] *= c;
 }
 
 template <typename T, int kDk>
@@ -870,44 +896,69 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs<T> a) {
     f32x4 S[kR];
 #pragma unroll
     for (int i = 0; i < kR; ++i) S[i] = a.h == nullptr ? f32x4{0.f, 0.f, 0.f, 0.f} : *(const f32x4 *)(a.h + state + (int64_t)i * d.dv);
+    // S holds the state divided by c, the product of the decays since S was last
+    // scaled: a token's decay costs no pass over S.
+    float c = 1.f;
+    // a token's operands, on their way while the one before is worked on
+    struct {
+        Run<T, kR> k, q;
+        Four<T> v;
+        float g, beta;
+    } next;
+    const auto fetch = [&](int64_t t) {
+        next.k.load(a.k + ((at0 + t) * d.hk + hk) * kDk + r0);
+        if (a.o != nullptr) next.q.load(a.q + ((at0 + t) * d.hk + hk) * kDk + r0);
+        next.v.load(a.v + ((at0 + t) * d.hv + hv) * d.dv + n);
+        next.g = a.g[(at0 + t) * d.hv + hv];
+        next.beta = a.beta[(at0 + t) * d.hv + hv];
+    };
+    if (len > 0) fetch(0);
     for (int64_t t = 0; t < len; ++t) {
         float k[kR], q[kR];
-        load_run<T, kR>(a.k + ((at0 + t) * d.hk + hk) * kDk + r0, k);
-        if (a.o != nullptr) load_run<T, kR>(a.q + ((at0 + t) * d.hk + hk) * kDk + r0, q);
-        const f32x4 v = load4(a.v + ((at0 + t) * d.hv + hv) * d.dv + n);
-        const float al = __expf(a.g[(at0 + t) * d.hv + hv]), bt = a.beta[(at0 + t) * d.hv + hv];
+        next.k.values(k);
+        if (a.o != nullptr) next.q.values(q);
+        const f32x4 v = next.v.values();
+        const float bt = next.beta;
+        c *= __expf(next.g);
+        if (t + 1 < len) fetch(t + 1);
+        if (!(c >= 0x1p-30f && c <= 0x1p30f)) {
+            scale_state(S, c);
+            c = 1.f;
+        }
         f32x4 p = {0.f, 0.f, 0.f, 0.f}, s = {0.f, 0.f, 0.f, 0.f};
         float kq = 0.f;
 #pragma unroll
         for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                S[i][c] *= al;
-                p[c] = fmaf(S[i][c], k[i], p[c]);
-            }
+            for (int x = 0; x < 4; ++x) p[x] = fmaf(S[i][x], k[i], p[x]);
         if (a.o != nullptr) {
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
                 kq = fmaf(k[i], q[i], kq);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[c] = fmaf(S[i][c], q[i], s[c]);
+                for (int x = 0; x < 4; ++x) s[x] = fmaf(S[i][x], q[i], s[x]);
             }
             kq = row_sum(kq);
         }
-        f32x4 u;
+        const float ic = 1.f / c;
+        f32x4 u, us;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) u[c] = bt * (v[c] - row_sum(p[c]));
+        for (int x = 0; x < 4; ++x) {
+            u[x] = bt * fmaf(-c, row_sum(p[x]), v[x]);
+            us[x] = u[x] * ic;
+        }
 #pragma unroll
         for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) S[i][c] = fmaf(k[i], u[c], S[i][c]);
+            for (int x = 0; x < 4; ++x) S[i][x] = fmaf(k[i], us[x], S[i][x]);
         if (a.o != nullptr) {
             f32x4 o;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = d.scale * fmaf(kq, u[c], row_sum(s[c]));
+            for (int x = 0; x < 4; ++x) o[x] = d.scale * fmaf(kq, u[x], c * row_sum(s[x]));
             if (lane < 8) store4(a.o + ((at0 + t) * d.hv + hv) * d.dv + n, o);
         }
     }
+    if (c != 1.f) scale_state(S, c);
     if (a.o != nullptr)
         for (int64_t t = len + (lane >> 3); t < d.T; t += 8)
             store4(a.o + ((at0 + t) * d.hv + hv) * d.dv + n, f32x4{0.f, 0.f, 0.f, 0.f});

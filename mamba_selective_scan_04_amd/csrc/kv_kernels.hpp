@@ -322,6 +322,14 @@ __global__ __launch_bounds__(256, kTiles == 2 && kD == 128 ? 2 : 3) void kv_attn
 #pragma unroll
             for (int s = 0; s < kD / 32; ++s) st.Q[s][nt] = load_straight(qp + s / 2 * 64 + grp * 16 + (s & 1) * 8);
         }
+        // used here, so that no wait for them stays in the loop below (where it
+        // would be one for the codes under way)
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+            for (int s = 0; s < kD / 32; ++s)
+#pragma unroll
+                for (int p = 0; p < kIn; ++p) asm volatile("" : "+v"(st.Q[s][nt].p[p]));
         const int32_t *table = d.table + (int64_t)b * d.max_pages;
         const int shift = 31 - __builtin_clz(d.page_len);
         // A step's two halves of 16 keys: their pages (-1: none) and scales.

@@ -25,9 +25,28 @@ import ctypes
 
 import torch
 
-from .bdssm import _check, _dtype_code, _p, _raise, _stream, _workspace, load
+from .bdssm import _check, _dtype_code, _raise, _workspace, load
 
 DELTA_CHUNK = 64        # BDSSM_DELTA_CHUNK
+
+
+def _p(t):
+    # an int: ctypes takes it for a pointer argument, and makes no object of it
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev, *tensors):
+    """The current stream of device `dev`, which must be the current device and
+    that of every tensor: the library launches on the current device, and a
+    pointer of another one would fault there."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors must be on the current device (cuda:%d), got cuda:%d"
+                         % (torch._C._cuda_getDevice(), dev))
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on cuda:%d (got cuda:%d)" % (dev, t.get_device()))
+    # the raw handle: making a torch.cuda.Stream of it costs 3 us a call
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 class DeltaShape(ctypes.Structure):
@@ -87,12 +106,13 @@ def delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True
     if want_chunks and h_chunks is None:
         h_chunks = torch.empty(_chunk_states(s, T), dtype=torch.float32, device=dev)
     _check(h_chunks, "h_chunks", torch.float32, _chunk_states(s, T))
+    stream = _stream(k.get_device(), q, v, g, beta, lens, h_init, o, h_final, h_chunks, ws)
     if ws is None:
         n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 0)
         ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)   # a bad shape: the call says so
     rc = load().bdssm_delta_scan(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
                                  _p(h_init), _p(o), _p(h_final), _p(h_chunks), _p(ws),
-                                 0 if ws is None else ws.numel(), _stream())
+                                 0 if ws is None else ws.numel(), stream)
     _raise("bdssm_delta_scan", rc)
     return o, h_final, h_chunks
 
@@ -109,6 +129,7 @@ def delta_scan_bwd(q, k, v, g, beta, h_chunks, do, scale=None, lens=None, dh_fin
     _check(h_chunks, "h_chunks", torch.float32, _chunk_states(s, T))
     _check(do, "do", k.dtype, tuple(v.shape))
     _check(dh_final, "dh_final", torch.float32, _state(s))
+    stream = _stream(k.get_device(), q, v, g, beta, lens, h_chunks, do, dh_final, ws)
     dq, dk, dv, dg, dbeta = (torch.empty_like(x) for x in (q, k, v, g, beta))
     dh = torch.empty(_state(s), dtype=torch.float32, device=dev) if want_dh_init else None
     if ws is None:
@@ -116,7 +137,7 @@ def delta_scan_bwd(q, k, v, g, beta, h_chunks, do, scale=None, lens=None, dh_fin
         ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)
     rc = load().bdssm_delta_scan_bwd(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
                                      _p(h_chunks), _p(do), _p(dh_final), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta),
-                                     _p(dh), _p(ws), 0 if ws is None else ws.numel(), _stream())
+                                     _p(dh), _p(ws), 0 if ws is None else ws.numel(), stream)
     _raise("bdssm_delta_scan_bwd", rc)
     return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dh_init": dh}
 
@@ -134,8 +155,9 @@ def delta_step(h_cache, q, k, v, g, beta, scale=None, lens=None, h_out=None, wan
     if want_o and o is None:
         o = torch.empty_like(v)
     _check(o, "o", k.dtype, tuple(v.shape))
+    stream = _stream(k.get_device(), h_cache, q, v, g, beta, lens, o, h_out)
     rc = load().bdssm_delta_step(ctypes.byref(s), T, _p(h_cache), _p(q), _p(k), _p(v), _p(g), _p(beta), scale,
-                                 _p(lens), _p(o), _p(h_out), _stream())
+                                 _p(lens), _p(o), _p(h_out), stream)
     _raise("bdssm_delta_step", rc)
     return o
 
@@ -191,8 +213,9 @@ def kv_commit(cache, k, v, page_table, ctx_lens, lens=None):
     """The rows' whole blocks of k, v into the pages behind ctx_lens, in place.
     Tokens behind a row's last whole block are not cached."""
     s, L = _kv(cache, k, v, page_table, ctx_lens, lens, 0)
+    stream = _stream(k.get_device(), v, page_table, ctx_lens, lens, *cache)
     rc = load().bdssm_kv_commit(ctypes.byref(s), L, _p(k), _p(v), _p(page_table), _p(ctx_lens), _p(lens), _p(cache.k),
-                                _p(cache.k_scale), _p(cache.v), _p(cache.v_scale), _stream())
+                                _p(cache.k_scale), _p(cache.v), _p(cache.v_scale), stream)
     _raise("bdssm_kv_commit", rc)
 
 
@@ -208,12 +231,13 @@ def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, 
     if o is None:
         o = torch.empty_like(q)
     _check(o, "o", k.dtype, tuple(q.shape))
+    stream = _stream(k.get_device(), q, v, page_table, ctx_lens, lens, o, ws, *cache)
     if ws is None:
         n = load().bdssm_kv_workspace_bytes(ctypes.byref(s), Lq)
         ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, k.device)   # a bad shape: the call says so
     rc = load().bdssm_kv_attn_step(ctypes.byref(s), L, Lq, _p(q), _p(k), _p(v), _p(cache.k), _p(cache.k_scale),
                                    _p(cache.v), _p(cache.v_scale), _p(page_table), _p(ctx_lens), _p(lens),
                                    1 if causal else 0, float(s.head_dim ** -0.5 if scale is None else scale), _p(o),
-                                   _p(ws), 0 if ws is None else ws.numel(), _stream())
+                                   _p(ws), 0 if ws is None else ws.numel(), stream)
     _raise("bdssm_kv_attn_step", rc)
     return o
