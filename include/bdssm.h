@@ -406,7 +406,8 @@ int bdssm_version(void);
  *           not touch the state, and o and every gradient are 0 there.
  * Keys are expected with beta_t |k_t|^2 <= 2 (normalised keys), without which
  * the recurrence itself diverges.
- * Limits: d_k and d_v 64 or 128; heads_v a multiple of heads_k, at most 65535.
+ * Limits: d_k and d_v 64 or 128; heads_v a multiple of heads_k, at most 65535;
+ * batch * heads_v < 2^22; T < 2^29.
  */
 typedef struct {
     int64_t batch;     /* >= 0, at most 65535 */
@@ -487,7 +488,8 @@ size_t bdssm_delta_workspace_bytes(const bdssm_delta_shape *shape, int64_t T, in
  *           more than max_pages * page_len count as that many).
  * Rows may share pages that they only read.
  * Limits: head_dim 64 or 128; page_len 16, 32, 64 or 128; heads_q a multiple of
- * heads_kv; batch at most 32767.
+ * heads_kv; batch and heads at most 32767; a row's positions and a call's
+ * workgroups (2^24) must be countable.
  */
 typedef enum {
     BDSSM_E4M3 = 0,   /* 8-bit float (4 exponent, 3 mantissa bits, largest 448) */
@@ -511,7 +513,8 @@ typedef struct {
  * blocks of k, v [batch, T, heads_kv, head_dim] become the pages from position
  * floor(ctx_lens[b] / page_len) of its table row on.  Tokens behind the last
  * whole block are left to the caller (they stay active tokens of
- * bdssm_kv_attn_step); pages and scales not named are left as they are.  lens
+ * bdssm_kv_attn_step); pages and scales not named are left as they are, and
+ * blocks that fall behind the row's max_pages entries are dropped.  lens
  * NULL: T for every row.  ctx_lens is read, not advanced.  The pages written by
  * one call must differ (else their content is one of the writers' or a mix).
  * scale = max(a r, 2^-126) with a the largest finite magnitude of the block and
@@ -537,7 +540,8 @@ int bdssm_kv_commit(const bdssm_kv_shape *shape, int64_t T, const void *k, const
  *         (a denoising step).  Else active token j only where j is not behind
  *         the query's own.
  *   scale multiplies the scores.  No mask but these; cached positions from
- *         ctx_lens[b] on are not seen, whatever their codes.
+ *         ctx_lens[b] on are not seen, whatever their codes, nor are active
+ *         tokens that a query does not see, infinities and NaN included.
  *   ws    ws_bytes >= bdssm_kv_workspace_bytes(shape, Lq).  Need not be cleared.
  */
 int bdssm_kv_attn_step(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, const void *q,

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int64_t kDeltaTarget = 448;         // workgroups of a chain that fill the chip, near two a CU
 constexpr int64_t kMost = (int64_t)1 << 40;   // elements of one tensor
+constexpr int64_t kMostGroups = 0xffffff;     // workgroups along a grid's axis: its 256 threads each are counted in 32 bits
 
 bool product_fits(std::initializer_list<int64_t> f) {
     int64_t n = 1;
@@ -55,10 +56,9 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
         return BDSSM_ERR_SHAPE;
     if (s->heads_v % s->heads_k != 0) return BDSSM_ERR_SHAPE;
     if ((s->d_k != 64 && s->d_k != 128) || (s->d_v != 64 && s->d_v != 128)) return BDSSM_ERR_SHAPE;
-    // a chain's workgroups are counted in 31 bits, segments included
-    if (s->batch * s->heads_v > ((int64_t)1 << 24)) return BDSSM_ERR_SHAPE;
-    // 2^31 - 1 chunks at most in a launch, and every tensor's elements countable
-    if (T > kMost || (T + 63) / 64 >= ((int64_t)1 << 31)) return BDSSM_ERR_SHAPE;
+    // up to 4 workgroups a chain, and of 512 threads a chunk, in a grid's axis; every
+    // tensor's elements countable
+    if (s->batch * s->heads_v > kMostGroups / 4 || T > kMost || (T + 63) / 64 > kMostGroups / 2) return BDSSM_ERR_SHAPE;
     if (!product_fits({s->batch, (T + 63) / 64, s->heads_v, s->d_k, s->d_v})) return BDSSM_ERR_SHAPE;
     return BDSSM_OK;
 }
@@ -77,7 +77,7 @@ int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
     const char *e = getenv("BDSSM_DELTA_SEGMENTS");
     if (e != nullptr && *e != 0) n = atoi(e);
     if (n > chunks) n = chunks;
-    if (n * s->batch > 65535) n = 65535 / (s->batch > 0 ? s->batch : 1);
+    if (n * s->batch * s->heads_v > kMostGroups / 4) n = kMostGroups / 4 / (s->batch * s->heads_v);
     return n < 1 ? 1 : (int)n;
 }
 
@@ -335,6 +335,9 @@ int bdssm_kv_commit(const bdssm_kv_shape *s, int64_t T, const void *k, const voi
     if (s->batch == 0 || T < s->page_len || s->n_pages == 0 || s->max_pages == 0) return BDSSM_OK;
     if (!k || !v || !page_table || !ctx_lens || !k_cache || !k_scale || !v_cache || !v_scale) return BDSSM_ERR_NULL;
     if (!all_aligned({k, v, page_table, ctx_lens, lens, k_cache, k_scale, v_cache, v_scale})) return BDSSM_ERR_ALIGN;
+    if (!product_fits({s->batch, T / s->page_len, s->heads_kv}) ||
+        s->batch * (T / s->page_len) * s->heads_kv > kMostGroups / 2)
+        return BDSSM_ERR_SHAPE;
     const KvSizes z = kv_sizes(s, T, 0);
     if (!distinct({{k, z.kv}, {v, z.kv}, {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row}},
                   {{k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale}}))
@@ -370,9 +373,8 @@ int bdssm_kv_attn_step(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const voi
     if (!all_aligned({q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, o, ws})) return BDSSM_ERR_ALIGN;
     const KvSizes z = kv_sizes(s, L, Lq);
     const KvPlan plan = kv_plan(s, Lq);
-    // workgroups are counted in 31 bits
     if (!product_fits({s->batch, s->heads_kv, plan.splits, plan.qtiles}) ||
-        s->batch * s->heads_kv * plan.splits * plan.qtiles > 0x70000000 || Lq * kv_group(s) > 0x7fffffff)
+        s->batch * s->heads_kv * plan.splits * plan.qtiles > kMostGroups - 8 * plan.qtiles || Lq * kv_group(s) > kMostGroups)
         return BDSSM_ERR_SHAPE;
     size_t part = 0;
     const size_t need = kv_workspace(s, plan, &part);

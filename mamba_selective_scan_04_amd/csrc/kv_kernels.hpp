@@ -25,97 +25,166 @@ struct KvDims {
     const int32_t *lens;    // [batch] active tokens, or null
 };
 
-// two fp32 values in the code's range -> two codes in the low or high half
+// four values in the code's range -> their codes
 template <int kCode>
 __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
     if constexpr (kCode == kE4m3) {
         int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     } else {
-        const auto q = [](float x) { return (uint32_t)(int)rintf(x) & 255u; };   // NaN: 0
-        return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+        // 1.5 * 2^23 more, the sum's rounding is to whole numbers (ties to even) and
+        // its lowest byte the number's
+        const auto q = [](float x) { return as_u(x + 0x1.8p23f); };
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(q(d), q(c), 0x0c0c0400u), __builtin_amdgcn_perm(q(b), q(a), 0x0c0c0400u),
+                                     0x05040100u);
     }
 }
 
 // ------------------------------------------------------------------ commit
 //
-// One workgroup per (block of the call, head, row and tensor): the block's
-// [page_len, d] values of one head in registers, their largest magnitude, then
-// the codes.  Bound by memory: 2 or 4 bytes in, 1 out a value.
+// A unit is one head of one block of the call, of k or of v: its [page_len, d]
+// values in registers, their largest magnitude, then the codes.  One wave takes a
+// unit of up to 2,048 values, four waves a larger one; neighbouring waves take
+// neighbouring heads.  Bound by memory: 2 or 4 bytes in, 1 out a value, if the
+// arithmetic is kept short: 65,536 tokens of 4 heads of 128 in bf16, pages of 16,
+// 32 us (6.2 TB/s read and written); with a workgroup to each unit and a plain
+// division to each value it was 57.
+//
+// The quotient value / scale is the correctly rounded one at five operations a
+// value, from r = 1 / scale correctly rounded once a unit: x r, then twice
+// q += r (x - q scale) with the remainder exact.  The second makes a faithful q
+// the correctly rounded one (Markstein, Computation of elementary functions on
+// the IBM RISC System/6000 processor, 1990).  The remainder is exact while
+// scale >= 2^-90 (x of less than scale / 2^11 is code 0 however it is rounded);
+// other scales, and units with infinities or NaN, take plain divisions.
 template <typename T>
 struct CommitArgs {
     const T *k, *v;
     uint8_t *kc, *vc;
     float *ks, *vs;
     int64_t T_tokens;
+    uint32_t blocks, jobs;   // whole blocks of T_tokens; units
     KvDims d;
 };
 
-template <typename T, int kCode, int kD, int kPerThread>
+// 8 stream values as they lie in memory
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+    uint4 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *(const uint4 *)p; }
+    __device__ __forceinline__ void values(float *x) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf_lo(u[j]);
+            x[2 * j + 1] = bf_hi(u[j]);
+        }
+    }
+    // the fp32 bits of the largest magnitude (those of infinities and NaN are larger than any value's)
+    __device__ __forceinline__ uint32_t top() const {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        const auto mag = [](uint32_t u) { return __builtin_bit_cast(u16x2, u & 0x7fff7fffu); };
+        const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(w.x), mag(w.y)),
+                                                  __builtin_elementwise_max(mag(w.z), mag(w.w)));
+        return (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
+    }
+};
+template <>
+struct Eight<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *(const f32x4 *)p;
+        b = *(const f32x4 *)(p + 4);
+    }
+    __device__ __forceinline__ void values(float *x) const {
+        *(f32x4 *)x = a;
+        *(f32x4 *)(x + 4) = b;
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = as_u(a[j]) & 0x7fffffffu, y = as_u(b[j]) & 0x7fffffffu;
+            m = max(m, max(x, y));
+        }
+        return m;
+    }
+};
+
+// kWaves waves a unit, kPer values a lane
+template <typename T, int kCode, int kD, int kPer, int kWaves>
 __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
     constexpr float kMax = kCode == kE4m3 ? 448.f : 127.f;
-    constexpr int kBytes = kD + 4;                       // LDS row of codes
-    __shared__ float part[4];
-    __shared__ __attribute__((aligned(16))) uint8_t codes[kPerThread * 256 / kD * kBytes];
+    constexpr int kThreads = kWaves * 64, kTotal = kPer * kThreads, kPage = kTotal / kD, kBytes = kD + 4;   // LDS row of codes
+    constexpr int kVecs = kPer / 8;
+    __shared__ uint32_t part[2][4];
+    __shared__ __attribute__((aligned(16))) uint8_t room[4 / kWaves][kPage * kBytes];
     const KvDims &d = a.d;
-    const bool is_v = blockIdx.z & 1;
-    const int b = blockIdx.z >> 1, h = blockIdx.y, page = d.page_len;
-    const int64_t blk = blockIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tid = threadIdx.x % kThreads;
+    const uint32_t job = blockIdx.x * (4 / kWaves) + wave / kWaves;
+    if (job >= a.jobs) return;
+    const int h = job % d.heads_kv;
+    const bool is_v = job / d.heads_kv & 1;
+    const uint32_t at_blk = job / d.heads_kv / 2, blk = at_blk % a.blocks, b = at_blk / a.blocks;
     int64_t n = a.T_tokens;
     if (d.lens != nullptr) n = d.lens[b] < n ? d.lens[b] : n;
-    if ((blk + 1) * page > n) return;                    // a block that is not whole
-    const int64_t at = (int64_t)(d.ctx[b] < 0 ? 0 : d.ctx[b]) / page + blk;
+    if ((int64_t)(blk + 1) * kPage > n) return;          // a block that is not whole
+    const int64_t at = (int64_t)(d.ctx[b] < 0 ? 0 : d.ctx[b]) / kPage + blk;
     if (at >= d.max_pages) return;
     const int id = d.table[(int64_t)b * d.max_pages + at];
     if (id < 0 || id >= d.n_pages) return;
-    const T *src = (is_v ? a.v : a.k) + (((int64_t)b * a.T_tokens + blk * page) * d.heads_kv + h) * kD;
-    constexpr int kVecs = (kPerThread + 7) / 8;
-    float x[kVecs][8];
-    float top = 0.f;
-    const int total = page * kD;
+    const T *src = (is_v ? a.v : a.k) + (((int64_t)b * a.T_tokens + (int64_t)blk * kPage) * d.heads_kv + h) * kD;
+    Eight<T> x[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        const int e = (threadIdx.x + i * 256) * 8;
-        if (e < total) {
-            const T *p = src + (int64_t)(e / kD) * d.heads_kv * kD + e % kD;
-            if constexpr (sizeof(T) == 2) {
-                const uint4 w = *(const uint4 *)p;
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const int e = (tid + i * kThreads) * 8;
+        x[i].load(src + (int64_t)(e / kD) * d.heads_kv * kD + e % kD);
+    }
+    // the largest of the unit's threads' values
+    const auto largest = [&](uint32_t m, uint32_t (&to)[4]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][2 * j] = bf_lo(u[j]);
-                    x[i][2 * j + 1] = bf_hi(u[j]);
-                }
-            } else {
-                *(f32x4 *)&x[i][0] = *(const f32x4 *)p;
-                *(f32x4 *)&x[i][4] = *(const f32x4 *)(p + 4);
-            }
+        for (int s = 1; s < 64; s <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, 64));
+        if constexpr (kWaves == 4) {
+            if ((threadIdx.x & 63) == 0) to[wave] = m;
+            __syncthreads();
+            m = max(max(to[0], to[1]), max(to[2], to[3]));
+        }
+        return (uint32_t)__builtin_amdgcn_readfirstlane(m);
+    };
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) top = max(top, x[i].top());
+    top = largest(top, part[0]);
+    const bool special = top >= 0x7f800000u;
+    if (special) {   // of the finite ones then
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float y[8];
+            x[i].values(y);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float m = fabsf(x[i][j]);
-                top = m < __builtin_inff() ? fmaxf(top, m) : top;   // the finite ones
+                const uint32_t u = as_u(y[j]) & 0x7fffffffu;
+                m = u < 0x7f800000u ? max(m, u) : m;
             }
         }
+        top = largest(m, part[1]);
     }
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const float scale = fmaxf(top * (1.f / kMax), 0x1p-126f);
+    const float scale = fmaxf(as_f(top) * (1.f / kMax), 0x1p-126f);
     const int64_t unit = (int64_t)id * d.heads_kv + h;
-    if (threadIdx.x == 0) (is_v ? a.vs : a.ks)[unit] = scale;
-    uint8_t *out = (is_v ? a.vc : a.kc) + unit * total;
+    if (tid == 0) (is_v ? a.vs : a.ks)[unit] = scale;
+    uint8_t *out = (is_v ? a.vc : a.kc) + unit * kTotal;
+    uint8_t *codes = room[wave / kWaves];
+    const auto write = [&](auto &&quotient) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int e = (threadIdx.x + i * 256) * 8;
-        if (e < total) {
+        for (int i = 0; i < kVecs; ++i) {
+            const int e = (tid + i * kThreads) * 8;
             float y[8];
+            x[i].values(y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float z = x[i][j] / scale;
-                y[j] = z != z ? z : fminf(fmaxf(z, -kMax), kMax);
-            }
+            for (int j = 0; j < 8; ++j) y[j] = quotient(y[j]);
             const uint2 w = make_uint2(to_codes<kCode>(y[0], y[1], y[2], y[3]), to_codes<kCode>(y[4], y[5], y[6], y[7]));
             if (is_v) {
                 *(uint32_t *)(codes + e / kD * kBytes + e % kD) = w.x;
@@ -124,11 +193,31 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
                 *(uint2 *)(out + e) = w;
             }
         }
+    };
+    if (special || scale < 0x1p-90f) {
+        write([&](float v) {
+            const float z = v / scale;
+            if (z != z) return kCode == kE4m3 ? z : 0.f;
+            return fminf(fmaxf(z, -kMax), kMax);
+        });
+    } else {
+        const float r = 1.f / scale;
+        write([&](float v) {
+            float q = v * r;
+            q = fmaf(fmaf(-q, scale, v), r, q);
+            return fmaf(fmaf(-q, scale, v), r, q);   // rounding makes it kMax at most
+        });
     }
     if (!is_v) return;
-    __syncthreads();
+    if constexpr (kWaves == 4) {
+        __syncthreads();
+    } else {   // a wave's LDS operations are done in order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
     // by channel: 16 tokens of one channel a thread
-    for (int e = threadIdx.x; e < total / 16; e += 256) {
+#pragma unroll
+    for (int e = tid; e < kTotal / 16; e += kThreads) {
         const int c = e % kD, t0 = e / kD * 16;
         uint32_t w[4];
 #pragma unroll
@@ -136,7 +225,7 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
             const uint8_t *p = codes + (t0 + 4 * j) * kBytes + c;
             w[j] = p[0] | (uint32_t)p[kBytes] << 8 | (uint32_t)p[2 * kBytes] << 16 | (uint32_t)p[3 * kBytes] << 24;
         }
-        *(uint4 *)(out + c * page + t0) = make_uint4(w[0], w[1], w[2], w[3]);
+        *(uint4 *)(out + c * kPage + t0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -482,11 +571,26 @@ __global__ __launch_bounds__(256, kTiles == 2 && kD == 128 ? 2 : 3) void kv_attn
                         }
                 }
                 T vals[kChan][8];
+                bool odd = false;   // infinities or NaN that not all of the queries see
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const T *row = vb + (key0 + j < n ? key0 + j : n - 1) * stride + col;
 #pragma unroll
                     for (int mt = 0; mt < kChan; ++mt) vals[mt][j] = row[mt * 16];
+                }
+                if (a.causal) {
+#pragma unroll
+                    for (int mt = 0; mt < kChan; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) odd |= !(fabsf(Stream<T>::load(&vals[mt][j])) < __builtin_inff());
+                    odd = __any(odd);
+                    if (odd) {   // 0 in the product (a probability of 0 times them is a NaN)
+#pragma unroll
+                        for (int mt = 0; mt < kChan; ++mt)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (!(fabsf(Stream<T>::load(&vals[mt][j])) < __builtin_inff())) vals[mt][j] = T(0);
+                    }
                 }
                 st.step(S, 1.f, [&](int mt) {
                     f32x4 x[2];
@@ -494,6 +598,21 @@ __global__ __launch_bounds__(256, kTiles == 2 && kD == 128 ? 2 : 3) void kv_attn
                     for (int j = 0; j < 8; ++j) x[j / 4][j % 4] = Stream<T>::load(&vals[mt][j]);
                     return split_frag<kIn>(x[0], x[1]);
                 });
+                // the queries that see them get them as they are
+#pragma unroll 1
+                for (int j = 0; odd && j < 32 && s * 32 + j < n; ++j) {
+                    const T *row = vb + (s * 32 + j) * stride + grp * 4;
+#pragma unroll
+                    for (int mt = 0; mt < kChan; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            asm volatile("" ::: "memory");   // one at a time: registers before speed here
+                            const float y = Stream<T>::load(row + mt * 16 + r);
+#pragma unroll
+                            for (int nt = 0; nt < kTiles; ++nt)
+                                if (!(fabsf(y) < __builtin_inff()) && s * 32 + j <= pos[nt]) st.O[mt][nt][r] += y;
+                        }
+                }
             }
         }
     }

@@ -10,13 +10,16 @@ namespace bdssm_host {
 
 template <typename T, int kCode, int kD>
 void commit_k(const KvCall &c, hipStream_t st) {
-    const CommitArgs<T> a{(const T *)c.k, (const T *)c.v, (uint8_t *)c.kc, (uint8_t *)c.vc, c.ks, c.vs, c.L, c.d};
-    const dim3 g((unsigned)(c.L / c.d.page_len), (unsigned)c.d.heads_kv, (unsigned)(c.batch * 2));
-    switch (c.d.page_len * kD / 256) {
-    case 4: case 8: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 8>), g, dim3(256), 0, st, a); break;
-    case 16: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 16>), g, dim3(256), 0, st, a); break;
-    case 32: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 32>), g, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 64>), g, dim3(256), 0, st, a); break;
+    const int64_t blocks = c.L / c.d.page_len, jobs = c.batch * blocks * c.d.heads_kv * 2;
+    const CommitArgs<T> a{(const T *)c.k, (const T *)c.v, (uint8_t *)c.kc, (uint8_t *)c.vc, c.ks, c.vs, c.L,
+                          (uint32_t)blocks, (uint32_t)jobs, c.d};
+    const dim3 one((unsigned)((jobs + 3) / 4)), four((unsigned)jobs);
+    switch (c.d.page_len * kD) {
+    case 1024: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 16, 1>), one, dim3(256), 0, st, a); break;
+    case 2048: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 32, 1>), one, dim3(256), 0, st, a); break;
+    case 4096: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 16, 4>), four, dim3(256), 0, st, a); break;
+    case 8192: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 32, 4>), four, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((kv_commit_kernel<T, kCode, kD, 64, 4>), four, dim3(256), 0, st, a); break;
     }
 }
 
