@@ -169,14 +169,16 @@ KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
 
 // A wave's query tiles: two where there are more than 16 rows (64 accumulators at
 // 128 channels; four tiles' 128 made the compiler spill, and ran at half the
-// speed).  Key ranges: until every CU has its workgroups of four waves, but at
+// speed), but one for fp32 streams of 128 channels, whose queries take three times
+// the registers (4 rows of 65,536 tokens and 64 queries: 146 us, 190 with two
+// tiles, which spill).  Key ranges: until every CU has its workgroups of four waves, but at
 // least one step of 32 keys for each wave of a range; beyond that up to three
 // times as many, of at least 2,048 keys, so that rows of different lengths (which
 // only the GPU knows) even out.
 KvPlan kv_plan(const bdssm_kv_shape *s, int64_t Lq) {
     const int64_t rows = Lq * kv_group(s);
     KvPlan p;
-    p.tiles = rows > 16 ? 2 : 1;
+    p.tiles = rows > 16 && !(s->dtype == BDSSM_F32 && s->head_dim == 128) ? 2 : 1;
     const int64_t qtiles = (rows + p.tiles * 16 - 1) / (p.tiles * 16);
     const int64_t units = s->batch * s->heads_kv * qtiles;
     const int64_t fill = 512;   // resident at once

@@ -357,7 +357,7 @@ __device__ __forceinline__ T uniform_load(const T *p) {
 }
 
 template <typename T, int kCode, int kD, int kTiles>
-__global__ __launch_bounds__(256, kTiles == 2 && kD == 128 ? 2 : 3) void kv_attn_kernel(AttnArgs<T> a) {
+__global__ __launch_bounds__(256, kTiles == 2 && (kD == 128 || sizeof(T) == 4) ? 2 : 3) void kv_attn_kernel(AttnArgs<T> a) {
     constexpr int kIn = Stream<T>::kParts, kRows = kTiles * 16, kChan = kD / 16, kORow = kD + 4;
     const KvDims &d = a.d;
     // the query tiles of one range of keys on one XCD, as the chains' column

@@ -29,8 +29,12 @@ void attn_k(const KvCall &c, hipStream_t st) {
                         (T *)c.o, c.part_o, c.part_ml, c.L, c.Lq, c.plan.splits, c.plan.qtiles, c.causal,
                         c.scale * 1.44269504088896341f, c.batch * c.d.heads_kv * c.plan.splits, c.d};
     const dim3 g((unsigned)((a.jobs + 7) / 8 * 8 * c.plan.qtiles));
-    if (c.plan.tiles == 1) hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 2>), g, dim3(256), 0, st, a);
+    bool two = false;
+    if constexpr (sizeof(T) == 2 || kD == 64) {   // as kv_plan has it
+        two = c.plan.tiles == 2;
+        if (two) hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 2>), g, dim3(256), 0, st, a);
+    }
+    if (!two) hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a);
     if (c.plan.splits > 1) {
         hipLaunchKernelGGL((kv_join_kernel<T, kD>), dim3((unsigned)(c.Lq * c.d.group), (unsigned)c.d.heads_kv, (unsigned)c.batch),
                            dim3(kD * 2), 0, st, c.part_o, c.part_ml, (T *)c.o, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
