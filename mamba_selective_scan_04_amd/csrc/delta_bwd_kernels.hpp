@@ -452,7 +452,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 sdb[r] = y * z;
                 l.U.put(t, n, u);
                 l.X.put(t, n, x);
-                if (t < m) Stream<T>::store(dvp + t * vstride + n, x);
+                if (t < m) Stream<T>::store(dvp + t * vstride + n, ib == 0x1p64f ? 0.f : x);   // beta 0: as `strength` has it
             }
             // four sums over 16 lanes together: halve the values as the lanes
 #pragma unroll
