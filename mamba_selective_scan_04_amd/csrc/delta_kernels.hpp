@@ -495,6 +495,7 @@ struct ChainArgs {
     float *h_chunks;      // null, or [batch, chunks, hv, dv, dk]
     float *agg;           // kAggregate: [batch, hv, segs, dk, dv + dk]
     int segs, per;        // segments, and chunks of each
+    int wanted;           // kAggregate: the segments whose maps are used
     int groups;           // batch * segs * hv
     DeltaDims d;
 };
@@ -649,6 +650,7 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
     s.hv = at.group % d.hv;
     s.b = at.group / d.hv / a.segs;
     const int seg = at.group / d.hv % a.segs, hk = s.hv / d.group;
+    if (kMode == kAggregate && seg >= a.wanted) return;
     s.lane = lane_id();
     s.wave = threadIdx.x >> 6;
     s.col = s.lane & 15;

@@ -16,7 +16,7 @@ using namespace bdssm_host;
 
 namespace {
 
-constexpr int64_t kDeltaTarget = 448;         // workgroups of a chain that fill the chip, near two a CU
+constexpr int64_t kCus = 256;
 constexpr int64_t kMost = (int64_t)1 << 40;   // elements of one tensor
 constexpr int64_t kMostGroups = 0xffffff;     // workgroups along a grid's axis: its 256 threads each are counted in 32 bits
 
@@ -66,12 +66,16 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 // Segments of a row's chunks (1: none).  A chain's step is a chunk's, whatever
 // the batch; cutting the row costs the aggregate pass over d_v + d_k columns
 // besides the chain's own d_v, so it pays from about four segments on, each of
-// 8 chunks at least.  65,536 tokens of 12 heads (24 groups): 4.7 ms whole, 1.14
-// ms in 10 segments, 1.06 in 16, 1.15 in 40; 192 groups of 64 chunks: 2% slower
-// in two segments than whole.  BDSSM_DELTA_SEGMENTS forces a count (tests).
+// 8 chunks at least.  As many as the aggregate pass runs at once (three workgroups
+// of 64 columns a CU, two for fp32 streams): one more round of them costs more
+// than shorter segments give.  65,536 tokens of 12 heads of 128 in bf16: 4.7 ms
+// whole, 1.04 in 10 segments, 0.97 in 16 (the rule's), 1.00 in 18, 1.10 in 24; of 4
+// heads in fp32: 0.85 in 32 (the rule's), 1.00 in 48, 1.11 in 72.  192 groups of
+// 64 chunks: 2% slower in two segments than whole.  BDSSM_DELTA_SEGMENTS forces a
+// count (tests).
 int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
-    const int64_t groups = s->batch * s->heads_v * (s->d_v / 64);
-    int64_t n = groups > 0 ? kDeltaTarget / groups : 1;
+    const int64_t blocks = s->batch * s->heads_v * ((s->d_v + s->d_k) / 64);
+    int64_t n = blocks > 0 ? kCus * (s->dtype == BDSSM_BF16 ? 3 : 2) / blocks : 1;
     if (n > chunks / 8) n = chunks / 8;
     if (n < 4) n = 1;
     const char *e = getenv("BDSSM_DELTA_SEGMENTS");

@@ -17,15 +17,16 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
                            c.o != nullptr ? (const T *)c.q : (const T *)nullptr, (const T *)c.k, c.g, c.beta, (Mats<kOut> *)c.mats,
                            (double *)nullptr, c.d);
     ChainArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const Mats<kOut> *)c.mats, c.h_init, (T *)c.o, c.h_final, c.h_chunks,
-                   c.agg, 1, c.d.chunks, (int)(c.batch * c.d.hv), c.d};
+                   c.agg, 1, c.d.chunks, 0, (int)(c.batch * c.d.hv), c.d};
     const auto grid = [&](int columns) { return dim3((unsigned)((a.groups + 7) / 8 * 8 * (columns / 64))); };
     if (c.segs > 1) {
         a.segs = c.segs;
         a.per = (c.d.chunks + c.segs - 1) / c.segs;
         a.groups *= c.segs;
+        const bool chain = c.o != nullptr || c.h_chunks != nullptr;
+        a.wanted = c.segs - (chain ? 1 : 0);   // the state behind the last comes from the chain
         hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
         // states alone: the join has the last
-        const bool chain = c.o != nullptr || c.h_chunks != nullptr;
         const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv};
         hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
         if (!chain) return;
