@@ -6,7 +6,9 @@
 //   X  = W^T dU            (= dR = dV)
 //   dS = exp(G_C) dS' + scale Q^T E dO - K^T E X
 // is a chain over the chunks from the last, with independent columns as in the
-// forward: delta_adjoint_kernel writes dS' of every chunk.  All else follows per
+// forward: delta_adjoint_kernel writes dS' of every chunk, over a long row of few
+// heads in segments that run at once, as in the forward: dS = M dS' + N over a
+// segment, its maps by the same kernel (kAggregate).  All else follows per
 // chunk from S, dS' (delta_grad_kernel).  With y = U / beta, Z = X / beta (the
 // rows' prediction errors and their adjoints' sources):
 //   dV = X,  dbeta_i = y_i.Z_i
@@ -32,7 +34,10 @@ struct AdjointArgs {
     const float *dh_final;            // null: zero
     float *dS;                        // [batch, chunks, hv, dv, dk]: dS' of each chunk
     float *dh_init;                   // null: not wanted
-    int groups;                       // batch * hv
+    float *agg;                       // kAggregate: [batch, hv, segs, dk, dv + dk]
+    const float *h_seg;               // null, or [batch, hv, segs, dk, dv]: dS' behind each segment
+    int segs, per;                    // segments, and chunks of each
+    int groups;                       // batch * segs * hv
     DeltaDims d;
 };
 
@@ -43,7 +48,7 @@ struct AdjointStage {
     Mats<3> m;
 };
 
-template <typename T, int kDk>
+template <typename T, int kDk, bool kAgg>
 struct Adjoint {
     static constexpr int kTiles = kDk / 16, kSteps = kDk / 32, kIn = Stream<T>::kParts;
     using Stage = AdjointStage<T, kDk>;
@@ -52,6 +57,7 @@ struct Adjoint {
     const T *kp, *qp, *op;
     int64_t kstride, vstride, len;
     int hv, b, wave, col, grp, n;
+    bool has_o;   // kAgg: not the identity's columns
 
     __device__ __forceinline__ int tokens(int c) const {
         const int64_t left = len - (int64_t)c * kChunk;
@@ -63,8 +69,10 @@ struct Adjoint {
     __device__ __forceinline__ void fill(Stage &l, int c) {
         const int64_t t0 = (int64_t)c * kChunk;
         l.k.template fill<4>(kp + t0 * kstride, koff);
-        l.q.template fill<4>(qp + t0 * kstride, koff);
-        l.o.template fill<4>(op + t0 * vstride, voff);
+        if (!kAgg || has_o) {
+            l.q.template fill<4>(qp + t0 * kstride, koff);
+            l.o.template fill<4>(op + t0 * vstride, voff);
+        }
         fill_mats(a.mats + ((int64_t)b * a.d.hv + hv) * a.d.chunks + c, &l.m);
     }
     __device__ __forceinline__ void store_columns(float *out) {
@@ -72,12 +80,13 @@ struct Adjoint {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) *(f32x4 *)(out + state_row(t, 0, 0) + lane_off) = S[t];
     }
-    __device__ __forceinline__ void store_state(float *out) {
-        const uint32_t lane_off = (uint32_t)(grp * 8 * a.d.dv + n);
+    // rows `ld` apart
+    __device__ __forceinline__ void store_state(float *out, int ld) {
+        const uint32_t lane_off = (uint32_t)(grp * 8 * ld + n);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * a.d.dv)[lane_off] = S[t][r];
+            for (int r = 0; r < 4; ++r) (out + state_row(t, 0, r) * ld)[lane_off] = S[t][r];
     }
     __device__ __forceinline__ void step(const Stage &l, int c) {
         const int m = tokens(c);
@@ -96,7 +105,7 @@ struct Adjoint {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
-                dO[mt] = l.o.values(mt, grp, wave * 16, col);
+                if (!kAgg || has_o) dO[mt] = l.o.values(mt, grp, wave * 16, col);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     U[mt][r] *= rest[r];
@@ -104,7 +113,7 @@ struct Adjoint {
                 }
             }
         }
-        upper_product<3, false, kIn>(l.m.P, dO, U);
+        if (!kAgg || has_o) upper_product<3, false, kIn>(l.m.P, dO, U);
         f32x4 X[4];
         upper_product<3>(l.m.W, U, X);
         const float last = l.m.e[kChunk - 1];
@@ -114,74 +123,84 @@ struct Adjoint {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 X[mt][r] *= -e[r];
-                dO[mt][r] *= a.d.scale * e[r];
+                if (!kAgg || has_o) dO[mt][r] *= a.d.scale * e[r];
             }
         }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[t][r] *= last;
-        add_columns(l.q, dO, S);
+        if (!kAgg || has_o) add_columns(l.q, dO, S);
         add_columns(l.k, X, S);
     }
 };
 
-template <typename T, int kDk>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(AdjointArgs<T> a) {
-    using C = Adjoint<T, kDk>;
-    constexpr bool kTwo = sizeof(T) == 2;
+// kTwo as in the forward's chain
+template <typename T, int kDk, bool kAgg, bool kTwo>
+__global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void delta_adjoint_kernel(AdjointArgs<T> a) {
+    using C = Adjoint<T, kDk, kAgg>;
     __shared__ __attribute__((aligned(16))) typename C::Stage l0;
     __shared__ __attribute__((aligned(16))) typename std::conditional<kTwo, typename C::Stage, char>::type l1;
     const DeltaDims &d = a.d;
-    const ChainPlace at = chain_place(d.dv / 64);
+    const ChainPlace at = chain_place((d.dv + (kAgg ? kDk : 0)) / 64);
     if (at.group >= a.groups) return;
     C s{{}, a};
     s.hv = at.group % d.hv;
-    s.b = at.group / d.hv;
-    const int hk = s.hv / d.group, lane = lane_id();
+    s.b = at.group / d.hv / a.segs;
+    const int seg = at.group / d.hv % a.segs, hk = s.hv / d.group, lane = lane_id();
+    if (kAgg && seg == 0) return;   // nothing is in front of it
     s.wave = threadIdx.x >> 6;
     s.col = lane & 15;
     s.grp = lane >> 4;
     s.n = at.col * 64 + s.wave * 16 + s.col;
+    s.has_o = !kAgg || at.col * 64 < d.dv;
     s.len = row_len(d, s.b);
     s.kstride = (int64_t)d.hk * kDk;
     s.vstride = (int64_t)d.hv * d.dv;
     const int64_t tok = (int64_t)s.b * d.T;
     s.kp = a.k + (tok * d.hk + hk) * kDk;
     s.qp = a.q + (tok * d.hk + hk) * kDk;
-    s.op = a.dout + (tok * d.hv + s.hv) * d.dv + at.col * 64;
-    const int chunks = (int)((s.len + kChunk - 1) / kChunk);
+    s.op = a.dout + (tok * d.hv + s.hv) * d.dv + (s.has_o ? at.col * 64 : 0);
+    const int chunks = (int)((s.len + kChunk - 1) / kChunk);   // the row's, of all segments
+    const int c0 = seg * a.per, c1 = c0 + a.per < chunks ? c0 + a.per : chunks;
     const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
+    const float *first = a.h_seg != nullptr ? a.h_seg + (head * a.segs + seg) * state : a.dh_final + head * state;
+    const bool zero = a.h_seg == nullptr && a.dh_final == nullptr;
 #pragma unroll
     for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s.S[t][r] = a.dh_final == nullptr ? 0.f : a.dh_final[head * state + (int64_t)state_row(t, s.grp, r) * d.dv + s.n];
-    auto keep = [&](int c) { s.store_columns(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state); };
-    int c = chunks - 1;
-    s.koff.set(s.kstride, c >= 0 ? s.tokens(c) : kChunk);   // the last chunk's; the others are full
-    s.voff.set(s.vstride, c >= 0 ? s.tokens(c) : kChunk);
+        for (int r = 0; r < 4; ++r) {
+            const int row = state_row(t, s.grp, r);
+            if (kAgg) s.S[t][r] = s.n - d.dv == row ? 1.f : 0.f;
+            else s.S[t][r] = zero ? 0.f : first[(int64_t)row * d.dv + s.n];
+        }
+    auto keep = [&](int c) {
+        if (!kAgg) s.store_columns(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
+    };
+    int c = c1 - 1;
+    s.koff.set(s.kstride, c >= c0 ? s.tokens(c) : kChunk);   // the last chunk's; the others are full
+    s.voff.set(s.vstride, c >= c0 ? s.tokens(c) : kChunk);
     if constexpr (kTwo) {
-        if (c >= 0) s.fill(l0, c);
+        if (c >= c0) s.fill(l0, c);
         s.koff.set(s.kstride, kChunk);
         s.voff.set(s.vstride, kChunk);
-        for (; c >= 0; c -= 2) {
+        for (; c >= c0; c -= 2) {
             // l0 is filled, l1 is read; the state's stores came after the loads
-            if (c < chunks - 1) loads_done<C::kTiles>();
+            if (c < c1 - 1) loads_done<C::kTiles>();
             else loads_done<0>();
             __syncthreads();
-            if (c > 0) s.fill(l1, c - 1);
+            if (c > c0) s.fill(l1, c - 1);
             keep(c);
             s.step(l0, c);
-            if (c == 0) break;
+            if (c == c0) break;
             loads_done<C::kTiles>();
             __syncthreads();
-            if (c > 1) s.fill(l0, c - 2);
+            if (c - 1 > c0) s.fill(l0, c - 2);
             keep(c - 1);
             s.step(l1, c - 1);
         }
     } else {
-        for (; c >= 0; --c) {
+        for (; c >= c0; --c) {
             __syncthreads();
             s.fill(l0, c);
             s.koff.set(s.kstride, kChunk);
@@ -192,7 +211,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_adjoint_kernel(Adjoint
             s.step(l0, c);
         }
     }
-    if (a.dh_init != nullptr) s.store_state(a.dh_init + head * state);
+    if (kAgg) s.store_state(a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk), d.dv + kDk);
+    else if (a.dh_init != nullptr && seg == 0) s.store_state(a.dh_init + head * state, d.dv);
 }
 
 // ------------------------------------------------------------ chunk gradients

@@ -726,7 +726,8 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
     }
 }
 
-// Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s.  One workgroup per
+// Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s (back: from the last
+// segment to the first).  One workgroup per
 // 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave per
 // kDk / 4 of the rows of M, read once by rows from memory.
 struct JoinArgs {
@@ -734,6 +735,7 @@ struct JoinArgs {
     float *h_seg;                // [batch, hv, segs, dk, dv] out, or null
     float *h_final;              // behind the last segment, or null
     int segs, dv;
+    bool back;
 };
 
 template <int kDk>
@@ -755,10 +757,11 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) out[(int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n] = h[i][r];
     };
+    const auto at = [&](int s) { return head * a.segs + (a.back ? a.segs - 1 - s : s); };
     // a segment's N and rows of M, loaded a segment ahead
     f32x4 N[kMine], M[kMine][kSteps][2];
     const auto fetch = [&](int s) {
-        const float *m = a.agg + (head * a.segs + s) * kDk * ld;
+        const float *m = a.agg + at(s) * kDk * ld;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int tile = wave * kMine + i;
@@ -775,7 +778,7 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
     const int last = a.h_final != nullptr ? a.segs : a.segs - 1;   // maps that are needed
     if (last > 0) fetch(0);
     for (int s = 0; s < a.segs; ++s) {
-        if (a.h_seg != nullptr) store(a.h_seg + (head * a.segs + s) * state);
+        if (a.h_seg != nullptr) store(a.h_seg + at(s) * state);
         if (s >= last) break;
         __syncthreads();   // the parts of the segment before are read
 #pragma unroll

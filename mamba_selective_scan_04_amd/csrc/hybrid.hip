@@ -65,19 +65,26 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 
 // Segments of a row's chunks (1: none).  A chain's step is a chunk's, whatever
 // the batch; cutting the row costs the aggregate pass over d_v + d_k columns
-// besides the chain's own d_v, so it pays from about four segments on, each of
-// 8 chunks at least.  As many as the aggregate pass runs at once (three workgroups
-// of 64 columns a CU, two for fp32 streams): one more round of them costs more
-// than shorter segments give.  65,536 tokens of 12 heads of 128 in bf16: 4.7 ms
-// whole, 1.04 in 10 segments, 0.97 in 16 (the rule's), 1.00 in 18, 1.10 in 24; of 4
-// heads in fp32: 0.85 in 32 (the rule's), 1.00 in 48, 1.11 in 72.  192 groups of
-// 64 chunks: 2% slower in two segments than whole.  BDSSM_DELTA_SEGMENTS forces a
-// count (tests).
-int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
+// besides the chain's own d_v, and the join's step for each segment, so it pays
+// from three segments of two chunks on.  No more than the aggregate pass runs at
+// once (three workgroups of 64 columns a CU, two for fp32 streams): another round
+// of them costs more than shorter segments give.  Nor more than makes the two
+// chains' steps and the join's (a sixth of theirs) least: n^2 = 4 chunks is near
+// that.  Microseconds of the forward, bf16, 128 by 128:
+//   1 row of 65,536 tokens, 12 heads   1: 5096   10: 1239   16 (the rule's): 966   24: 1101
+//   4 rows of 4,096 tokens, 16 heads   1: 424    3 (the rule's): 359   6: 392   16: 471
+//   8 rows of 4,096 tokens, 12 heads   1 (the rule's): 474   2: 502   4: 548
+//   1 row of 2,048 tokens, 2 heads     1: 149    4: 86   8: 71   12: 76   24: 101
+//   1 row of 1,024 tokens, 1 head of 64 by 64   1: 62   4: 45   8 (the rule's): 39   12: 41
+// Backward the same of the adjoint's passes, whose larger stages leave room for two
+// workgroups a CU (fp32: one): the first of these 6890 us whole, 2990 in 10 segments.
+// BDSSM_DELTA_SEGMENTS forces a count (tests).
+int delta_segments(const bdssm_delta_shape *s, int64_t chunks, bool bwd) {
     const int64_t blocks = s->batch * s->heads_v * ((s->d_v + s->d_k) / 64);
-    int64_t n = blocks > 0 ? kCus * (s->dtype == BDSSM_BF16 ? 3 : 2) / blocks : 1;
-    if (n > chunks / 8) n = chunks / 8;
-    if (n < 4) n = 1;
+    int64_t n = blocks > 0 ? kCus * ((s->dtype == BDSSM_BF16 ? 3 : 2) - (bwd ? 1 : 0)) / blocks : 1;
+    if (n > chunks / 2) n = chunks / 2;
+    while (n * n > 4 * chunks) --n;
+    if (n < 3) n = 1;
     const char *e = getenv("BDSSM_DELTA_SEGMENTS");
     if (e != nullptr && *e != 0) n = atoi(e);
     if (n > chunks) n = chunks;
@@ -86,16 +93,16 @@ int delta_segments(const bdssm_delta_shape *s, int64_t chunks) {
 }
 
 struct DeltaSizes {
-    size_t qk, vo, gate, state, hchunks, units, agg;
+    size_t qk, vo, gate, state, hchunks, units, map;   // map: a segment's, of every head
     bool bf16;
-    int segs;
+    int segs, segs_bwd;
     // the workspace: the chunks' matrices and the segments' maps; for the backward
-    // the matrices, the summed log decays and the states' adjoints
+    // the matrices, the summed log decays, the states' adjoints and the maps
     size_t mats() const { return units * (bf16 ? sizeof(Mats<2>) : sizeof(Mats<3>)); }
-    size_t fwd() const { return mats() + (segs > 1 ? agg + state * segs : 0); }
+    size_t fwd() const { return mats() + (segs > 1 ? (map + state) * segs : 0); }
     size_t mats3() const { return units * sizeof(Mats<3>); }
     size_t sums() const { return units * kChunk * 8; }
-    size_t bwd() const { return mats3() + sums() + hchunks; }
+    size_t bwd() const { return mats3() + sums() + hchunks + (segs_bwd > 1 ? (map + state) * segs_bwd : 0); }
 };
 
 DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
@@ -109,8 +116,9 @@ DeltaSizes delta_sizes(const bdssm_delta_shape *s, int64_t T) {
     z.hchunks = z.state * chunks;
     z.units = (size_t)s->batch * s->heads_v * chunks;
     z.bf16 = s->dtype == BDSSM_BF16;
-    z.segs = delta_segments(s, (int64_t)chunks);
-    z.agg = (size_t)s->batch * s->heads_v * z.segs * s->d_k * (s->d_v + s->d_k) * 4;
+    z.segs = delta_segments(s, (int64_t)chunks, false);
+    z.segs_bwd = delta_segments(s, (int64_t)chunks, true);
+    z.map = (size_t)s->batch * s->heads_v * s->d_k * (s->d_v + s->d_k) * 4;
     return z;
 }
 
@@ -263,7 +271,7 @@ int bdssm_delta_scan(const bdssm_delta_shape *s, int64_t T, const void *q, const
     c.mats = ws;
     c.segs = z.segs;
     c.agg = (float *)((char *)ws + z.mats());
-    c.h_seg = (float *)((char *)ws + z.mats() + z.agg);
+    c.h_seg = (float *)((char *)ws + z.mats() + z.map * z.segs);
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_delta_scan<uint16_t>(c, st);
     else launch_delta_scan<float>(c, st);
@@ -296,6 +304,9 @@ int bdssm_delta_scan_bwd(const bdssm_delta_shape *s, int64_t T, const void *q, c
     c.mats = w;
     c.G = (double *)(w + z.mats3());
     c.dS = (float *)(w + z.mats3() + z.sums());
+    c.segs = z.segs_bwd;
+    c.agg = (float *)(w + z.mats3() + z.sums() + z.hchunks);
+    c.h_seg = (float *)(w + z.mats3() + z.sums() + z.hchunks + z.map * z.segs_bwd);
     c.dq = dq;
     c.dk_out = dk;
     c.dv_out = dv;

@@ -27,7 +27,7 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
         a.wanted = c.segs - (chain ? 1 : 0);   // the state behind the last comes from the chain
         hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
         // states alone: the join has the last
-        const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv};
+        const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv, false};
         hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
         if (!chain) return;
         a.h_init = c.h_seg;
@@ -52,9 +52,24 @@ void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
     if (c.d.chunks > 0)
         hipLaunchKernelGGL((delta_prep_kernel<T, kDk, 3>), gp, dim3(kDeltaThreads), 0, st, (const T *)c.q, (const T *)c.k, c.g, c.beta,
                            (Mats<3> *)c.mats, c.G, c.d);
-    const AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.mats, c.dh_final, c.dS, c.dh_init, (int)(c.batch * c.d.hv), c.d};
-    const dim3 gc((unsigned)((a.groups + 7) / 8 * 8 * (c.d.dv / 64)));
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk>), gc, dim3(kDeltaThreads), 0, st, a);
+    AdjointArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.dout, (const Mats<3> *)c.mats, c.dh_final, c.dS, c.dh_init,
+                     c.agg, nullptr, 1, c.d.chunks, (int)(c.batch * c.d.hv), c.d};
+    const auto grid = [&](int columns) { return dim3((unsigned)((a.groups + 7) / 8 * 8 * (columns / 64))); };
+    if (c.segs > 1) {
+        a.segs = c.segs;
+        a.per = (c.d.chunks + c.segs - 1) / c.segs;
+        a.groups *= c.segs;
+        hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk, true, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
+        const JoinArgs j{c.agg, c.dh_final, c.h_seg, nullptr, c.segs, c.d.dv, true};
+        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
+        a.h_seg = c.h_seg;
+    }
+    const dim3 gc = grid(c.d.dv);
+    const bool two = sizeof(T) == 2 && (int64_t)a.groups * (c.d.dv / 64) <= 256;
+    if constexpr (sizeof(T) == 2) {
+        if (two) hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk, false, true>), gc, dim3(kDeltaThreads), 0, st, a);
+    }
+    if (!two) hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk, false, false>), gc, dim3(kDeltaThreads), 0, st, a);
     if (c.d.chunks == 0) return;
     const GradArgs<T> ga{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const T *)c.dout, (const Mats<3> *)c.mats,
                          c.G, c.beta, c.h_chunks, c.dS, (T *)c.dq, (T *)c.dk_out, (T *)c.dv_out, c.dg, c.dbeta, c.d};

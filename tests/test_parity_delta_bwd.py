@@ -107,3 +107,28 @@ def test_reference_against_differences():
         c[name] = base
         want = float((grads[grad] * step).sum())
         assert abs((up - down) / (2 * e) - want) <= 1e-6 * max(1.0, abs(want)), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("segs", [2, 3, 5])
+@pytest.mark.parametrize("heads", [(1, 2, 64, 128), (2, 2, 128, 64)])
+def test_segments(dev, heads, segs, dtype, monkeypatch):
+    """The adjoint's chunks in segments that run at once; rows that end inside one, or have none."""
+    monkeypatch.setenv("BDSSM_DELTA_SEGMENTS", str(segs))
+    c = inputs(3, 330, *heads, dtype, seed=15, device=dev, resets=[100, 200], lens=[330, 65, 0])
+    got, ref = both(c)
+    check_all(got, ref, 3.0)             # as above, and each segment's map once more on the state's adjoint
+    again = both(c)[0]
+    assert all(torch.equal(got[n], again[n]) for n in NAMES)
+    check_all(*both(c, h=False, dh=False), 3.0)
+
+
+@pytest.mark.gpu
+def test_long_row_is_segmented(dev, monkeypatch):
+    c = inputs(1, 2100, 1, 1, 128, 64, torch.bfloat16, seed=16, device=dev)
+    s = m.DeltaShape(1, 1, 1, 128, 64, 1)
+    check_all(*both(c), 3.0)
+    maps = m.delta_workspace_bytes(s, 2100, True)
+    monkeypatch.setenv("BDSSM_DELTA_SEGMENTS", "1")
+    assert maps > m.delta_workspace_bytes(s, 2100, True)   # it was: the segments' maps take room
