@@ -168,15 +168,11 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
     const int c0 = seg * a.per, c1 = c0 + a.per < chunks ? c0 + a.per : chunks;
     const int64_t state = (int64_t)kDk * d.dv, head = (int64_t)s.b * d.hv + s.hv;
     const float *first = a.h_seg != nullptr ? a.h_seg + (head * a.segs + seg) * state : a.dh_final + head * state;
-    const bool zero = a.h_seg == nullptr && a.dh_final == nullptr;
 #pragma unroll
     for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = state_row(t, s.grp, r);
-            if (kAgg) s.S[t][r] = s.n - d.dv == row ? 1.f : 0.f;
-            else s.S[t][r] = zero ? 0.f : first[(int64_t)row * d.dv + s.n];
-        }
+        for (int r = 0; r < 4; ++r) s.S[t][r] = kAgg && s.n - d.dv == state_row(t, s.grp, r) ? 1.f : 0.f;
+    if (!kAgg && (a.h_seg != nullptr || a.dh_final != nullptr)) load_state<kDk>(first, d.dv, s.grp, s.n, s.S);
     auto keep = [&](int c) {
         if (!kAgg) s.store_columns(a.dS + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
     };

@@ -48,18 +48,19 @@ __device__ __forceinline__ int64_t row_len(const DeltaDims &d, int b) {
     return n < 0 ? 0 : (n < d.T ? n : d.T);
 }
 
-// Inclusive sums of the chunk's log decays, by the first wave (g: the lane's
-// own, 0 behind the last token).
+// Inclusive sums of kTokens log decays, by the first wave (g: the lane's own, 0
+// behind the last token).
+template <int kTokens = kChunk>
 __device__ __forceinline__ void chunk_decays(float g, double *G) {
     if (threadIdx.x < 64) {
         const int t = threadIdx.x;
         double x = (double)fmaxf(g, -1e4f);
 #pragma unroll
-        for (int s = 1; s < 64; s <<= 1) {
+        for (int s = 1; s < kTokens; s <<= 1) {
             const double up = __shfl_up(x, s, 64);
             if (t >= s) x += up;
         }
-        G[t] = x;
+        if (t < kTokens) G[t] = x;
     }
 }
 
@@ -510,6 +511,17 @@ struct ChainStage {
     typename MatsUsed<kMode == kOutputs ? Stream<T>::kOutParts : 0>::type m;
 };
 
+// A column's rows of a state [dk, dv] into its tiles.  (With a test for null at
+// each load the compiler made as many branches, and the loads ran one by one.)
+template <int kDk>
+__device__ __forceinline__ void load_state(const float *h, int dv, int grp, int n, f32x4 *S) {
+    const uint32_t lane_off = (uint32_t)(grp * 8 * dv + n);
+#pragma unroll
+    for (int t = 0; t < kDk / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][r] = (h + state_row(t, 0, r) * dv)[lane_off];
+}
+
 template <typename T, int kDk, int kMode>
 struct Chain {
     static constexpr bool kWithO = kMode == kOutputs;
@@ -685,10 +697,9 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
     for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = state_row(t, s.grp, r);
-            if (kMode == kAggregate) s.S[t][r] = s.n - d.dv == row ? 1.f : 0.f;
-            else s.S[t][r] = a.h_init == nullptr ? 0.f : a.h_init[(head * a.segs + seg) * state + (int64_t)row * d.dv + s.n];
+            s.S[t][r] = kMode == kAggregate && s.n - d.dv == state_row(t, s.grp, r) ? 1.f : 0.f;
         }
+    if (kMode != kAggregate && a.h_init != nullptr) load_state<kDk>(a.h_init + (head * a.segs + seg) * state, d.dv, s.grp, s.n, s.S);
     auto keep = [&](int c) {
         if (kMode != kAggregate && a.h_chunks != nullptr)
             s.store_columns(a.h_chunks + (((int64_t)s.b * d.chunks + c) * d.hv + s.hv) * state);
@@ -759,10 +770,13 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
     const int ld = a.dv + kDk;
     f32x4 h[kMine];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
+    for (int i = 0; i < kMine; ++i) h[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.h_init != nullptr) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            h[i][r] = a.h_init == nullptr ? 0.f : a.h_init[head * state + (int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n];
+        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[i][r] = a.h_init[head * state + (int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n];
+    }
     const auto store = [&](float *out) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
@@ -830,11 +844,11 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
 // dk / 8 consecutive rows), so the state is read once and written once however
 // many tokens there are.  Both sums over the rows (S^T k and S^T q of the
 // decayed state; o = S^T q + (k.q) u) fold over the 8 row groups together.
-// One token is bound by the launch (1 row of 16 heads: 3.9 us); a block of 16 of
-// 64 rows of 16 heads of 128 by 128 takes 40 us for 147 MB (3.7 TB/s), half of
-// the issue slots busy with three operations to each element of the state and
-// token.  32 columns a wave: the sums' exchanges are shared by four columns a lane,
-// and the state's 64 registers leave three waves a SIMD.
+// One token is bound by the launch (1 row of 16 heads: 3.9 us) or by memory (64
+// rows of 16 heads of 128 by 128: 21.5 us with its launch, 6.2 TB/s); each further
+// token adds 2 us there, three operations to each element of the state.  32 columns
+// a wave: the sums' exchanges are shared by four columns a lane, and the state's 64
+// registers leave three waves a SIMD.
 template <typename T>
 struct StepArgs {
     const T *q, *k, *v;
@@ -917,7 +931,11 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs<T> a) {
     const int64_t state = (((int64_t)b * d.hv + hv) * kDk + r0) * d.dv + n;
     f32x4 S[kR];
 #pragma unroll
-    for (int i = 0; i < kR; ++i) S[i] = a.h == nullptr ? f32x4{0.f, 0.f, 0.f, 0.f} : *(const f32x4 *)(a.h + state + (int64_t)i * d.dv);
+    for (int i = 0; i < kR; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.h != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kR; ++i) S[i] = *(const f32x4 *)(a.h + state + (int64_t)i * d.dv);
+    }
     // S holds the state divided by c, the product of the decays since S was last
     // scaled: a token's decay costs no pass over S.
     float c = 1.f;
@@ -987,6 +1005,182 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs<T> a) {
     if (a.h_out != nullptr && !(len == 0 && a.h == a.h_out)) {
 #pragma unroll
         for (int i = 0; i < kR; ++i) *(f32x4 *)(a.h_out + state + (int64_t)i * d.dv) = S[i];
+    }
+}
+
+// The same for blocks of bf16 tokens, 16 tokens at a time in the chunked form above
+// with matrix instructions: the token by token kernel's three operations to each
+// element of the state and token bound it from some tokens on.  One wave per 32
+// columns of one head's state, in registers as the chains' (tile nt holds columns
+// n + nt, so that a lane's pairs of columns are neighbours in memory).  U comes by
+// substitution over the 16 tokens, (I + diag(beta) A) U = diag(beta) R, each
+// token's row of U handed to the other lane groups in turn.  64 rows of 16 heads of
+// 128 by 128 and 16 tokens: 33 us for 147 MB (4.4 TB/s; by token 54), bound by
+// memory and a wave's start and end: two waves a SIMD, three spill and take 42.  The
+// state goes on in three bf16 parts, so that it keeps its 32 bits.
+
+// x of lane group kFrom (16 lanes) in all four
+template <int kFrom>
+__device__ __forceinline__ float of_group(float x) {
+    const auto h = __builtin_amdgcn_permlane16_swap(as_u(x), as_u(x), false, false);
+    const auto w = __builtin_amdgcn_permlane32_swap(h[kFrom & 1], h[kFrom & 1], false, false);
+    return as_f(w[kFrom >> 1]);
+}
+
+// a wave's LDS operations are done in order: this one only keeps the compiler's
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int kDk>
+__global__ __launch_bounds__(64, 2) void delta_block_kernel(StepArgs<uint16_t> a) {
+    constexpr int kTiles = kDk / 16, kSteps = kDk / 32, kSub = 16;
+    __shared__ __attribute__((aligned(16))) uint16_t K[kSub][kDk + 8];
+    __shared__ __attribute__((aligned(16))) float L[kSub][kSub];   // [j][i]: beta_i A_ij
+    __shared__ __attribute__((aligned(16))) float e[kSub], rest[kSub], strength_of[kSub];
+    __shared__ double G[kSub];
+    const DeltaDims &d = a.d;
+    const int hv = blockIdx.y, b = blockIdx.z, hk = hv / d.group;
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4, n = blockIdx.x * 32 + 2 * col;
+    const int64_t len = row_len(d, b), at0 = (int64_t)b * d.T, state = ((int64_t)b * d.hv + hv) * kDk * d.dv + blockIdx.x * 32;
+    const uint32_t lane_off = (uint32_t)(grp * 8 * d.dv) + 2 * col;   // of its pairs of columns in the state
+    const bool with_o = a.o != nullptr;
+    const uint16_t *qp = with_o ? a.q : a.k;   // without outputs: any
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 S[2][kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) S[0][t] = S[1][t] = zero;
+    if (a.h != nullptr) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float2 w = *(const float2 *)(a.h + state + state_row(t, 0, r) * d.dv + lane_off);
+                S[0][t][r] = w.x;
+                S[1][t][r] = w.y;
+            }
+    }
+    for (int64_t t0 = 0; t0 < len; t0 += kSub) {
+        const int m = len - t0 < kSub ? (int)(len - t0) : kSub;
+        const int64_t row = at0 + t0;
+        const int64_t kat = ((row + (col < m ? col : m - 1)) * d.hk + hk) * kDk + grp * 8;   // tokens behind the last repeat it
+        Frag<1> kf[kSteps], qf[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            kf[s] = load_straight(a.k + kat + s * 32);
+            qf[s] = load_straight(qp + kat + s * 32);
+        }
+        uint32_t v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = grp * 4 + r;
+            v[r] = *(const uint32_t *)(a.v + ((row + (i < m ? i : m - 1)) * d.hv + hv) * d.dv + n);
+        }
+        wave_order();   // the last 16 tokens' reads
+        chunk_decays<kSub>(lane < m ? a.g[(row + lane) * d.hv + hv] : 0.f, G);
+        if (lane < kSub) strength_of[lane] = lane < m ? a.beta[(row + lane) * d.hv + hv] : 0.f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) *(uint4 *)&K[col][s * 32 + grp * 8] = __builtin_bit_cast(uint4, kf[s].p[0]);
+        wave_order();
+        const double end = G[kSub - 1], Gc = G[col];
+        if (lane < kSub) {
+            e[lane] = decay(Gc);
+            rest[lane] = lane < m ? decay(end - Gc) : 0.f;
+        }
+        // rows k token 4 grp + r; columns k and q token
+        f32x4 A = zero, P = zero;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            A = mma(kf[s], kf[s], A);
+            P = mma(kf[s], qf[s], P);
+        }
+        const f32x4 bt = *(const f32x4 *)(strength_of + grp * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = grp * 4 + r;
+            const double g = G[i];
+            A[r] = col < i ? bt[r] * decay(g - Gc) * A[r] : 0.f;   // A is symmetric but for this
+            P[r] = i <= col ? decay(Gc - g) * P[r] : 0.f;          // P_ji as the A operand of P U has it
+        }
+        *(f32x4 *)&L[col][grp * 4] = A;
+        wave_order();
+        f32x4 U[2] = {zero, zero}, O[2] = {zero, zero};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const Frag<3> Sp = split_frag<3>(S[nt][2 * s], S[nt][2 * s + 1]);
+                U[nt] = mma(kf[s], Sp, U[nt]);
+                if (with_o) O[nt] = mma(qf[s], first_parts<2>(Sp), O[nt]);
+            }
+        const f32x4 ev = *(const f32x4 *)(e + grp * 4), rv = *(const f32x4 *)(rest + grp * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            U[0][r] = bt[r] * fmaf(-ev[r], U[0][r], bf_lo(v[r]));
+            U[1][r] = bt[r] * fmaf(-ev[r], U[1][r], bf_hi(v[r]));
+        }
+        const auto eliminate = [&](auto from) {
+            constexpr int g0 = decltype(from)::value;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 l = *(const f32x4 *)&L[g0 * 4 + j][grp * 4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float u = of_group<g0>(U[nt][j]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) U[nt][r] = fmaf(-l[r], u, U[nt][r]);
+                }
+            }
+        };
+        eliminate(std::integral_constant<int, 0>{});
+        eliminate(std::integral_constant<int, 1>{});
+        eliminate(std::integral_constant<int, 2>{});
+        eliminate(std::integral_constant<int, 3>{});
+        if (with_o) {
+            const Frag<2> Pf = split_frag<2>(P, zero);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) O[nt][r] *= ev[r];
+                O[nt] = mma(Pf, split_frag<2>(U[nt], zero), O[nt]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (grp * 4 + r < m)
+                    *(uint32_t *)(a.o + ((row + grp * 4 + r) * d.hv + hv) * d.dv + n) = pk_rne(d.scale * O[0][r], d.scale * O[1][r]);
+        }
+        if (t0 + kSub >= len && a.h_out == nullptr) break;   // the state is not wanted
+        const float last = decay(end);
+        Frag<3> Up[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = rv[r] * U[nt][r];
+            Up[nt] = split_frag<3>(x, zero);
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const uint16_t *p = &K[grp * 4][t / 2 * 32 + col / 4 * 8 + (t & 1) * 4 + col % 4];
+            constexpr int kRow = kDk + 8;
+            const Frag<1> kt = {{frag_of(p[0] | (uint32_t)p[kRow] << 16, p[2 * kRow] | (uint32_t)p[3 * kRow] << 16, 0u, 0u)}};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[nt][t][r] *= last;
+                S[nt][t] = mma(kt, Up[nt], S[nt][t]);
+            }
+        }
+    }
+    if (with_o)
+        for (int64_t t = len + grp; t < d.T; t += 4) *(uint32_t *)(a.o + ((at0 + t) * d.hv + hv) * d.dv + n) = 0u;
+    if (a.h_out != nullptr && !(len == 0 && a.h == a.h_out)) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *(float2 *)(a.h_out + state + state_row(t, 0, r) * d.dv + lane_off) = make_float2(S[0][t][r], S[1][t][r]);
     }
 }
 

@@ -95,13 +95,29 @@ void launch_delta_scan<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) {
     else launch_scan_k<BDSSM_TIN, 128>(c, st);
 }
 
-template <>
-void launch_delta_step<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) {
-    using T = BDSSM_TIN;
+// Tokens from which the step goes 16 at a time (bf16; fp32 streams' parts would not
+// fit the registers).  64 rows of 16 heads of 128 by 128, read only / in place, in
+// us: 4 tokens 19.7 / 26.1 by token and 19.9 / 31.9 by sixteen; 6: 24.6 / 30.2 and
+// 20.3 / 31.9; 8: 29.8 / 35.3 and 20.7 / 31.9; 16: 48.9 / 54.3 and 22.4 / 34.0; 64:
+// 163 / 168 and 62 / 71.
+constexpr int kBlockFrom = 6;
+
+template <typename T>
+void launch_step(const DeltaCall &c, hipStream_t st) {
     const StepArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, c.g, c.beta, c.h_init, (T *)c.o, c.h_final, c.d};
     const dim3 g((unsigned)(c.d.dv / 32), (unsigned)c.d.hv, (unsigned)c.batch);
+    if constexpr (sizeof(T) == 2) {
+        if (c.d.T >= kBlockFrom) {
+            if (c.dk == 64) hipLaunchKernelGGL((delta_block_kernel<64>), g, dim3(64), 0, st, a);
+            else hipLaunchKernelGGL((delta_block_kernel<128>), g, dim3(64), 0, st, a);
+            return;
+        }
+    }
     if (c.dk == 64) hipLaunchKernelGGL((delta_step_kernel<T, 64>), g, dim3(64), 0, st, a);
     else hipLaunchKernelGGL((delta_step_kernel<T, 128>), g, dim3(64), 0, st, a);
 }
+
+template <>
+void launch_delta_step<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) { launch_step<BDSSM_TIN>(c, st); }
 
 }  // namespace bdssm_host

@@ -231,7 +231,7 @@ for path in glob.glob(os.path.join(os.path.dirname(HERE), "mamba_selective_scan_
 
 @pytest.mark.skipif(not ROWS, reason="no resource report (run the build first)")
 @pytest.mark.parametrize("kernel,count", [("delta_prep_kernelIt", 4), ("delta_chain_kernelIt", 8), ("delta_adjoint_kernelIt", 6),
-                                          ("delta_grad_kernelIt", 8), ("delta_step_kernelI[tf]", 4), ("delta_join_kernel", 4),
+                                          ("delta_grad_kernelIt", 8), ("delta_step_kernelI[tf]", 4), ("delta_block_kernel", 2), ("delta_join_kernel", 4),
                                           ("kv_commit_kernelI[tf]", 40), ("kv_attn_kernelI[tf]", 14), ("kv_join_kernel", 4)])
 def test_kernels_do_not_spill(kernel, count):
     got = [r for r in ROWS if re.search(kernel, r["kernel"])]

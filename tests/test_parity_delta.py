@@ -147,3 +147,25 @@ def test_long_row_is_segmented(dev):
     o, h, _ = m.delta_scan(*args(c), h_init=c["h"])
     check(o, r["o"], "o", 2.0)
     check(h, r["h"], "h", 2.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [4, 5, 6, 7, 15, 16, 17, 31, 50])
+def test_step_of_every_length(dev, T, dtype):
+    """Either way of the step, rows that end inside its 16 tokens, the state cleared on the way."""
+    lens = [T, T - 1, 1, 0]
+    c = inputs(4, T, 2, 4, 128 if T % 2 else 64, 64, dtype, seed=17, device=dev, lens=lens, resets=[T // 2])
+    for b, n in enumerate(lens):
+        for name in ("q", "k", "v", "g", "beta"):
+            c[name][b, n:] = float("nan")
+    r = reference(c, h=c["h"])
+    h = torch.empty_like(c["h"])
+    o = m.delta_step(c["h"], *args(c), lens=c["lens"], h_out=h)
+    check(o, r["o"], "o")
+    check(h, r["h"], "h")
+    assert all((o[b, n:] == 0).all() for b, n in enumerate(lens))
+    assert torch.equal(m.delta_step(c["h"], *args(c), lens=c["lens"]), o)      # read only: the same bits
+    h0 = c["h"].clone()
+    assert m.delta_step(h0, None, *args(c)[1:], lens=c["lens"], h_out=h0, want_o=False) is None
+    assert torch.equal(h0, h)
+    check(m.delta_step(None, *args(c), lens=c["lens"]), reference(c)["o"], "from zero")
