@@ -338,6 +338,14 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         const int64_t chunk_at = (((int64_t)b * d.chunks + c) * d.hv + hv) * state;
         const float *Sg = a.S + chunk_at, *dSg = a.dS + chunk_at;
         const uint32_t col_off = (uint32_t)(n * kDk + grp * 8);
+        // the gates before all else: a wait for them is one for what was asked for earlier
+        double g_sum = 0.;
+        float beta = 1.f;
+        if (threadIdx.x < kChunk) {
+            const int t = (int)threadIdx.x < m ? threadIdx.x : m - 1;
+            g_sum = a.G[unit * kChunk + threadIdx.x];
+            beta = a.beta[at + (int64_t)t * d.hv];
+        }
         __syncthreads();   // the last head's reads of LDS are done
         fill_mats<kWaves>(a.mats + unit, &l.m);
         if constexpr (kBf16) {
@@ -354,8 +362,8 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         load_columns(Sg);
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
-            l.G[t] = a.G[unit * kChunk + t];
-            l.ib[t] = t < m ? 1.f / strength(a.beta[at + (int64_t)t * d.hv]) : 1.f;
+            l.G[t] = g_sum;
+            l.ib[t] = t < m ? 1.f / strength(beta) : 1.f;
         }
         const auto value_tile = [&](int mt) {
             if constexpr (kBf16) {

@@ -248,7 +248,7 @@ __device__ __forceinline__ void block_of(int tile, int *it, int *jt) {
 // chunks enough: 65,536 bf16 tokens of 12 heads of 128 in 181 us, 0.76 GB of tokens
 // in and matrices out at 4.2 TB/s; W in three parts, so that U keeps its 32 bits.
 template <typename T, int kDk, int kPF>
-__global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__restrict__ q, const T *__restrict__ k,
+__global__ __launch_bounds__(kDeltaThreads, sizeof(T) == 2 ? 3 : 1) void delta_prep_kernel(const T *__restrict__ q, const T *__restrict__ k,
                                                                   const float *__restrict__ g,
                                                                   const float *__restrict__ beta, Mats<kPF> *__restrict__ mats,
                                                                   double *__restrict__ Gs, DeltaDims d) {
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(const T *__re
         for (int s = 0; s < kDk / 32; ++s) {
             const auto ki = l.k.row(it * 16 + col, s, grp), kj = l.k.row(jt * 16 + col, s, grp);
             kk[x] = mma(ki, kj, kk[x]);
-            if (q != nullptr) kq[x] = mma(kj, l.q.row(it * 16 + col, s, grp), kq[x]);
+            kq[x] = mma(kj, l.q.row(it * 16 + col, s, grp), kq[x]);   // without q: not used
         }
     }
     __syncthreads();   // the tiles are read: N takes their place
