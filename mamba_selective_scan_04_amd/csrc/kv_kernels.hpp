@@ -242,8 +242,10 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // channel's row.  32 keys are two pages at most, the same for the whole wave:
 // their numbers and scales come by scalar loads.
 //
-// Probabilities enter their product as bf16 (two parts for fp32 streams: three)
-// after the page's value scale is multiplied in; scores, maxima, sums and
+// Probabilities enter their product in two bf16 parts (2^-16; fp32 streams: three,
+// exact) after the page's value scale is multiplied in: in one part they would
+// leave as much of an error as the output's own rounding (1.4 times the error of
+// the whole for 2 us less of 32 at 65,536 tokens).  Scores, maxima, sums and
 // outputs are fp32.  The running maximum moves only when a score passes it by
 // 2^8: probabilities stay below 2^8 and the outputs are seldom rescaled.
 //
@@ -252,7 +254,7 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // through the workspace and kv_join_kernel.
 //
 // Measured at 128 channels, pages of 16, 64 query rows a key head (16 tokens of 4
-// heads, two query tiles): 65,536 e4m3 tokens of 4 heads in 29 us (2.3 TB/s), 4 rows
+// heads, two query tiles): 65,536 e4m3 tokens of 4 heads in 30 us (2.2 TB/s), 4 rows
 // of up to 262,144 int8 tokens in 222 us (3.0 TB/s).  Registers leave two waves a
 // SIMD, whose conversion of codes and softmax keep the vector units busy for 45% of
 // the time (int8's codes take three times as many instructions as e4m3's: 99 us
@@ -296,7 +298,7 @@ __device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
 
 // the probabilities' parts
 template <typename T>
-constexpr int kProbParts = sizeof(T) == 2 ? 1 : 3;
+constexpr int kProbParts = sizeof(T) == 2 ? 2 : 3;
 
 template <typename T, int kD, int kTiles>
 struct AttnState {
