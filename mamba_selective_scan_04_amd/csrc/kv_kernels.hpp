@@ -254,13 +254,13 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // through the workspace and kv_join_kernel.
 //
 // Measured at 128 channels, pages of 16, 64 query rows a key head (16 tokens of 4
-// heads, two query tiles): 65,536 e4m3 tokens of 4 heads in 30 us (2.2 TB/s), 4 rows
-// of up to 262,144 int8 tokens in 222 us (3.0 TB/s).  Registers leave two waves a
-// SIMD, whose conversion of codes and softmax keep the vector units busy for 45% of
-// the time (int8's codes take three times as many instructions as e4m3's: 99 us
-// against 83 for 4 rows of 65,536) and wait for the codes in the rest.  At 64
-// channels and 3 query rows (64 rows of up to 8,192 int8 tokens, one tile): 38 us,
-// 4.5 TB/s, bound by memory and the rows' different ends.
+// heads, two query tiles): 65,536 e4m3 tokens of 4 heads in 32 us (2.1 TB/s), 4 rows
+// of up to 262,144 int8 tokens in 229 us (2.9 TB/s).  Registers leave two waves a
+// SIMD, whose conversion of codes and softmax keep the vector units busy for 40% of
+// the time (int8's codes take three times as many instructions as e4m3's: with one
+// part 99 us against 83 for 4 rows of 65,536) and wait for the codes in the rest.
+// At 64 channels and 3 query rows (64 rows of up to 8,192 int8 tokens, one tile):
+// 41 us, 4.2 TB/s, bound by memory and the rows' different ends.
 template <typename T>
 struct AttnArgs {
     const T *q, *k, *v;
