@@ -34,7 +34,7 @@ struct AdjointArgs {
     const float *dh_final;            // null: zero
     float *dS;                        // [batch, chunks, hv, dv, dk]: dS' of each chunk
     float *dh_init;                   // null: not wanted
-    float *agg;                       // kAggregate: [batch, hv, segs, dk, dv + dk]
+    float *agg;                       // kAgg: as the chain's
     const float *h_seg;               // null, or [batch, hv, segs, dk, dv]: dS' behind each segment
     int segs, per;                    // segments, and chunks of each
     int groups;                       // batch * segs * hv
@@ -210,8 +210,11 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
             s.step(l0, c);
         }
     }
-    if (kAgg) s.store_state(a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk), d.dv + kDk);
-    else if (a.dh_init != nullptr && seg == 0) s.store_state(a.dh_init + head * state, d.dv);
+    if (kAgg) {
+        float *map = a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk);
+        if (s.has_o) s.store_state(map, d.dv);
+        else store_map<kDk>(map + kDk * d.dv, s.grp, s.n - d.dv, s.S);
+    } else if (a.dh_init != nullptr && seg == 0) s.store_state(a.dh_init + head * state, d.dv);
 }
 
 // ------------------------------------------------------------ chunk gradients

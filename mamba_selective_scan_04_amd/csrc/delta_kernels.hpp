@@ -496,7 +496,7 @@ struct ChainArgs {
     T *o;                 // kOutputs
     float *h_final;       // null: not wanted
     float *h_chunks;      // null, or [batch, chunks, hv, dv, dk]
-    float *agg;           // kAggregate: [batch, hv, segs, dk, dv + dk]
+    float *agg;           // kAggregate: [batch, hv, segs], N [dk, dv] and M (store_map)
     int segs, per;        // segments, and chunks of each
     int wanted;           // kAggregate: the segments whose maps are used
     int groups;           // batch * segs * hv
@@ -520,6 +520,18 @@ __device__ __forceinline__ void load_state(const float *h, int dv, int grp, int 
     for (int t = 0; t < kDk / 16; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = (h + state_row(t, 0, r) * dv)[lane_off];
+}
+
+// Column j of a segment's M from its tiles, as the join reads it: A fragments (tile of
+// rows, step of 32 columns), each in two halves of four floats a lane.  (By rows, each
+// lane of the join's loads had a line of its own.)
+template <int kDk>
+__device__ __forceinline__ void store_map(float *M, int grp, int j, const f32x4 *S) {
+    const int at = (j / 32 * 2 + (j % 8) / 4) * 256 + j % 32 / 8 * 64 + grp * 16 + j % 4;
+#pragma unroll
+    for (int t = 0; t < kDk / 16; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) M[at + t * (kDk / 32) * 512 + r * 4] = S[t][r];
 }
 
 template <typename T, int kDk, int kMode>
@@ -733,7 +745,9 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
         }
     }
     if (kMode == kAggregate) {
-        s.store_state(a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk), d.dv + kDk);
+        float *map = a.agg + (head * a.segs + seg) * kDk * (d.dv + kDk);
+        if (s.has_v) s.store_state(map, d.dv);
+        else store_map<kDk>(map + kDk * d.dv, s.grp, s.n - d.dv, s.S);
         return;
     }
     if (a.h_final != nullptr && seg == a.segs - 1) s.store_state(a.h_final + head * state, d.dv);
@@ -749,10 +763,11 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
 
 // Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s (back: from the last
 // segment to the first).  One workgroup per
-// 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave per
-// kDk / 4 of the rows of M, read once by rows from memory.  Serial over the
-// segments, 3 us each at 128 by 128 (16 segments of 12 heads: 48 us); the next
-// segment's maps are on their way meanwhile.
+// 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave to each
+// 16 rows of M, read as its fragments (store_map).  Serial over the segments, 2 us
+// each at 128 by 128 (16 segments of 12 heads: 35 us; 49 with M by rows, whose loads
+// touched a line for each lane); the next two segments' maps are on their way
+// meanwhile.
 struct JoinArgs {
     const float *agg, *h_init;   // h_init null: zero
     float *h_seg;                // [batch, hv, segs, dk, dv] out, or null
@@ -762,12 +777,11 @@ struct JoinArgs {
 };
 
 template <int kDk>
-__global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
-    constexpr int kTiles = kDk / 16, kMine = kTiles / 4, kSteps = kDk / 32;
+__global__ __launch_bounds__(kDk * 4) void delta_join_kernel(JoinArgs a) {
+    constexpr int kMine = 1, kSteps = kDk / 32;   // a wave's tiles of 16 rows
     __shared__ uint4 part[kSteps][3][64];
     const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4, n = blockIdx.x * 16 + col;
     const int64_t head = blockIdx.y, state = (int64_t)kDk * a.dv;
-    const int ld = a.dv + kDk;
     f32x4 h[kMine];
 #pragma unroll
     for (int i = 0; i < kMine; ++i) h[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -784,28 +798,30 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
             for (int r = 0; r < 4; ++r) out[(int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n] = h[i][r];
     };
     const auto at = [&](int s) { return head * a.segs + (a.back ? a.segs - 1 - s : s); };
-    // a segment's N and rows of M, loaded a segment ahead
-    f32x4 N[kMine], M[kMine][kSteps][2];
-    const auto fetch = [&](int s) {
-        const float *m = a.agg + at(s) * kDk * ld;
+    // a segment's N and rows of M, loaded two segments ahead
+    struct Map {
+        f32x4 N[kMine], M[kMine][kSteps][2];
+    } m0, m1;
+    const auto fetch = [&](int s, Map &to) {
+        const float *m = a.agg + at(s) * kDk * (a.dv + kDk);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int tile = wave * kMine + i;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) N[i][r] = m[(int64_t)state_row(tile, grp, r) * ld + n];
-            const float *row = m + (int64_t)(tile / 2 * 32 + col / 4 * 8 + (tile & 1) * 4 + col % 4) * ld + a.dv + grp * 8;
+            for (int r = 0; r < 4; ++r) to.N[i][r] = m[(int64_t)state_row(tile, grp, r) * a.dv + n];
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x) {
-                M[i][x][0] = *(const f32x4 *)(row + x * 32);
-                M[i][x][1] = *(const f32x4 *)(row + x * 32 + 4);
-            }
+            for (int x = 0; x < kSteps; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    to.M[i][x][y] = *(const f32x4 *)(m + kDk * a.dv + ((tile * kSteps + x) * 2 + y) * 256 + lane * 4);
         }
     };
     const int last = a.h_final != nullptr ? a.segs : a.segs - 1;   // maps that are needed
-    if (last > 0) fetch(0);
-    for (int s = 0; s < a.segs; ++s) {
+    if (last > 0) fetch(0, m0);
+    if (last > 1) fetch(1, m1);
+    const auto turn = [&](int s, Map &now) {   // whether there is another
         if (a.h_seg != nullptr) store(a.h_seg + at(s) * state);
-        if (s >= last) break;
+        if (s >= last) return false;
         __syncthreads();   // the parts of the segment before are read
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -819,20 +835,29 @@ __global__ __launch_bounds__(256) void delta_join_kernel(JoinArgs a) {
         Frag<3> mf[kMine][kSteps];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            h[i] = N[i];
+            h[i] = now.N[i];
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x) mf[i][x] = split_frag<3>(M[i][x][0], M[i][x][1]);
+            for (int x = 0; x < kSteps; ++x) mf[i][x] = split_frag<3>(now.M[i][x][0], now.M[i][x][1]);
         }
-        if (s + 1 < last) fetch(s + 1);
+        if (s + 2 < last) fetch(s + 2, now);
         __syncthreads();
+        f32x4 odd[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) odd[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < kSteps; ++x) {
             Frag<3> y;
 #pragma unroll
             for (int p = 0; p < 3; ++p) y.p[p] = __builtin_bit_cast(bf16x8, part[x][p][lane]);
+            // two sums side by side: each of its own would wait for its last product
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) h[i] = mma(mf[i][x], y, h[i]);
+            for (int i = 0; i < kMine; ++i) (x & 1 ? odd : h)[i] = mma(mf[i][x], y, (x & 1 ? odd : h)[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) h[i] += odd[i];
+        return s + 1 < a.segs;
+    };
+    for (int s = 0; turn(s, m0) && turn(s + 1, m1); s += 2) {
     }
     if (a.h_final != nullptr) store(a.h_final + head * state);
 }

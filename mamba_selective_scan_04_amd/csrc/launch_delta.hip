@@ -28,7 +28,7 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
         hipLaunchKernelGGL((delta_chain_kernel<T, kDk, kAggregate, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
         // states alone: the join has the last
         const JoinArgs j{c.agg, c.h_init, chain ? c.h_seg : nullptr, chain ? nullptr : c.h_final, c.segs, c.d.dv, false};
-        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
+        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(kDk * 4), 0, st, j);
         if (!chain) return;
         a.h_init = c.h_seg;
     }
@@ -61,7 +61,7 @@ void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
         a.groups *= c.segs;
         hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk, true, false>), grid(c.d.dv + kDk), dim3(kDeltaThreads), 0, st, a);
         const JoinArgs j{c.agg, c.dh_final, c.h_seg, nullptr, c.segs, c.d.dv, true};
-        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(256), 0, st, j);
+        hipLaunchKernelGGL((delta_join_kernel<kDk>), dim3((unsigned)(c.d.dv / 16), (unsigned)(c.batch * c.d.hv)), dim3(kDk * 4), 0, st, j);
         a.h_seg = c.h_seg;
     }
     const dim3 gc = grid(c.d.dv);
