@@ -462,7 +462,8 @@ int bdssm_delta_step(const bdssm_delta_shape *shape, int64_t T, const float *h_c
  * Outputs, all overwritten:
  *   dq, dk    [batch, T, heads_k, d_k] stream dtype, summed over the value heads
  *             that share them;  dv [batch, T, heads_v, d_v] stream dtype;
- *   dg, dbeta [batch, T, heads_v] fp32;
+ *   dg, dbeta [batch, T, heads_v] fp32; dg keeps its precision where decays are
+ *             strong, and is 0 at tokens that clear the state;
  *   dh_init   NULL, or [batch, heads_v, d_k, d_v] fp32: dJ/dh_init (with h_init
  *             NULL, the gradient at zero).
  *   ws        ws_bytes >= bdssm_delta_workspace_bytes(shape, T, 1).

@@ -15,12 +15,18 @@
 //   dQ = scale E dO S^T + DP K,        DP_ij = scale D_ij dO_i.U_j  (j <= i)
 //   dK = diag(exp(G_C - G_j)) U dS'^T - E X S^T + DP^T Q + (DA + DA^T) K,
 //        DA_ij = -D_ij X_i.U_j  (j < i)
-// Every decay enters through G: reading tokens carry exp(G_i), writing tokens
-// exp(-G_j), so its gradient is row products of what is at hand,
-//   dG_i = dO_i.O_i - X_i.(V - y)_i - U_i.Z_i   (+ <S', dS'> at the last token),
-//   dg_i = sum of dG_j over j >= i in the chunk,
-// and needs neither dQ nor dK: those may be computed to their own type's
-// precision while dg and dbeta keep 32 bits.
+// A token's decay weighs what passes it, from a token (or the state) before it to
+// it or a token (or the state) behind it:
+//   dg_t = sum over j < t <= i of w_ij + sum over i >= t of r_i + sum over j < t of c_j
+//          + exp(G_C) <S, dS'>,
+//   w_ij = D_ij (scale (q_i.k_j) (dO_i.U_j) - (k_i.k_j) (X_i.U_j))
+//   r_i  = exp(G_i) (scale (S^T q_i).dO_i - (S^T k_i).X_i)
+//   c_j  = exp(G_C - G_j) (dS'^T k_j).U_j
+// Each term is summed where it counts.  (As a difference of sums by row and by
+// column, the terms that do not pass t would cancel in theory only, and leave their
+// roundings in the small gradient of a strong decay.)  The sums need neither dQ nor
+// dK: those may be computed to their own type's precision while dg and dbeta keep
+// 32 bits, U and X in the products above three parts.
 #pragma once
 
 #include "delta_kernels.hpp"
@@ -230,29 +236,68 @@ struct GradArgs {
     DeltaDims d;
 };
 
-// U and X between the two halves of the kernel, [64][dv] by rows: two parts for
-// bf16 streams (their results are rounded to bf16), fp32 else.
+// U and X between the two halves of the kernel, [64][dv] by rows: for bf16 streams
+// two parts (the results are rounded to bf16) and the third in a tile of its own,
+// for dg; fp32 else.
 template <typename T, int kDv>
 struct RowTile;
 template <int kDv>
 struct RowTile<uint16_t, kDv> {
+    using Third = Tile<uint16_t, kDv>;
     Tile<uint16_t, kDv> p[2];
-    __device__ __forceinline__ void put(int r, int c, float v) {
+    __device__ __forceinline__ void put(int r, int c, float v, Third &third) {
         const uint32_t h = pk_rne(v, v);
+        const float low = v - bf_lo(h);
+        const uint32_t mid = pk_rne(low, low);
         const int at = (int)(p[0].piece(r, c / 8) - p[0].e) + c % 8;
         p[0].e[at] = (uint16_t)h;
-        p[1].e[at] = (uint16_t)pk_rne(v - bf_lo(h), 0.f);
+        p[1].e[at] = (uint16_t)mid;
+        third.e[at] = (uint16_t)pk_rne(low - bf_lo(mid), 0.f);
     }
     __device__ __forceinline__ Frag<2> get(int r, int s, int grp) const {
         return Frag<2>{{p[0].row(r, s, grp).p[0], p[1].row(r, s, grp).p[0]}};
     }
+    __device__ __forceinline__ Frag<3> all(int r, int s, int grp, const Third &third) const {
+        return Frag<3>{{p[0].row(r, s, grp).p[0], p[1].row(r, s, grp).p[0], third.row(r, s, grp).p[0]}};
+    }
 };
 template <int kDv>
 struct RowTile<float, kDv> {
+    using Third = char;
     Tile<float, kDv> p;
-    __device__ __forceinline__ void put(int r, int c, float v) { p.e[(int)(p.piece(r, c / 4) - p.e) + c % 4] = v; }
+    __device__ __forceinline__ void put(int r, int c, float v, Third &) { p.e[(int)(p.piece(r, c / 4) - p.e) + c % 4] = v; }
     __device__ __forceinline__ Frag<3> get(int r, int s, int grp) const { return p.row(r, s, grp); }
+    __device__ __forceinline__ Frag<3> all(int r, int s, int grp, const Third &) const { return get(r, s, grp); }
 };
+
+// x of another lane of the row of 16 (0 where there is none), and x plus that
+template <int kCtrl>
+__device__ __forceinline__ float of_lane(float x) {
+    return as_f(__builtin_amdgcn_update_dpp(0, as_u(x), kCtrl, 0xf, 0xf, false));
+}
+template <int kCtrl>
+__device__ __forceinline__ float plus_lanes(float x) {
+    return x + of_lane<kCtrl>(x);
+}
+// sums over a row's lanes up to each (row_shr:1, 2, 4, 8), and from each on (row_shl)
+__device__ __forceinline__ float sums_to(float x) { return plus_lanes<0x118>(plus_lanes<0x114>(plus_lanes<0x112>(plus_lanes<0x111>(x)))); }
+__device__ __forceinline__ float sums_from(float x) { return plus_lanes<0x108>(plus_lanes<0x104>(plus_lanes<0x102>(plus_lanes<0x101>(x)))); }
+// x of the same lane in each of the four rows
+__device__ __forceinline__ f32x4 of_rows(float x) {
+    const auto h = __builtin_amdgcn_permlane16_swap(as_u(x), as_u(x), false, false);
+    const auto even = __builtin_amdgcn_permlane32_swap(h[0], h[0], false, false);
+    const auto odd = __builtin_amdgcn_permlane32_swap(h[1], h[1], false, false);
+    return f32x4{as_f(even[0]), as_f(odd[0]), as_f(even[1]), as_f(odd[1])};
+}
+// Four values' sums over the 16 lanes of a row together, the values halved as the
+// lanes: lane col < 4 of the row holds that of x[col].
+__device__ __forceinline__ float sum_columns(f32x4 x, int col) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = plus_lanes<0xb1>(x[r]);            // lane ^ 1
+    const bool odd = col & 1;
+    const float a = plus_lanes<0x4e>(odd ? x[1] : x[0]), b = plus_lanes<0x4e>(odd ? x[3] : x[2]);   // lane ^ 2
+    return plus_lanes<0x128>(plus_lanes<0x124>(col & 2 ? b : a));          // row_ror:4, row_ror:8
+}
 
 // eight consecutive fp32 values as parts
 template <int kParts>
@@ -264,24 +309,34 @@ template <typename T, int kDk, int kDv>
 struct GradLds {
     static constexpr int kOut = Stream<T>::kOutParts;
     Tile<T, kDk> k, q;
-    typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o, v;   // dO, V (fp32 streams: from memory)
+    // dO, V (fp32 streams: from memory); V's room then holds U's third part
+    typename std::conditional<sizeof(T) == 2, Tile<T, kDv>, char>::type o, v;
     union {
         Mats<3> m;
         struct {
             RowTile<T, kDv> U, X;
-            uint4 pairs[8][kOut][64];   // B fragments of a token by token matrix: (column tile, step)
+            union {
+                uint4 pairs[8][kOut][64];   // B fragments of a token by token matrix: (column tile, step)
+                struct {                    // of dg and dbeta, before the pairs
+                    typename RowTile<T, kDv>::Third x;   // X's third part
+                    float db[kDv / 16][kChunk];          // dbeta of a wave's columns
+                    // of a 16 x 16 block of w: sums over its rows from each row on, over
+                    // its columns before each column, and over all of it
+                    float from[kBlocks][16], before[kBlocks][16], all[kBlocks];
+                } g;
+            };
         };
     };
     double G[kChunk];
     float e[kChunk], rest[kChunk], ib[kChunk];   // ib: 1 / beta
-    float dG[kDv / 16][kChunk], db[kDv / 16][kChunk];
+    float r[kDv / 16][kChunk], c[kDv / 16][kChunk];   // r_i and c_j of a wave's columns
     float ends[kDv / 16];
 };
 
 // One workgroup per (chunk, query/key head, batch) and a wave per 16 columns of
 // v: each value head of the group in turn, dQ and dK summed over them in
-// registers.  First by columns as in the chains (U, O, dU, X and the row
-// products), then by rows: a wave takes 16 of dk (two such, or half the tokens,
+// registers.  First by columns as in the chains (U, dU, X and the row products of
+// r, c and dbeta), then the blocks of w for dg, a wave to each, then by rows: a wave takes 16 of dk (two such, or half the tokens,
 // where waves and dk do not pair up) and forms dQ^T, dK^T as products over dv
 // (rows of S, dS' from memory, each read once) and over the chunk's tokens.  The
 // token by token matrices (DP for dQ, DP and DA + DA^T for dK) are formed in
@@ -398,10 +453,10 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             l.e[threadIdx.x] = l.m.e[threadIdx.x];
             l.rest[threadIdx.x] = l.m.rest[threadIdx.x];
         }
-        // by columns: R, U, O and dO's part of dG
-        f32x4 U[4], X[4], dG[4];
+        // by columns: R, U and the row products as they come
+        f32x4 U[4], X[4], es[4];   // es: E K S
         {
-            f32x4 R[4], O[4];
+            f32x4 R[4];
             {
                 f32x4 ks[4], qs[4];
 #pragma unroll
@@ -421,27 +476,22 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 load_columns(dSg);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
-                    const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = value_tile(mt);
+                    const f32x4 e = *(const f32x4 *)(l.m.e + mt * 16 + grp * 4), v = value_tile(mt), dO = dout_tile(mt);
+                    f32x4 x;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        R[mt][r] = fmaf(-e[r], ks[mt][r], v[r]);
-                        O[mt][r] = d.scale * e[r] * qs[mt][r];
+                        es[mt][r] = e[r] * ks[mt][r];
+                        R[mt][r] = v[r] - es[mt][r];
+                        x[r] = d.scale * e[r] * qs[mt][r] * dO[r];
                     }
+                    const float sum = sum_columns(x, col);
+                    if (col < 4) l.r[wave][mt * 16 + grp * 4 + col] = sum;
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
             lower_product<3>(l.m.W, R, U);
-            __builtin_amdgcn_sched_barrier(0);
-            lower_product<3, false>(l.m.P, U, O);
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                const f32x4 dO = dout_tile(mt);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dG[mt][r] = dO[r] * O[mt][r];
-            }
         }
         __builtin_amdgcn_sched_barrier(0);
-        float end = 0.f;   // <S, dS'> exp(G_C) (by rows, below) + sum of U (K dS') rows
         {
             f32x4 dU[4];
 #pragma unroll
@@ -458,11 +508,14 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 const f32x4 rest = *(const f32x4 *)(l.m.rest + mt * 16 + grp * 4);
+                f32x4 x;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     dU[mt][r] *= rest[r];
-                    end = fmaf(U[mt][r], dU[mt][r], end);
+                    x[r] = U[mt][r] * dU[mt][r];
                 }
+                const float sum = sum_columns(x, col);
+                if (col < 4) l.c[wave][mt * 16 + grp * 4 + col] = sum;
             }
             __builtin_amdgcn_sched_barrier(0);
             {
@@ -475,49 +528,103 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
             upper_product<3>(l.m.W, dU, X);
         }
         __syncthreads();   // the matrices are read: U and X take their place
-        float sdG[4], sdb[4];   // row sums over this wave's columns, lane r = col of each result row set
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const f32x4 v = value_tile(mt);
+            f32x4 sr, sdb;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = mt * 16 + grp * 4 + r;
-                const float u = U[mt][r], x = X[mt][r], ib = l.ib[t], y = u * ib, z = x * ib;
-                sdG[r] = dG[mt][r] - x * (v[r] - y) - u * z;
-                sdb[r] = y * z;
-                l.U.put(t, n, u);
-                l.X.put(t, n, x);
+                const float u = U[mt][r], x = X[mt][r], ib = l.ib[t];
+                sr[r] = -es[mt][r] * x;
+                sdb[r] = u * ib * (x * ib);
+                l.U.put(t, n, u, l.v);
+                l.X.put(t, n, x, l.g.x);
                 if (t < m) Stream<T>::store(dvp + t * vstride + n, ib == 0x1p64f ? 0.f : x);   // beta 0: as `strength` has it
             }
-            // four sums over 16 lanes together: halve the values as the lanes
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                sdG[r] += __shfl_xor(sdG[r], 1, 64);
-                sdb[r] += __shfl_xor(sdb[r], 1, 64);
-            }
-            const bool odd = col & 1, two = col & 2;
-            float g0 = odd ? sdG[1] : sdG[0], g1 = odd ? sdG[3] : sdG[2], b0 = odd ? sdb[1] : sdb[0], b1 = odd ? sdb[3] : sdb[2];
-            g0 += __shfl_xor(g0, 2, 64);
-            g1 += __shfl_xor(g1, 2, 64);
-            b0 += __shfl_xor(b0, 2, 64);
-            b1 += __shfl_xor(b1, 2, 64);
-            float g = two ? g1 : g0, db = two ? b1 : b0;
-            g += __shfl_xor(g, 4, 64);
-            db += __shfl_xor(db, 4, 64);
-            g += __shfl_xor(g, 8, 64);
-            db += __shfl_xor(db, 8, 64);
-            if (col < 4) {   // lane col holds row 2 (col / 2) + col % 2
-                l.dG[wave][mt * 16 + grp * 4 + col] = g;
-                l.db[wave][mt * 16 + grp * 4 + col] = db;
+            const float sum = sum_columns(sr, col), db = sum_columns(sdb, col);
+            if (col < 4) {
+                l.r[wave][mt * 16 + grp * 4 + col] += sum;
+                l.g.db[wave][mt * 16 + grp * 4 + col] = db;
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
-        // by rows: products over dv
         const auto dout_row = [&](int r, int s) {
             if constexpr (kBf16) return l.o.row(r, s, grp);
             else return load_straight(dop + (r < m ? r : m - 1) * vstride + s * 32 + grp * 8);
         };
+        // dg's blocks of w (rows i, columns j)
+#pragma unroll 1
+        for (int f = wave; f < kBlocks; f += kWaves) {
+            int it, jt;
+            block_of(f, &it, &jt);
+            const int i0 = it * 16, j = jt * 16 + col;
+            f32x4 ou = {0.f, 0.f, 0.f, 0.f}, xu[2] = {ou, ou}, qk = ou, kk = ou;   // xu: two sums side by side
+#pragma unroll
+            for (int s = 0; s < kVSteps; ++s) {
+                const Frag<3> u = l.U.all(j, s, grp, l.v);
+                ou = mma(dout_row(i0 + col, s), u, ou);
+                xu[s & 1] = mma(l.X.all(i0 + col, s, grp, l.g.x), u, xu[s & 1]);
+            }
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const auto kj = l.k.row(j, s, grp);
+                qk = mma(l.q.row(i0 + col, s, grp), kj, qk);
+                kk = mma(l.k.row(i0 + col, s, grp), kj, kk);
+            }
+            f32x4 w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = i0 + grp * 4 + r;
+                w[r] = j < i && i < m ? decay(l.G[i] - l.G[j]) * (d.scale * qk[r] * ou[r] - kk[r] * (xu[0][r] + xu[1][r])) : 0.f;
+            }
+            // of each column, over the rows from its lane's on
+            w[2] += w[3];
+            w[1] += w[2];
+            w[0] += w[1];
+            const f32x4 g = of_rows(w[0]);   // the lane groups' sums
+            const float last = grp < 3 ? g[3] : 0.f, behind = grp < 2 ? g[2] + last : last, rows_behind = grp < 1 ? g[1] + behind : behind;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                w[r] += rows_behind;
+                if (it == jt && col >= grp * 4 + r) w[r] = 0.f;   // on the diagonal, columns before the row
+            }
+            const float from = sum_columns(w, col), to = sums_to((g[0] + g[1]) + (g[2] + g[3])), before = of_lane<0x111>(to);
+            if (col < 4) l.g.from[f][grp * 4 + col] = from;
+            if (grp == 0) l.g.before[f][col] = before;
+            if (lane == 15) l.g.all[f] = to;
+        }
+        __syncthreads();
+        float gate = 0.f, r_sum = 0.f, c_sum = 0.f;   // gate: dg of token threadIdx.x but for the state's way through the chunk
+        if (threadIdx.x < kChunk) {
+            const int t = threadIdx.x, tb = t >> 4;
+            float db = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                r_sum += l.r[w][t];
+                c_sum += l.c[w][t];
+                db += l.g.db[w][t];
+            }
+            if (t < m) a.dbeta[at + (int64_t)t * d.hv] = db;
+#pragma unroll
+            for (int f = 0; f < kBlocks; ++f) {
+                int it, jt;
+                block_of(f, &it, &jt);
+                if (it == tb) gate += l.g.from[f][t & 15];
+                else if (jt == tb) gate += l.g.before[f][t & 15];
+                else if (it > tb && jt < tb) gate += l.g.all[f];
+            }
+        }
+        __syncthreads();   // read: the pairs take their place
+        if (threadIdx.x < kChunk) {   // r from token t on, c before it
+            const float from = sums_from(r_sum), to = sums_to(c_sum);
+            const auto of = [](float x, int i) { return as_f(__builtin_amdgcn_readlane(as_u(x), i)); };   // a row's whole sum
+            const float r3 = grp < 3 ? of(from, 48) : 0.f, r2 = grp < 2 ? of(from, 32) + r3 : r3;
+            const float c0 = grp > 0 ? of(to, 15) : 0.f, c1 = grp > 1 ? of(to, 31) + c0 : c0;
+            gate += from + (grp < 1 ? of(from, 16) + r2 : r2);
+            gate += of_lane<0x111>(to) + (grp > 2 ? of(to, 47) + c1 : c1);
+        }
+        // by rows: products over dv
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -565,7 +672,7 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
                 }
             }
         }
-        if (tk0 == 0) end = fmaf(l.e[kChunk - 1], dot, end);   // each row of dk once
+        float end = tk0 == 0 ? l.e[kChunk - 1] * dot : 0.f;   // exp(G_C) <S, dS'>, each row of dk once
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) end += __shfl_xor(end, s, 64);
         if (lane == 0) l.ends[wave] = end;
@@ -641,23 +748,10 @@ __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
         pass(std::integral_constant<int, 2>{});
         if (threadIdx.x < kChunk) {
             const int t = threadIdx.x;
-            float s = 0.f, db = 0.f, ends = 0.f;
+            float ends = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                s += l.dG[w][t];
-                db += l.db[w][t];
-                ends += l.ends[w];
-            }
-            if (t == kChunk - 1) s += ends;
-#pragma unroll
-            for (int w = 1; w < 64; w <<= 1) {
-                const float up = __shfl_down(s, w, 64);
-                if (t + w < 64) s += up;
-            }
-            if (t < m) {
-                a.dg[at + (int64_t)t * d.hv] = s;
-                a.dbeta[at + (int64_t)t * d.hv] = db;
-            }
+            for (int w = 0; w < kWaves; ++w) ends += l.ends[w];
+            if (t < m) a.dg[at + (int64_t)t * d.hv] = gate + ends;
         }
     }
     const int col = lane_id() & 15, grp = lane_id() >> 4;
