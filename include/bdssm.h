@@ -547,6 +547,8 @@ int bdssm_kv_commit(const bdssm_kv_shape *shape, int64_t T, const void *k, const
  *   scale multiplies the scores.  No mask but these; cached positions from
  *         ctx_lens[b] on are not seen, whatever their codes, nor are active
  *         tokens that a query does not see, infinities and NaN included.
+ *         Infinities of one sign among a channel of the active values that a
+ *         query sees make its output that infinity; both signs or a NaN, a NaN.
  *   ws    ws_bytes >= bdssm_kv_workspace_bytes(shape, Lq).  Need not be cleared.
  */
 int bdssm_kv_attn_step(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, const void *q,

@@ -296,6 +296,53 @@ __device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
     return frag_of(w[0], w[1], w[2], w[3]);
 }
 
+// A channel's values of eight active tokens as they lie in memory, and as a fragment.
+// `seen` gathers whether any of them is an infinity or a NaN (two bf16 values an
+// instruction, 0 times an fp32 value is a NaN), clear() makes those 0.
+template <typename T>
+struct Tokens;
+template <>
+struct Tokens<uint16_t> {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    struct Seen {
+        u16x2 top = {0, 0};
+        __device__ __forceinline__ bool special() const { return (top.x > top.y ? top.x : top.y) >= 0x7f80; }
+    };
+    uint32_t w[4];
+    __device__ __forceinline__ void put(int j, const uint16_t *p) { w[j / 2] = j & 1 ? w[j / 2] | (uint32_t)*p << 16 : *p; }
+    __device__ __forceinline__ void look(Seen &s) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.top = __builtin_elementwise_max(s.top, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+            if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+        }
+    }
+    __device__ __forceinline__ Frag<1> frag() const { return Frag<1>{{frag_of(w[0], w[1], w[2], w[3])}}; }
+};
+template <>
+struct Tokens<float> {
+    struct Seen {
+        float zero = 0.f;
+        __device__ __forceinline__ bool special() const { return zero != zero; }
+    };
+    f32x4 v[2];
+    __device__ __forceinline__ void put(int j, const float *p) { v[j / 4][j % 4] = *p; }
+    __device__ __forceinline__ void look(Seen &s) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s.zero = fmaf(v[j / 4][j % 4], 0.f, s.zero);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!(fabsf(v[j / 4][j % 4]) < __builtin_inff())) v[j / 4][j % 4] = 0.f;
+    }
+    __device__ __forceinline__ Frag<3> frag() const { return split_frag<3>(v[0], v[1]); }
+};
+
 // the probabilities' parts
 template <typename T>
 constexpr int kProbParts = sizeof(T) == 2 ? 2 : 3;
@@ -581,34 +628,24 @@ __global__ __launch_bounds__(256, kTiles == 2 && (kD == 128 || sizeof(T) == 4) ?
                             S[t][nt][r] = key < n && key <= pos[nt] ? S[t][nt][r] * a.scale : -__builtin_inff();
                         }
                 }
-                T vals[kChan][8];
-                bool odd = false;   // infinities or NaN that not all of the queries see
+                Tokens<T> vals[kChan];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const T *row = vb + (key0 + j < n ? key0 + j : n - 1) * stride + col;
 #pragma unroll
-                    for (int mt = 0; mt < kChan; ++mt) vals[mt][j] = row[mt * 16];
+                    for (int mt = 0; mt < kChan; ++mt) vals[mt].put(j, row + mt * 16);
                 }
-                if (a.causal) {
+                // Infinities and NaN: 0 in the product (a probability of 0 times them, be
+                // it a hidden token's or a part of a split one, is a NaN), then added
+                typename Tokens<T>::Seen seen;
 #pragma unroll
-                    for (int mt = 0; mt < kChan; ++mt)
+                for (int mt = 0; mt < kChan; ++mt) vals[mt].look(seen);
+                const bool odd = __any(seen.special());
+                if (odd) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) odd |= !(fabsf(Stream<T>::load(&vals[mt][j])) < __builtin_inff());
-                    odd = __any(odd);
-                    if (odd) {   // 0 in the product (a probability of 0 times them is a NaN)
-#pragma unroll
-                        for (int mt = 0; mt < kChan; ++mt)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (!(fabsf(Stream<T>::load(&vals[mt][j])) < __builtin_inff())) vals[mt][j] = T(0);
-                    }
+                    for (int mt = 0; mt < kChan; ++mt) vals[mt].clear();
                 }
-                st.step(S, 1.f, [&](int mt) {
-                    f32x4 x[2];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j / 4][j % 4] = Stream<T>::load(&vals[mt][j]);
-                    return split_frag<kIn>(x[0], x[1]);
-                });
+                st.step(S, 1.f, [&](int mt) { return vals[mt].frag(); });
                 // the queries that see them get them as they are
 #pragma unroll 1
                 for (int j = 0; odd && j < 32 && s * 32 + j < n; ++j) {
