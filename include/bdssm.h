@@ -406,8 +406,9 @@ int bdssm_version(void);
  *           not touch the state, and o and every gradient are 0 there.
  * Keys are expected with beta_t |k_t|^2 <= 2 (normalised keys), without which
  * the recurrence itself diverges.  Inputs are finite but for g: whole chunks of
- * 64 tokens are worked on at once, and an infinity or NaN may reach the tokens
- * before it in its chunk too.  In bdssm_delta_scan and its backward a beta of
+ * 64 tokens are worked on at once, and an infinity or NaN (or an fp32 magnitude
+ * that bf16 rounds to infinity, 3.39e38) may reach the tokens before it in its
+ * chunk too.  In bdssm_delta_scan and its backward a beta of
  * less than 2^-64 counts as 2^-64 (no difference in 32 bits but to a state and
  * inputs of that size); dv is 0 there.
  * Limits: d_k and d_v 64 or 128; heads_v a multiple of heads_k, at most 65535;

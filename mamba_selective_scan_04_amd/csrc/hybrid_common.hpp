@@ -16,12 +16,13 @@
 //
 // Precision.  States, corrections and their adjoints are fp32.  A product with
 // an fp32 operand runs on bf16 matrix instructions by splitting the operand
-// into bf16 parts: three parts cut by truncation hold all 24 bits of an fp32
-// value (8 each), so a product with a bf16 operand is exact up to the fp32
-// accumulation at three instructions; two fp32 operands take the six products
-// of parts i, j with i + j <= 2 (what is left out is below 2^-23 of the term).
-// Two parts (the second rounded to nearest) leave an error of at most 2^-16 of
-// the value and serve where the result is rounded to bf16.
+// into bf16 parts, each the rest rounded to nearest: three hold all 24 bits of an
+// fp32 value (the second is at most 2^-8 of it, the third 2^-17), so a product with
+// a bf16 operand is exact up to the fp32 accumulation at three instructions; two
+// fp32 operands take the six products of parts i, j with i + j <= 2 (what is left
+// out is at most 2^-24 + 2^-34 of the term, of either sign).  Two parts leave an
+// error of at most 2^-17 of the value and serve where the result is rounded to bf16.
+// (Parts cut by truncation cost the same and leave out up to 2^-21, all of one sign.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -57,8 +58,8 @@ __device__ __forceinline__ uint32_t pk_cut(float a, float b) {
 }
 
 // a less the low (b less the high) bf16 of a pair, in one instruction: the dot
-// product with (-1, 0) or (0, -1) on top of a.  Exact where the pair was cut from
-// (a, b).  The factors are kept in scalar registers: as inline constants of
+// product with (-1, 0) or (0, -1) on top of a.  Exact where the pair is (a, b)
+// rounded.  The factors are kept in scalar registers: as inline constants of
 // this instruction they came out as other values.
 __device__ __forceinline__ float less_low(float a, uint32_t pair) {
     uint32_t f = 0x0000bf80u;
@@ -71,20 +72,15 @@ __device__ __forceinline__ float less_high(float b, uint32_t pair) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, f), b, false);
 }
 
-// (a, b) as kParts packed bf16 pairs whose sum is the pair: one part rounds to
-// nearest; two: the second rounds what the first leaves; three are exact.
+// (a, b) as kParts packed bf16 pairs, each the rest rounded to nearest: three are exact.
 template <int kParts>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t *out) {
-    if constexpr (kParts == 1) {
-        out[0] = pk_rne(a, b);
-    } else if constexpr (kParts == 2) {
-        out[0] = pk_rne(a, b);
-        out[1] = pk_rne(less_low(a, out[0]), less_high(b, out[0]));
-    } else {
-        out[0] = pk_cut(a, b);
-        const float ra = less_low(a, out[0]), rb = less_high(b, out[0]);
-        out[1] = pk_cut(ra, rb);
-        out[2] = pk_cut(less_low(ra, out[1]), less_high(rb, out[1]));
+    out[0] = pk_rne(a, b);
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) {
+        a = less_low(a, out[i - 1]);
+        b = less_high(b, out[i - 1]);
+        out[i] = pk_rne(a, b);
     }
 }
 
