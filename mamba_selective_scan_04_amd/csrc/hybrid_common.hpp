@@ -203,12 +203,12 @@ __device__ __forceinline__ Frag<3> load_straight(const float *p) {
 typedef __attribute__((address_space(3))) void lds_ptr;
 __device__ __forceinline__ void load_lds(const void *src, uint32_t off, void *base) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr *)base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(src), "s"(at) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(src), "s"(at) : "m0", "memory");
 }
 // ... from a lane's own address
 __device__ __forceinline__ void load_lds(const void *src, void *base) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr *)base);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(at) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(at) : "m0", "memory");
 }
 // Until no more than the kLater youngest memory operations of the wave are under
 // way (they finish in order).
