@@ -31,7 +31,6 @@ constexpr int kChunk = 64;                 // BDSSM_DELTA_CHUNK
 constexpr int kDeltaThreads = 256;
 constexpr int kBlocks = 10;                // 16x16 blocks on and below the diagonal of a chunk's matrix
 constexpr int kFrags = 6;                  // A fragments (16 x 32) that hold them
-constexpr int kFragBytes = 1024;           // of one part: 16 bytes a lane
 
 struct DeltaDims {
     int64_t T;
@@ -762,8 +761,7 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
 }
 
 // Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s (back: from the last
-// segment to the first).  One workgroup per
-// 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave to each
+// segment to the first).  One workgroup per 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave to each
 // 16 rows of M, read as its fragments (store_map).  Serial over the segments, 2 us
 // each at 128 by 128 (16 segments of 12 heads: 35 us; 49 with M by rows, whose loads
 // touched a line for each lane); the next two segments' maps are on their way
@@ -778,43 +776,33 @@ struct JoinArgs {
 
 template <int kDk>
 __global__ __launch_bounds__(kDk * 4) void delta_join_kernel(JoinArgs a) {
-    constexpr int kMine = 1, kSteps = kDk / 32;   // a wave's tiles of 16 rows
+    constexpr int kSteps = kDk / 32;
     __shared__ uint4 part[kSteps][3][64];
     const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4, n = blockIdx.x * 16 + col;
     const int64_t head = blockIdx.y, state = (int64_t)kDk * a.dv;
-    f32x4 h[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) h[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t mine = (int64_t)state_row(wave, grp, 0) * a.dv + n;   // of the lane's four rows, dv apart
+    f32x4 h = {0.f, 0.f, 0.f, 0.f};
     if (a.h_init != nullptr) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) h[i][r] = a.h_init[head * state + (int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n];
+        for (int r = 0; r < 4; ++r) h[r] = a.h_init[head * state + mine + r * a.dv];
     }
     const auto store = [&](float *out) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) out[(int64_t)state_row(wave * kMine + i, grp, r) * a.dv + n] = h[i][r];
+        for (int r = 0; r < 4; ++r) out[mine + r * a.dv] = h[r];
     };
     const auto at = [&](int s) { return head * a.segs + (a.back ? a.segs - 1 - s : s); };
-    // a segment's N and rows of M, loaded two segments ahead
+    // a segment's N and the wave's 16 rows of M, loaded two segments ahead
     struct Map {
-        f32x4 N[kMine], M[kMine][kSteps][2];
+        f32x4 N, M[kSteps][2];
     } m0, m1;
     const auto fetch = [&](int s, Map &to) {
         const float *m = a.agg + at(s) * kDk * (a.dv + kDk);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int tile = wave * kMine + i;
+        for (int r = 0; r < 4; ++r) to.N[r] = m[mine + r * a.dv];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to.N[i][r] = m[(int64_t)state_row(tile, grp, r) * a.dv + n];
+        for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    to.M[i][x][y] = *(const f32x4 *)(m + kDk * a.dv + ((tile * kSteps + x) * 2 + y) * 256 + lane * 4);
-        }
+            for (int y = 0; y < 2; ++y) to.M[x][y] = *(const f32x4 *)(m + kDk * a.dv + ((wave * kSteps + x) * 2 + y) * 256 + lane * 4);
     };
     const int last = a.h_final != nullptr ? a.segs : a.segs - 1;   // maps that are needed
     if (last > 0) fetch(0, m0);
@@ -823,38 +811,28 @@ __global__ __launch_bounds__(kDk * 4) void delta_join_kernel(JoinArgs a) {
         if (a.h_seg != nullptr) store(a.h_seg + at(s) * state);
         if (s >= last) return false;
         __syncthreads();   // the parts of the segment before are read
+        uint32_t lo[3], hi[3];
+        split_pair<3>(h[0], h[1], lo);
+        split_pair<3>(h[2], h[3], hi);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int tile = wave * kMine + i;
-            uint32_t lo[3], hi[3];
-            split_pair<3>(h[i][0], h[i][1], lo);
-            split_pair<3>(h[i][2], h[i][3], hi);
+        for (int p = 0; p < 3; ++p) ((uint2 *)&part[wave / 2][p][lane])[wave & 1] = make_uint2(lo[p], hi[p]);
+        Frag<3> mf[kSteps];
+        h = now.N;
 #pragma unroll
-            for (int p = 0; p < 3; ++p) ((uint2 *)&part[tile / 2][p][lane])[tile & 1] = make_uint2(lo[p], hi[p]);
-        }
-        Frag<3> mf[kMine][kSteps];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            h[i] = now.N[i];
-#pragma unroll
-            for (int x = 0; x < kSteps; ++x) mf[i][x] = split_frag<3>(now.M[i][x][0], now.M[i][x][1]);
-        }
+        for (int x = 0; x < kSteps; ++x) mf[x] = split_frag<3>(now.M[x][0], now.M[x][1]);
         if (s + 2 < last) fetch(s + 2, now);
         __syncthreads();
-        f32x4 odd[kMine];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) odd[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        f32x4 odd = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < kSteps; ++x) {
             Frag<3> y;
 #pragma unroll
             for (int p = 0; p < 3; ++p) y.p[p] = __builtin_bit_cast(bf16x8, part[x][p][lane]);
-            // two sums side by side: each of its own would wait for its last product
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) (x & 1 ? odd : h)[i] = mma(mf[i][x], y, (x & 1 ? odd : h)[i]);
+            // two sums side by side: one of its own would wait for its last product
+            if (x & 1) odd = mma(mf[x], y, odd);
+            else h = mma(mf[x], y, h);
         }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) h[i] += odd[i];
+        h += odd;
         return s + 1 < a.segs;
     };
     for (int s = 0; turn(s, m0) && turn(s + 1, m1); s += 2) {

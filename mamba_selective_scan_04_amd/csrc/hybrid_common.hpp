@@ -12,7 +12,7 @@
 // lane group g = l / 16 hold rows 4g..4g+3 and 16+4g..16+4g+3; taking those
 // eight as k slots 8g..8g+7 makes them a B fragment as they are.  The A operand
 // is then read as two runs of four: columns 4g.. and 16+4g.. of the slice
-// ("paired order" below).
+// ("paired order").
 //
 // Precision.  States, corrections and their adjoints are fp32.  A product with
 // an fp32 operand runs on bf16 matrix instructions by splitting the operand
@@ -167,25 +167,7 @@ struct Stream<float> {
     __device__ static void store(float *p, float v) { *p = v; }
 };
 
-// A fragment in paired order from eight elements of a row: p[0..3], p[16..19].
-__device__ __forceinline__ Frag<1> load_paired(const uint16_t *p) {
-    const uint2 a = *(const uint2 *)p, b = *(const uint2 *)(p + 16);
-    Frag<1> f;
-    f.p[0] = frag_of(a.x, a.y, b.x, b.y);
-    return f;
-}
-__device__ __forceinline__ Frag<3> load_paired(const float *p) {
-    return split_frag<3>(*(const f32x4 *)p, *(const f32x4 *)(p + 16));
-}
-// The same from kParts planes of bf16 parts, `plane` elements apart.
-template <int kParts>
-__device__ __forceinline__ Frag<kParts> load_planes(const uint16_t *p, int plane) {
-    Frag<kParts> f;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) f.p[i] = load_paired(p + i * plane).p[0];
-    return f;
-}
-// ... and with eight consecutive k (both operands read from memory).
+// A fragment of eight consecutive k of a row (both operands read from memory).
 __device__ __forceinline__ Frag<1> load_straight(const uint16_t *p) {
     Frag<1> f;
     f.p[0] = __builtin_bit_cast(bf16x8, *(const uint4 *)p);
