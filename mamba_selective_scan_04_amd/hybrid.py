@@ -8,7 +8,8 @@ The gated delta rule:
 Shapes: q, k [batch, T, heads_k, d_k]; v, o [batch, T, heads_v, d_v]; g (log
 decay), beta [batch, T, heads_v] fp32; states [batch, heads_v, d_k, d_v] fp32;
 lens [batch] int32 or None.  q, k, v, o share fp32 or bf16.  scale None:
-d_k ** -0.5.
+d_k ** -0.5.  ws (delta_scan, delta_scan_bwd, kv_attn_step): the caller's own
+workspace, a contiguous tensor of the library's *_workspace_bytes.
 
 Attention over the paged 8-bit cache:
   kv_cache(n_pages, heads_kv, head_dim, page_len, code) -> KvCache
@@ -28,6 +29,17 @@ import torch
 from .bdssm import _check, _dtype_code, _raise, _workspace, load
 
 DELTA_CHUNK = 64        # BDSSM_DELTA_CHUNK
+
+
+def _room(ws, name, *args):
+    """The workspace to use and its bytes: the caller's, or a new one of what the
+    library asks for (a shape it does not take asks for none: the call says so)."""
+    if ws is None:
+        n = getattr(load(), name)(*args[:-1])
+        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, args[-1])
+        return ws, 0 if ws is None else ws.numel()
+    _check(ws, "ws")   # contiguous: its elements are as many bytes as it has
+    return ws, ws.numel() * ws.element_size()
 
 
 def _p(t):
@@ -107,12 +119,10 @@ def delta_scan(q, k, v, g, beta, scale=None, h_init=None, lens=None, want_o=True
         h_chunks = torch.empty(_chunk_states(s, T), dtype=torch.float32, device=dev)
     _check(h_chunks, "h_chunks", torch.float32, _chunk_states(s, T))
     stream = _stream(k.get_device(), q, v, g, beta, lens, h_init, o, h_final, h_chunks, ws)
-    if ws is None:
-        n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 0)
-        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)   # a bad shape: the call says so
+    ws, room = _room(ws, "bdssm_delta_workspace_bytes", ctypes.byref(s), T, 0, dev)
     rc = load().bdssm_delta_scan(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
                                  _p(h_init), _p(o), _p(h_final), _p(h_chunks), _p(ws),
-                                 0 if ws is None else ws.numel(), stream)
+                                 room, stream)
     _raise("bdssm_delta_scan", rc)
     return o, h_final, h_chunks
 
@@ -132,12 +142,10 @@ def delta_scan_bwd(q, k, v, g, beta, h_chunks, do, scale=None, lens=None, dh_fin
     stream = _stream(k.get_device(), q, v, g, beta, lens, h_chunks, do, dh_final, ws)
     dq, dk, dv, dg, dbeta = (torch.empty_like(x) for x in (q, k, v, g, beta))
     dh = torch.empty(_state(s), dtype=torch.float32, device=dev) if want_dh_init else None
-    if ws is None:
-        n = load().bdssm_delta_workspace_bytes(ctypes.byref(s), T, 1)
-        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, dev)
+    ws, room = _room(ws, "bdssm_delta_workspace_bytes", ctypes.byref(s), T, 1, dev)
     rc = load().bdssm_delta_scan_bwd(ctypes.byref(s), T, _p(q), _p(k), _p(v), _p(g), _p(beta), scale, _p(lens),
                                      _p(h_chunks), _p(do), _p(dh_final), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta),
-                                     _p(dh), _p(ws), 0 if ws is None else ws.numel(), stream)
+                                     _p(dh), _p(ws), room, stream)
     _raise("bdssm_delta_scan_bwd", rc)
     return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dh_init": dh}
 
@@ -232,12 +240,10 @@ def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, 
         o = torch.empty_like(q)
     _check(o, "o", k.dtype, tuple(q.shape))
     stream = _stream(k.get_device(), q, v, page_table, ctx_lens, lens, o, ws, *cache)
-    if ws is None:
-        n = load().bdssm_kv_workspace_bytes(ctypes.byref(s), Lq)
-        ws = _workspace(n if n != ctypes.c_size_t(-1).value else 0, k.device)   # a bad shape: the call says so
+    ws, room = _room(ws, "bdssm_kv_workspace_bytes", ctypes.byref(s), Lq, k.device)
     rc = load().bdssm_kv_attn_step(ctypes.byref(s), L, Lq, _p(q), _p(k), _p(v), _p(cache.k), _p(cache.k_scale),
                                    _p(cache.v), _p(cache.v_scale), _p(page_table), _p(ctx_lens), _p(lens),
                                    1 if causal else 0, float(s.head_dim ** -0.5 if scale is None else scale), _p(o),
-                                   _p(ws), 0 if ws is None else ws.numel(), stream)
+                                   _p(ws), room, stream)
     _raise("bdssm_kv_attn_step", rc)
     return o
