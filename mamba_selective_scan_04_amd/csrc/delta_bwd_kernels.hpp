@@ -142,7 +142,7 @@ struct Adjoint {
 };
 
 // Bound as the forward's chain by a step's latency: 8 rows of 4,096 bf16 tokens of
-// 12 heads of 128 (192 workgroups, one a CU, unsegmented) in 390 to 408 us, 6.2 us a
+// 12 heads of 128 (192 workgroups, one a CU, unsegmented) in 359 us, 5.6 us a
 // chunk, 100 KB of it read and written by each workgroup.  kTwo as in the forward's
 // chain.
 template <typename T, int kDk, bool kAgg, bool kTwo>
@@ -343,9 +343,12 @@ struct GradLds {
 // turn, two result tiles to a B fragment as they stand, and shared through LDS.
 // One workgroup a CU: the tiles, the matrices and U, X take nearly all of its LDS,
 // and the states are read straight into fragments.  8 rows of 4,096 bf16 tokens of
-// 12 heads of 128: 805 to 841 us for 1.7 GB (2.1 TB/s), in which matrix instructions are
-// busy for 160 us, LDS for 200 and other vector instructions for 210; what it
-// waits for is its own start (loading a chunk with nothing else to do: 40%).
+// 12 heads of 128: 828 us for 1.7 GB (2.1 TB/s), in which matrix instructions are
+// busy for 162 us, LDS for 193 and other vector instructions for 249; its waves wait
+// for memory or a barrier 47% of the time, most of it while a chunk is loaded.  The
+// blocks of w are 65 us of it: their three parts of U and X are read for themselves.
+// fp32 streams of 128 by 128 spill (10 vector registers, 43 with shared heads): the
+// same training layer takes 3.4 ms in fp32.
 template <typename T, int kDk, int kDv, bool kShared>
 __global__ __launch_bounds__(kDv * 4, 1) void delta_grad_kernel(GradArgs<T> a) {
     using L = GradLds<T, kDk, kDv>;

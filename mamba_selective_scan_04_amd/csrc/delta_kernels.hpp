@@ -244,8 +244,8 @@ __device__ __forceinline__ void block_of(int tile, int *it, int *jt) {
 // by 16x16 blocks: wave j inverts diagonal block j by substitution (a lane per
 // column), then runs down block column j: X_i = inv_ii sum_k N_ik X_k, in fp32
 // matrix instructions, X_k staying in registers.  Bound by memory where there are
-// chunks enough: 65,536 bf16 tokens of 12 heads of 128 in 181 us, 0.76 GB of tokens
-// in and matrices out at 4.2 TB/s; W in three parts, so that U keeps its 32 bits.
+// chunks enough: 65,536 bf16 tokens of 12 heads of 128 in 160 us, 0.76 GB of tokens
+// in and matrices out at 4.7 TB/s; W in three parts, so that U keeps its 32 bits.
 template <typename T, int kDk, int kPF>
 __global__ __launch_bounds__(kDeltaThreads, sizeof(T) == 2 ? 3 : 1) void delta_prep_kernel(const T *__restrict__ q, const T *__restrict__ k,
                                                                   const float *__restrict__ g,
@@ -661,10 +661,11 @@ __device__ __forceinline__ ChainPlace chain_place(int cols) {
 
 // Bound by the latency of a step (products with the state, W, P, the state's
 // update, each waiting for the one before) times the row's chunks: 3.3 us a step
-// of 128 by 128 with outputs, whatever the batch.  Where workgroups fill the chip
-// no unit is busy above 40% (65,536 bf16 tokens of 12 heads of 128: the aggregate
-// pass in 433 us and the outputs in 458 us; matrix instructions 37% of the cycles,
-// LDS 30%, other vector instructions 25%): 64 columns a workgroup, because 16 a
+// of 128 by 128 with outputs while workgroups have a CU of their own (5.9 where it
+// writes its chunk states too).  Where workgroups fill the chip
+// no unit is busy above 42% (65,536 bf16 tokens of 12 heads of 128: the aggregate
+// pass in 373 us and the outputs in 355 us; matrix instructions 42% and 33% of the
+// cycles, LDS 35% and 25%, other vector instructions 28% and 20%): 64 columns a workgroup, because 16 a
 // wave is what its S, R, U, O and fragments leave room for at two workgroups a CU.
 //
 // kTwo: a second set of tiles in LDS, filled while a step computes: one
@@ -763,8 +764,8 @@ __global__ __launch_bounds__(kDeltaThreads, kTwo || sizeof(T) == 4 ? 1 : 2) void
 // Through the segments: h[0] = h_init, h[s + 1] = M_s h[s] + N_s (back: from the last
 // segment to the first).  One workgroup per 16 columns and head: the state in LDS parts (B fragments of 32 dk), a wave to each
 // 16 rows of M, read as its fragments (store_map).  Serial over the segments, 2 us
-// each at 128 by 128 (16 segments of 12 heads: 35 us; 49 with M by rows, whose loads
-// touched a line for each lane); the next two segments' maps are on their way
+// each at 128 by 128 (16 segments of 12 heads: 33 us; with M by rows, whose loads
+// touched a line for each lane, 49 where this took 35); the next two segments' maps are on their way
 // meanwhile.
 struct JoinArgs {
     const float *agg, *h_init;   // h_init null: zero
@@ -1018,7 +1019,7 @@ __global__ __launch_bounds__(64) void delta_step_kernel(StepArgs<T> a) {
 // n + nt, so that a lane's pairs of columns are neighbours in memory).  U comes by
 // substitution over the 16 tokens, (I + diag(beta) A) U = diag(beta) R, each
 // token's row of U handed to the other lane groups in turn.  64 rows of 16 heads of
-// 128 by 128 and 16 tokens: 33 us for 147 MB (4.4 TB/s; by token 54), bound by
+// 128 by 128 and 16 tokens in place: 34 us for 147 MB (4.3 TB/s; by token 54), bound by
 // memory and a wave's start and end: two waves a SIMD, three spill and take 42.  The
 // state goes on in three bf16 parts, so that it keeps its 32 bits.
 

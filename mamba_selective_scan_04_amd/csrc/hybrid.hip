@@ -70,14 +70,14 @@ int check_delta(const bdssm_delta_shape *s, int64_t T) {
 // once (three workgroups of 64 columns a CU, two for fp32 streams): another round
 // of them costs more than shorter segments give.  Nor more than makes the two
 // chains' steps and the join's (a sixth of theirs) least: n^2 = 4 chunks is near
-// that.  Microseconds of the forward, bf16, 128 by 128:
-//   1 row of 65,536 tokens, 12 heads   1: 5096   10: 1239   16 (the rule's): 966   24: 1101
-//   4 rows of 4,096 tokens, 16 heads   1: 424    3 (the rule's): 359   6: 392   16: 471
-//   8 rows of 4,096 tokens, 12 heads   1 (the rule's): 474   2: 502   4: 548
-//   1 row of 2,048 tokens, 2 heads     1: 149    4: 86   8: 71   12: 76   24: 101
-//   1 row of 1,024 tokens, 1 head of 64 by 64   1: 62   4: 45   8 (the rule's): 39   12: 41
-// Backward the same of the adjoint's passes, whose larger stages leave room for two
-// workgroups a CU (fp32: one): the first of these 6890 us whole, 2990 in 10 segments.
+// that.  Backward the same of the adjoint's passes, whose larger stages leave room
+// for two workgroups a CU (fp32: one).  Microseconds of the forward / the backward
+// (the rule's counts in the last column), bf16, 128 by 128 but the last:
+//   1 row of 65,536 tokens, 12 heads  1: 4071 / 7017  10: 1026 / 3125  16: 926 / 3075  24: 1060 / 3202   16 / 10
+//   4 rows of 4,096 tokens, 16 heads  1: 312 / 956    3: 306 / 975     6: 338 / 1039   16: 409 / 1105    3 / 1
+//   8 rows of 4,096 tokens, 12 heads  1: 348 / 1272   2: 420 / 1424    4: 465 / 1498                     1 / 1
+//   1 row of 2,048 tokens, 2 heads    1: 119 / 188    4: 71 / 126      8: 56 / 100     24: 77 / 115      11 / 11
+//   1 row of 1,024 tokens, 1 of 64    1: 50 / 85      4: 35 / 68       8: 30 / 58      12: 33 / 61       8 / 8
 // BDSSM_DELTA_SEGMENTS forces a count (tests).
 int delta_segments(const bdssm_delta_shape *s, int64_t chunks, bool bwd) {
     const int64_t blocks = s->batch * s->heads_v * ((s->d_v + s->d_k) / 64);
@@ -182,11 +182,21 @@ KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
 // A wave's query tiles: two where there are more than 16 rows (64 accumulators at
 // 128 channels; four tiles' 128 made the compiler spill, and ran at half the
 // speed), but one for fp32 streams of 128 channels, whose queries take three times
-// the registers (4 rows of 65,536 tokens and 64 queries: 146 us, 190 with two
-// tiles, which spill).  Key ranges: until every CU has its workgroups of four waves, but at
-// least one step of 32 keys for each wave of a range; beyond that up to three
-// times as many, of at least 2,048 keys, so that rows of different lengths (which
-// only the GPU knows) even out.
+// the registers (4 rows of 65,536 tokens and 64 queries: 138 us; 190 with two
+// tiles, which spilled, where one took 146).  Key ranges: 512 workgroups, two a CU,
+// as many as the 66 KB of LDS of 128 channels leave room for (64 channels': three
+// or four a CU, and no faster for it), but at least one step of 32 keys for each
+// wave of a range; beyond that up to three times as many, of at least 2,048 keys,
+// so that rows of different lengths (which only the GPU knows) even out.  The table's
+// width stands for the context, so a table wider than the rows' contexts makes
+// shorter ranges than these.  Microseconds by the number of ranges, the rule's in
+// brackets:
+//   64 rows of up to 8,192, 64 channels   2: 50   3: 45   [4: 42]   6: 44   8: 40   16: 45
+//   16 rows of 8,192, 64 channels         2: 45   [4: 35]   6: 34   8: 36   16: 41   32: 55
+//   16 rows of 8,192, 128 channels        2: 66   3: 60   [4: 50]   6: 60   8: 58   16: 73
+//   1 row of 65,536, 128 channels         32: 38   48: 35   [64: 31]   96: 41   128: 41   256: 58
+//   4 rows of up to 262,144, 128 channels 16: 257   32: 207   [48: 217]   96: 234   128: 249
+//   1 row of 65,536 in a table of 4, 8 and 32 times its width: 41, 47 and 47
 KvPlan kv_plan(const bdssm_kv_shape *s, int64_t Lq) {
     const int64_t rows = Lq * kv_group(s);
     KvPlan p;

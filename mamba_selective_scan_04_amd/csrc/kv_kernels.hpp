@@ -5,9 +5,10 @@
 // Cache.  A page holds page_len tokens of every key/value head, with one scale
 // for each page and head: value = code * scale.  Keys are kept by token
 // ([page_len][d]), values by channel ([d][page_len]): both are then the A
-// operand of their product as they lie in memory (scores: rows keys, sum over
-// d; outputs: rows d, sum over keys), 16 bytes of codes a lane, and no operand
-// passes through LDS.
+// operand of their product in the order in which they lie in memory (scores: rows
+// keys, sum over d; outputs: rows d, sum over keys), 16 bytes of codes a lane.  They
+// go straight from memory into a buffer of each wave's own in LDS, a step ahead,
+// and are read back as fragments.
 #pragma once
 
 #include <type_traits>
@@ -242,10 +243,10 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // channel's row.  32 keys are two pages at most, the same for the whole wave:
 // their numbers and scales come by scalar loads.
 //
-// Probabilities enter their product in two bf16 parts (2^-16; fp32 streams: three,
+// Probabilities enter their product in two bf16 parts (2^-17; fp32 streams: three,
 // exact) after the page's value scale is multiplied in: in one part they would
 // leave as much of an error as the output's own rounding (1.4 times the error of
-// the whole for 2 us less of 32 at 65,536 tokens).  Scores, maxima, sums and
+// the whole for 2 us less at 65,536 tokens).  Scores, maxima, sums and
 // outputs are fp32.  The running maximum moves only when a score passes it by
 // 2^8: probabilities stay below 2^8 and the outputs are seldom rescaled.
 //
@@ -254,13 +255,16 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(CommitArgs<T> a) {
 // through the workspace and kv_join_kernel.
 //
 // Measured at 128 channels, pages of 16, 64 query rows a key head (16 tokens of 4
-// heads, two query tiles): 65,536 e4m3 tokens of 4 heads in 32 us (2.1 TB/s), 4 rows
-// of up to 262,144 int8 tokens in 229 us (2.9 TB/s).  Registers leave two waves a
-// SIMD, whose conversion of codes and softmax keep the vector units busy for 40% of
+// heads, two query tiles), with the join: 65,536 e4m3 tokens of 4 heads in 31 us (2.2
+// TB/s), 4 rows of up to 262,144 int8 tokens in 215 to 256 us from one run to another
+// (2.6 to 3.1 TB/s).  Registers leave two waves a
+// SIMD, whose conversion of codes and softmax keep the vector units busy for 39% of
 // the time (int8's codes take three times as many instructions as e4m3's: with one
 // part 99 us against 83 for 4 rows of 65,536) and wait for the codes in the rest.
 // At 64 channels and 3 query rows (64 rows of up to 8,192 int8 tokens, one tile):
-// 41 us, 4.2 TB/s, bound by memory and the rows' different ends.
+// 46 to 50 us (3.4 to 3.7 TB/s; 42 where the same codes are read again), bound by
+// memory and the rows' different ends.  fp32 streams: 42 us for the first (a tile of
+// queries a wave, in three parts), 138 for 4 rows of 65,536 where bf16 takes 87.
 template <typename T>
 struct AttnArgs {
     const T *q, *k, *v;
@@ -747,7 +751,7 @@ __global__ __launch_bounds__(256, kTiles == 2 && (kD == 128 || sizeof(T) == 4) ?
 
 // Joins the ranges of one query row: a workgroup each.  The ranges' weights in LDS
 // (kMaxSplits at a time), then eight groups of threads go round the ranges, four
-// channels a thread.  4 to 7 us, most of it the launch.
+// channels a thread.  5 to 7 us, most of it the launch.
 constexpr int kMaxSplits = 1024;
 
 template <typename T, int kD>

@@ -33,6 +33,10 @@ void launch_scan_k(const DeltaCall &c, hipStream_t st) {
         a.h_init = c.h_seg;
     }
     const dim3 gc = grid(c.d.dv);
+    // Two sets of tiles while there is a CU for each workgroup.  1,024 tokens of heads of
+    // 128 by 128, us with two / one: 64 workgroups 72 / 77, 192: 88 / 94, 256: 95 / 106,
+    // 288: 153 / 123, 512: 195 / 168 (the backward 160 / 169, 325 / 339, 411 / 428,
+    // 530 / 478, 808 / 771).
     const bool two = sizeof(T) == 2 && (int64_t)a.groups * (c.d.dv / 64) <= 256;
     if (c.o != nullptr) {
         if constexpr (sizeof(T) == 2) {
@@ -65,7 +69,7 @@ void launch_bwd_k(const DeltaCall &c, hipStream_t st) {
         a.h_seg = c.h_seg;
     }
     const dim3 gc = grid(c.d.dv);
-    const bool two = sizeof(T) == 2 && (int64_t)a.groups * (c.d.dv / 64) <= 256;
+    const bool two = sizeof(T) == 2 && (int64_t)a.groups * (c.d.dv / 64) <= 256;   // as the forward
     if constexpr (sizeof(T) == 2) {
         if (two) hipLaunchKernelGGL((delta_adjoint_kernel<T, kDk, false, true>), gc, dim3(kDeltaThreads), 0, st, a);
     }
@@ -95,11 +99,12 @@ void launch_delta_scan<BDSSM_TIN>(const DeltaCall &c, hipStream_t st) {
     else launch_scan_k<BDSSM_TIN, 128>(c, st);
 }
 
-// Tokens from which the step goes 16 at a time (bf16; fp32 streams' parts would not
-// fit the registers).  64 rows of 16 heads of 128 by 128, read only / in place, in
-// us: 4 tokens 19.7 / 26.1 by token and 19.9 / 31.9 by sixteen; 6: 24.6 / 30.2 and
-// 20.3 / 31.9; 8: 29.8 / 35.3 and 20.7 / 31.9; 16: 48.9 / 54.3 and 22.4 / 34.0; 64:
-// 163 / 168 and 62 / 71.
+// Tokens from which the step goes 16 at a time (bf16; fp32 streams go by token at any
+// length).  64 rows of 16 heads of 128 by 128, read only / in place, in us: 4 tokens
+// 19.5 / 26.1 by token and 19.7 / 30.8 by sixteen; 5: 21.9 / 28.0 and 20.0 / 31.1; 6:
+// 24.5 / 30.1 and 20.1 / 31.4; 8: 29.6 / 35.0 and 20.6 / 31.9; 16: 48.9 / 54.5 and
+// 22.3 / 33.9; 64: 163 / 168 and 62 / 71.  Less work (1 or 8 rows, or heads of 64) is
+// the call's 10 to 11 us either way up to 8 tokens, and 16 tokens 12 to 18 by token.
 constexpr int kBlockFrom = 6;
 
 template <typename T>
