@@ -29,8 +29,10 @@ Printed: one JSON line on stdout (progress goes to stderr).
   cpu_baseline the fp64 CPU oracle timed on a bounded sample of the same step
   configs      the other workloads (65K b1, 262K b1 / b4 / b16, the 87M and
                350M training shapes), each with its times, algorithmic GB/s,
-               HBM and issue-slot fractions, errors against the oracle and an
-               oracle time extrapolated from sampled channels
+               HBM or issue-slot fractions and its worst error against the
+               oracle; --config-details: every call's bytes and launch forms,
+               errors by output and an oracle time extrapolated from sampled
+               channels
   roof_probe   the probed FMA, exp2 and scan-mix issue rates and the HBM read
                bandwidth of this chip (libbdssm_probe.so)
 
@@ -815,8 +817,39 @@ def run_training(name, opts, m, synth, torch, steps, warmup, check=True):
     return res
 
 
+def short(x, digits=7):
+    """Every float of a JSON object to `digits` significant digits: no less than
+    a run resolves."""
+    if isinstance(x, float):
+        return float("%.*g" % (digits, x))
+    if isinstance(x, dict):
+        return {k: short(v, digits) for k, v in x.items()}
+    if isinstance(x, (list, tuple)):
+        return [short(v, digits) for v in x]
+    return x
+
+
+def config_brief(r):
+    """A config's record in the printed line: its times and rates and the worst
+    error.  (With all of config_summary the line is longer than what a run's
+    captured output keeps, and nothing of it can be read.)"""
+    of = lambda k, *fs: {f: r[k][f] for f in fs if f in r[k]}  # noqa: E731
+    if "seq" in r:
+        out = {k: of(k, "ms", "GBs", "slot_frac") for k in (
+            "train_scan", "train_scan_blocks", "train_scan_bwd", "train_scan_blocks_bwd", "all_block_step", "full_scan")}
+    else:
+        out = {"step": of("step", "ms", "GBs", "hbm_frac"), "prefill": of("prefill", "ms", "GBs", "hbm_frac", "slot_frac"),
+               "block_step": of("block_step", "us_graph"), "commit": of("commit", "us_graph"),
+               "generation_tokens_per_s": r["generation_tokens_per_s"]}
+        if r.get("baseline_full_scan"):
+            out["baseline_full_scan"] = of("baseline_full_scan", "ms")
+    if "worst_rel_err" in r:
+        out["worst_rel_err"] = r["worst_rel_err"]
+    return short(out, 4)
+
+
 def config_summary(r):
-    """The compact per-workload record of the configs object."""
+    """A config's whole record (--config-details)."""
     if "seq" in r:
         keys = ("train_scan", "train_scan_blocks", "train_scan_bwd", "train_scan_blocks_bwd", "all_block_step",
                 "full_scan")
@@ -845,6 +878,9 @@ def main():
     ap.add_argument("--workload", default="infer_65k_b8")
     ap.add_argument("--no-configs", action="store_true", help="headline workload only (no configs object)")
     ap.add_argument("--config-steps", type=int, default=10, help="timed steps per config")
+    ap.add_argument("--config-details", action="store_true",
+                    help="each config's whole record: bytes, eager and cold launches, errors by output, "
+                         "the oracle's sample (a line of some 20 KB)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-baseline-scan", action="store_true")
     ap.add_argument("--eager", action="store_true", help="launch block steps eagerly (no graph)")
@@ -905,7 +941,7 @@ def main():
         log("[bench] copy calibration: 3 x 1 GiB device copies")
     if "seq" in wl:
         r = run_training(args.workload, args, m, synth, torch, args.steps, args.warmup)
-        print(json.dumps(train_line(args, r, torch)), flush=True)
+        print(json.dumps(short(train_line(args, r, torch))), flush=True)
         return 0
     if args.block_len or args.d_state:
         print("--block-len / --d-state apply to the training workloads", file=sys.stderr)
@@ -921,16 +957,17 @@ def main():
     configs = None
     if default_run and not args.no_configs:
         configs = {}
+        record = config_summary if args.config_details else config_brief
         for name in CONFIG_WORKLOADS:
             if name == args.workload:
-                configs[name] = config_summary(head)
+                configs[name] = record(head)
                 continue
             if "seq" in synth.WORKLOADS[name]:
                 r = run_training(name, argparse.Namespace(), m, synth, torch, args.config_steps, 2)
             else:
                 r = run_inference(name, argparse.Namespace(), m, synth, torch, probe, args.config_steps, 2)
-            configs[name] = config_summary(r)
-    print(json.dumps(inference_line(args, head, probes, configs)), flush=True)
+            configs[name] = record(r)
+    print(json.dumps(short(inference_line(args, head, probes, configs))), flush=True)
     return 0
 
 
