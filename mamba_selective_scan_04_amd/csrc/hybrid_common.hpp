@@ -72,15 +72,18 @@ __device__ __forceinline__ float less_high(float b, uint32_t pair) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, f), b, false);
 }
 
-// (a, b) as kParts packed bf16 pairs, each the rest rounded to nearest: three are exact.
-template <int kParts>
+// (a, b) as kParts packed bf16 pairs, each the rest rounded to nearest: three are
+// exact.  kCut: cut instead (less than 2^-7 of the value is left for the second, 2^-15
+// for the third), so that no finite value has an infinite part, nor a sum of the
+// parts passes it.
+template <int kParts, bool kCut = false>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t *out) {
-    out[0] = pk_rne(a, b);
+    out[0] = kCut ? pk_cut(a, b) : pk_rne(a, b);
 #pragma unroll
     for (int i = 1; i < kParts; ++i) {
         a = less_low(a, out[i - 1]);
         b = less_high(b, out[i - 1]);
-        out[i] = pk_rne(a, b);
+        out[i] = kCut ? pk_cut(a, b) : pk_rne(a, b);
     }
 }
 
@@ -95,13 +98,13 @@ __device__ __forceinline__ bf16x8 frag_of(uint32_t a, uint32_t b, uint32_t c, ui
 }
 
 // two result tiles' registers -> a B fragment in paired order
-template <int kParts>
+template <int kParts, bool kCut = false>
 __device__ __forceinline__ Frag<kParts> split_frag(f32x4 t0, f32x4 t1) {
     uint32_t w[4][kParts];
-    split_pair<kParts>(t0[0], t0[1], w[0]);
-    split_pair<kParts>(t0[2], t0[3], w[1]);
-    split_pair<kParts>(t1[0], t1[1], w[2]);
-    split_pair<kParts>(t1[2], t1[3], w[3]);
+    split_pair<kParts, kCut>(t0[0], t0[1], w[0]);
+    split_pair<kParts, kCut>(t0[2], t0[3], w[1]);
+    split_pair<kParts, kCut>(t1[0], t1[1], w[2]);
+    split_pair<kParts, kCut>(t1[2], t1[3], w[3]);
     Frag<kParts> f;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) f.p[i] = frag_of(w[0][i], w[1][i], w[2][i], w[3][i]);
