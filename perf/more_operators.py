@@ -1,0 +1,521 @@
+"""Cases and plain forms of what stands around the hybrid layer's scans.
+
+* conv: the short causal convolution in front of a scan, in its three uses: a
+  prompt (scan), the active tokens behind a cached state (step), a training
+  step (train).  With width W and channel c
+      p_t = bias_c + sum_{j < W} w_{c,j} u_{t-W+1+j},   y_t = p_t or silu(p_t);
+  the state is the last W - 1 inputs.  Tokens at and behind lens[b] are padding
+  (y = 0, no state, no gradient); where starts[b, t] is set a document begins:
+  no tap reaches in front of it.
+* norm: root-mean-square norm with the residual's addition, to the stream's
+  type or to 8-bit codes with scales, and its gradients.  h = x + res, rounded
+  to res's type; y = w h / sqrt(mean(h^2) + eps).
+* weights: the attention weight that each cached page gets from the active
+  queries, added to what it had.  evict: the pages of least weight leave a row.
+
+run() computes them by elementary torch operations in 32 bits (64 for a norm's
+sum of squares, whose last bit decides codes beside a border), or, with `own`
+set, through this repository's package.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+STREAM = {"bf16": torch.bfloat16, "f32": torch.float32}
+CODE = {"e4m3": torch.float8_e4m3fn, "i8": torch.int8}
+QMAX = {"e4m3": 448.0, "i8": 127.0}
+TINY = 2.0 ** -126
+EPS = 1e-5
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    return [
+        # a 65,536-token prompt: the half of the in-projection that goes to the scan, d_inner 2048
+        dict(name="conv prompt 65k b1", op="conv", use="scan", batch=1, T=65536, ch=2048, extra=2048, width=4, dtype="bf16",
+             silu=True, bias=True, ragged=False, starts=False, init=False),
+        # one sequence, one token: queries, keys and values of 8 + 8 + 16 heads of 128
+        dict(name="conv step b1 token", op="conv", use="step", batch=1, T=1, ch=4096, extra=0, width=4, dtype="bf16",
+             silu=True, bias=False, ragged=False, starts=False, init=True),
+        # sixty-four sequences finish a 16-token block, d_inner 2048
+        dict(name="conv step b64 block", op="conv", use="step", batch=64, T=16, ch=2048, extra=2048, width=4, dtype="bf16",
+             silu=True, bias=True, ragged=True, starts=False, init=True),
+        # a training step's layer of the 87M shape, forward and backward
+        dict(name="conv train 87m", op="conv", use="train", batch=8, T=4096, ch=1536, extra=0, width=4, dtype="bf16",
+             silu=True, bias=True, ragged=False, starts=False, init=False),
+        # packed documents of odd length in fp32, a channel count that no vector divides
+        dict(name="conv train packed f32", op="conv", use="train", batch=2, T=2041, ch=1021, extra=0, width=4, dtype="f32",
+             silu=True, bias=True, ragged=True, starts=True, init=True),
+        # in front of an 8-bit projection of a 65,536-token prompt, d_model 1024, fp32 residual stream
+        dict(name="norm codes 65k", op="norm", out="e4m3", rows=65536, ch=1024, group=0, dtype="bf16", res="f32"),
+        # one 16-token block of one sequence, d_model 768
+        dict(name="norm block b1", op="norm", out="y", rows=16, ch=768, group=0, dtype="bf16", res="bf16"),
+        # a training step's rows of the 87M shape, forward and backward
+        dict(name="norm train 87m", op="norm", out="train", rows=32768, ch=768, group=0, dtype="bf16", res="bf16"),
+        # a denoising step's queries over 65,536 cached tokens
+        dict(name="weights 65k b1", op="weights", batch=1, ctx=65536, Lq=16, heads_q=16, heads_kv=4, d=128, page=16, code="e4m3",
+             dtype="bf16", ragged=False, init=True),
+        # token-by-token decoding of many sequences
+        dict(name="weights decode b64", op="weights", batch=64, ctx=8192, Lq=1, heads_q=12, heads_kv=4, d=64, page=32, code="i8",
+             dtype="bf16", ragged=True, init=True),
+        # four rows of up to 262,144 tokens down to 65,536
+        dict(name="evict 262k b4", op="evict", batch=4, ctx=262144, page=16, budget=4096, sink=4, recent=64, ragged=True),
+        # sixty-four short rows, a few pages over their budget each
+        dict(name="evict decode b64", op="evict", batch=64, ctx=8192, page=32, budget=192, sink=1, recent=4, ragged=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("conv", "conv", "conv", "norm", "norm", "weights", "weights", "evict"))
+    dtype = rng.choice(("bf16", "bf16", "f32"))
+    if op == "conv":
+        use = rng.choice(("scan", "step", "train", "train"))
+        ch = _log(rng, 1, 8192)
+        if rng.random() < 0.6:
+            ch = -(-ch // 8) * 8
+        extra = rng.choice((0, 0, 8, ch, rng.randint(1, 100)))
+        batch, T = _log(rng, 1, 64), _log(rng, 1, 64 if use == "step" else 5000 if use == "train" else 30000)
+        T = max(1, min(T, (40000000 if use == "train" else 60000000) // (batch * (ch + extra))))
+        return dict(op=op, use=use, batch=batch, T=T, ch=ch, extra=extra, width=rng.choice((2, 3, 4, 4)), dtype=dtype,
+                    silu=rng.random() < 0.8, bias=rng.random() < 0.6, ragged=rng.random() < 0.5,
+                    starts=use != "step" and rng.random() < 0.3, init=rng.random() < 0.5)
+    if op == "norm":
+        ch = _log(rng, 1, 20000)
+        if rng.random() < 0.6:
+            ch = -(-ch // 128) * 128
+        out = rng.choice(("y", "train", "train", "e4m3", "i8"))
+        return dict(op=op, out=out, rows=min(_log(rng, 1, 65536), max(1, 20000000 // ch)), ch=ch,
+                    group=128 if ch % 128 == 0 and rng.random() < 0.5 else 0, dtype=dtype,
+                    res=rng.choice(("none", "f32", dtype)))
+    batch, page = _log(rng, 1, 64), rng.choice((16, 32, 64, 128))
+    if op == "evict":
+        ctx = min(_log(rng, 1, 262144), 1048576 // batch)
+        pages = -(-ctx // page)
+        budget = rng.randint(0, pages)
+        sink = rng.randint(0, min(4, budget))
+        return dict(op=op, batch=batch, ctx=ctx, page=page, budget=budget, sink=sink,
+                    recent=rng.randint(0, min(64, budget - sink)), ragged=rng.random() < 0.7)
+    heads_kv, d = rng.choice((1, 2, 3, 4, 8)), rng.choice((64, 128))
+    heads_q = heads_kv * rng.choice((1, 2, 3, 4, 6, 8))
+    Lq = _log(rng, 1, 64)
+    ctx = min(_log(rng, 1, 131072), 120000000 // (batch * heads_kv * d), 60000000 // (batch * heads_q * Lq))
+    return dict(op=op, batch=batch, ctx=max(1, ctx), Lq=Lq, heads_q=heads_q, heads_kv=heads_kv, d=d, page=page,
+                code=rng.choice(("e4m3", "i8")), dtype=dtype, ragged=rng.random() < 0.7, init=rng.random() < 0.7)
+
+
+# ----------------------------------------------------------------- inputs
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed) * 6271 + 29)
+    return g
+
+
+def _randn(gen, *shape):
+    return torch.randn(*shape, generator=gen, device=DEV)
+
+
+def _lens(gen, batch, top, low=0):
+    """Lengths of a padded batch: the first row is full, the last has `low`."""
+    n = low + (torch.rand(batch, generator=gen, device=DEV) * (top - low + 1)).to(torch.int32)
+    n = n.clamp(max=top)
+    n[-1] = low
+    n[0] = top
+    return n.to(torch.int32)
+
+
+def _prepare_conv(c, gen, s, dt):
+    b, T, ch, W = (c[n] for n in ("batch", "T", "ch", "width"))
+    # the projection that u is a part of
+    s["p"] = _randn(gen, b, T, ch + c["extra"]).to(dt)
+    s["u"] = s["p"][..., c["extra"] // 2: c["extra"] // 2 + ch]
+    s["w"] = _randn(gen, ch, W) * W ** -0.5
+    s["bias"] = _randn(gen, ch) * 0.2 if c["bias"] else None
+    s["c"] = _randn(gen, b, W - 1, ch).to(dt) if c["init"] else None
+    s["lens"] = _lens(gen, b, T) if c["ragged"] else None
+    # a document starts about every 200 tokens
+    s["starts"] = torch.rand(b, T, generator=gen, device=DEV) < 1 / 200 if c["starts"] else None
+    if c["use"] == "train":
+        s["dy"] = _randn(gen, b, T, ch).to(dt)
+        s["dc"] = _randn(gen, b, W - 1, ch).to(dt)
+    return s
+
+
+def _prepare_norm(c, gen, s, dt):
+    n = (c["rows"], c["ch"])
+    size = 0.1 + 3 * torch.rand(c["rows"], 1, generator=gen, device=DEV)
+    x = _randn(gen, *n)
+    # a few channels an order of magnitude larger than the rest, as residual streams have
+    big = torch.rand(c["ch"], generator=gen, device=DEV) < 0.01
+    x = torch.where(big, 10 * x, x) * size
+    s["x"] = (x if c["res"] == "none" else 0.3 * _randn(gen, *n)).to(dt)
+    s["res"] = None if c["res"] == "none" else x.to(STREAM[c["res"]])
+    s["w"] = 1 + 0.2 * _randn(gen, c["ch"])
+    if c["out"] == "train":
+        s["dy"] = _randn(gen, *n).to(dt)
+        s["dh"] = None if c["res"] == "none" else _randn(gen, *n).to(s["res"].dtype)
+    return s
+
+
+def _prepare_weights(c, gen, s, dt):
+    b, Lq, hq, hkv, d, page = (c[n] for n in ("batch", "Lq", "heads_q", "heads_kv", "d", "page"))
+    per = -(-c["ctx"] // page) + 1
+    n_pages = b * per + 1
+    s["table"] = torch.randperm(n_pages, generator=gen, device=DEV)[: b * per].reshape(b, per).to(torch.int32).contiguous()
+    n = n_pages * hkv * page * d
+    if c["code"] == "i8":
+        k = torch.randint(-127, 128, (n,), generator=gen, device=DEV, dtype=torch.int8)
+    else:
+        k = (_randn(gen, n) * 120).clamp_(-448, 448).to(CODE[c["code"]])
+    s["kc"] = k.reshape(n_pages, hkv, page, d)
+    unit = 1 / (120 if c["code"] == "e4m3" else 73)  # the codes' spread
+    s["ks"] = unit * (0.5 + torch.rand(n_pages, hkv, generator=gen, device=DEV))
+    # the cache's other half, which the weights do not need
+    s["vc"] = torch.zeros(n_pages, hkv, d, page, device=DEV, dtype=torch.int8).view(k.dtype)
+    s["vs"] = torch.zeros_like(s["ks"])
+    s["ctx"] = _lens(gen, b, c["ctx"], c["ctx"] // 4) if c["ragged"] else torch.full((b,), c["ctx"], dtype=torch.int32, device=DEV)
+    s["lens"] = _lens(gen, b, Lq, 1) if c["ragged"] else None
+    s["q"] = _randn(gen, b, Lq, hq, d).to(dt)
+    s["scale"] = d ** -0.5
+    s["mass"] = _randn(gen, b, per).square() if c["init"] else None
+    # what the attention returned: the cache's part, and up to as much again from active keys
+    w, _ = _scores(s, s["q"].float())
+    top = w.amax(-1, keepdim=True).clamp(min=-1e30)
+    lse = (top[..., 0] + (w - top).exp().sum(-1).log()).clamp(min=-1e30)
+    lse = lse.reshape(b, hkv, hq // hkv, Lq).permute(0, 3, 1, 2).reshape(b, Lq, hq)
+    s["lse"] = (lse + torch.rand(b, Lq, hq, generator=gen, device=DEV) * 0.7).contiguous()
+    return s
+
+
+def prepare(case, seed):
+    gen, c, s = _gen(seed), case, {"case": dict(case)}
+    if c["op"] == "conv":
+        return _prepare_conv(c, gen, s, STREAM[c["dtype"]])
+    if c["op"] == "norm":
+        return _prepare_norm(c, gen, s, STREAM[c["dtype"]])
+    if c["op"] == "weights":
+        return _prepare_weights(c, gen, s, STREAM[c["dtype"]])
+    b, page = c["batch"], c["page"]
+    per = -(-c["ctx"] // page) + 2
+    s["table"] = torch.randperm(b * per, generator=gen, device=DEV).reshape(b, per).to(torch.int32)
+    s["ctx"] = _lens(gen, b, c["ctx"], c["ctx"] // 4) if c["ragged"] else torch.full((b,), c["ctx"], dtype=torch.int32, device=DEV)
+    # a few pages hold most of the weight; many never had any that 32 bits hold
+    mass = (_randn(gen, b, per) * 3 - 4).exp()
+    s["mass"] = torch.where(torch.rand(b, per, generator=gen, device=DEV) < 0.3, torch.zeros_like(mass), mass)
+    return s
+
+
+# ------------------------------------------------------------ plain forms
+
+def _conv(u, w, bias, silu, lens, starts, c):
+    """-> y, last state, both fp32 (u, c fp32)."""
+    b, T, ch = u.shape
+    W = w.shape[1]
+    dev = u.device
+    first = u.new_zeros(b, W - 1, ch) if c is None else c
+    n = torch.full((b,), T, device=dev) if lens is None else lens.clamp(0, T).long()
+    keep = torch.arange(T, device=dev)[None] < n[:, None]
+    u = torch.where(keep[..., None], u, torch.zeros_like(u))       # padding may hold anything
+    x = torch.cat([first, u], 1)                                   # x[:, t + W - 1] is token t
+    doc = torch.zeros(b, T, dtype=torch.int64, device=dev) if starts is None else (starts & keep).long().cumsum(1)
+    doc = torch.cat([doc.new_zeros(b, W - 1), doc], 1)
+    p = u.new_zeros(b, T, ch) if bias is None else bias.expand(b, T, ch)
+    for j in range(W):
+        tap = x[:, j:j + T]
+        if starts is not None:
+            tap = torch.where((doc[:, j:j + T] == doc[:, W - 1:])[..., None], tap, torch.zeros_like(tap))
+        p = p + w[:, j] * tap
+    y = p / (1 + torch.exp(-p)) if silu else p
+    at = n[:, None] + torch.arange(W - 1, device=dev)              # the last W - 1 inputs
+    last = torch.take_along_dim(x, at[..., None], 1)
+    if starts is not None and T:
+        here = torch.take_along_dim(doc, (n + W - 2)[:, None], 1)  # the document of the last token
+        last = torch.where((torch.take_along_dim(doc, at, 1) == here)[..., None], last, torch.zeros_like(last))
+    return torch.where(keep[..., None], y, torch.zeros_like(y)), last
+
+
+def _plain_conv(s):
+    c, dt = s["case"], s["u"].dtype
+    f = lambda x: None if x is None else x.float()  # noqa: E731
+    if c["use"] != "train":
+        y, last = _conv(s["u"].float(), s["w"], s["bias"], c["silu"], s["lens"], s["starts"], f(s["c"]))
+        return dict(y=y.to(dt), c=last.to(dt))
+    first = s["c"] if s["c"] is not None else s["u"].new_zeros(c["batch"], c["width"] - 1, c["ch"])
+    ins = dict(du=s["u"], dw=s["w"], dbias=s["bias"], dc_init=first)
+    ins = {n: x.detach().float().requires_grad_() for n, x in ins.items() if x is not None}
+    with torch.enable_grad():
+        y, last = _conv(ins["du"], ins["dw"], ins.get("dbias"), c["silu"], s["lens"], s["starts"], ins["dc_init"])
+        grads = dict(zip(ins, torch.autograd.grad([y, last], list(ins.values()), [s["dy"].float(), s["dc"].float()])))
+    out = dict(y=y.detach().to(dt), dw=grads["dw"], du=grads["du"].to(dt), dc_init=grads["dc_init"].to(dt))
+    return dict(out, dbias=grads["dbias"]) if s["bias"] is not None else out
+
+
+def _plain_norm(s):
+    c, dt = s["case"], s["x"].dtype
+    h = s["x"] if s["res"] is None else (s["x"].float() + s["res"].float()).to(s["res"].dtype)
+    hf = h.float()
+    r = ((hf.double().square().mean(-1, keepdim=True) + EPS) ** -0.5).float()
+    y = (hf * r) * s["w"]
+    out = {} if s["res"] is None else dict(h=h)
+    if c["out"] == "y":
+        return dict(out, y=y.to(dt))
+    if c["out"] in CODE:
+        q = QMAX[c["out"]]
+        g = y.reshape(c["rows"], -1, c["group"] or c["ch"])
+        scale = (g.abs().amax(-1) / q).clamp(min=TINY)
+        z = (g / scale[..., None]).clamp(-q, q).reshape(y.shape)
+        return dict(out, codes=z.round().to(torch.int8) if c["out"] == "i8" else z.to(CODE["e4m3"]), scales=scale)
+    dy = s["dy"].float()
+    dn = dy * s["w"]
+    n = hf * r
+    dh = r * (dn - n * (dn * n).mean(-1, keepdim=True))
+    if s["dh"] is not None:
+        dh = dh + s["dh"].float()
+        out["dres"] = dh.to(h.dtype)
+    return dict(out, y=y.to(dt), dx=dh.to(dt), dw=(dy * n).sum(0))
+
+
+def _keys(s, b0, b1, to):
+    """Cached keys of rows b0..b1 as [rows, heads, tokens, d] in type `to`."""
+    c = s["case"]
+    t = s["table"][b0:b1].long()
+    k = s["kc"].view(torch.uint8)[t].view(s["kc"].dtype).to(to) * s["ks"][t].to(to)[..., None, None]
+    return k.permute(0, 2, 1, 3, 4).reshape(b1 - b0, c["heads_kv"], -1, c["d"])
+
+
+def _scores(s, q):
+    """[batch, heads_kv, group * Lq, cached positions], -inf where not seen; and which queries there are."""
+    c = s["case"]
+    b, Lq, hq, hkv, d = (c[n] for n in ("batch", "Lq", "heads_q", "heads_kv", "d"))
+    k = _keys(s, 0, b, q.dtype)
+    q = q.reshape(b, Lq, hkv, hq // hkv, d).permute(0, 2, 3, 1, 4).reshape(b, hkv, -1, d)
+    w = s["scale"] * (q @ k.transpose(-1, -2).contiguous())
+    seen = torch.arange(k.shape[2], device=k.device)[None] < s["ctx"][:, None]
+    n = torch.full((b,), Lq, device=k.device) if s["lens"] is None else s["lens"].clamp(0, Lq)
+    there = (torch.arange(Lq, device=k.device)[None] < n[:, None])[:, None, None].expand(b, hkv, hq // hkv, Lq)
+    return w.masked_fill(~seen[:, None, None], -math.inf), there.reshape(b, hkv, -1)
+
+
+def _plain_weights(s):
+    c = s["case"]
+    b, hkv = c["batch"], c["heads_kv"]
+    w, there = _scores(s, s["q"].float())
+    lse = s["lse"].reshape(b, c["Lq"], hkv, -1).permute(0, 2, 3, 1).reshape(b, hkv, -1)
+    p = (w - lse[..., None]).exp().masked_fill(~there[..., None], 0)
+    mass = p.sum((1, 2)).reshape(b, -1, c["page"]).sum(-1)
+    return mass if s["mass"] is None else s["mass"] + mass
+
+
+def _plain_evict(s):
+    c = s["case"]
+    table, mass, ctx = s["table"], s["mass"], s["ctx"].long()
+    b, per = table.shape
+    whole = (ctx // c["page"])[:, None]
+    at = torch.arange(per, device=table.device)[None].expand(b, per)
+    free = (at >= c["sink"]) & (at < whole - c["recent"])          # may leave
+    # the least weight first, equal ones by their place; those that stay behind all of them
+    order = mass.argsort(dim=1, stable=True)
+    order = order.gather(1, (~free.gather(1, order)).int().argsort(dim=1, stable=True))
+    rank = torch.empty_like(order).scatter_(1, order, at.contiguous())
+    gone = (whole - c["budget"]).clamp(min=0)
+    leave = free & (rank < gone)
+    # kept pages, those that left, what lay behind the context
+    cls = torch.where(leave, 1, torch.where(at * c["page"] < ctx[:, None], 0, 2))
+    to = cls.argsort(dim=1, stable=True)
+    moved = torch.where(leave, torch.zeros_like(mass), mass).gather(1, to)
+    return dict(table=table.gather(1, to), ctx=(ctx - gone[:, 0] * c["page"]).to(torch.int32), mass=moved)
+
+
+def _own(s):
+    import mamba_selective_scan_04_amd as m
+    c = s["case"]
+    if c["op"] == "conv":
+        kw = dict(bias=s["bias"], silu=c["silu"], lens=s["lens"])
+        if c["use"] == "step":
+            last = torch.empty(c["batch"], c["width"] - 1, c["ch"], dtype=s["u"].dtype, device=DEV)
+            y = m.conv_step(s["c"], s["u"], s["w"], c_out=last, **kw)
+            return dict(y=y, c=last)
+        y, last = m.conv_scan(s["u"], s["w"], starts=s["starts"], c_init=s["c"], **kw)
+        if c["use"] == "scan":
+            return dict(y=y, c=last)
+        g = m.conv_scan_bwd(s["u"], s["w"], s["dy"], starts=s["starts"], c_init=s["c"], dc_final=s["dc"], want_dc_init=True, **kw)
+        return dict({n: x for n, x in g.items() if x is not None}, y=y)
+    if c["op"] == "norm":
+        out = {}
+        if c["out"] in CODE:
+            codes, scales, h = m.rms_norm_codes(s["x"], s["w"], res=s["res"], eps=EPS, code=CODE[c["out"]], group=c["group"])
+            out = dict(codes=codes, scales=scales)
+        else:
+            y, h, rstd = m.rms_norm(s["x"], s["w"], res=s["res"], eps=EPS, want_rstd=c["out"] == "train")
+            out = dict(y=y)
+        if s["res"] is not None:
+            out["h"] = h
+        if c["out"] == "train":
+            g = m.rms_norm_bwd(h, s["w"], rstd, s["dy"], dh=s["dh"])
+            out.update(dx=g["dx"], dw=g["dw"])
+            if s["res"] is not None:
+                out["dres"] = g["dres"]
+        return out
+    if c["op"] == "weights":
+        return m.kv_attn_weights(m.KvCache(s["kc"], s["ks"], s["vc"], s["vs"]), s["q"], s["lse"], s["table"], s["ctx"],
+                                 lens=s["lens"], scale=s["scale"], mass=s["mass"])
+    table, ctx, mass = m.kv_evict(s["table"], s["ctx"], s["mass"], c["page"], c["budget"], sink=c["sink"], recent=c["recent"])
+    return dict(table=table, ctx=ctx, mass=mass)
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"conv": _plain_conv, "norm": _plain_norm, "weights": _plain_weights, "evict": _plain_evict}[state["case"]["op"]](state)
+
+
+# ------------------------------------------------------------------- work
+
+def work(case):
+    c = case
+    e = 2 if c.get("dtype") == "bf16" else 4
+    if c["op"] == "conv":
+        n = c["batch"] * c["T"] * c["ch"]
+        state = c["batch"] * (c["width"] - 1) * c["ch"] * e
+        par = c["ch"] * (c["width"] + (1 if c["bias"] else 0)) * 4
+        first = state if c["init"] else 0
+        if c["use"] == "train":   # u, dy and dc in; y, du, dc_init and the parameters' gradients out
+            return dict(bytes=4 * n * e + first + 2 * state + 2 * par, flops=(6 * c["width"] + 16) * n)
+        return dict(bytes=2 * n * e + first + state + par, flops=(2 * c["width"] + 4) * n)
+    if c["op"] == "norm":
+        n = c["rows"] * c["ch"]
+        er = {"none": 0, "f32": 4, "bf16": 2}[c["res"]]
+        if c["out"] == "train":   # x, res, dy and dh in; h, y, dx (and dres where its type is another) out
+            other = er if er != e else 0
+            return dict(bytes=n * (4 * e + 3 * er + other) + 8 * c["ch"], flops=18 * n)
+        out = e if c["out"] == "y" else 1 + 4 / (c["group"] or c["ch"])
+        return dict(bytes=n * (e + 2 * er + out) + 4 * c["ch"], flops=6 * n)
+    if c["op"] == "weights":
+        keys = c["batch"] * c["ctx"] * (5 / 8 if c["ragged"] else 1)
+        rows = c["batch"] * c["Lq"] * c["heads_q"]
+        mass = 4 * c["batch"] * (c["ctx"] // c["page"] + 1)
+        return dict(bytes=keys * c["heads_kv"] * c["d"] + rows * (c["d"] * e + 4) + (2 if c["init"] else 1) * mass,
+                    flops=2 * keys * c["Lq"] * c["heads_q"] * c["d"])
+    n = c["batch"] * (c["ctx"] // c["page"] + 2)
+    return dict(bytes=16 * n, flops=4 * n)
+
+
+# ------------------------------------------------------------------ exact
+
+def _exact_conv(s):
+    """Token by token in 64 bits: the last inputs in hand, dropped where a document starts."""
+    c = s["case"]
+    b, T, ch, W = (c[n] for n in ("batch", "T", "ch", "width"))
+    train = c["use"] == "train"
+    n = s["lens"].clamp(0, T).long() if s["lens"] is not None else torch.full((b,), T, device=DEV)
+    live = torch.arange(T, device=DEV)[None] < n[:, None]
+    u = s["u"].double().masked_fill(~live[..., None], 0)
+    w = s["w"].double()
+    bias = s["bias"].double() if s["bias"] is not None else None
+    hist = list((s["c"].double() if s["c"] is not None else torch.zeros(b, W - 1, ch, dtype=torch.float64, device=DEV)).unbind(1))
+    y = torch.zeros(b, T, ch, dtype=torch.float64, device=DEV)
+    # slope of the activation, and the inputs each token saw (for the gradients)
+    slope, saw = (torch.zeros_like(y), [torch.zeros_like(y) for _ in range(W - 1)]) if train else (None, None)
+    keep = (~s["starts"]).double() if s["starts"] is not None else None
+    for t in range(T):
+        on = live[:, t, None]
+        if keep is not None:
+            hist = [torch.where(on, x * keep[:, t, None], x) for x in hist]
+        p = u[:, t] * w[:, W - 1]
+        if bias is not None:
+            p = p + bias
+        for j in range(W - 1):
+            p = p + hist[j] * w[:, j]
+        sg = torch.sigmoid(p) if c["silu"] else None
+        y[:, t] = torch.where(on, p * sg if c["silu"] else p, torch.zeros_like(p))
+        if train:
+            slope[:, t] = sg * (1 + p * (1 - sg)) if c["silu"] else 1.0
+            for j in range(W - 1):
+                saw[j][:, t] = hist[j]
+        later = hist[1:] + [u[:, t]]
+        hist = later if s["lens"] is None else [torch.where(on, x, z) for x, z in zip(later, hist)]
+    if not train:
+        return dict(y=y, c=torch.stack(hist, 1))
+    dy = s["dy"].double().masked_fill(~live[..., None], 0)
+    dp = torch.where(live[..., None], dy * slope, torch.zeros_like(dy))
+    dw = torch.stack([(dp * x).sum((0, 1)) for x in saw] + [(dp * u).sum((0, 1))], 1)
+    du = torch.zeros_like(u)
+    back = list(s["dc"].double().unbind(1))                        # what flows to the inputs in hand
+    zero = torch.zeros_like(back[0])
+    for t in reversed(range(T)):
+        on = live[:, t, None]
+        d = [zero] + back[:-1]
+        d = [x + dp[:, t] * w[:, j] for j, x in enumerate(d)]
+        du[:, t] = torch.where(on, back[-1] + dp[:, t] * w[:, W - 1], zero)
+        if keep is not None:
+            d = [x * keep[:, t, None] for x in d]
+        back = [torch.where(on, x, z) for x, z in zip(d, back)]
+    out = dict(y=y, du=du, dw=dw, dc_init=torch.stack(back, 1))
+    return dict(out, dbias=dp.sum((0, 1))) if bias is not None else out
+
+
+def _exact_norm(s):
+    c = s["case"]
+    h = s["x"] if s["res"] is None else (s["x"].double() + s["res"].double()).to(s["res"].dtype)
+    out = {} if s["res"] is None else dict(h=h.double())
+    h, w = h.double(), s["w"].double()
+    norm = torch.sqrt(h.pow(2).sum(1, keepdim=True) / c["ch"] + EPS)
+    n = h / norm
+    if c["out"] == "y":
+        return dict(out, y=w * n)
+    if c["out"] in CODE:
+        q = QMAX[c["out"]]
+        y = (w * n).reshape(c["rows"], -1, c["group"] or c["ch"])
+        step = (y.abs().max(-1).values / q).clamp(min=TINY)
+        z = (y / step[..., None]).reshape(c["rows"], c["ch"]).float()
+        # e4m3's rounding of a 64-bit quotient (by way of 32 bits); int8's borders are decided in 32 bits
+        return dict(out, codes=z.clamp(-q, q).to(CODE["e4m3"]).double() if c["out"] == "e4m3" else None, scales=step)
+    dy = s["dy"].double()
+    g = dy * w
+    dh = g / norm - h * (g * h).sum(1, keepdim=True) / (c["ch"] * norm ** 3)
+    if s["dh"] is not None:
+        dh = dh + s["dh"].double()
+        out["dres"] = dh
+    return dict(out, y=w * n, dx=dh, dw=torch.einsum("rc,rc->c", dy, n))
+
+
+def _exact_weights(s):
+    c = s["case"]
+    out = torch.zeros(s["table"].shape, dtype=torch.float64, device=DEV) if s["mass"] is None else s["mass"].double()
+    group = c["heads_q"] // c["heads_kv"]
+    for r in range(c["batch"]):
+        n = c["Lq"] if s["lens"] is None else min(max(int(s["lens"][r]), 0), c["Lq"])
+        ctx = int(s["ctx"][r])
+        K = _keys(s, r, r + 1, torch.float64)[0, :, :ctx]
+        got = torch.zeros(s["table"].shape[1] * c["page"], dtype=torch.float64, device=DEV)
+        for h in range(c["heads_q"]):
+            w = s["scale"] * (K[h // group] @ s["q"][r, :n, h].double().T)
+            got[:ctx] += torch.exp(w - s["lse"][r, :n, h].double()).sum(1)
+        out[r] += got.reshape(-1, c["page"]).sum(1)
+    return out
+
+
+def _exact_evict(s):
+    """Row by row on the host: the candidates sorted by weight and place, the least ones taken out."""
+    c = s["case"]
+    mass = s["mass"].double().tolist()
+    for r, row in enumerate(mass):
+        ctx = int(s["ctx"][r])
+        whole, used = ctx // c["page"], -(-ctx // c["page"])
+        free = sorted((row[i], i) for i in range(c["sink"], whole - c["recent"]))
+        gone = {i for _, i in free[:max(0, whole - c["budget"])]}
+        mass[r] = [x for i, x in enumerate(row[:used]) if i not in gone] + [0.0] * len(gone) + row[used:]
+    return dict(table=None, ctx=None, mass=torch.tensor(mass, dtype=torch.float64, device=DEV))
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"conv": _exact_conv, "norm": _exact_norm, "weights": _exact_weights, "evict": _exact_evict}[case["op"]](s)
