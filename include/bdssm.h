@@ -562,6 +562,191 @@ int bdssm_kv_attn_step(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, const
  * shape is invalid. */
 size_t bdssm_kv_workspace_bytes(const bdssm_kv_shape *shape, int64_t Lq);
 
+/*
+ * bdssm_kv_attn_step with one more output:
+ *   lse   NULL, or [batch, Lq, heads_q] fp32 out: the natural logarithm of the
+ *         sum of exp(score) over what the query sees; -inf where it sees
+ *         nothing, and for queries from n on.
+ */
+int bdssm_kv_attn_step_ex(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, const void *q,
+                          const void *k, const void *v, const void *k_cache, const float *k_scale,
+                          const void *v_cache, const float *v_scale, const int32_t *page_table,
+                          const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
+                          void *o, float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The attention weight that the queries give to each cached page:
+ *   out[b, p] = mass[b, p] + sum over queries i < min(Lq, lens[b]), heads h and
+ *               the cached tokens j of page p of exp(scale q_ih . k_j - lse_ih)
+ *   q     [batch, Lq, heads_q, head_dim] stream dtype, as in the attention
+ *   lse   [batch, Lq, heads_q] fp32, what the attention returned: with it a
+ *         query's weights and those of its active tokens sum to 1.  A query of
+ *         lse -inf saw nothing and gives nothing.
+ *   mass  NULL (zero) or [batch, max_pages] fp32: weight from before.
+ *   out   [batch, max_pages] fp32; may be mass (in place).  A position of the
+ *         table behind the context, or that holds no page, keeps mass.
+ * Values are not read.  Sums are taken in a fixed order.
+ */
+int bdssm_kv_attn_weights(const bdssm_kv_shape *shape, int64_t Lq, const void *q, const float *lse,
+                          const void *k_cache, const float *k_scale, const int32_t *page_table,
+                          const int32_t *ctx_lens, const int32_t *lens, float scale,
+                          const float *mass, float *out, hipStream_t stream);
+
+/*
+ * Eviction: of the W = floor(ctx_lens[b] / page_len) whole pages of row b's
+ * context, max(0, W - budget) leave it: those of least mass among all but the
+ * first sink and the last recent ones; of equal mass, those that lie first.
+ * A NaN counts as the largest mass, -0 as 0.
+ *   page_table, ctx_lens, mass  in, as above (mass [batch, max_pages]).
+ *   table_out, mass_out  [batch, max_pages] out: the row's pages in their order,
+ *         without those that left; then those (mass 0), the next that a commit
+ *         writes; then what lay behind the context, as it was.  A partly filled
+ *         last page stays.
+ *   ctx_out [batch] out: the tokens that are left in the context.
+ * The cache itself is not touched: keys keep what position they were given.
+ * Pages that rows share must not be evicted (the next commit would write them).
+ * Limits: sink + recent <= budget; max_pages at most 2^18; page_len as above.
+ */
+int bdssm_kv_evict(int64_t batch, int64_t max_pages, int64_t page_len, int64_t budget, int64_t sink,
+                   int64_t recent, const int32_t *page_table, const int32_t *ctx_lens,
+                   const float *mass, int32_t *table_out, int32_t *ctx_out, float *mass_out,
+                   hipStream_t stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Around the scans.  Both kinds of recurrent layer run their projections
+ * through a short causal convolution, and every layer starts with a norm.
+ *
+ * The short causal convolution.  For each channel by itself, of width W:
+ *   p_t = bias + sum_{j < W} w[j] u_{t-W+1+j},   y_t = p_t, or silu(p_t)
+ *   u       [batch, T, channels] stream dtype, a channel's neighbours next to
+ *           each other; tokens u_stride and rows u_batch_stride elements apart,
+ *           so that u may be a slice of a wider projection, from any element on
+ *   w       [channels, W] fp32;  bias [channels] fp32 or NULL
+ *   lens    NULL, or [batch] int32: tokens at and behind lens[b] are padding
+ *           (values below 0 count as 0, above T as T): whatever they hold, y
+ *           and gradients are 0 there and the state is as if they were not.
+ *   starts  NULL, or [batch, T] uint8: nonzero where a document starts.  No tap
+ *           reaches in front of it (as the delta rule's g of -inf).
+ *   state   [batch, W-1, channels] stream dtype: the inputs of the last W-1
+ *           tokens, the newest last, 0 in front of a document's start.
+ * The two-stream training form, every block from the clean stream's state, is
+ * the call on the blocks as rows (batch * T/L of L tokens), with the clean
+ * tokens in front of each block as c_init.
+ * Limits: W 2, 3 or 4; y, states and gradients (but du) contiguous.
+ */
+typedef struct {
+    int64_t batch;           /* >= 0 */
+    int64_t channels;        /* >= 1 */
+    int64_t width;           /* W: 2, 3 or 4 */
+    int64_t u_stride;        /* elements from a token to the next, >= channels */
+    int64_t u_batch_stride;  /* elements from a row to the next; rows do not overlap */
+    int32_t dtype;           /* bdssm_dtype of u, y and the state */
+} bdssm_conv_shape;
+
+/*
+ * Over whole rows (prefill, training forward).
+ *   silu     nonzero: y = silu(p).
+ *   c_init   NULL (zero) or the state in front of token 0.
+ *   y        [batch, T, channels] out, or NULL (state only).
+ *   c_final  NULL, or out: the state behind the row's last token.
+ */
+int bdssm_conv_scan(const bdssm_conv_shape *shape, int64_t T, const void *u, const float *w,
+                    const float *bias, int silu, const int32_t *lens, const uint8_t *starts,
+                    const void *c_init, void *y, void *c_final, hipStream_t stream);
+
+/*
+ * On the active tokens (T of any length, meant for one token to a block).
+ *   c_cache  NULL (zero) or the state in front of the first token.
+ *   y        NULL (state only), or out.
+ *   c_out    NULL (a denoising step: the cache is read only), or out: the state
+ *            behind the row's last token.  May be c_cache (a commit in place).
+ */
+int bdssm_conv_step(const bdssm_conv_shape *shape, int64_t T, const void *c_cache, const void *u,
+                    const float *w, const float *bias, int silu, const int32_t *lens, void *y,
+                    void *c_out, hipStream_t stream);
+
+/*
+ * Gradients of bdssm_conv_scan, given the same inputs.
+ *   dy        [batch, T, channels] stream dtype: dJ/dy.
+ *   dc_final  NULL (zero) or [batch, W-1, channels] stream dtype: dJ/dc_final.
+ * Outputs, all overwritten:
+ *   du        as u, of strides du_stride and du_batch_stride (what lies between
+ *             the slices is left as it is); stream dtype.
+ *   dw        [channels, W] fp32;  dbias NULL, or [channels] fp32.
+ *   dc_init   NULL, or [batch, W-1, channels] stream dtype (with c_init NULL,
+ *             the gradient at zero).
+ *   ws        ws_bytes >= bdssm_conv_workspace_bytes(shape, T).
+ * Sums are taken in a fixed order: results are bitwise reproducible.
+ */
+int bdssm_conv_scan_bwd(const bdssm_conv_shape *shape, int64_t T, const void *u, const float *w,
+                        const float *bias, int silu, const int32_t *lens, const uint8_t *starts,
+                        const void *c_init, const void *dy, const void *dc_final, void *du,
+                        int64_t du_stride, int64_t du_batch_stride, float *dw, float *dbias,
+                        void *dc_init, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of bdssm_conv_scan_bwd; (size_t)-1 if the shape is invalid. */
+size_t bdssm_conv_workspace_bytes(const bdssm_conv_shape *shape, int64_t T);
+
+/*
+ * Root-mean-square norm with the residual's addition.  For each row:
+ *   h = x + res, rounded to res's type (without res, h is x)
+ *   r = 1 / sqrt(mean(h^2) + eps)        the sum of squares in 64 bits, r rounded to fp32
+ *   y = w (h r)                          in fp32, rounded to the stream's type or to codes
+ *   x, y    [rows, channels] stream dtype
+ *   res, h  [rows, channels] of res_dtype
+ *   w       [channels] fp32;  eps >= 0
+ * Limits: channels at most 32768; res_dtype the stream's, or fp32.
+ */
+typedef struct {
+    int64_t rows;
+    int64_t channels;
+    int32_t dtype;       /* bdssm_dtype of x, y, dy, dx */
+    int32_t res_dtype;   /* bdssm_dtype of res, h, dh, dres; without res, dtype */
+} bdssm_norm_shape;
+
+/*
+ *   res   NULL, or in.
+ *   h     out where there is a res (NULL without one).  May be res (in place).
+ *   rstd  NULL, or [rows] fp32 out: r, for the backward.
+ */
+int bdssm_rms_norm(const bdssm_norm_shape *shape, const void *x, const void *res, const float *w,
+                   double eps, void *y, void *h, float *rstd, hipStream_t stream);
+
+/*
+ * The norm in 8 bits, each `group` channels of a row with one scale: group 0
+ * (the whole row) or 128 (a divisor of channels).
+ *   code    bdssm_code
+ *   codes   [rows, channels] out
+ *   scales  [rows, channels / group] (group 0: [rows]) fp32 out: max(a / m, 2^-126)
+ *           with a the largest finite |y| of the group and m 448 (e4m3) or 127
+ *           (int8); code = y / scale (fp32 divisions) to nearest even.
+ * Infinities become the largest code, NaN a NaN (e4m3) or 0 (int8).
+ */
+int bdssm_rms_norm_codes(const bdssm_norm_shape *shape, const void *x, const void *res,
+                         const float *w, double eps, int code, int64_t group, void *codes,
+                         float *scales, void *h, hipStream_t stream);
+
+/*
+ * Gradients of bdssm_rms_norm.
+ *   h     what the forward wrote (without res: x);  rstd: the same call's.
+ *   dy    [rows, channels] stream dtype: dJ/dy.
+ *   dh    NULL (zero) or [rows, channels] of res_dtype: what reaches h from
+ *         elsewhere (the residual stream behind this layer).
+ * Outputs, overwritten:
+ *   dx    [rows, channels] stream dtype;  dres NULL, or the same of res_dtype
+ *         (the gradient of x + res is that of either);
+ *   dw    [channels] fp32.
+ *   ws    ws_bytes >= bdssm_norm_workspace_bytes(shape).
+ * Sums are taken in a fixed order: results are bitwise reproducible.
+ */
+int bdssm_rms_norm_bwd(const bdssm_norm_shape *shape, const void *h, const float *w,
+                       const float *rstd, const void *dy, const void *dh, void *dx, void *dres,
+                       float *dw, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of bdssm_rms_norm_bwd; (size_t)-1 if the shape is invalid. */
+size_t bdssm_norm_workspace_bytes(const bdssm_norm_shape *shape);
+
 #ifdef __cplusplus
 }
 #endif

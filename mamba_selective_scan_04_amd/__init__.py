@@ -15,5 +15,8 @@ from .bdssm import (  # noqa: F401
 )
 from .hybrid import (  # noqa: F401
     delta_scan, delta_scan_bwd, delta_step, delta_workspace_bytes, DeltaShape, DELTA_CHUNK,
-    kv_cache, kv_commit, kv_attn_step, KvCache, KvShape,
+    kv_cache, kv_commit, kv_attn_step, kv_attn_weights, kv_evict, KvCache, KvShape,
+)
+from .layer import (  # noqa: F401
+    conv_scan, conv_step, conv_scan_bwd, ConvShape, rms_norm, rms_norm_codes, rms_norm_bwd, NormShape,
 )

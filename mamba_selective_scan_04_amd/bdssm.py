@@ -43,7 +43,11 @@ EXPORTS = PLAIN + tuple(f + "_ex" for f in PLAIN) + (
     "bdssm_status_str", "bdssm_version") + (
     # the hybrid layer's other operators (hybrid.py)
     "bdssm_delta_scan", "bdssm_delta_scan_bwd", "bdssm_delta_step", "bdssm_delta_workspace_bytes",
-    "bdssm_kv_commit", "bdssm_kv_attn_step", "bdssm_kv_workspace_bytes")
+    "bdssm_kv_commit", "bdssm_kv_attn_step", "bdssm_kv_workspace_bytes", "bdssm_kv_attn_step_ex",
+    "bdssm_kv_attn_weights", "bdssm_kv_evict",
+    # those around the scans (layer.py)
+    "bdssm_conv_scan", "bdssm_conv_step", "bdssm_conv_scan_bwd", "bdssm_conv_workspace_bytes",
+    "bdssm_rms_norm", "bdssm_rms_norm_codes", "bdssm_rms_norm_bwd", "bdssm_norm_workspace_bytes")
 
 
 class BdssmError(RuntimeError):
@@ -106,6 +110,18 @@ def load():
     lib.bdssm_kv_commit.argtypes = [P, I] + [P] * 10
     lib.bdssm_kv_attn_step.argtypes = [P, I, I] + [P] * 10 + [ctypes.c_int, N, P, P, Z, P]
     lib.bdssm_kv_workspace_bytes.argtypes = [P, I]
+    lib.bdssm_kv_attn_step_ex.argtypes = [P, I, I] + [P] * 10 + [ctypes.c_int, N, P, P, P, Z, P]
+    lib.bdssm_kv_attn_weights.argtypes = [P, I] + [P] * 7 + [N, P, P, P]
+    lib.bdssm_kv_evict.argtypes = [I] * 6 + [P] * 7
+    K, D = ctypes.c_int, ctypes.c_double
+    lib.bdssm_conv_scan.argtypes = [P, I, P, P, P, K] + [P] * 6
+    lib.bdssm_conv_step.argtypes = [P, I, P, P, P, P, K] + [P] * 4
+    lib.bdssm_conv_scan_bwd.argtypes = [P, I, P, P, P, K] + [P] * 6 + [I, I] + [P] * 4 + [Z, P]
+    lib.bdssm_conv_workspace_bytes.argtypes = [P, I]
+    lib.bdssm_rms_norm.argtypes = [P, P, P, P, D] + [P] * 4
+    lib.bdssm_rms_norm_codes.argtypes = [P, P, P, P, D, K, I] + [P] * 4
+    lib.bdssm_rms_norm_bwd.argtypes = [P] * 10 + [Z, P]
+    lib.bdssm_norm_workspace_bytes.argtypes = [P]
     for f in EXPORTS:
         getattr(lib, f).restype = ctypes.c_size_t if "workspace" in f else ctypes.c_int
     lib.bdssm_workspace_bytes.argtypes = [S, I]

@@ -9,7 +9,8 @@ The kernel launchers live in launch_*.hip; each is compiled twice, once per
 stream type (-DBDSSM_TIN=float and -DBDSSM_TIN=uint16_t, the bf16 bits), so
 that the template instantiations spread over parallel compiler processes.
 bdssm.hip holds the scan's C ABI and launch plans, hybrid.hip those of the
-hybrid layer's other operators.  Objects go to _build/.
+hybrid layer's other operators, layer.hip those of the operators around them.
+launch_evict.hip, which knows no stream type, is compiled once.  Objects go to _build/.
 libbdssm_probe.so (csrc/roof_probe.hip) holds the benchmark's
 microbenchmarks; it is not part of the scan library.
 
@@ -33,9 +34,14 @@ HEADERS = [os.path.join(CSRC, h) for h in (
     os.path.join(ROOT, "include", "bdssm.h")]
 # the hybrid layer's operators include none of the scan's kernels
 HYBRID_HEADERS = [os.path.join(CSRC, h) for h in ("hybrid_common.hpp", "delta_kernels.hpp", "delta_bwd_kernels.hpp", "kv_kernels.hpp",
-                                                  "hybrid_launch.hpp",
+                                                  "evict_kernels.hpp", "hybrid_launch.hpp",
                                                   "host_checks.hpp")] + [os.path.join(ROOT, "include", "bdssm.h")]
-HYBRID_UNITS = ("launch_delta", "launch_kv")
+# nor do those around the scans
+LAYER_HEADERS = [os.path.join(CSRC, h) for h in ("hybrid_common.hpp", "kv_kernels.hpp", "layer_common.hpp", "conv_kernels.hpp", "norm_kernels.hpp",
+                                                 "layer_launch.hpp",
+                                                 "host_checks.hpp")] + [os.path.join(ROOT, "include", "bdssm.h")]
+HYBRID_UNITS = ("launch_delta", "launch_kv", "launch_weights")
+LAYER_UNITS = ("launch_conv", "launch_norm")
 LAUNCH_UNITS = ("launch_chunk", "launch_bidir", "launch_block", "launch_bwd", "launch_bwd_general")
 STREAM_TYPES = (("f32", "float"), ("bf16", "uint16_t"))
 LIB = os.path.join(HERE, "libbdssm.so")
@@ -62,8 +68,8 @@ def hipcc():
 
 def units():
     """(source, object, extra flags) of every translation unit."""
-    out = [(os.path.join(CSRC, u + ".hip"), os.path.join(BUILD_DIR, u + ".o"), []) for u in ("bdssm", "hybrid")]
-    for u in LAUNCH_UNITS + HYBRID_UNITS:
+    out = [(os.path.join(CSRC, u + ".hip"), os.path.join(BUILD_DIR, u + ".o"), []) for u in ("bdssm", "hybrid", "launch_evict", "layer")]
+    for u in LAUNCH_UNITS + HYBRID_UNITS + LAYER_UNITS:
         for tag, ctype in STREAM_TYPES:
             out.append((os.path.join(CSRC, u + ".hip"), os.path.join(BUILD_DIR, "%s.%s.o" % (u, tag)),
                         ["-DBDSSM_TIN=" + ctype]))
@@ -72,11 +78,13 @@ def units():
 
 def headers_of(src):
     name = os.path.splitext(os.path.basename(src))[0]
-    return HYBRID_HEADERS if name in HYBRID_UNITS + ("hybrid",) else HEADERS
+    if name in LAYER_UNITS + ("layer",):
+        return LAYER_HEADERS
+    return HYBRID_HEADERS if name in HYBRID_UNITS + ("hybrid", "launch_evict") else HEADERS
 
 
 def sources():
-    return sorted({s for s, _, _ in units()} | set(HEADERS) | set(HYBRID_HEADERS)) + [PROBE_SRC]
+    return sorted({s for s, _, _ in units()} | set(HEADERS) | set(HYBRID_HEADERS) | set(LAYER_HEADERS)) + [PROBE_SRC]
 
 
 def up_to_date():

@@ -1,0 +1,311 @@
+// conv_kernels.hpp -- the short causal convolution in front of a scan, for each
+// channel by itself:
+//   p_t = bias + sum_{j < W} w_j u_{t-W+1+j},   y_t = p_t or silu(p_t),
+// and its gradients
+//   dp_t = dy_t y'(p_t),  du_s = sum_{d < W} w_{W-1-d} dp_{s+d},
+//   dw_j = sum_t dp_t u_{t-W+1+j},  dbias = sum_t dp_t.
+// Inputs in front of the row come from its state (the last W - 1 inputs, kept as
+// they are); a token that starts a document sees none but its own.
+//
+// Memory is the bound: 2 W + 4 operations a value against 4 bytes (bf16).  A lane
+// takes up to eight neighbouring channels (16 bytes) and a chunk of consecutive
+// tokens, keeping the last W - 1 inputs in registers, so that each input is read
+// once but for the W - 1 in front of a chunk.
+#pragma once
+
+#include "layer_common.hpp"
+
+namespace bdssm_dev {
+
+template <typename T>
+struct ConvArgs {
+    const T *u;
+    int64_t ld, batch_ld;      // elements from a token to the next, from a row to the next
+    const float *w, *bias;
+    const int32_t *lens;       // [batch] or null
+    const uint8_t *starts;     // [batch, T] or null
+    const T *c_init;           // [batch, W - 1, ch] or null
+    T *y, *c_final;            // either may be null
+    int64_t T_tokens, jobs;    // jobs: lanes * chunks * batch
+    int64_t chunk, chunks;     // tokens of a chunk, chunks of a row
+    int ch, lanes, silu;
+    // backward
+    const T *dy, *dc_final;
+    T *du, *dc_init;
+    int64_t du_ld, du_batch_ld;
+    float *parts;              // [part][W + 1][ch]
+    int row_lanes;             // lanes of a row of the workgroup (a power of two)
+    int64_t rows;              // chunks in all
+    int groups, n_parts;       // workgroups across the channels, and along the chunks
+};
+
+// 1 / (1 + exp(-p)).  exp as 2^x, whose argument's rounding moves it by |p| 2^-24 of
+// itself at most; the sigmoid moves by as much where it is small (p far below 0) and
+// by less elsewhere.
+__device__ __forceinline__ float sigmoid(float p) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(p * -1.44269504088896341f));
+}
+
+// How many tokens behind the last document's start a token is, as far as taps care.
+__device__ __forceinline__ int age_after(const uint8_t *starts, int64_t t, int age) {
+    return starts != nullptr && starts[t] ? 0 : age + 1;
+}
+constexpr int kOld = 1 << 20;
+
+// The W - 1 inputs in front of token t0 (hist[0] the oldest) and their age.
+template <typename T, int kW, int kN>
+__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int64_t t0, int c0, int n_ch, Run<T, kN> (&hist)[kW - 1]) {
+    const T *ub = a.u + b * a.batch_ld + c0;
+#pragma unroll
+    for (int j = 0; j < kW - 1; ++j) {
+        const int64_t t = t0 - (kW - 1) + j;
+        if (t >= 0) hist[j].load(ub + t * a.ld, n_ch);
+        else if (a.c_init != nullptr) hist[j].load(a.c_init + (b * (kW - 1) + t + kW - 1) * a.ch + c0, n_ch);
+        else hist[j].zero();
+    }
+    int age = kOld;   // of token t0 - 1
+    if (a.starts != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kW - 1; ++j) {
+            const int64_t t = t0 - (kW - 1) + j;
+            if (t >= 0) age = age_after(a.starts + b * a.T_tokens, t, age);
+        }
+    }
+    return age;
+}
+
+template <int kW, int kN>
+__device__ __forceinline__ void conv_weights(const float *w, const float *bias, int c0, int n_ch, float (&wt)[kN][kW], float (&bs)[kN]) {
+    if (n_ch >= kN) {
+        __builtin_memcpy(wt, w + (int64_t)c0 * kW, sizeof wt);
+        if (bias != nullptr) __builtin_memcpy(bs, bias + c0, sizeof bs);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+#pragma unroll
+            for (int j = 0; j < kW; ++j) wt[i][j] = i < n_ch ? w[(int64_t)(c0 + i) * kW + j] : 0.f;
+            bs[i] = i < n_ch && bias != nullptr ? bias[c0 + i] : 0.f;
+        }
+    }
+    if (bias == nullptr) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) bs[i] = 0.f;
+    }
+}
+
+// Without y a lane goes over the row's last W - 1 tokens alone.
+template <typename T, int kW, int kN>
+__global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
+    constexpr int kAhead = 4;   // tokens read at a time
+    const int64_t job = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (job >= a.jobs) return;
+    const int lane = (int)(job % a.lanes);
+    const int64_t chunk = job / a.lanes % a.chunks;
+    const int64_t b = job / a.lanes / a.chunks;
+    const int c0 = lane * kN, n_ch = a.ch - c0;
+    int64_t n = a.T_tokens;
+    if (a.lens != nullptr) n = a.lens[b] < 0 ? 0 : a.lens[b] < n ? a.lens[b] : n;
+    int64_t t0 = chunk * a.chunk, t1 = t0 + a.chunk < a.T_tokens ? t0 + a.chunk : a.T_tokens;
+    if (a.y == nullptr) {
+        t0 = n > kW - 1 ? n - (kW - 1) : 0;
+        t1 = n;
+    }
+    const int64_t stop = t1 < n ? t1 : n;   // of the tokens that are read
+    T *yb = a.y == nullptr ? nullptr : a.y + b * a.T_tokens * a.ch + c0;
+    const bool last = a.c_final != nullptr && (a.y == nullptr || (n > t0 && n <= t1) || (n == 0 && chunk == 0));
+    if (t0 < stop || last) {
+        float wt[kN][kW], bs[kN];
+        conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
+        Run<T, kN> hist[kW - 1];
+        int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
+        const T *ub = a.u + b * a.batch_ld + c0;
+        const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+        for (int64_t t = t0; t < stop; t += kAhead) {
+            Run<T, kN> x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (t + i < stop) x[i].load(ub + (t + i) * a.ld, n_ch);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (t + i >= stop) break;
+                if (starts != nullptr) {
+                    age = age_after(starts, t + i, age);
+#pragma unroll
+                    for (int j = 0; j < kW - 1; ++j)
+                        if (kW - 1 - j > age) hist[j].zero();
+                }
+                if (yb != nullptr) {
+                    float p[kN];
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        p[e] = bs[e];
+#pragma unroll
+                        for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
+                        p[e] = fmaf(wt[e][kW - 1], x[i].at(e), p[e]);
+                    }
+                    if (a.silu) {
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
+                    }
+                    Run<T, kN> out;
+                    out.put(p);
+                    out.store(yb + (t + i) * a.ch, n_ch);
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
+                hist[kW - 2] = x[i];
+            }
+        }
+        if (last) {
+            // kept where no document started behind it (the age of a row of no tokens is none)
+#pragma unroll
+            for (int j = 0; j < kW - 1; ++j) {
+                if (kW - 2 - j > age) hist[j].zero();
+                hist[j].store(a.c_final + (b * (kW - 1) + j) * a.ch + c0, n_ch);
+            }
+        }
+    }
+    if (yb != nullptr) {
+        Run<T, kN> none;
+        none.zero();
+        for (int64_t t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + t * a.ch, n_ch);
+    }
+}
+
+// Gradients.  A lane sweeps its chunk and the W - 1 tokens behind it forward in
+// time, the inputs' last W - 1 values and the W - 1 unfinished sums of du in
+// registers; du_s is whole once dp_{s+W-1} is there.  The parameters' sums of a
+// workgroup's chunks join in LDS in a fixed order and go to `parts`.
+template <typename T, int kW, int kN>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs<T> a) {
+    constexpr int kAhead = 4, kSums = kN * (kW + 1);
+    __shared__ float sums[256 * kSums];
+    const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
+    const int lane = group * a.row_lanes + (int)(threadIdx.x & (a.row_lanes - 1));
+    const int per = 256 / a.row_lanes;                        // chunks of the workgroup at a time
+    const int c0 = lane * kN, n_ch = a.ch - c0;
+    float dw[kN][kW], db[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) dw[e][j] = 0.f;
+    }
+    float wt[kN][kW], bs[kN];
+    if (n_ch > 0) conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
+    for (int64_t row = (int64_t)part * per + threadIdx.x / a.row_lanes; n_ch > 0 && row < a.rows; row += (int64_t)a.n_parts * per) {
+        const int64_t chunk = row % a.chunks;
+        const int64_t b = row / a.chunks;
+        int64_t n = a.T_tokens;
+        if (a.lens != nullptr) n = a.lens[b] < 0 ? 0 : a.lens[b] < n ? a.lens[b] : n;
+        const int64_t t0 = chunk * a.chunk, t1 = t0 + a.chunk < a.T_tokens ? t0 + a.chunk : a.T_tokens;
+        float open[kW - 1][kN];                               // open[d - 1]: du of token t - d
+        Run<T, kN> hist[kW - 1];
+        int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
+#pragma unroll
+        for (int d = 0; d < kW - 1; ++d)
+#pragma unroll
+            for (int e = 0; e < kN; ++e) open[d][e] = 0.f;
+        const T *ub = a.u + b * a.batch_ld + c0, *dyb = a.dy + b * a.T_tokens * a.ch + c0;
+        const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+        T *dub = a.du + b * a.du_batch_ld + c0;
+        for (int64_t t = t0; t < t1 + kW - 1; t += kAhead) {
+            Run<T, kN> x[kAhead], g[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (t + i < n && t + i < t1 + kW - 1) {
+                    x[i].load(ub + (t + i) * a.ld, n_ch);
+                    g[i].load(dyb + (t + i) * a.ch, n_ch);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t s = t + i;
+                if (s >= t1 + kW - 1) break;
+                float dp[kN];
+#pragma unroll
+                for (int e = 0; e < kN; ++e) dp[e] = 0.f;
+                if (s < n) {
+                    if (starts != nullptr) {
+                        age = age_after(starts, s, age);
+#pragma unroll
+                        for (int j = 0; j < kW - 1; ++j)
+                            if (kW - 1 - j > age) hist[j].zero();
+                    }
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        dp[e] = g[i].at(e);
+                        if (a.silu) {
+                            float p = bs[e];
+#pragma unroll
+                            for (int j = 0; j < kW - 1; ++j) p = fmaf(wt[e][j], hist[j].at(e), p);
+                            p = fmaf(wt[e][kW - 1], x[i].at(e), p);
+                            const float sg = sigmoid(p);
+                            dp[e] *= sg * fmaf(p, 1.f - sg, 1.f);
+                        }
+                    }
+                    if (s < t1) {
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) {
+                            db[e] += dp[e];
+#pragma unroll
+                            for (int j = 0; j < kW - 1; ++j) dw[e][j] = fmaf(dp[e], hist[j].at(e), dw[e][j]);
+                            dw[e][kW - 1] = fmaf(dp[e], x[i].at(e), dw[e][kW - 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 1; d < kW; ++d)
+                        if (starts == nullptr || d <= age) {
+#pragma unroll
+                            for (int e = 0; e < kN; ++e) open[d - 1][e] = fmaf(wt[e][kW - 1 - d], dp[e], open[d - 1][e]);
+                        }
+                }
+                // token s - (W - 1) is whole (in front of the row: an input of the state)
+                const int64_t at = s - (kW - 1);
+                const bool state = at < 0 && a.dc_init != nullptr;
+                if (at >= t0 || state) {
+                    if (s >= n && at < n && a.dc_final != nullptr && n - 1 - at <= age) {
+                        // it is in the last state too: of a row of fewer tokens than that, more than once
+                        Run<T, kN> dc;
+                        dc.load(a.dc_final + (b * (kW - 1) + at - n + kW - 1) * a.ch + c0, n_ch);
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) open[kW - 2][e] += dc.at(e);
+                    }
+                    Run<T, kN> out;
+                    out.put(open[kW - 2]);
+                    if (state) out.store(a.dc_init + (b * (kW - 1) + at + kW - 1) * a.ch + c0, n_ch);
+                    else out.store(dub + at * a.du_ld, n_ch);
+                }
+#pragma unroll
+                for (int d = kW - 2; d > 0; --d)
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) open[d][e] = open[d - 1][e];
+#pragma unroll
+                for (int e = 0; e < kN; ++e) open[0][e] = wt[e][kW - 1] * dp[e];
+                if (s < n) {
+#pragma unroll
+                    for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
+                    hist[kW - 2] = x[i];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) sums[(e * (kW + 1) + j) * 256 + threadIdx.x] = dw[e][j];
+        sums[(e * (kW + 1) + kW) * 256 + threadIdx.x] = db[e];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < a.row_lanes * kSums; o += 256) {
+        // neighbouring threads take neighbouring channels of one tap
+        const int wide = a.row_lanes * kN, j = o / wide, cc = o % wide, l = cc / kN, e = cc % kN;
+        const int c = group * wide + cc;
+        if (c >= a.ch) continue;
+        float s = 0.f;
+        for (int r = 0; r < per; ++r) s += sums[(e * (kW + 1) + j) * 256 + r * a.row_lanes + l];
+        a.parts[((int64_t)part * (kW + 1) + j) * a.ch + c] = s;
+    }
+}
+
+}  // namespace bdssm_dev

@@ -1,12 +1,10 @@
 // hybrid.hip -- C ABI and argument checks of the hybrid layer's operators: the
-// gated delta rule and attention over the paged 8-bit cache.  As in bdssm.hip,
+// gated delta rule, attention over the paged 8-bit cache and eviction from it.  As in bdssm.hip,
 // every argument is checked on the host before the first HIP call.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
 #include <stdlib.h>
-
-#include <initializer_list>
 
 #include "bdssm.h"
 #include "host_checks.hpp"
@@ -17,36 +15,6 @@ using namespace bdssm_host;
 namespace {
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kMost = (int64_t)1 << 40;   // elements of one tensor
-constexpr int64_t kMostGroups = 0xffffff;     // workgroups along a grid's axis: its 256 threads each are counted in 32 bits
-
-bool product_fits(std::initializer_list<int64_t> f) {
-    int64_t n = 1;
-    for (int64_t x : f) {
-        if (x == 0) return true;
-        if (x > kMost / n) return false;
-        n *= x;
-    }
-    return true;
-}
-
-bool all_aligned(std::initializer_list<const void *> ps) {
-    for (const void *p : ps)
-        if (!aligned16(p)) return false;
-    return true;
-}
-
-// No output may overlap an input or another output.
-bool distinct(std::initializer_list<Range> ins, std::initializer_list<Range> outs) {
-    for (const Range &o : outs) {
-        for (const Range &i : ins)
-            if (overlaps(o, i)) return false;
-        for (const Range &p : outs)
-            if (&p != &o && overlaps(o, p)) return false;
-    }
-    return true;
-}
-
 // ------------------------------------------------------------- delta rule
 
 int check_delta(const bdssm_delta_shape *s, int64_t T) {
@@ -164,7 +132,7 @@ int check_kv(const bdssm_kv_shape *s, int64_t L) {
 int64_t kv_group(const bdssm_kv_shape *s) { return s->heads_q / s->heads_kv; }
 
 struct KvSizes {
-    size_t q, kv, cache, scale, table, row;
+    size_t q, kv, cache, scale, table, row, lse;
 };
 
 KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
@@ -176,6 +144,7 @@ KvSizes kv_sizes(const bdssm_kv_shape *s, int64_t L, int64_t Lq) {
     z.scale = (size_t)s->n_pages * s->heads_kv * 4;
     z.table = (size_t)s->batch * s->max_pages * 4;
     z.row = (size_t)s->batch * 4;
+    z.lse = (size_t)s->batch * Lq * s->heads_q * 4;
     return z;
 }
 
@@ -243,6 +212,50 @@ KvCall kv_call(const bdssm_kv_shape *s, int64_t L, const void *k, const void *v,
     c.d.ctx = ctx;
     c.d.lens = lens;
     return c;
+}
+
+int attn_step(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const void *q, const void *k, const void *v,
+                       const void *k_cache, const float *k_scale, const void *v_cache, const float *v_scale,
+                       const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
+                       void *o, float *lse, void *ws, size_t ws_bytes, hipStream_t st) {
+    const int rc = check_kv(s, L);
+    if (rc) return rc;
+    if (Lq < 0 || Lq > L) return BDSSM_ERR_SHAPE;
+    if (s->batch == 0 || Lq == 0) return BDSSM_OK;
+    const bool cached = s->n_pages > 0 && s->max_pages > 0;
+    if (!q || !k || !v || !o || !ctx_lens || (cached && (!k_cache || !k_scale || !v_cache || !v_scale || !page_table)))
+        return BDSSM_ERR_NULL;
+    if (!all_aligned({q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, o, lse, ws})) return BDSSM_ERR_ALIGN;
+    const KvSizes z = kv_sizes(s, L, Lq);
+    const KvPlan plan = kv_plan(s, Lq);
+    if (!product_fits({s->batch, s->heads_kv, plan.splits, plan.qtiles}) ||
+        s->batch * s->heads_kv * plan.splits * plan.qtiles > kMostGroups - 8 * plan.qtiles || Lq * kv_group(s) > kMostGroups)
+        return BDSSM_ERR_SHAPE;
+    size_t part = 0;
+    const size_t need = kv_workspace(s, plan, &part);
+    if (!distinct({{q, z.q}, {k, z.kv}, {v, z.kv}, {k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale},
+                   {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row}},
+                  {{o, z.q}, {lse, z.lse}, {ws, need}}))
+        return BDSSM_ERR_ALIAS;
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return BDSSM_ERR_WORKSPACE;
+    KvCall c = kv_call(s, L, k, v, page_table, ctx_lens, lens);
+    c.q = q;
+    c.kc = const_cast<void *>(k_cache);
+    c.ks = const_cast<float *>(k_scale);
+    c.vc = const_cast<void *>(v_cache);
+    c.vs = const_cast<float *>(v_scale);
+    c.o = o;
+    c.lse = lse;
+    c.Lq = Lq;
+    c.causal = causal != 0;
+    c.scale = scale;
+    c.plan = plan;
+    c.part_o = (float *)ws;
+    c.part_ml = (float *)((char *)ws + part);
+    (void)hipGetLastError();
+    if (s->dtype == BDSSM_BF16) launch_kv_attn<uint16_t>(c, st);
+    else launch_kv_attn<float>(c, st);
+    return launch_status();
 }
 
 }  // namespace
@@ -390,42 +403,64 @@ int bdssm_kv_attn_step(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const voi
                        const void *k_cache, const float *k_scale, const void *v_cache, const float *v_scale,
                        const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
                        void *o, void *ws, size_t ws_bytes, hipStream_t st) {
-    const int rc = check_kv(s, L);
+    return attn_step(s, L, Lq, q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, causal, scale, o, nullptr, ws,
+                     ws_bytes, st);
+}
+
+int bdssm_kv_attn_step_ex(const bdssm_kv_shape *s, int64_t L, int64_t Lq, const void *q, const void *k, const void *v,
+                          const void *k_cache, const float *k_scale, const void *v_cache, const float *v_scale,
+                          const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens, int causal, float scale,
+                          void *o, float *lse, void *ws, size_t ws_bytes, hipStream_t st) {
+    return attn_step(s, L, Lq, q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, causal, scale, o, lse, ws, ws_bytes,
+                     st);
+}
+
+int bdssm_kv_attn_weights(const bdssm_kv_shape *s, int64_t Lq, const void *q, const float *lse, const void *k_cache, const float *k_scale,
+                          const int32_t *page_table, const int32_t *ctx_lens, const int32_t *lens, float scale, const float *mass,
+                          float *out, hipStream_t st) {
+    const int rc = check_kv(s, Lq);
     if (rc) return rc;
-    if (Lq < 0 || Lq > L) return BDSSM_ERR_SHAPE;
-    if (s->batch == 0 || Lq == 0) return BDSSM_OK;
-    const bool cached = s->n_pages > 0 && s->max_pages > 0;
-    if (!q || !k || !v || !o || !ctx_lens || (cached && (!k_cache || !k_scale || !v_cache || !v_scale || !page_table)))
-        return BDSSM_ERR_NULL;
-    if (!all_aligned({q, k, v, k_cache, k_scale, v_cache, v_scale, page_table, ctx_lens, lens, o, ws})) return BDSSM_ERR_ALIGN;
-    const KvSizes z = kv_sizes(s, L, Lq);
-    const KvPlan plan = kv_plan(s, Lq);
-    if (!product_fits({s->batch, s->heads_kv, plan.splits, plan.qtiles}) ||
-        s->batch * s->heads_kv * plan.splits * plan.qtiles > kMostGroups - 8 * plan.qtiles || Lq * kv_group(s) > kMostGroups)
-        return BDSSM_ERR_SHAPE;
-    size_t part = 0;
-    const size_t need = kv_workspace(s, plan, &part);
-    if (!distinct({{q, z.q}, {k, z.kv}, {v, z.kv}, {k_cache, z.cache}, {k_scale, z.scale}, {v_cache, z.cache}, {v_scale, z.scale},
-                   {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row}},
-                  {{o, z.q}, {ws, need}}))
+    if (s->batch == 0 || s->max_pages == 0) return BDSSM_OK;
+    if (!out || !page_table || !ctx_lens || (Lq > 0 && (!q || !lse)) || (s->n_pages > 0 && (!k_cache || !k_scale))) return BDSSM_ERR_NULL;
+    if (!all_aligned({q, lse, k_cache, k_scale, page_table, ctx_lens, lens, mass, out})) return BDSSM_ERR_ALIGN;
+    if ((s->max_pages * s->page_len + kWeightKeys - 1) / kWeightKeys > kMostGroups) return BDSSM_ERR_SHAPE;
+    const KvSizes z = kv_sizes(s, 0, Lq);
+    if (!distinct({{q, z.q}, {lse, z.lse}, {k_cache, z.cache}, {k_scale, z.scale}, {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row},
+                   {mass == out ? nullptr : mass, z.table}},
+                  {{out, z.table}}))
         return BDSSM_ERR_ALIAS;
-    if (need > 0 && (ws == nullptr || ws_bytes < need)) return BDSSM_ERR_WORKSPACE;
-    KvCall c = kv_call(s, L, k, v, page_table, ctx_lens, lens);
+    KvCall c = kv_call(s, Lq, nullptr, nullptr, page_table, ctx_lens, lens);
     c.q = q;
+    c.lse = const_cast<float *>(lse);
     c.kc = const_cast<void *>(k_cache);
     c.ks = const_cast<float *>(k_scale);
-    c.vc = const_cast<void *>(v_cache);
-    c.vs = const_cast<float *>(v_scale);
-    c.o = o;
     c.Lq = Lq;
-    c.causal = causal != 0;
     c.scale = scale;
-    c.plan = plan;
-    c.part_o = (float *)ws;
-    c.part_ml = (float *)((char *)ws + part);
+    c.mass = mass;
+    c.mass_out = out;
     (void)hipGetLastError();
-    if (s->dtype == BDSSM_BF16) launch_kv_attn<uint16_t>(c, st);
-    else launch_kv_attn<float>(c, st);
+    if (s->dtype == BDSSM_BF16) launch_kv_weights<uint16_t>(c, st);
+    else launch_kv_weights<float>(c, st);
+    return launch_status();
+}
+
+int bdssm_kv_evict(int64_t batch, int64_t max_pages, int64_t page_len, int64_t budget, int64_t sink, int64_t recent,
+                   const int32_t *page_table, const int32_t *ctx_lens, const float *mass, int32_t *table_out, int32_t *ctx_out,
+                   float *mass_out, hipStream_t st) {
+    if (batch < 0 || batch > 32767 || max_pages < 0 || max_pages > kEvictMostPages) return BDSSM_ERR_SHAPE;
+    if (page_len != 16 && page_len != 32 && page_len != 64 && page_len != 128) return BDSSM_ERR_SHAPE;
+    if (budget < 0 || sink < 0 || recent < 0 || sink > budget || recent > budget - sink) return BDSSM_ERR_SHAPE;
+    if (batch == 0) return BDSSM_OK;
+    if (!ctx_lens || !ctx_out || (max_pages > 0 && (!page_table || !mass || !table_out || !mass_out))) return BDSSM_ERR_NULL;
+    if (!all_aligned({page_table, ctx_lens, mass, table_out, ctx_out, mass_out})) return BDSSM_ERR_ALIGN;
+    const size_t all = (size_t)batch * max_pages * 4, row = (size_t)batch * 4;
+    if (!distinct({{page_table, all}, {ctx_lens, row}, {mass, all}}, {{table_out, all}, {ctx_out, row}, {mass_out, all}}))
+        return BDSSM_ERR_ALIAS;
+    const auto most = [&](int64_t x) { return (int)(x < max_pages ? x : max_pages); };   // of a row's pages
+    const EvictArgs a{page_table, ctx_lens, mass, table_out, ctx_out, mass_out, (int)max_pages, (int)page_len, most(budget), most(sink),
+                      most(recent)};
+    (void)hipGetLastError();
+    launch_kv_evict(a, batch, st);
     return launch_status();
 }
 

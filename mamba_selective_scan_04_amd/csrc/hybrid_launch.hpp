@@ -10,6 +10,7 @@
 #include "bdssm.h"
 #include "delta_bwd_kernels.hpp"
 #include "delta_kernels.hpp"
+#include "evict_kernels.hpp"
 #include "kv_kernels.hpp"
 
 namespace bdssm_host {
@@ -58,6 +59,9 @@ struct KvCall {
     const void *q, *k, *v;
     void *kc, *vc, *o;
     float *ks, *vs, *part_o, *part_ml;
+    float *lse;                  // out of the attention, into the weights
+    const float *mass;
+    float *mass_out;
     int64_t batch, L, Lq;
     int head_dim, code, causal;
     float scale;
@@ -69,6 +73,11 @@ template <typename T>
 void launch_kv_commit(const KvCall &c, hipStream_t st);
 template <typename T>
 void launch_kv_attn(const KvCall &c, hipStream_t st);
+template <typename T>
+void launch_kv_weights(const KvCall &c, hipStream_t st);
+template <> void launch_kv_weights<float>(const KvCall &, hipStream_t);
+template <> void launch_kv_weights<uint16_t>(const KvCall &, hipStream_t);
+void launch_kv_evict(const EvictArgs &a, int64_t batch, hipStream_t st);
 template <> void launch_kv_commit<float>(const KvCall &, hipStream_t);
 template <> void launch_kv_commit<uint16_t>(const KvCall &, hipStream_t);
 template <> void launch_kv_attn<float>(const KvCall &, hipStream_t);

@@ -271,6 +271,7 @@ struct AttnArgs {
     const uint8_t *kc, *vc;
     const float *ks, *vs;
     T *o;
+    float *lse;                // [batch, Lq, heads_q] or null
     float *part_o, *part_ml;   // [unit][split][rows][d], [unit][split][rows][2]
     int64_t L, Lq;
     int splits, qtiles, causal;
@@ -278,6 +279,11 @@ struct AttnArgs {
     int64_t jobs;              // batch * heads_kv * splits
     KvDims d;
 };
+
+// log2 of a sum of powers of two over 2^top, as a natural logarithm; -inf without any
+__device__ __forceinline__ float log_sum(float top, float sum) {
+    return sum != 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -__builtin_inff();
+}
 
 constexpr float kNone = -3.4028235e38f;   // the maximum before any key: the lowest finite value
 
@@ -733,7 +739,13 @@ __global__ __launch_bounds__(256, kTiles == 2 && (kD == 128 || sizeof(T) == 4) ?
     // alone: the row's sums are in every wave's lanes; share them by row
     if (wave == 0 && grp == 0) {
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt) ml[0][nt * 16 + col][1] = sum[nt];
+        for (int nt = 0; nt < kTiles; ++nt) {
+            ml[0][nt * 16 + col][1] = sum[nt];
+            const int64_t row = (int64_t)qt * kRows + nt * 16 + col;
+            if (a.lse != nullptr && row < a.Lq * d.group)
+                a.lse[((int64_t)b * a.Lq + row / d.group) * d.heads_q + h * d.group + row % d.group] =
+                    log_sum(top[nt], row < rows ? sum[nt] : 0.f);
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < kRows * kD / 4; e += 256) {
@@ -757,8 +769,8 @@ __global__ __launch_bounds__(256, kTiles == 2 && (kD == 128 || sizeof(T) == 4) ?
 constexpr int kMaxSplits = 1024;
 
 template <typename T, int kD>
-__global__ __launch_bounds__(kD * 2) void kv_join_kernel(const float *part_o, const float *part_ml, T *o, int64_t L, int64_t Lq,
-                                                         int splits, int qtiles, int kRows, KvDims d) {
+__global__ __launch_bounds__(kD * 2) void kv_join_kernel(const float *part_o, const float *part_ml, T *o, float *lse, int64_t L,
+                                                         int64_t Lq, int splits, int qtiles, int kRows, KvDims d) {
     constexpr int kThreads = kD * 2, kLanes = kD / 4, kGroups = kThreads / kLanes;
     __shared__ float w[kMaxSplits];
     __shared__ float red[kThreads / 64][2];
@@ -768,14 +780,14 @@ __global__ __launch_bounds__(kD * 2) void kv_join_kernel(const float *part_o, co
     int64_t n = L;
     if (d.lens != nullptr) n = d.lens[b] < 0 ? 0 : d.lens[b] < n ? d.lens[b] : n;
     const int64_t nq = n < Lq ? n : Lq;
-    T *op = o + (((int64_t)b * Lq + row / d.group) * d.heads_q + h * d.group + row % d.group) * kD;
+    const int64_t query = ((int64_t)b * Lq + row / d.group) * d.heads_q + h * d.group + row % d.group;
+    T *op = o + query * kD;
     const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes, c = lane * 4;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    float sum = 0.f;
+    float sum = 0.f, top = kNone;
     if (row < nq * d.group) {
         const int64_t unit = ((int64_t)b * d.heads_kv + h) * qtiles + row / kRows;
         const int64_t at = unit * splits * kRows + row % kRows;
-        float top = kNone;
         for (int s = threadIdx.x; s < splits; s += kThreads) top = fmaxf(top, part_ml[(at + (int64_t)s * kRows) * 2]);
 #pragma unroll
         for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
@@ -812,6 +824,7 @@ __global__ __launch_bounds__(kD * 2) void kv_join_kernel(const float *part_o, co
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kThreads / 64; ++i) sum += red[i][1];
+    if (lse != nullptr && threadIdx.x == 0) lse[query] = log_sum(top, sum);
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -26,7 +26,7 @@ void commit_k(const KvCall &c, hipStream_t st) {
 template <typename T, int kCode, int kD>
 void attn_k(const KvCall &c, hipStream_t st) {
     const AttnArgs<T> a{(const T *)c.q, (const T *)c.k, (const T *)c.v, (const uint8_t *)c.kc, (const uint8_t *)c.vc, c.ks, c.vs,
-                        (T *)c.o, c.part_o, c.part_ml, c.L, c.Lq, c.plan.splits, c.plan.qtiles, c.causal,
+                        (T *)c.o, c.lse, c.part_o, c.part_ml, c.L, c.Lq, c.plan.splits, c.plan.qtiles, c.causal,
                         c.scale * 1.44269504088896341f, c.batch * c.d.heads_kv * c.plan.splits, c.d};
     const dim3 g((unsigned)((a.jobs + 7) / 8 * 8 * c.plan.qtiles));
     bool two = false;
@@ -37,7 +37,7 @@ void attn_k(const KvCall &c, hipStream_t st) {
     if (!two) hipLaunchKernelGGL((kv_attn_kernel<T, kCode, kD, 1>), g, dim3(256), 0, st, a);
     if (c.plan.splits > 1) {
         hipLaunchKernelGGL((kv_join_kernel<T, kD>), dim3((unsigned)(c.Lq * c.d.group), (unsigned)c.d.heads_kv, (unsigned)c.batch),
-                           dim3(kD * 2), 0, st, c.part_o, c.part_ml, (T *)c.o, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
+                           dim3(kD * 2), 0, st, c.part_o, c.part_ml, (T *)c.o, c.lse, c.L, c.Lq, c.plan.splits, c.plan.qtiles,
                            c.plan.tiles * 16, c.d);
     }
 }

@@ -1,0 +1,102 @@
+// launch_norm.hip -- launchers of the norm's kernels.
+// Compiled once per stream type (BDSSM_TIN = float, or uint16_t for bf16).
+#include "layer_launch.hpp"
+
+#ifndef BDSSM_TIN
+#error "compiled once per stream type: -DBDSSM_TIN=float or -DBDSSM_TIN=uint16_t"
+#endif
+
+namespace bdssm_host {
+
+template <typename T, typename R>
+NormArgs<T, R> norm_args(const NormCall &c) {
+    NormArgs<T, R> a{};
+    a.x = (const T *)c.x;
+    a.res = (const R *)c.res;
+    a.w = c.w;
+    a.eps = c.eps;
+    a.inv_ch = 1. / c.ch;
+    a.y = (T *)c.y;
+    a.codes = c.codes;
+    a.scales = c.scales;
+    a.group = (int)c.group;
+    a.h = (R *)c.h;
+    a.rstd = c.rstd;
+    a.rows = c.rows;
+    a.ch = c.ch;
+    a.dy = (const T *)c.dy;
+    a.dh = (const R *)c.dh;
+    a.dx = (T *)c.dx;
+    a.dres = (R *)c.dres;
+    a.parts = c.parts;
+    return a;
+}
+
+// calls f with the threads and vectors of a row of ch channels, at most kNormHeld
+template <typename F>
+void with_row(int ch, F &&f) {
+    if (ch <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    else if (ch <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    else if (ch <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    else if (ch <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+}
+
+template <typename T, typename R>
+void norm_k(const NormCall &c, hipStream_t st) {
+    const NormArgs<T, R> a = norm_args<T, R>(c);
+    if (c.ch > kNormHeld) {
+        const dim3 g((unsigned)c.groups), t(1024);
+        if (c.code == kE4m3) hipLaunchKernelGGL((norm_wide_kernel<T, R, kE4m3>), g, t, 0, st, a);
+        else if (c.code == kI8) hipLaunchKernelGGL((norm_wide_kernel<T, R, kI8>), g, t, 0, st, a);
+        else hipLaunchKernelGGL((norm_wide_kernel<T, R, kOutStream>), g, t, 0, st, a);
+        return;
+    }
+    with_row(c.ch, [&](auto threads, auto vecs) {
+        constexpr int kThreads = decltype(threads)::value, kVecs = decltype(vecs)::value;
+        const dim3 g((unsigned)c.groups), t(kThreads > 256 ? kThreads : 256);
+        if (c.code == kE4m3) hipLaunchKernelGGL((norm_kernel<T, R, kE4m3, kThreads, kVecs>), g, t, 0, st, a);
+        else if (c.code == kI8) hipLaunchKernelGGL((norm_kernel<T, R, kI8, kThreads, kVecs>), g, t, 0, st, a);
+        else hipLaunchKernelGGL((norm_kernel<T, R, kOutStream, kThreads, kVecs>), g, t, 0, st, a);
+    });
+}
+
+template <typename T, typename R>
+void norm_bwd_k(const NormCall &c, hipStream_t st) {
+    const NormArgs<T, R> a = norm_args<T, R>(c);
+    if (c.groups == 0) return;
+    if (c.ch > kNormHeld) {
+        hipLaunchKernelGGL((norm_wide_bwd_kernel<T, R>), dim3((unsigned)c.groups), dim3(1024), 0, st, a);
+        return;
+    }
+    with_row(c.ch, [&](auto threads, auto vecs) {
+        constexpr int kThreads = decltype(threads)::value, kVecs = decltype(vecs)::value;
+        hipLaunchKernelGGL((norm_bwd_kernel<T, R, kThreads, kVecs>), dim3((unsigned)c.groups), dim3(kThreads > 256 ? kThreads : 256), 0, st, a);
+    });
+}
+
+template <>
+void launch_norm<BDSSM_TIN>(const NormCall &c, hipStream_t st) {
+    using T = BDSSM_TIN;
+    if constexpr (sizeof(T) == 2) {
+        if (c.wide) return norm_k<T, float>(c, st);
+    }
+    norm_k<T, T>(c, st);
+}
+
+template <>
+void launch_norm_bwd<BDSSM_TIN>(const NormCall &c, hipStream_t st) {
+    using T = BDSSM_TIN;
+    bool done = false;
+    if constexpr (sizeof(T) == 2) {
+        if (c.wide) {
+            norm_bwd_k<T, float>(c, st);
+            done = true;
+        }
+    }
+    if (!done) norm_bwd_k<T, T>(c, st);
+    hipLaunchKernelGGL((parts_sum_kernel<16>), dim3((unsigned)((c.ch + 63) / 64)), dim3(1024), 0, st, c.parts, c.groups, 1, 0, c.ch, c.dw,
+                       nullptr);
+}
+
+}  // namespace bdssm_host

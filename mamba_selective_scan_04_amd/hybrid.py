@@ -14,8 +14,10 @@ workspace, a contiguous tensor of the library's *_workspace_bytes.
 Attention over the paged 8-bit cache:
   kv_cache(n_pages, heads_kv, head_dim, page_len, code) -> KvCache
   kv_commit(cache, k, v, page_table, ctx_lens, lens=None)
-  kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None)
-Shapes: k, v [batch, L, heads_kv, head_dim]; q, o [batch, Lq, heads_q,
+  kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None, want_lse=False)
+  kv_attn_weights(cache, q, lse, page_table, ctx_lens, lens=None, scale=None, mass=None) -> mass
+  kv_evict(page_table, ctx_lens, mass, page_len, budget, sink=0, recent=0) -> (page_table, ctx_lens, mass)
+Shapes: mass [batch, max_pages], lse [batch, Lq, heads_q] fp32; k, v [batch, L, heads_kv, head_dim]; q, o [batch, Lq, heads_q,
 head_dim]; page_table [batch, max_pages], ctx_lens, lens [batch] int32.
 
 All tensors contiguous and on the current CUDA (HIP) device; work
@@ -227,10 +229,13 @@ def kv_commit(cache, k, v, page_table, ctx_lens, lens=None):
     _raise("bdssm_kv_commit", rc)
 
 
-def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None, o=None, ws=None):
+def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, scale=None, o=None, ws=None, want_lse=False,
+                 lse=None):
     """Attention of the active tokens' queries over the cache and the active keys
-    and values -> o.  Lq <= L queries a row: those of its last active tokens.
-    causal: among the active tokens; scale None: head_dim ** -0.5."""
+    and values -> o, or (o, lse) with want_lse or lse.  Lq <= L queries a row: those
+    of its last active tokens.  causal: among the active tokens; scale None:
+    head_dim ** -0.5.  lse [batch, Lq, heads_q] fp32: the logarithm of each query's
+    sum of exponentials, for kv_attn_weights."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [batch, Lq, heads_q, head_dim]")
     s, L = _kv(cache, k, v, page_table, ctx_lens, lens, q.shape[2])
@@ -239,11 +244,78 @@ def kv_attn_step(cache, q, k, v, page_table, ctx_lens, lens=None, causal=False, 
     if o is None:
         o = torch.empty_like(q)
     _check(o, "o", k.dtype, tuple(q.shape))
-    stream = _stream(k.get_device(), q, v, page_table, ctx_lens, lens, o, ws, *cache)
+    if want_lse and lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _check(lse, "lse", torch.float32, q.shape[:3])
+    stream = _stream(k.get_device(), q, v, page_table, ctx_lens, lens, o, lse, ws, *cache)
     ws, room = _room(ws, "bdssm_kv_workspace_bytes", ctypes.byref(s), Lq, k.device)
-    rc = load().bdssm_kv_attn_step(ctypes.byref(s), L, Lq, _p(q), _p(k), _p(v), _p(cache.k), _p(cache.k_scale),
-                                   _p(cache.v), _p(cache.v_scale), _p(page_table), _p(ctx_lens), _p(lens),
-                                   1 if causal else 0, float(s.head_dim ** -0.5 if scale is None else scale), _p(o),
-                                   _p(ws), room, stream)
-    _raise("bdssm_kv_attn_step", rc)
-    return o
+    ins = (ctypes.byref(s), L, Lq, _p(q), _p(k), _p(v), _p(cache.k), _p(cache.k_scale), _p(cache.v), _p(cache.v_scale),
+           _p(page_table), _p(ctx_lens), _p(lens), 1 if causal else 0,
+           float(s.head_dim ** -0.5 if scale is None else scale), _p(o))
+    if lse is None:
+        _raise("bdssm_kv_attn_step", load().bdssm_kv_attn_step(*ins, _p(ws), room, stream))
+        return o
+    _raise("bdssm_kv_attn_step_ex", load().bdssm_kv_attn_step_ex(*ins, _p(lse), _p(ws), room, stream))
+    return o, lse
+
+
+def kv_attn_weights(cache, q, lse, page_table, ctx_lens, lens=None, scale=None, mass=None, out=None):
+    """The attention weight of the queries on each cached page, added to mass
+    (None: zero) -> out [batch, max_pages] fp32 (out=mass: in place).  q, lse and
+    scale: those of kv_attn_step(..., want_lse=True)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, Lq, heads_q, head_dim]")
+    if not isinstance(cache, KvCache) or not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
+        raise ValueError("cache must be a KvCache with k [n_pages, heads_kv, page_len, head_dim]")
+    if cache.k.dtype not in CODES:
+        raise TypeError("the cache's codes must be float8_e4m3fn or int8, got %s" % cache.k.dtype)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    if lse is None:
+        raise ValueError("lse is needed for the weights")
+    batch, Lq, hq, d = q.shape
+    n_pages, hkv, page = cache.k.shape[:3]
+    shape = (batch, page_table.shape[1])
+    _check(q, "q")
+    _check(lse, "lse", torch.float32, (batch, Lq, hq))
+    _check(cache.k, "cache.k", cache.k.dtype, (n_pages, hkv, page, d))
+    _check(cache.k_scale, "cache.k_scale", torch.float32, (n_pages, hkv))
+    _check(page_table, "page_table", torch.int32, shape)
+    _check(ctx_lens, "ctx_lens", torch.int32, (batch,))
+    _check(lens, "lens", torch.int32, (batch,))
+    _check(mass, "mass", torch.float32, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    _check(out, "out", torch.float32, shape)
+    s = KvShape(batch, hq, hkv, d, page, n_pages, shape[1], _dtype_code(q), CODES[cache.k.dtype])
+    stream = _stream(q.get_device(), lse, cache.k, cache.k_scale, page_table, ctx_lens, lens, mass, out)
+    rc = load().bdssm_kv_attn_weights(ctypes.byref(s), Lq, _p(q), _p(lse), _p(cache.k), _p(cache.k_scale), _p(page_table),
+                                      _p(ctx_lens), _p(lens), float(d ** -0.5 if scale is None else scale), _p(mass), _p(out),
+                                      stream)
+    _raise("bdssm_kv_attn_weights", rc)
+    return out
+
+
+def kv_evict(page_table, ctx_lens, mass, page_len, budget, sink=0, recent=0, table_out=None, ctx_out=None, mass_out=None):
+    """The pages of least mass out of each row's context, down to budget whole
+    pages, the first sink and the last recent ones kept -> (page_table, ctx_lens,
+    mass) of the rows as they are then.  Pages that left follow those that stay:
+    the next commit writes them."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    if ctx_lens is None or mass is None:
+        raise ValueError("ctx_lens and mass are needed")
+    shape, batch = page_table.shape, page_table.shape[0]
+    _check(page_table, "page_table", torch.int32)
+    _check(ctx_lens, "ctx_lens", torch.int32, (batch,))
+    _check(mass, "mass", torch.float32, shape)
+    outs = [torch.empty_like(x) if y is None else y
+            for x, y in ((page_table, table_out), (ctx_lens, ctx_out), (mass, mass_out))]
+    _check(outs[0], "table_out", torch.int32, shape)
+    _check(outs[1], "ctx_out", torch.int32, (batch,))
+    _check(outs[2], "mass_out", torch.float32, shape)
+    stream = _stream(page_table.get_device(), ctx_lens, mass, *outs)
+    rc = load().bdssm_kv_evict(batch, shape[1], page_len, budget, sink, recent, _p(page_table), _p(ctx_lens), _p(mass),
+                               _p(outs[0]), _p(outs[1]), _p(outs[2]), stream)
+    _raise("bdssm_kv_evict", rc)
+    return tuple(outs)
