@@ -8,9 +8,11 @@
 // they are); a token that starts a document sees none but its own.
 //
 // Memory is the bound: 2 W + 4 operations a value against 4 bytes (bf16).  A lane
-// takes up to eight neighbouring channels (16 bytes) and a chunk of consecutive
-// tokens, keeping the last W - 1 inputs in registers, so that each input is read
-// once but for the W - 1 in front of a chunk.
+// takes four neighbouring channels and a chunk of consecutive tokens, keeping the last
+// W - 1 inputs in registers, so that each input is read once but for the W - 1 in
+// front of a chunk.  (Eight channels of bf16, 16 bytes a load, need 165 registers
+// instead of 100, and so fewer waves: 65,536 tokens of 2,048 channels 207 us instead
+// of 124.)
 #pragma once
 
 #include "layer_common.hpp"
@@ -26,8 +28,8 @@ struct ConvArgs {
     const uint8_t *starts;     // [batch, T] or null
     const T *c_init;           // [batch, W - 1, ch] or null
     T *y, *c_final;            // either may be null
-    int64_t T_tokens, jobs;    // jobs: lanes * chunks * batch
-    int64_t chunk, chunks;     // tokens of a chunk, chunks of a row
+    int64_t jobs;              // lanes * chunks * batch
+    int T_tokens, chunk, chunks;   // tokens of a row and of a chunk, chunks of a row
     int ch, lanes, silu;
     // backward
     const T *dy, *dc_final;
@@ -47,19 +49,19 @@ __device__ __forceinline__ float sigmoid(float p) {
 }
 
 // How many tokens behind the last document's start a token is, as far as taps care.
-__device__ __forceinline__ int age_after(const uint8_t *starts, int64_t t, int age) {
+__device__ __forceinline__ int age_after(const uint8_t *starts, int t, int age) {
     return starts != nullptr && starts[t] ? 0 : age + 1;
 }
-constexpr int kOld = 1 << 20;
+constexpr int kOld = 1 << 30;   // at least as far; stays below 2^31 over a row
 
 // The W - 1 inputs in front of token t0 (hist[0] the oldest) and their age.
 template <typename T, int kW, int kN>
-__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int64_t t0, int c0, int n_ch, Run<T, kN> (&hist)[kW - 1]) {
+__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int t0, int c0, int n_ch, Run<T, kN> (&hist)[kW - 1]) {
     const T *ub = a.u + b * a.batch_ld + c0;
 #pragma unroll
     for (int j = 0; j < kW - 1; ++j) {
-        const int64_t t = t0 - (kW - 1) + j;
-        if (t >= 0) hist[j].load(ub + t * a.ld, n_ch);
+        const int t = t0 - (kW - 1) + j;
+        if (t >= 0) hist[j].load(ub + (int64_t)t * a.ld, n_ch);
         else if (a.c_init != nullptr) hist[j].load(a.c_init + (b * (kW - 1) + t + kW - 1) * a.ch + c0, n_ch);
         else hist[j].zero();
     }
@@ -67,7 +69,7 @@ __device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int
     if (a.starts != nullptr) {
 #pragma unroll
         for (int j = 0; j < kW - 1; ++j) {
-            const int64_t t = t0 - (kW - 1) + j;
+            const int t = t0 - (kW - 1) + j;
             if (t >= 0) age = age_after(a.starts + b * a.T_tokens, t, age);
         }
     }
@@ -93,24 +95,28 @@ __device__ __forceinline__ void conv_weights(const float *w, const float *bias, 
     }
 }
 
+// Tokens that a row has.
+template <typename T>
+__device__ __forceinline__ int conv_len(const ConvArgs<T> &a, int64_t b) {
+    const int n = a.lens == nullptr ? a.T_tokens : a.lens[b];
+    return n < 0 ? 0 : n < a.T_tokens ? n : a.T_tokens;
+}
+
 // Without y a lane goes over the row's last W - 1 tokens alone.
 template <typename T, int kW, int kN>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
-    constexpr int kAhead = 4;   // tokens read at a time
+    constexpr int kAhead = 6;   // tokens read at a time: a multiple of W - 1, so that no input moves
     const int64_t job = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (job >= a.jobs) return;
-    const int lane = (int)(job % a.lanes);
-    const int64_t chunk = job / a.lanes % a.chunks;
+    const int lane = (int)(job % a.lanes), chunk = (int)(job / a.lanes % a.chunks);
     const int64_t b = job / a.lanes / a.chunks;
-    const int c0 = lane * kN, n_ch = a.ch - c0;
-    int64_t n = a.T_tokens;
-    if (a.lens != nullptr) n = a.lens[b] < 0 ? 0 : a.lens[b] < n ? a.lens[b] : n;
-    int64_t t0 = chunk * a.chunk, t1 = t0 + a.chunk < a.T_tokens ? t0 + a.chunk : a.T_tokens;
+    const int c0 = lane * kN, n_ch = a.ch - c0, n = conv_len(a, b);
+    int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
     if (a.y == nullptr) {
         t0 = n > kW - 1 ? n - (kW - 1) : 0;
         t1 = n;
     }
-    const int64_t stop = t1 < n ? t1 : n;   // of the tokens that are read
+    const int stop = t1 < n ? t1 : n;   // of the tokens that are read
     T *yb = a.y == nullptr ? nullptr : a.y + b * a.T_tokens * a.ch + c0;
     const bool last = a.c_final != nullptr && (a.y == nullptr || (n > t0 && n <= t1) || (n == 0 && chunk == 0));
     if (t0 < stop || last) {
@@ -120,41 +126,61 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
         int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
         const T *ub = a.u + b * a.batch_ld + c0;
         const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
-        for (int64_t t = t0; t < stop; t += kAhead) {
-            Run<T, kN> x[kAhead];
+        const auto token = [&](int t, const Run<T, kN> &x) {
+            if (starts != nullptr) {
+                age = age_after(starts, t, age);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (t + i < stop) x[i].load(ub + (t + i) * a.ld, n_ch);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (t + i >= stop) break;
-                if (starts != nullptr) {
-                    age = age_after(starts, t + i, age);
-#pragma unroll
-                    for (int j = 0; j < kW - 1; ++j)
-                        if (kW - 1 - j > age) hist[j].zero();
-                }
-                if (yb != nullptr) {
-                    float p[kN];
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) {
-                        p[e] = bs[e];
-#pragma unroll
-                        for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
-                        p[e] = fmaf(wt[e][kW - 1], x[i].at(e), p[e]);
-                    }
-                    if (a.silu) {
-#pragma unroll
-                        for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
-                    }
-                    Run<T, kN> out;
-                    out.put(p);
-                    out.store(yb + (t + i) * a.ch, n_ch);
-                }
-#pragma unroll
-                for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
-                hist[kW - 2] = x[i];
+                for (int j = 0; j < kW - 1; ++j)
+                    if (kW - 1 - j > age) hist[j].zero();
             }
+            if (yb != nullptr) {
+                float p[kN];
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    p[e] = bs[e];
+#pragma unroll
+                    for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
+                    p[e] = fmaf(wt[e][kW - 1], x.at(e), p[e]);
+                }
+                if (a.silu) {
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
+                }
+                Run<T, kN> out;
+                out.put(p);
+                out.store(yb + (int64_t)t * a.ch, n_ch);
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
+            hist[kW - 2] = x;
+        };
+        int t = t0;
+        if (t + kAhead <= stop) {   // the next tokens on their way while these are worked on
+            Run<T, kN> x[kAhead], next[kAhead];
+            const auto fetch = [&](Run<T, kN> (&to)[kAhead], int t) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) to[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
+            };
+            fetch(x, t);
+            for (; t + 2 * kAhead <= stop; t += kAhead) {
+                fetch(next, t + kAhead);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) token(t + i, x[i]);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) x[i] = next[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) token(t + i, x[i]);
+            t += kAhead;
+        }
+        {   // fewer than kAhead are left
+            Run<T, kN> x[kAhead - 1];
+#pragma unroll
+            for (int i = 0; i < kAhead - 1; ++i)
+                if (t + i < stop) x[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
+#pragma unroll
+            for (int i = 0; i < kAhead - 1; ++i)
+                if (t + i < stop) token(t + i, x[i]);
         }
         if (last) {
             // kept where no document started behind it (the age of a row of no tokens is none)
@@ -168,17 +194,19 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     if (yb != nullptr) {
         Run<T, kN> none;
         none.zero();
-        for (int64_t t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + t * a.ch, n_ch);
+        for (int t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + (int64_t)t * a.ch, n_ch);
     }
 }
 
 // Gradients.  A lane sweeps its chunk and the W - 1 tokens behind it forward in
 // time, the inputs' last W - 1 values and the W - 1 unfinished sums of du in
-// registers; du_s is whole once dp_{s+W-1} is there.  The parameters' sums of a
-// workgroup's chunks join in LDS in a fixed order and go to `parts`.
+// registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
+// but at a row's ends (chunks are multiples of 6).  The parameters' sums of a workgroup's chunks join in LDS in
+// a fixed order and go to `parts`.
 template <typename T, int kW, int kN>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs<T> a) {
-    constexpr int kAhead = 4, kSums = kN * (kW + 1);
+__global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
+    constexpr int kAhead = kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
+    static_assert(kAhead >= kW - 1 && 6 % kAhead == 0, "a chunk is whole groups; what its first one completes lies in front of it");
     __shared__ float sums[256 * kSums];
     const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
     const int lane = group * a.row_lanes + (int)(threadIdx.x & (a.row_lanes - 1));
@@ -194,11 +222,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs<T> a) {
     float wt[kN][kW], bs[kN];
     if (n_ch > 0) conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
     for (int64_t row = (int64_t)part * per + threadIdx.x / a.row_lanes; n_ch > 0 && row < a.rows; row += (int64_t)a.n_parts * per) {
-        const int64_t chunk = row % a.chunks;
+        const int chunk = (int)(row % a.chunks);
         const int64_t b = row / a.chunks;
-        int64_t n = a.T_tokens;
-        if (a.lens != nullptr) n = a.lens[b] < 0 ? 0 : a.lens[b] < n ? a.lens[b] : n;
-        const int64_t t0 = chunk * a.chunk, t1 = t0 + a.chunk < a.T_tokens ? t0 + a.chunk : a.T_tokens;
+        const int n = conv_len(a, b), t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
         float open[kW - 1][kN];                               // open[d - 1]: du of token t - d
         Run<T, kN> hist[kW - 1];
         int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
@@ -209,85 +235,106 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs<T> a) {
         const T *ub = a.u + b * a.batch_ld + c0, *dyb = a.dy + b * a.T_tokens * a.ch + c0;
         const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
         T *dub = a.du + b * a.du_batch_ld + c0;
-        for (int64_t t = t0; t < t1 + kW - 1; t += kAhead) {
-            Run<T, kN> x[kAhead], g[kAhead];
+        // dp of token s, and what it adds to; own: the token is one of the chunk's
+        const auto token = [&](int s, const Run<T, kN> &x, const Run<T, kN> &g, bool own, float (&dp)[kN]) {
+            if (starts != nullptr) {
+                age = age_after(starts, s, age);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (t + i < n && t + i < t1 + kW - 1) {
-                    x[i].load(ub + (t + i) * a.ld, n_ch);
-                    g[i].load(dyb + (t + i) * a.ch, n_ch);
+                for (int j = 0; j < kW - 1; ++j)
+                    if (kW - 1 - j > age) hist[j].zero();
+            }
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                dp[e] = g.at(e);
+                if (a.silu) {
+                    float p = bs[e];
+#pragma unroll
+                    for (int j = 0; j < kW - 1; ++j) p = fmaf(wt[e][j], hist[j].at(e), p);
+                    p = fmaf(wt[e][kW - 1], x.at(e), p);
+                    const float sg = sigmoid(p);
+                    dp[e] *= sg * fmaf(p, 1.f - sg, 1.f);
+                }
+            }
+            if (own) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    db[e] += dp[e];
+#pragma unroll
+                    for (int j = 0; j < kW - 1; ++j) dw[e][j] = fmaf(dp[e], hist[j].at(e), dw[e][j]);
+                    dw[e][kW - 1] = fmaf(dp[e], x.at(e), dw[e][kW - 1]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int64_t s = t + i;
-                if (s >= t1 + kW - 1) break;
-                float dp[kN];
+            for (int d = 1; d < kW; ++d)
+                if (starts == nullptr || d <= age) {
 #pragma unroll
-                for (int e = 0; e < kN; ++e) dp[e] = 0.f;
-                if (s < n) {
-                    if (starts != nullptr) {
-                        age = age_after(starts, s, age);
-#pragma unroll
-                        for (int j = 0; j < kW - 1; ++j)
-                            if (kW - 1 - j > age) hist[j].zero();
-                    }
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) {
-                        dp[e] = g[i].at(e);
-                        if (a.silu) {
-                            float p = bs[e];
-#pragma unroll
-                            for (int j = 0; j < kW - 1; ++j) p = fmaf(wt[e][j], hist[j].at(e), p);
-                            p = fmaf(wt[e][kW - 1], x[i].at(e), p);
-                            const float sg = sigmoid(p);
-                            dp[e] *= sg * fmaf(p, 1.f - sg, 1.f);
-                        }
-                    }
-                    if (s < t1) {
-#pragma unroll
-                        for (int e = 0; e < kN; ++e) {
-                            db[e] += dp[e];
-#pragma unroll
-                            for (int j = 0; j < kW - 1; ++j) dw[e][j] = fmaf(dp[e], hist[j].at(e), dw[e][j]);
-                            dw[e][kW - 1] = fmaf(dp[e], x[i].at(e), dw[e][kW - 1]);
-                        }
-                    }
-#pragma unroll
-                    for (int d = 1; d < kW; ++d)
-                        if (starts == nullptr || d <= age) {
-#pragma unroll
-                            for (int e = 0; e < kN; ++e) open[d - 1][e] = fmaf(wt[e][kW - 1 - d], dp[e], open[d - 1][e]);
-                        }
-                }
-                // token s - (W - 1) is whole (in front of the row: an input of the state)
-                const int64_t at = s - (kW - 1);
-                const bool state = at < 0 && a.dc_init != nullptr;
-                if (at >= t0 || state) {
-                    if (s >= n && at < n && a.dc_final != nullptr && n - 1 - at <= age) {
-                        // it is in the last state too: of a row of fewer tokens than that, more than once
-                        Run<T, kN> dc;
-                        dc.load(a.dc_final + (b * (kW - 1) + at - n + kW - 1) * a.ch + c0, n_ch);
-#pragma unroll
-                        for (int e = 0; e < kN; ++e) open[kW - 2][e] += dc.at(e);
-                    }
-                    Run<T, kN> out;
-                    out.put(open[kW - 2]);
-                    if (state) out.store(a.dc_init + (b * (kW - 1) + at + kW - 1) * a.ch + c0, n_ch);
-                    else out.store(dub + at * a.du_ld, n_ch);
+                    for (int e = 0; e < kN; ++e) open[d - 1][e] = fmaf(wt[e][kW - 1 - d], dp[e], open[d - 1][e]);
                 }
 #pragma unroll
-                for (int d = kW - 2; d > 0; --d)
+            for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
+            hist[kW - 2] = x;
+        };
+        const auto shift = [&](const float (&dp)[kN]) {
 #pragma unroll
-                    for (int e = 0; e < kN; ++e) open[d][e] = open[d - 1][e];
+            for (int d = kW - 2; d > 0; --d)
 #pragma unroll
-                for (int e = 0; e < kN; ++e) open[0][e] = wt[e][kW - 1] * dp[e];
-                if (s < n) {
+                for (int e = 0; e < kN; ++e) open[d][e] = open[d - 1][e];
 #pragma unroll
-                    for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
-                    hist[kW - 2] = x[i];
+            for (int e = 0; e < kN; ++e) open[0][e] = wt[e][kW - 1] * dp[e];
+        };
+        const int inside = t1 < n ? t1 : n, end = t1 + kW - 1;
+        int t = t0;
+        while (t < end) {
+            // whole groups of the chunk's own tokens; the first one, whose first W - 1 tokens
+            // complete none of the chunk's, only where they complete none of the state's either
+            const bool first = t == t0 && (t0 > 0 || a.dc_init == nullptr);
+            if (t + kAhead <= inside && (first || t >= t0 + kW - 1)) {
+                Run<T, kN> x[kAhead], g[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    x[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
+                    g[i].load(dyb + (int64_t)(t + i) * a.ch, n_ch);
                 }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    float dp[kN];
+                    token(t + i, x[i], g[i], true, dp);
+                    if (!first || i >= kW - 1) {
+                        Run<T, kN> out;
+                        out.put(open[kW - 2]);
+                        out.store(dub + (int64_t)(t + i - (kW - 1)) * a.du_ld, n_ch);
+                    }
+                    shift(dp);
+                }
+                t += kAhead;
+                continue;
             }
+            float dp[kN];
+#pragma unroll
+            for (int e = 0; e < kN; ++e) dp[e] = 0.f;
+            if (t < n) {
+                Run<T, kN> x, g;
+                x.load(ub + (int64_t)t * a.ld, n_ch);
+                g.load(dyb + (int64_t)t * a.ch, n_ch);
+                token(t, x, g, t < t1, dp);
+            }
+            // token t - (W - 1) is whole (in front of the row: an input of the state)
+            const int at = t - (kW - 1);
+            const bool state = at < 0 && a.dc_init != nullptr;
+            if (at >= t0 || state) {
+                if (t >= n && at < n && a.dc_final != nullptr && n - 1 - at <= age) {   // it is in the last state too
+                    Run<T, kN> dc;
+                    dc.load(a.dc_final + (b * (kW - 1) + at - n + kW - 1) * a.ch + c0, n_ch);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) open[kW - 2][e] += dc.at(e);
+                }
+                Run<T, kN> out;
+                out.put(open[kW - 2]);
+                if (state) out.store(a.dc_init + (b * (kW - 1) + at + kW - 1) * a.ch + c0, n_ch);
+                else out.store(dub + (int64_t)at * a.du_ld, n_ch);
+            }
+            shift(dp);
+            ++t;
         }
     }
 #pragma unroll

@@ -21,10 +21,10 @@ ConvArgs<T> conv_args(const ConvCall &c) {
     a.c_init = (const T *)c.c_init;
     a.y = (T *)c.y;
     a.c_final = (T *)c.c_final;
-    a.T_tokens = c.T;
+    a.T_tokens = (int)c.T;
     a.jobs = c.plan.jobs;
     a.chunk = c.plan.chunk;
-    a.chunks = c.plan.chunks;
+    a.chunks = (int)c.plan.chunks;
     a.ch = c.ch;
     a.lanes = c.plan.lanes;
     a.silu = c.silu;
@@ -34,7 +34,7 @@ ConvArgs<T> conv_args(const ConvCall &c) {
 template <>
 void launch_conv<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     using T = BDSSM_TIN;
-    constexpr int kN = kConvLane<T>;
+    constexpr int kN = kConvLane;
     const ConvArgs<T> a = conv_args<T>(c);
     const dim3 g((unsigned)((c.plan.jobs + c.plan.block - 1) / c.plan.block)), t(c.plan.block);
     if (c.width == 4) hipLaunchKernelGGL((conv_kernel<T, 4, kN>), g, t, 0, st, a);
@@ -45,7 +45,7 @@ void launch_conv<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
 template <>
 void launch_conv_bwd<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     using T = BDSSM_TIN;
-    constexpr int kN = kConvBwdLane;
+    constexpr int kN = kConvLane;
     ConvArgs<T> a = conv_args<T>(c);
     a.dy = (const T *)c.dy;
     a.dc_final = (const T *)c.dc_final;

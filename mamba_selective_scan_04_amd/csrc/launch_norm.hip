@@ -32,14 +32,21 @@ NormArgs<T, R> norm_args(const NormCall &c) {
     return a;
 }
 
+template <int kThreads_, int kV_, int kVecs_>
+struct Row {
+    static constexpr int kThreads = kThreads_, kV = kV_, kVecs = kVecs_;
+};
+
 // calls f with the threads and vectors of a row of ch channels, at most kNormHeld
 template <typename F>
 void with_row(int ch, F &&f) {
-    if (ch <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-    else if (ch <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-    else if (ch <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    else if (ch <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+    if (ch <= 256) f(Row<64, 4, 1>{});
+    else if (ch <= 512) f(Row<64, 4, 2>{});
+    else if (ch <= 768) f(Row<64, 4, 3>{});
+    else if (ch <= 1024) f(Row<64, 4, 4>{});
+    else if (ch <= 2048) f(Row<256, 8, 1>{});
+    else if (ch <= 4096) f(Row<256, 8, 2>{});
+    else f(Row<1024, 8, 1>{});
 }
 
 template <typename T, typename R>
@@ -52,12 +59,13 @@ void norm_k(const NormCall &c, hipStream_t st) {
         else hipLaunchKernelGGL((norm_wide_kernel<T, R, kOutStream>), g, t, 0, st, a);
         return;
     }
-    with_row(c.ch, [&](auto threads, auto vecs) {
-        constexpr int kThreads = decltype(threads)::value, kVecs = decltype(vecs)::value;
+    with_row(c.ch, [&](auto row) {
+        using W = decltype(row);
+        constexpr int kThreads = W::kThreads;
         const dim3 g((unsigned)c.groups), t(kThreads > 256 ? kThreads : 256);
-        if (c.code == kE4m3) hipLaunchKernelGGL((norm_kernel<T, R, kE4m3, kThreads, kVecs>), g, t, 0, st, a);
-        else if (c.code == kI8) hipLaunchKernelGGL((norm_kernel<T, R, kI8, kThreads, kVecs>), g, t, 0, st, a);
-        else hipLaunchKernelGGL((norm_kernel<T, R, kOutStream, kThreads, kVecs>), g, t, 0, st, a);
+        if (c.code == kE4m3) hipLaunchKernelGGL((norm_kernel<T, R, kE4m3, kThreads, W::kV, W::kVecs>), g, t, 0, st, a);
+        else if (c.code == kI8) hipLaunchKernelGGL((norm_kernel<T, R, kI8, kThreads, W::kV, W::kVecs>), g, t, 0, st, a);
+        else hipLaunchKernelGGL((norm_kernel<T, R, kOutStream, kThreads, W::kV, W::kVecs>), g, t, 0, st, a);
     });
 }
 
@@ -69,9 +77,10 @@ void norm_bwd_k(const NormCall &c, hipStream_t st) {
         hipLaunchKernelGGL((norm_wide_bwd_kernel<T, R>), dim3((unsigned)c.groups), dim3(1024), 0, st, a);
         return;
     }
-    with_row(c.ch, [&](auto threads, auto vecs) {
-        constexpr int kThreads = decltype(threads)::value, kVecs = decltype(vecs)::value;
-        hipLaunchKernelGGL((norm_bwd_kernel<T, R, kThreads, kVecs>), dim3((unsigned)c.groups), dim3(kThreads > 256 ? kThreads : 256), 0, st, a);
+    with_row(c.ch, [&](auto row) {
+        using W = decltype(row);
+        constexpr int kThreads = W::kThreads;
+        hipLaunchKernelGGL((norm_bwd_kernel<T, R, kThreads, W::kV, W::kVecs>), dim3((unsigned)c.groups), dim3(kThreads > 256 ? kThreads : 256), 0, st, a);
     });
 }
 

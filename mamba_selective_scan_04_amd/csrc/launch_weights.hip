@@ -13,7 +13,7 @@ void weights_k(const KvCall &c, hipStream_t st) {
     const WeightArgs<T> a{(const T *)c.q, c.lse, (const uint8_t *)c.kc, c.ks, c.mass, c.mass_out, c.Lq, c.scale * 1.44269504088896341f, c.d};
     const int64_t tokens = (int64_t)c.d.max_pages * c.d.page_len;
     hipLaunchKernelGGL((kv_weights_kernel<T, kCode, kD>), dim3((unsigned)((tokens + kWeightKeys - 1) / kWeightKeys), (unsigned)c.batch),
-                       dim3(256), 0, st, a);
+                       dim3(kWeightWaves * 64), 0, st, a);
 }
 
 template <>

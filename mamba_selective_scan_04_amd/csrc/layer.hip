@@ -13,6 +13,8 @@ using namespace bdssm_host;
 
 namespace {
 
+constexpr int64_t kCus = 256;
+
 size_t value_bytes(int32_t dtype) { return dtype == BDSSM_BF16 ? 2 : 4; }
 
 // ------------------------------------------------------------ convolution
@@ -34,10 +36,12 @@ int check_conv(const bdssm_conv_shape *s, int64_t T) {
     if (s == nullptr) return BDSSM_ERR_NULL;
     if (s->dtype != BDSSM_F32 && s->dtype != BDSSM_BF16) return BDSSM_ERR_DTYPE;
     if (s->width < 2 || s->width > 4 || s->channels < 1 || s->channels > 0x7fffff00 || T < 0 || s->batch < 0) return BDSSM_ERR_SHAPE;
-    if (!product_fits({s->batch, T, s->channels}) || !product_fits({s->batch, s->channels, 4}) || T > kMost) return BDSSM_ERR_SHAPE;
+    if (!product_fits({s->batch, T, s->channels}) || !product_fits({s->batch, s->channels, 4}) || T > kConvMost) return BDSSM_ERR_SHAPE;
     int64_t n;
     return extent(s, T, s->u_stride, s->u_batch_stride, &n) ? BDSSM_OK : BDSSM_ERR_SHAPE;
 }
+
+int64_t within(int64_t x, int64_t low, int64_t high) { return x < low ? low : x > high ? high : x; }
 
 int64_t power_from(int64_t x, int64_t low, int64_t high) {   // the least power of two from x on, within low .. high
     int64_t p = low;
@@ -45,33 +49,42 @@ int64_t power_from(int64_t x, int64_t low, int64_t high) {   // the least power 
     return p;
 }
 
-// Tokens of a lane: so many that about 16 waves a CU share the work, for each chunk
-// reads W - 1 tokens in front of its own again.  One chunk where a lane has to have
-// read the state before it is written (in place), or only the state is wanted.
+// Tokens of a lane: so many that about 16 waves a CU share the work, but 4 to 66 (each
+// chunk reads the W - 1 tokens in front of its own again).  Microseconds by the least
+// and the most of them:
+//   64 rows of 16 tokens, 2,048 channels, bf16   2: 6.0   4: 5.8   6: 7.1   12: 9.1
+//   2 rows of 2,041, 1,021 channels, fp32        2: 11.8   4: 10.8   6: 11.4   12: 14.0
+//   1 row of 65,536, 2,048 channels, bf16        12: 128   24: 116   48: 118   66: 116
+//   8 rows of 4,096, 1,536 channels, bf16        12: 48   24: 45   48: 43   66: 42
+// One chunk where a lane has to have read the state before it is written (in place),
+// or only the state is wanted.
 ConvPlan conv_plan(const bdssm_conv_shape *s, int64_t T, bool whole) {
     ConvPlan p{};
-    const int n = s->dtype == BDSSM_BF16 ? kConvLane<uint16_t> : kConvLane<float>;
-    p.lanes = (int)((s->channels + n - 1) / n);
-    const int64_t work = s->batch * T * p.lanes;
-    p.chunk = whole ? (T > 0 ? T : 1) : power_from(work / (256 * 16 * 64), 4, 64);
+    p.lanes = (int)((s->channels + kConvLane - 1) / kConvLane);
+    const int64_t most = kCus * 16 * 64, work = s->batch * T * p.lanes;
+    p.chunk = (int)(whole ? (T > 0 ? T : 1) : within((work + most - 1) / most, 4, 66));
     p.chunks = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;
     p.jobs = s->batch * p.chunks * p.lanes;
     p.block = p.jobs < 256 * 256 ? 64 : 256;   // few lanes: spread over the CUs
     return p;
 }
 
-// Backward: 12 waves a CU; the parameters' sums of a workgroup's chunks make a part,
-// at most 2,048 of them.
+// Backward: as many workgroups as run at once (three a CU, by registers), and as many
+// chunks as they take at a time, or as there are rows: a second round of a few would
+// take as long as the first.  Each workgroup's sums of the parameters' gradients make
+// a part.
 ConvPlan conv_bwd_plan(const bdssm_conv_shape *s, int64_t T) {
     ConvPlan p{};
-    p.lanes = (int)((s->channels + kConvBwdLane - 1) / kConvBwdLane);
+    p.lanes = (int)((s->channels + kConvLane - 1) / kConvLane);
     p.row_lanes = (int)power_from(p.lanes, 1, 64);
     p.groups = (p.lanes + p.row_lanes - 1) / p.row_lanes;
-    p.chunk = power_from(s->batch * T * p.lanes / (256 * 12 * 64), 8, 64);
+    const int64_t per = 256 / p.row_lanes, most = p.groups < kCus * 3 ? kCus * 3 / p.groups : 1;
+    int64_t chunks = s->batch > 0 ? most * per / s->batch : 1;
+    if (chunks < 1) chunks = 1;
+    p.chunk = (int)((T + chunks - 1) / chunks + 5) / 6 * 6;   // whole groups, see conv_bwd_kernel
+    if (p.chunk == 0) p.chunk = 6;
     p.chunks = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;
-    const int64_t per = 256 / p.row_lanes, parts = (s->batch * p.chunks + per - 1) / per;
-    int64_t most = 2048;
-    if (most * p.groups > kMostGroups) most = kMostGroups / p.groups;
+    const int64_t parts = (s->batch * p.chunks + per - 1) / per;
     p.n_parts = (int)(parts < most ? parts : most);
     return p;
 }

@@ -15,17 +15,14 @@ namespace bdssm_host {
 
 using namespace bdssm_dev;
 
-// Channels of a lane: 16 bytes forward; backward, whose sums take 2 W + 1 registers
-// a channel, four.
-template <typename T>
-constexpr int kConvLane = 16 / sizeof(T);
-constexpr int kConvBwdLane = 4;
+constexpr int kConvLane = 4;       // channels of a lane
+constexpr int kConvMost = (1 << 30) - 1;   // tokens of a row
 
 // How the convolution's work is cut: rows in `chunks` of `chunk` tokens; backward,
 // workgroups of 256 / row_lanes chunks at a time.
 struct ConvPlan {
-    int64_t chunk, chunks, jobs;
-    int lanes, block;                        // forward
+    int64_t chunks, jobs;
+    int chunk, lanes, block;                       // forward
     int row_lanes, groups, n_parts;          // backward
 };
 

@@ -4,8 +4,7 @@
 //   g = w dy,  n = h r,  dh = r (g - n mean(g n)) + dh_out,  dw = sum over rows of dy n.
 //
 // Memory is the bound.  A row lies in the registers of kThreads threads (a wave for
-// up to 1,024 channels), each vector of eight channels 16 or 32 bytes of a lane, so
-// that it is read once; a workgroup goes over several rows with the weights kept,
+// up to 1,024 channels), so that it is read once; a workgroup goes over several rows with the weights kept,
 // the next row's loads on their way while one is worked on.
 //
 // Sums of squares are taken in 64 bits: they then round to the same 32-bit r however
@@ -80,8 +79,9 @@ __device__ __forceinline__ double inverse_root(double m) {
 }
 
 // A vector of weights as floats, 0 behind the channels.
-__device__ __forceinline__ Run<float, 8> weights_at(const float *w, int at, int left) {
-    Run<float, 8> v;
+template <int kV>
+__device__ __forceinline__ Run<float, kV> weights_at(const float *w, int at, int left) {
+    Run<float, kV> v;
     v.zero();
     if (left > 0) v.load(w + at, left);
     return v;
@@ -91,10 +91,11 @@ template <int kCode>
 constexpr float kCodeMax = kCode == kE4m3 ? 448.f : 127.f;
 
 // the largest finite magnitude
-__device__ __forceinline__ float largest_of(const float (&y)[8]) {
+template <int kV>
+__device__ __forceinline__ float largest_of(const float (&y)[kV]) {
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kV; ++e) {
         const float m = fabsf(y[e]);
         top = fmaxf(top, m < __builtin_inff() ? m : 0.f);
     }
@@ -104,16 +105,16 @@ __device__ __forceinline__ float largest_of(const float (&y)[8]) {
 // y / scale to codes.  The correctly rounded quotient in five operations, as in the
 // cache's commit, where the scale leaves its remainders exact; infinities become the
 // largest code, NaN a NaN or 0.
-template <int kCode>
-__device__ __forceinline__ Run<uint8_t, 8> codes_of(const float (&y)[8], float scale) {
-    float q[8];
+template <int kCode, int kV>
+__device__ __forceinline__ Run<uint8_t, kV> codes_of(const float (&y)[kV], float scale) {
+    float q[kV];
     if (scale < 0x1p-90f || !(scale < 0x1p90f)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = y[e] / scale;
+        for (int e = 0; e < kV; ++e) q[e] = y[e] / scale;
     } else {
         const float r = 1.f / scale;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kV; ++e) {
             float p = y[e] * r;
             p = fmaf(fmaf(-p, scale, y[e]), r, p);
             p = fmaf(fmaf(-p, scale, y[e]), r, p);
@@ -121,22 +122,25 @@ __device__ __forceinline__ Run<uint8_t, 8> codes_of(const float (&y)[8], float s
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kV; ++e) {
         if (kCode == kI8 && q[e] != q[e]) q[e] = 0.f;
         if (q[e] == q[e]) q[e] = fminf(fmaxf(q[e], -kCodeMax<kCode>), kCodeMax<kCode>);
     }
-    Run<uint8_t, 8> out;
-    const uint32_t c[2] = {to_codes<kCode>(q[0], q[1], q[2], q[3]), to_codes<kCode>(q[4], q[5], q[6], q[7])};
-    __builtin_memcpy(out.v, c, 8);
+    Run<uint8_t, kV> out;
+#pragma unroll
+    for (int e = 0; e < kV; e += 4) {
+        const uint32_t c = to_codes<kCode>(q[e], q[e + 1], q[e + 2], q[e + 3]);
+        __builtin_memcpy(out.v + e, &c, 4);
+    }
     return out;
 }
 
 constexpr int kOutStream = -1;   // kCode of norms that write the stream's type
 
-// kVecs vectors of eight channels a thread, vector i of thread t the channels from
-// 8 (i kThreads + t) on.  One row at a time for kThreads of more than a wave (of as
+// kVecs vectors of kV channels a thread, vector i of thread t the channels from
+// kV (i kThreads + t) on.  One row at a time for kThreads of more than a wave (of as
 // many threads the workgroup), four (one a wave) otherwise.
-template <typename T, typename R, int kCode, int kThreads, int kVecs>
+template <typename T, typename R, int kCode, int kThreads, int kV, int kVecs>
 __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(NormArgs<T, R> a) {
     __shared__ double red[2][16];
     int turn = 0;
@@ -144,15 +148,15 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
     const int rows_at_once = kThreads == 64 ? 4 : 1;
     int64_t row = (int64_t)blockIdx.x * rows_at_once + (kThreads == 64 ? threadIdx.x >> 6 : 0);
     const int64_t step = (int64_t)gridDim.x * rows_at_once;
-    Run<float, 8> w[kVecs];
-    Run<T, 8> x[kVecs];
-    Run<R, 8> res[kVecs];
+    Run<float, kV> w[kVecs];
+    Run<T, kV> x[kVecs];
+    Run<R, kV> res[kVecs];
     int at[kVecs], left[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        at[i] = 8 * (i * kThreads + tid);
+        at[i] = kV * (i * kThreads + tid);
         left[i] = a.ch - at[i];
-        w[i] = weights_at(a.w, at[i], left[i]);
+        w[i] = weights_at<kV>(a.w, at[i], left[i]);
     }
     const auto fetch = [&](int64_t r) {
 #pragma unroll
@@ -165,24 +169,24 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
     };
     if (row < a.rows) fetch(row);
     for (; row < a.rows; row += step) {
-        float h[kVecs][8];
+        float h[kVecs][kV];
         double sum = 0.;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = left[i] > 0 ? x[i].at(e) : 0.f;
+            for (int e = 0; e < kV; ++e) h[i][e] = left[i] > 0 ? x[i].at(e) : 0.f;
             if (a.res != nullptr && left[i] > 0) {
-                Run<R, 8> hr;
-                float s[8];
+                Run<R, kV> hr;
+                float s[kV];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = h[i][e] + res[i].at(e);
+                for (int e = 0; e < kV; ++e) s[e] = h[i][e] + res[i].at(e);
                 hr.put(s);
                 hr.store(a.h + row * a.ch + at[i], left[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = hr.at(e);
+                for (int e = 0; e < kV; ++e) h[i][e] = hr.at(e);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fma((double)h[i][e], (double)h[i][e], sum);
+            for (int e = 0; e < kV; ++e) sum = fma((double)h[i][e], (double)h[i][e], sum);
         }
         if (row + step < a.rows) fetch(row + step);
         sum = row_sum<kThreads>(sum, red, turn);
@@ -192,9 +196,9 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * r) * w[i].v[e];
+            for (int e = 0; e < kV; ++e) h[i][e] = (h[i][e] * r) * w[i].v[e];
             if constexpr (kCode == kOutStream) {
-                Run<T, 8> out;
+                Run<T, kV> out;
                 out.put(h[i]);
                 if (left[i] > 0) out.store(a.y + row * a.ch + at[i], left[i]);
             }
@@ -211,46 +215,46 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 float m = top;
-                if (!whole) {   // 128 channels: 16 lanes' vectors
+                if (!whole) {   // 128 channels: neighbouring lanes' vectors
                     m = big[i];
 #pragma unroll
-                    for (int s = 1; s < 16; s <<= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
+                    for (int s = 1; s < 128 / kV; s <<= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
                 }
                 const float scale = fmaxf(m / kCodeMax<kCode>, 0x1p-126f);
-                if (whole ? tid == 0 && i == 0 : (tid & 15) == 0 && left[i] > 0)
+                if (whole ? tid == 0 && i == 0 : (tid & (128 / kV - 1)) == 0 && left[i] > 0)
                     a.scales[whole ? row : row * (a.ch / 128) + at[i] / 128] = scale;
-                const Run<uint8_t, 8> out = codes_of<kCode>(h[i], scale);
+                const Run<uint8_t, kV> out = codes_of<kCode, kV>(h[i], scale);
                 if (left[i] > 0) out.store(a.codes + row * a.ch + at[i], left[i]);
             }
         }
     }
 }
 
-template <typename T, typename R, int kThreads, int kVecs>
+template <typename T, typename R, int kThreads, int kV, int kVecs>
 __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kernel(NormArgs<T, R> a) {
     __shared__ float red[2][16];
-    __shared__ float joined[kThreads == 64 ? 4 : 1][kThreads == 64 ? 64 * kVecs * 8 : 1];
+    __shared__ float joined[kThreads == 64 ? 4 : 1][kThreads == 64 ? 64 * kVecs * kV : 1];
     int turn = 0;
     const int tid = kThreads == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int rows_at_once = kThreads == 64 ? 4 : 1;
     int64_t row = (int64_t)blockIdx.x * rows_at_once + (kThreads == 64 ? threadIdx.x >> 6 : 0);
     const int64_t step = (int64_t)gridDim.x * rows_at_once;
-    Run<float, 8> w[kVecs];
-    float dw[kVecs][8];
-    Run<R, 8> h[kVecs], up[kVecs];
-    Run<T, 8> dy[kVecs];
+    Run<float, kV> w[kVecs];
+    float dw[kVecs][kV];
+    Run<R, kV> h[kVecs], up[kVecs];
+    Run<T, kV> dy[kVecs];
     float r_next = 0.f;
     int at[kVecs], left[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        at[i] = 8 * (i * kThreads + tid);
+        at[i] = kV * (i * kThreads + tid);
         left[i] = a.ch - at[i];
-        w[i] = weights_at(a.w, at[i], left[i]);
+        w[i] = weights_at<kV>(a.w, at[i], left[i]);
         h[i].zero();
         up[i].zero();
         dy[i].zero();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+        for (int e = 0; e < kV; ++e) dw[i][e] = 0.f;
     }
     const auto fetch = [&](int64_t r) {
         r_next = a.rstd[r];
@@ -265,14 +269,14 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
     };
     if (row < a.rows) fetch(row);
     for (; row < a.rows; row += step) {
-        float n[kVecs][8], g[kVecs][8], sum = 0.f;
-        Run<R, 8> more[kVecs];
+        float n[kVecs][kV], g[kVecs][kV], sum = 0.f;
+        Run<R, kV> more[kVecs];
         const float r = r_next;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             more[i] = up[i];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kV; ++e) {
                 const float d = dy[i].at(e);
                 n[i][e] = h[i].at(e) * r;
                 g[i][e] = d * w[i].v[e];
@@ -286,15 +290,15 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
         for (int i = 0; i < kVecs; ++i) {
             if (left[i] <= 0) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kV; ++e) {
                 g[i][e] = r * fmaf(-n[i][e], mean, g[i][e]);
                 if (a.dh != nullptr) g[i][e] += more[i].at(e);
             }
-            Run<T, 8> dx;
+            Run<T, kV> dx;
             dx.put(g[i]);
             dx.store(a.dx + row * a.ch + at[i], left[i]);
             if (a.dres != nullptr) {
-                Run<R, 8> out;
+                Run<R, kV> out;
                 out.put(g[i]);
                 out.store(a.dres + row * a.ch + at[i], left[i]);
             }
@@ -307,19 +311,19 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) joined[wave][(i * 8 + e) * 64 + tid] = dw[i][e];
+            for (int e = 0; e < kV; ++e) joined[wave][(i * kV + e) * 64 + tid] = dw[i][e];
         __syncthreads();
         for (int c = threadIdx.x; c < a.ch; c += 256) {
-            const int o = (c / 512 * 8 + c % 8) * 64 + c % 512 / 8;
+            const int o = (c / (64 * kV) * kV + c % kV) * 64 + c % (64 * kV) / kV;
             part[c] = joined[0][o] + joined[1][o] + joined[2][o] + joined[3][o];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             if (left[i] <= 0) continue;
-            Run<float, 8> out;
+            Run<float, kV> out;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) out.v[e] = dw[i][e];
+            for (int e = 0; e < kV; ++e) out.v[e] = dw[i][e];
             out.store(part + at[i], left[i]);
         }
     }
@@ -372,7 +376,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs<T, R> a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = h.at(e);
             }
-            const Run<float, 8> w = weights_at(a.w, at, left);
+            const Run<float, 8> w = weights_at<8>(a.w, at, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = (y[e] * r) * w.v[e];
         };
@@ -405,7 +409,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs<T, R> a) {
                 }
                 const float scale = fmaxf(m / kCodeMax<kCode>, 0x1p-126f);
                 if (whole ? at == 0 : (threadIdx.x & 15) == 0) a.scales[whole ? row : row * (a.ch / 128) + at / 128] = scale;
-                codes_of<kCode>(y, scale).store(a.codes + r0 + at, left);
+                codes_of<kCode, 8>(y, scale).store(a.codes + r0 + at, left);
             }
         }
     }
@@ -428,7 +432,7 @@ __global__ __launch_bounds__(1024) void norm_wide_bwd_kernel(NormArgs<T, R> a) {
             Run<T, 8> dy;
             h.load(a.h + r0 + at, left);
             dy.load(a.dy + r0 + at, left);
-            const Run<float, 8> w = weights_at(a.w, at, left);
+            const Run<float, 8> w = weights_at<8>(a.w, at, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 d[e] = dy.at(e);
