@@ -56,7 +56,7 @@ constexpr int kOld = 1 << 30;   // at least as far; stays below 2^31 over a row
 
 // The W - 1 inputs in front of token t0 (hist[0] the oldest) and their age.
 template <typename T, int kW, int kN>
-__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int t0, int c0, int n_ch, Run<T, kN> (&hist)[kW - 1]) {
+__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int t0, int c0, int n_ch, Vals<T, kN> (&hist)[kW - 1]) {
     const T *ub = a.u + b * a.batch_ld + c0;
 #pragma unroll
     for (int j = 0; j < kW - 1; ++j) {
@@ -122,11 +122,11 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     if (t0 < stop || last) {
         float wt[kN][kW], bs[kN];
         conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
-        Run<T, kN> hist[kW - 1];
+        Vals<T, kN> hist[kW - 1];
         int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
         const T *ub = a.u + b * a.batch_ld + c0;
         const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
-        const auto token = [&](int t, const Run<T, kN> &x) {
+        const auto token = [&](int t, const Vals<T, kN> &x) {
             if (starts != nullptr) {
                 age = age_after(starts, t, age);
 #pragma unroll
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 #pragma unroll
                     for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
                 }
-                Run<T, kN> out;
+                Vals<T, kN> out;
                 out.put(p);
                 out.store(yb + (int64_t)t * a.ch, n_ch);
             }
@@ -156,8 +156,8 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
         };
         int t = t0;
         if (t + kAhead <= stop) {   // the next tokens on their way while these are worked on
-            Run<T, kN> x[kAhead], next[kAhead];
-            const auto fetch = [&](Run<T, kN> (&to)[kAhead], int t) {
+            Vals<T, kN> x[kAhead], next[kAhead];
+            const auto fetch = [&](Vals<T, kN> (&to)[kAhead], int t) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) to[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
             };
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
             t += kAhead;
         }
         {   // fewer than kAhead are left
-            Run<T, kN> x[kAhead - 1];
+            Vals<T, kN> x[kAhead - 1];
 #pragma unroll
             for (int i = 0; i < kAhead - 1; ++i)
                 if (t + i < stop) x[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
         }
     }
     if (yb != nullptr) {
-        Run<T, kN> none;
+        Vals<T, kN> none;
         none.zero();
         for (int t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + (int64_t)t * a.ch, n_ch);
     }
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         const int64_t b = row / a.chunks;
         const int n = conv_len(a, b), t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
         float open[kW - 1][kN];                               // open[d - 1]: du of token t - d
-        Run<T, kN> hist[kW - 1];
+        Vals<T, kN> hist[kW - 1];
         int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
 #pragma unroll
         for (int d = 0; d < kW - 1; ++d)
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
         T *dub = a.du + b * a.du_batch_ld + c0;
         // dp of token s, and what it adds to; own: the token is one of the chunk's
-        const auto token = [&](int s, const Run<T, kN> &x, const Run<T, kN> &g, bool own, float (&dp)[kN]) {
+        const auto token = [&](int s, const Vals<T, kN> &x, const Vals<T, kN> &g, bool own, float (&dp)[kN]) {
             if (starts != nullptr) {
                 age = age_after(starts, s, age);
 #pragma unroll
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
             // complete none of the chunk's, only where they complete none of the state's either
             const bool first = t == t0 && (t0 > 0 || a.dc_init == nullptr);
             if (t + kAhead <= inside && (first || t >= t0 + kW - 1)) {
-                Run<T, kN> x[kAhead], g[kAhead];
+                Vals<T, kN> x[kAhead], g[kAhead];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     x[i].load(ub + (int64_t)(t + i) * a.ld, n_ch);
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
                     float dp[kN];
                     token(t + i, x[i], g[i], true, dp);
                     if (!first || i >= kW - 1) {
-                        Run<T, kN> out;
+                        Vals<T, kN> out;
                         out.put(open[kW - 2]);
                         out.store(dub + (int64_t)(t + i - (kW - 1)) * a.du_ld, n_ch);
                     }
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
 #pragma unroll
             for (int e = 0; e < kN; ++e) dp[e] = 0.f;
             if (t < n) {
-                Run<T, kN> x, g;
+                Vals<T, kN> x, g;
                 x.load(ub + (int64_t)t * a.ld, n_ch);
                 g.load(dyb + (int64_t)t * a.ch, n_ch);
                 token(t, x, g, t < t1, dp);
@@ -323,12 +323,12 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
             const bool state = at < 0 && a.dc_init != nullptr;
             if (at >= t0 || state) {
                 if (t >= n && at < n && a.dc_final != nullptr && n - 1 - at <= age) {   // it is in the last state too
-                    Run<T, kN> dc;
+                    Vals<T, kN> dc;
                     dc.load(a.dc_final + (b * (kW - 1) + at - n + kW - 1) * a.ch + c0, n_ch);
 #pragma unroll
                     for (int e = 0; e < kN; ++e) open[kW - 2][e] += dc.at(e);
                 }
-                Run<T, kN> out;
+                Vals<T, kN> out;
                 out.put(open[kW - 2]);
                 if (state) out.store(a.dc_init + (b * (kW - 1) + at + kW - 1) * a.ch + c0, n_ch);
                 else out.store(dub + (int64_t)at * a.du_ld, n_ch);

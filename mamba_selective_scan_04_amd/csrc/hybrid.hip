@@ -423,7 +423,7 @@ int bdssm_kv_attn_weights(const bdssm_kv_shape *s, int64_t Lq, const void *q, co
     if (s->batch == 0 || s->max_pages == 0) return BDSSM_OK;
     if (!out || !page_table || !ctx_lens || (Lq > 0 && (!q || !lse)) || (s->n_pages > 0 && (!k_cache || !k_scale))) return BDSSM_ERR_NULL;
     if (!all_aligned({q, lse, k_cache, k_scale, page_table, ctx_lens, lens, mass, out})) return BDSSM_ERR_ALIGN;
-    if ((s->max_pages * s->page_len + kWeightKeys - 1) / kWeightKeys > kMostGroups / 2) return BDSSM_ERR_SHAPE;
+    if ((s->max_pages * s->page_len + kWeightKeys - 1) / kWeightKeys > kMostGroups / 2 || Lq * kv_group(s) > kMostGroups) return BDSSM_ERR_SHAPE;
     const KvSizes z = kv_sizes(s, 0, Lq);
     if (!distinct({{q, z.q}, {lse, z.lse}, {k_cache, z.cache}, {k_scale, z.scale}, {page_table, z.table}, {ctx_lens, z.row}, {lens, z.row},
                    {mass == out ? nullptr : mass, z.table}},

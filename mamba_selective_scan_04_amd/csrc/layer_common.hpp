@@ -15,7 +15,7 @@ namespace bdssm_dev {
 // tensor): the loads and stores are declared so, and are one instruction of up to
 // 16 bytes all the same.
 template <typename T, int kN>
-struct Run {
+struct Vals {
     T v[kN];
     __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(v, p, sizeof v); }
     __device__ __forceinline__ void store(T *p) const { __builtin_memcpy(p, v, sizeof v); }

@@ -80,8 +80,8 @@ __device__ __forceinline__ double inverse_root(double m) {
 
 // A vector of weights as floats, 0 behind the channels.
 template <int kV>
-__device__ __forceinline__ Run<float, kV> weights_at(const float *w, int at, int left) {
-    Run<float, kV> v;
+__device__ __forceinline__ Vals<float, kV> weights_at(const float *w, int at, int left) {
+    Vals<float, kV> v;
     v.zero();
     if (left > 0) v.load(w + at, left);
     return v;
@@ -106,7 +106,7 @@ __device__ __forceinline__ float largest_of(const float (&y)[kV]) {
 // cache's commit, where the scale leaves its remainders exact; infinities become the
 // largest code, NaN a NaN or 0.
 template <int kCode, int kV>
-__device__ __forceinline__ Run<uint8_t, kV> codes_of(const float (&y)[kV], float scale) {
+__device__ __forceinline__ Vals<uint8_t, kV> codes_of(const float (&y)[kV], float scale) {
     float q[kV];
     if (scale < 0x1p-90f || !(scale < 0x1p90f)) {
 #pragma unroll
@@ -126,7 +126,7 @@ __device__ __forceinline__ Run<uint8_t, kV> codes_of(const float (&y)[kV], float
         if (kCode == kI8 && q[e] != q[e]) q[e] = 0.f;
         if (q[e] == q[e]) q[e] = fminf(fmaxf(q[e], -kCodeMax<kCode>), kCodeMax<kCode>);
     }
-    Run<uint8_t, kV> out;
+    Vals<uint8_t, kV> out;
 #pragma unroll
     for (int e = 0; e < kV; e += 4) {
         const uint32_t c = to_codes<kCode>(q[e], q[e + 1], q[e + 2], q[e + 3]);
@@ -148,9 +148,9 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
     const int rows_at_once = kThreads == 64 ? 4 : 1;
     int64_t row = (int64_t)blockIdx.x * rows_at_once + (kThreads == 64 ? threadIdx.x >> 6 : 0);
     const int64_t step = (int64_t)gridDim.x * rows_at_once;
-    Run<float, kV> w[kVecs];
-    Run<T, kV> x[kVecs];
-    Run<R, kV> res[kVecs];
+    Vals<float, kV> w[kVecs];
+    Vals<T, kV> x[kVecs];
+    Vals<R, kV> res[kVecs];
     int at[kVecs], left[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
 #pragma unroll
             for (int e = 0; e < kV; ++e) h[i][e] = left[i] > 0 ? x[i].at(e) : 0.f;
             if (a.res != nullptr && left[i] > 0) {
-                Run<R, kV> hr;
+                Vals<R, kV> hr;
                 float s[kV];
 #pragma unroll
                 for (int e = 0; e < kV; ++e) s[e] = h[i][e] + res[i].at(e);
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
 #pragma unroll
             for (int e = 0; e < kV; ++e) h[i][e] = (h[i][e] * r) * w[i].v[e];
             if constexpr (kCode == kOutStream) {
-                Run<T, kV> out;
+                Vals<T, kV> out;
                 out.put(h[i]);
                 if (left[i] > 0) out.store(a.y + row * a.ch + at[i], left[i]);
             }
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_kernel(N
                 const float scale = fmaxf(m / kCodeMax<kCode>, 0x1p-126f);
                 if (whole ? tid == 0 && i == 0 : (tid & (128 / kV - 1)) == 0 && left[i] > 0)
                     a.scales[whole ? row : row * (a.ch / 128) + at[i] / 128] = scale;
-                const Run<uint8_t, kV> out = codes_of<kCode, kV>(h[i], scale);
+                const Vals<uint8_t, kV> out = codes_of<kCode, kV>(h[i], scale);
                 if (left[i] > 0) out.store(a.codes + row * a.ch + at[i], left[i]);
             }
         }
@@ -239,10 +239,10 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
     const int rows_at_once = kThreads == 64 ? 4 : 1;
     int64_t row = (int64_t)blockIdx.x * rows_at_once + (kThreads == 64 ? threadIdx.x >> 6 : 0);
     const int64_t step = (int64_t)gridDim.x * rows_at_once;
-    Run<float, kV> w[kVecs];
+    Vals<float, kV> w[kVecs];
     float dw[kVecs][kV];
-    Run<R, kV> h[kVecs], up[kVecs];
-    Run<T, kV> dy[kVecs];
+    Vals<R, kV> h[kVecs], up[kVecs];
+    Vals<T, kV> dy[kVecs];
     float r_next = 0.f;
     int at[kVecs], left[kVecs];
 #pragma unroll
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
     if (row < a.rows) fetch(row);
     for (; row < a.rows; row += step) {
         float n[kVecs][kV], g[kVecs][kV], sum = 0.f;
-        Run<R, kV> more[kVecs];
+        Vals<R, kV> more[kVecs];
         const float r = r_next;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -294,11 +294,11 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
                 g[i][e] = r * fmaf(-n[i][e], mean, g[i][e]);
                 if (a.dh != nullptr) g[i][e] += more[i].at(e);
             }
-            Run<T, kV> dx;
+            Vals<T, kV> dx;
             dx.put(g[i]);
             dx.store(a.dx + row * a.ch + at[i], left[i]);
             if (a.dres != nullptr) {
-                Run<R, kV> out;
+                Vals<R, kV> out;
                 out.put(g[i]);
                 out.store(a.dres + row * a.ch + at[i], left[i]);
             }
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kThreads > 256 ? kThreads : 256) void norm_bwd_kern
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             if (left[i] <= 0) continue;
-            Run<float, kV> out;
+            Vals<float, kV> out;
 #pragma unroll
             for (int e = 0; e < kV; ++e) out.v[e] = dw[i][e];
             out.store(part + at[i], left[i]);
@@ -343,13 +343,13 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs<T, R> a) {
 #pragma unroll 1
         for (int at = 8 * threadIdx.x; at < a.ch; at += 8 * 1024) {
             const int left = a.ch - at;
-            Run<T, 8> x;
+            Vals<T, 8> x;
             x.load(a.x + r0 + at, left);
             float h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = x.at(e);
             if (a.res != nullptr) {
-                Run<R, 8> hr;
+                Vals<R, 8> hr;
                 hr.load(a.res + r0 + at, left);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] += hr.at(e);
@@ -366,17 +366,17 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs<T, R> a) {
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = r;
         const auto output = [&](int at, int left, float (&y)[8]) {
             if (a.res != nullptr) {
-                Run<R, 8> h;
+                Vals<R, 8> h;
                 h.load(a.h + r0 + at, left);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = h.at(e);
             } else {
-                Run<T, 8> h;
+                Vals<T, 8> h;
                 h.load(a.x + r0 + at, left);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = h.at(e);
             }
-            const Run<float, 8> w = weights_at<8>(a.w, at, left);
+            const Vals<float, 8> w = weights_at<8>(a.w, at, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = (y[e] * r) * w.v[e];
         };
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs<T, R> a) {
             float y[8];
             output(at, left, y);
             if constexpr (kCode == kOutStream) {
-                Run<T, 8> out;
+                Vals<T, 8> out;
                 out.put(y);
                 out.store(a.y + r0 + at, left);
             } else {
@@ -428,11 +428,11 @@ __global__ __launch_bounds__(1024) void norm_wide_bwd_kernel(NormArgs<T, R> a) {
         const int64_t r0 = row * a.ch;
         const float r = a.rstd[row];
         const auto terms = [&](int at, int left, float (&d)[8], float (&n)[8], float (&g)[8]) {
-            Run<R, 8> h;
-            Run<T, 8> dy;
+            Vals<R, 8> h;
+            Vals<T, 8> dy;
             h.load(a.h + r0 + at, left);
             dy.load(a.dy + r0 + at, left);
-            const Run<float, 8> w = weights_at<8>(a.w, at, left);
+            const Vals<float, 8> w = weights_at<8>(a.w, at, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 d[e] = dy.at(e);
@@ -457,12 +457,12 @@ __global__ __launch_bounds__(1024) void norm_wide_bwd_kernel(NormArgs<T, R> a) {
             const int left = a.ch - at;
             float d[8], n[8], g[8];
             terms(at, left, d, n, g);
-            Run<R, 8> up;
+            Vals<R, 8> up;
             up.zero();
             if (a.dh != nullptr) up.load(a.dh + r0 + at, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-n[e], mean, g[e]) + up.at(e);
-            Run<T, 8> dx;
+            Vals<T, 8> dx;
             dx.put(g);
             dx.store(a.dx + r0 + at, left);
             if (a.dres != nullptr) {
