@@ -352,7 +352,7 @@ def _own(s):
         out = {}
         if c["out"] in CODE:
             codes, scales, h = m.rms_norm_codes(s["x"], s["w"], res=s["res"], eps=EPS, code=CODE[c["out"]], group=c["group"])
-            out = dict(codes=codes, scales=scales)
+            out = dict(codes=codes, scales=scales.reshape(c["rows"], -1))
         else:
             y, h, rstd = m.rms_norm(s["x"], s["w"], res=s["res"], eps=EPS, want_rstd=c["out"] == "train")
             out = dict(y=y)
