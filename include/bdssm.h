@@ -649,7 +649,8 @@ typedef struct {
  *   silu     nonzero: y = silu(p).
  *   c_init   NULL (zero) or the state in front of token 0.
  *   y        [batch, T, channels] out, or NULL (state only).
- *   c_final  NULL, or out: the state behind the row's last token.
+ *   c_final  NULL, or out: the state behind the row's last token.  May be
+ *            c_init (in place).
  */
 int bdssm_conv_scan(const bdssm_conv_shape *shape, int64_t T, const void *u, const float *w,
                     const float *bias, int silu, const int32_t *lens, const uint8_t *starts,

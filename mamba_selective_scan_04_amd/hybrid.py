@@ -285,7 +285,7 @@ def kv_attn_weights(cache, q, lse, page_table, ctx_lens, lens=None, scale=None, 
     _check(lens, "lens", torch.int32, (batch,))
     _check(mass, "mass", torch.float32, shape)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = lse.new_empty(shape)
     _check(out, "out", torch.float32, shape)
     s = KvShape(batch, hq, hkv, d, page, n_pages, shape[1], _dtype_code(q), CODES[cache.k.dtype])
     stream = _stream(q.get_device(), lse, cache.k, cache.k_scale, page_table, ctx_lens, lens, mass, out)

@@ -79,10 +79,10 @@ def conv_scan(u, w, bias=None, silu=True, lens=None, starts=None, c_init=None, w
     s, T = _conv(u, w, bias, lens, starts)
     _check(c_init, "c_init", u.dtype, _conv_state(s))
     if y is None and want_y:
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
     _check(y, "y", u.dtype, u.shape)
     if c_final is None:
-        c_final = torch.empty(_conv_state(s), dtype=u.dtype, device=u.device)
+        c_final = u.new_empty(_conv_state(s))
     _check(c_final, "c_final", u.dtype, _conv_state(s))
     stream = _stream(u.get_device(), w, bias, lens, starts, c_init, y, c_final)
     rc = load().bdssm_conv_scan(ctypes.byref(s), T, _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens), _p(starts),
@@ -99,7 +99,7 @@ def conv_step(c_cache, u, w, bias=None, silu=True, lens=None, c_out=None, want_y
     _check(c_cache, "c_cache", u.dtype, _conv_state(s))
     _check(c_out, "c_out", u.dtype, _conv_state(s))
     if y is None and want_y:
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
     _check(y, "y", u.dtype, u.shape)
     stream = _stream(u.get_device(), c_cache, w, bias, lens, y, c_out)
     rc = load().bdssm_conv_step(ctypes.byref(s), T, _p(c_cache), _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens),
@@ -119,17 +119,16 @@ def conv_scan_bwd(u, w, dy, bias=None, silu=True, lens=None, starts=None, c_init
         raise ValueError("dy is needed for the gradients")
     _check(dy, "dy", u.dtype, u.shape)
     _check(dc_final, "dc_final", u.dtype, _conv_state(s))
-    dev = u.device
     if du is None:
-        du = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        du = torch.empty_like(u, memory_format=torch.contiguous_format)
     if not isinstance(du, torch.Tensor) or du.dtype is not u.dtype or du.shape != u.shape or not du.is_cuda:
         raise ValueError("du must be on the GPU with u's shape and type")
     ld = _strides(du, "du")
-    dw = torch.empty(w.shape, dtype=torch.float32, device=dev)
-    dbias = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=dev)
-    dc = torch.empty(_conv_state(s), dtype=u.dtype, device=dev) if want_dc_init else None
+    dw = torch.empty_like(w)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dc = u.new_empty(_conv_state(s)) if want_dc_init else None
     stream = _stream(u.get_device(), w, bias, lens, starts, c_init, dy, dc_final, du, ws)
-    ws, room = _room(ws, "bdssm_conv_workspace_bytes", ctypes.byref(s), T, dev)
+    ws, room = _room(ws, "bdssm_conv_workspace_bytes", ctypes.byref(s), T, u.device)
     rc = load().bdssm_conv_scan_bwd(ctypes.byref(s), T, _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens), _p(starts),
                                     _p(c_init), _p(dy), _p(dc_final), _p(du), *ld, _p(dw), _p(dbias), _p(dc), _p(ws), room,
                                     stream)
@@ -170,7 +169,7 @@ def rms_norm(x, w, res=None, eps=1e-5, want_rstd=False, y=None, h=None):
     if y is None:
         y = torch.empty_like(x)
     _check(y, "y", x.dtype, x.shape)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
+    rstd = w.new_empty(x.shape[:-1]) if want_rstd else None
     stream = _stream(x.get_device(), w, res, y, out)
     rc = load().bdssm_rms_norm(ctypes.byref(s), _p(x), _p(res), _p(w), eps, _p(y), _p(out), _p(rstd), stream)
     _raise("bdssm_rms_norm", rc)
@@ -182,11 +181,12 @@ def rms_norm_codes(x, w, res=None, eps=1e-5, code=torch.float8_e4m3fn, group=0, 
     a row (group 0: scales [...]) or each 128 channels (scales [..., channels / 128])."""
     if code not in CODES:
         raise TypeError("code must be torch.float8_e4m3fn or torch.int8")
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (a row) or 128, got %r" % (group,))
     s = _norm(x, w, res)
     out = _norm_h(x, res, h)
-    codes = torch.empty(x.shape, dtype=code, device=x.device)
-    scales = torch.empty(x.shape[:-1] + (x.shape[-1] // group,) if group else x.shape[:-1], dtype=torch.float32,
-                         device=x.device)
+    codes = torch.empty_like(x, dtype=code)
+    scales = w.new_empty(x.shape[:-1] + (x.shape[-1] // group,) if group else x.shape[:-1])
     stream = _stream(x.get_device(), w, res, out)
     rc = load().bdssm_rms_norm_codes(ctypes.byref(s), _p(x), _p(res), _p(w), eps, CODES[code], group, _p(codes),
                                      _p(scales), _p(out), stream)
