@@ -286,7 +286,8 @@ def kv_attn_weights(cache, q, lse, page_table, ctx_lens, lens=None, scale=None, 
     _check(mass, "mass", torch.float32, shape)
     if out is None:
         out = lse.new_empty(shape)
-    _check(out, "out", torch.float32, shape)
+    else:
+        _check(out, "out", torch.float32, shape)
     s = KvShape(batch, hq, hkv, d, page, n_pages, shape[1], _dtype_code(q), CODES[cache.k.dtype])
     stream = _stream(q.get_device(), lse, cache.k, cache.k_scale, page_table, ctx_lens, lens, mass, out)
     rc = load().bdssm_kv_attn_weights(ctypes.byref(s), Lq, _p(q), _p(lse), _p(cache.k), _p(cache.k_scale), _p(page_table),
@@ -309,11 +310,11 @@ def kv_evict(page_table, ctx_lens, mass, page_len, budget, sink=0, recent=0, tab
     _check(page_table, "page_table", torch.int32)
     _check(ctx_lens, "ctx_lens", torch.int32, (batch,))
     _check(mass, "mass", torch.float32, shape)
+    _check(table_out, "table_out", torch.int32, shape)
+    _check(ctx_out, "ctx_out", torch.int32, (batch,))
+    _check(mass_out, "mass_out", torch.float32, shape)
     outs = [torch.empty_like(x) if y is None else y
             for x, y in ((page_table, table_out), (ctx_lens, ctx_out), (mass, mass_out))]
-    _check(outs[0], "table_out", torch.int32, shape)
-    _check(outs[1], "ctx_out", torch.int32, (batch,))
-    _check(outs[2], "mass_out", torch.float32, shape)
     stream = _stream(page_table.get_device(), ctx_lens, mass, *outs)
     rc = load().bdssm_kv_evict(batch, shape[1], page_len, budget, sink, recent, _p(page_table), _p(ctx_lens), _p(mass),
                                _p(outs[0]), _p(outs[1]), _p(outs[2]), stream)

@@ -78,12 +78,14 @@ def conv_scan(u, w, bias=None, silu=True, lens=None, starts=None, c_init=None, w
     starts[b, t] is set a document begins, in front of which no tap reaches."""
     s, T = _conv(u, w, bias, lens, starts)
     _check(c_init, "c_init", u.dtype, _conv_state(s))
-    if y is None and want_y:
+    if y is not None:
+        _check(y, "y", u.dtype, u.shape)
+    elif want_y:
         y = torch.empty_like(u, memory_format=torch.contiguous_format)
-    _check(y, "y", u.dtype, u.shape)
-    if c_final is None:
+    if c_final is not None:
+        _check(c_final, "c_final", u.dtype, _conv_state(s))
+    else:
         c_final = u.new_empty(_conv_state(s))
-    _check(c_final, "c_final", u.dtype, _conv_state(s))
     stream = _stream(u.get_device(), w, bias, lens, starts, c_init, y, c_final)
     rc = load().bdssm_conv_scan(ctypes.byref(s), T, _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens), _p(starts),
                                 _p(c_init), _p(y), _p(c_final), stream)
@@ -98,9 +100,10 @@ def conv_step(c_cache, u, w, bias=None, silu=True, lens=None, c_out=None, want_y
     s, T = _conv(u, w, bias, lens, None)
     _check(c_cache, "c_cache", u.dtype, _conv_state(s))
     _check(c_out, "c_out", u.dtype, _conv_state(s))
-    if y is None and want_y:
+    if y is not None:
+        _check(y, "y", u.dtype, u.shape)
+    elif want_y:
         y = torch.empty_like(u, memory_format=torch.contiguous_format)
-    _check(y, "y", u.dtype, u.shape)
     stream = _stream(u.get_device(), c_cache, w, bias, lens, y, c_out)
     rc = load().bdssm_conv_step(ctypes.byref(s), T, _p(c_cache), _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens),
                                 _p(y), _p(c_out), stream)
@@ -155,7 +158,7 @@ def _norm_h(x, res, h):
             raise ValueError("h is x without a residual")
         return None
     if h is None:
-        h = torch.empty_like(res)
+        return torch.empty_like(res)
     _check(h, "h", res.dtype, x.shape)
     return h
 
@@ -168,7 +171,8 @@ def rms_norm(x, w, res=None, eps=1e-5, want_rstd=False, y=None, h=None):
     out = _norm_h(x, res, h)
     if y is None:
         y = torch.empty_like(x)
-    _check(y, "y", x.dtype, x.shape)
+    else:
+        _check(y, "y", x.dtype, x.shape)
     rstd = w.new_empty(x.shape[:-1]) if want_rstd else None
     stream = _stream(x.get_device(), w, res, y, out)
     rc = load().bdssm_rms_norm(ctypes.byref(s), _p(x), _p(res), _p(w), eps, _p(y), _p(out), _p(rstd), stream)
