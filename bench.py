@@ -43,7 +43,7 @@ scan instead.  --crossover sweeps the context length from 8K to 64K tokens;
 (context only); --roof-probe prints the microbenchmarks alone.
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME]
-                       [--no-configs] [--crossover] [--model-loop] [--roof-probe]
+                       [--no-configs] [--crossover] [--model-loop [--short-conv]] [--roof-probe]
 """
 import argparse
 import ctypes
@@ -905,6 +905,8 @@ def main():
                          "the fused scan, no attention): cached block-restricted step against the "
                          "full-sequence rescan, at 8K and 64K context")
     ap.add_argument("--layers", type=int, default=24, help="--model-loop: layers of the stack")
+    ap.add_argument("--short-conv", action="store_true",
+                    help="--model-loop: with a short causal convolution in front of each scan, and the library's norm")
     ap.add_argument("--roof-probe", action="store_true", help="print the microbenchmarks alone")
     args = ap.parse_args()
 
@@ -1149,8 +1151,11 @@ def model_loop_main(args, m, synth, torch):
     x-projection to the low-rank dt and B, C, dt-projection, the fused scan
     with dt = softplus(dt_raw + bias) and the silu(z) gate, out-projection,
     residual), batch 8, d_model 768, d_inner 1536, 16 states, dt rank 48.  The
-    projections are plain torch GEMMs; there are no attention layers and no
-    short convolution.  Per denoising step of one 16-token block it times
+    projections are plain torch GEMMs; there are no attention layers.  With
+    --short-conv x goes through a short causal convolution of width 4 (its last
+    three inputs cached beside the scan's state, and committed with it), and the
+    norm with the residual's addition is the library's; without it there is no
+    convolution and the norm is torch operations.  Per denoising step of one 16-token block it times
       cached: the block's 16 tokens through every layer, each layer's scan a
               block_step from that layer's cache (plus, per block, the commit
               pass of the clean tokens, reported apart);
@@ -1173,17 +1178,30 @@ def model_loop_main(args, m, synth, torch):
     layers = []
     for i in range(nl):
         A, Dskip = synth.params(D, NS, 900 + i, "default", dev)
-        layers.append(dict(norm=torch.ones(dm, device=dev, dtype=dtype), w_x=w((dm, D), dm),
+        conv = {} if not args.short_conv else dict(
+            norm32=torch.ones(dm, device=dev), w_c=torch.randn((D, 4), generator=g, device=dev) / 2, b_c=torch.zeros(D, device=dev))
+        layers.append(dict(conv, norm=torch.ones(dm, device=dev, dtype=dtype), w_x=w((dm, D), dm),
                            w_z=w((dm, D), dm), w_p=w((D, R + 2 * NS), D), w_dt=w((R, D), R),
                            dt_bias=torch.full((D,), math.log(math.expm1(0.05)), device=dev),
                            A=A, Dskip=Dskip, w_out=w((D, dm), D)))
 
-    def mixer_inputs(lay, X):
-        """[batch, T, d_model] -> the scan's x, dt_raw, B, C, z ([batch, T, .])"""
-        b, T = X.shape[0], X.shape[1]
-        h = X.view(-1, dm)
-        h = (h.float() * torch.rsqrt(h.float().pow(2).mean(-1, keepdim=True) + 1e-5)).to(dtype) * lay["norm"]
-        x = torch.mm(h, lay["w_x"])
+    def mixer_inputs(lay, X, conv=None):
+        """[batch, T, d_model] -> the scan's x, dt_raw, B, C, z ([batch, T, .]).
+        conv: the layer's short convolution, of x.  X may be a pair, the residual
+        stream and what the last layer adds to it; its sum replaces the first."""
+        if args.short_conv:
+            res, add = X if isinstance(X, list) else (None, X)
+            h, sum_, _ = m.rms_norm(add, lay["norm32"], res=res)
+            b, T = h.shape[0], h.shape[1]
+            if isinstance(X, list):
+                X[0] = sum_
+            h = h.view(-1, dm)
+            x = conv(torch.mm(h, lay["w_x"]).view(b, T, D)).view(-1, D)
+        else:
+            b, T = X.shape[0], X.shape[1]
+            h = X.view(-1, dm)
+            h = (h.float() * torch.rsqrt(h.float().pow(2).mean(-1, keepdim=True) + 1e-5)).to(dtype) * lay["norm"]
+            x = torch.mm(h, lay["w_x"])
         z = torch.mm(h, lay["w_z"])
         p = torch.mm(x, lay["w_p"])
         dt = torch.mm(p[:, :R], lay["w_dt"])
@@ -1192,39 +1210,52 @@ def model_loop_main(args, m, synth, torch):
         return (x.view(b, T, D), dt.view(b, T, D), Bm.view(b, T, NS), Cm.view(b, T, NS), z.view(b, T, D))
 
     def layer_out(lay, X, y):
-        return X + torch.mm(y.view(-1, D), lay["w_out"]).view(X.shape)
+        add = torch.mm(y.view(-1, D), lay["w_out"])
+        if args.short_conv:
+            res = X[0] if isinstance(X, list) else X
+            return [res, add.view(res.shape)]
+        return X + add.view(X.shape)
+
+    def stack_out(X):
+        return X[0] + X[1] if isinstance(X, list) else X
+
+    # the last three inputs of each layer's convolution, where there is one
+    conv_caches = [torch.zeros(batch, 3, D, dtype=dtype, device=dev) for _ in range(nl)] if args.short_conv else [None] * nl
+
+    def conv_of(lay, call):
+        return lambda x: call(x, lay["w_c"], bias=lay["b_c"])
 
     def cached_step(X, caches):
-        for lay, h in zip(layers, caches):
-            x, dt, Bm, Cm, z = mixer_inputs(lay, X)
+        for lay, h, c in zip(layers, caches, conv_caches):
+            x, dt, Bm, Cm, z = mixer_inputs(lay, X, conv_of(lay, lambda u, w_c, bias: m.conv_step(c, u, w_c, bias=bias)))
             y = m.block_step(h, x, dt, Bm, Cm, lay["A"], lay["Dskip"], dt_bias=lay["dt_bias"],
                              dt_softplus=True, z=z)
             X = layer_out(lay, X, y)
-        return X
+        return stack_out(X)
 
-    def commit_pass(X, caches):
-        for lay, h in zip(layers, caches):
-            x, dt, Bm, Cm, z = mixer_inputs(lay, X)
+    def commit_pass(X, caches, convs):
+        for lay, h, c in zip(layers, caches, convs):
+            x, dt, Bm, Cm, z = mixer_inputs(lay, X, conv_of(lay, lambda u, w_c, bias: m.conv_step(c, u, w_c, bias=bias, c_out=c)))
             _, y = m.commit(h, x, dt, Bm, Cm, lay["A"], lay["Dskip"], want_y=True,
                             dt_bias=lay["dt_bias"], dt_softplus=True, z=z)
             X = layer_out(lay, X, y)
-        return X
+        return stack_out(X)
 
     def full_step(X, ws):
         for lay in layers:
-            x, dt, Bm, Cm, z = mixer_inputs(lay, X)
+            x, dt, Bm, Cm, z = mixer_inputs(lay, X, conv_of(lay, lambda u, w_c, bias: m.conv_scan(u, w_c, bias=bias)[0]))
             y = m.full_scan(x, dt, Bm, Cm, lay["A"], lay["Dskip"], ws=ws, dt_bias=lay["dt_bias"],
                             dt_softplus=True, z=z)
             X = layer_out(lay, X, y)
-        return X
+        return stack_out(X)
 
     def prefill_pass(X, caches, ws):
-        for lay, h in zip(layers, caches):
-            x, dt, Bm, Cm, z = mixer_inputs(lay, X)
+        for lay, h, c in zip(layers, caches, conv_caches):
+            x, dt, Bm, Cm, z = mixer_inputs(lay, X, conv_of(lay, lambda u, w_c, bias: m.conv_scan(u, w_c, bias=bias, c_final=c)[0]))
             _, y = m.prefill(x, dt, Bm, Cm, lay["A"], lay["Dskip"], L, h_cache=h, want_y=True, ws=ws,
                              dt_bias=lay["dt_bias"], dt_softplus=True, z=z)
             X = layer_out(lay, X, y)
-        return X
+        return stack_out(X)
 
     def time_calls(fn, reps):
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -1273,14 +1304,16 @@ def model_loop_main(args, m, synth, torch):
         step_graph_ms = time_calls(gr.replay, 50) if graph_ok else None
         del gr, out_g
         ccaches = [c.clone() for c in caches]
-        commit_ms = time_calls(lambda: commit_pass(Xb, ccaches), 5)
+        cconvs = [c if c is None else c.clone() for c in conv_caches]
+        commit_ms = time_calls(lambda: commit_pass(Xb, ccaches, cconvs), 5)
         full_ms = time_calls(lambda: full_step(Xf, wsf), 2)
         # the scans alone, for the share of the step they take
-        scan_in = mixer_inputs(layers[0], Xb)
+        same = lambda x: x  # noqa: E731
+        scan_in = mixer_inputs(layers[0], Xb, same)
         scan_ms = nl * time_calls(lambda: m.block_step(caches[0], *scan_in[:4], layers[0]["A"], layers[0]["Dskip"],
                                                        dt_bias=layers[0]["dt_bias"], dt_softplus=True,
                                                        z=scan_in[4]), 50)
-        full_in = mixer_inputs(layers[0], Xf)
+        full_in = mixer_inputs(layers[0], Xf, same)
         full_scan_ms = nl * time_calls(lambda: m.full_scan(*full_in[:4], layers[0]["A"], layers[0]["Dskip"], ws=wsf,
                                                            dt_bias=layers[0]["dt_bias"], dt_softplus=True,
                                                            z=full_in[4]), 2)
@@ -1307,8 +1340,8 @@ def model_loop_main(args, m, synth, torch):
         "n_gpus": 1, "steps": S, "warmup": 1, "ms_per_step": r["cached_step_ms"],
         "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
         "data": "synthetic (random weights)",
-        "config": {"workload": "random-weight Mamba-1 stack, no attention, eager launches "
-                               "(cached step also from a HIP graph)",
+        "config": {"workload": "random-weight Mamba-1 stack, no attention%s, eager launches "
+                               "(cached step also from a HIP graph)" % (", short convolution" if args.short_conv else ""),
                    "batch": batch, "d_model": dm, "d_inner": D, "d_state": NS, "dt_rank": R,
                    "layers": nl, "block": L, "denoising_steps": S},
         "rows": rows,

@@ -35,17 +35,38 @@ struct Vals {
 #pragma unroll
         for (int i = 0; i < kN; ++i) v[i] = T(0);
     }
-    __device__ __forceinline__ float at(int i) const { return Stream<T>::load(v + i); }
+    __device__ __forceinline__ float at(int i) const { return v[i]; }
     __device__ __forceinline__ void put(const float *x) {
-        if constexpr (sizeof(T) == 2 && kN % 2 == 0) {
-            uint32_t w[kN / 2];
 #pragma unroll
-            for (int i = 0; i < kN / 2; ++i) w[i] = pk_rne(x[2 * i], x[2 * i + 1]);
-            __builtin_memcpy(v, w, sizeof v);
-        } else {
+        for (int i = 0; i < kN; ++i) v[i] = x[i];
+    }
+};
+// bf16 in pairs: two of them a register
+template <int kN>
+struct Vals<uint16_t, kN> {
+    uint32_t w[kN / 2];
+    __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(w, p, sizeof w); }
+    __device__ __forceinline__ void store(uint16_t *p) const { __builtin_memcpy(p, w, sizeof w); }
+    __device__ __forceinline__ void load(const uint16_t *p, int n) {
+        if (n >= kN) return load(p);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) Stream<T>::store(v + i, x[i]);
-        }
+        for (int i = 0; i < kN / 2; ++i)
+            w[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+    __device__ __forceinline__ void store(uint16_t *p, int n) const {
+        if (n >= kN) return store(p);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (i < n) p[i] = (uint16_t)(w[i / 2] >> i % 2 * 16);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int i) const { return i % 2 ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]); }
+    __device__ __forceinline__ void put(const float *x) {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) w[i] = pk_rne(x[2 * i], x[2 * i + 1]);
     }
 };
 
