@@ -633,7 +633,8 @@ int bdssm_kv_evict(int64_t batch, int64_t max_pages, int64_t page_len, int64_t b
  * The two-stream training form, every block from the clean stream's state, is
  * the call on the blocks as rows (batch * T/L of L tokens), with the clean
  * tokens in front of each block as c_init.
- * Limits: W 2, 3 or 4; T < 2^30; y, states and gradients (but du) contiguous.
+ * Limits: W 2, 3 or 4; T < 2^30; y, states and gradients (but du) contiguous; a
+ * call's workgroups (2^24) must be countable.
  */
 typedef struct {
     int64_t batch;           /* >= 0 */

@@ -102,7 +102,8 @@ __device__ __forceinline__ int conv_len(const ConvArgs<T> &a, int64_t b) {
     return n < 0 ? 0 : n < a.T_tokens ? n : a.T_tokens;
 }
 
-// Without y a lane goes over the row's last W - 1 tokens alone.
+// The row's first chunk writes its last state: it alone has read the first one, which
+// may lie in the same place.
 template <typename T, int kW, int kN>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     constexpr int kAhead = 6;   // tokens read at a time: a multiple of W - 1, so that no input moves
@@ -111,21 +112,27 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     const int lane = (int)(job % a.lanes), chunk = (int)(job / a.lanes % a.chunks);
     const int64_t b = job / a.lanes / a.chunks;
     const int c0 = lane * kN, n_ch = a.ch - c0, n = conv_len(a, b);
-    int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
-    if (a.y == nullptr) {
-        t0 = n > kW - 1 ? n - (kW - 1) : 0;
-        t1 = n;
-    }
+    const int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
     const int stop = t1 < n ? t1 : n;   // of the tokens that are read
-    T *yb = a.y == nullptr ? nullptr : a.y + b * a.T_tokens * a.ch + c0;
-    const bool last = a.c_final != nullptr && (a.y == nullptr || (n > t0 && n <= t1) || (n == 0 && chunk == 0));
-    if (t0 < stop || last) {
+    const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+    Vals<T, kN> hist[kW - 1];
+    int age = kOld;
+    if (a.y != nullptr && t0 < stop) age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
+    if (chunk == 0 && a.c_final != nullptr) {
+        Vals<T, kN> last[kW - 1];
+        const int old = conv_history<T, kW, kN>(a, b, n, c0, n_ch, last);   // of token n - 1
+#pragma unroll
+        for (int j = 0; j < kW - 1; ++j) {
+            if (kW - 2 - j > old) last[j].zero();   // a document started behind it
+            last[j].store(a.c_final + (b * (kW - 1) + j) * a.ch + c0, n_ch);
+        }
+    }
+    if (a.y == nullptr) return;
+    T *yb = a.y + b * a.T_tokens * a.ch + c0;
+    if (t0 < stop) {
         float wt[kN][kW], bs[kN];
         conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
-        Vals<T, kN> hist[kW - 1];
-        int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
         const T *ub = a.u + b * a.batch_ld + c0;
-        const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
         const auto token = [&](int t, const Vals<T, kN> &x) {
             if (starts != nullptr) {
                 age = age_after(starts, t, age);
@@ -133,23 +140,21 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
                 for (int j = 0; j < kW - 1; ++j)
                     if (kW - 1 - j > age) hist[j].zero();
             }
-            if (yb != nullptr) {
-                float p[kN];
+            float p[kN];
 #pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    p[e] = bs[e];
+            for (int e = 0; e < kN; ++e) {
+                p[e] = bs[e];
 #pragma unroll
-                    for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
-                    p[e] = fmaf(wt[e][kW - 1], x.at(e), p[e]);
-                }
-                if (a.silu) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
-                }
-                Vals<T, kN> out;
-                out.put(p);
-                out.store(yb + (int64_t)t * a.ch, n_ch);
+                for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
+                p[e] = fmaf(wt[e][kW - 1], x.at(e), p[e]);
             }
+            if (a.silu) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
+            }
+            Vals<T, kN> out;
+            out.put(p);
+            out.store(yb + (int64_t)t * a.ch, n_ch);
 #pragma unroll
             for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
             hist[kW - 2] = x;
@@ -182,20 +187,10 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
             for (int i = 0; i < kAhead - 1; ++i)
                 if (t + i < stop) token(t + i, x[i]);
         }
-        if (last) {
-            // kept where no document started behind it (the age of a row of no tokens is none)
-#pragma unroll
-            for (int j = 0; j < kW - 1; ++j) {
-                if (kW - 2 - j > age) hist[j].zero();
-                hist[j].store(a.c_final + (b * (kW - 1) + j) * a.ch + c0, n_ch);
-            }
-        }
     }
-    if (yb != nullptr) {
-        Vals<T, kN> none;
-        none.zero();
-        for (int t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + (int64_t)t * a.ch, n_ch);
-    }
+    Vals<T, kN> none;
+    none.zero();
+    for (int t = stop > t0 ? stop : t0; t < t1; ++t) none.store(yb + (int64_t)t * a.ch, n_ch);
 }
 
 // Gradients.  A lane sweeps its chunk and the W - 1 tokens behind it forward in

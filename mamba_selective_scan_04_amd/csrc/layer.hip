@@ -56,13 +56,12 @@ int64_t power_from(int64_t x, int64_t low, int64_t high) {   // the least power 
 //   2 rows of 2,041, 1,021 channels, fp32        2: 11.8   4: 10.8   6: 11.4   12: 14.0
 //   1 row of 65,536, 2,048 channels, bf16        12: 128   24: 116   48: 118   66: 116
 //   8 rows of 4,096, 1,536 channels, bf16        12: 48   24: 45   48: 43   66: 42
-// One chunk where a lane has to have read the state before it is written (in place),
-// or only the state is wanted.
-ConvPlan conv_plan(const bdssm_conv_shape *s, int64_t T, bool whole) {
+// One chunk where only the state is wanted.
+ConvPlan conv_plan(const bdssm_conv_shape *s, int64_t T, bool state_only) {
     ConvPlan p{};
     p.lanes = (int)((s->channels + kConvLane - 1) / kConvLane);
     const int64_t most = kCus * 16 * 64, work = s->batch * T * p.lanes;
-    p.chunk = (int)(whole ? (T > 0 ? T : 1) : within((work + most - 1) / most, 4, 66));
+    p.chunk = (int)(state_only ? (T > 0 ? T : 1) : within((work + most - 1) / most, 4, 66));
     p.chunks = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;
     p.jobs = s->batch * p.chunks * p.lanes;
     p.block = p.jobs < 256 * 256 ? 64 : 256;   // few lanes: spread over the CUs
@@ -130,7 +129,7 @@ int conv_forward(const bdssm_conv_shape *s, int64_t T, const void *u, const floa
     c.c_init = c_init;
     c.y = y;
     c.c_final = c_final;
-    c.plan = conv_plan(s, T, !y || (c_final && c_final == c_init));
+    c.plan = conv_plan(s, T, !y);
     if ((c.plan.jobs + c.plan.block - 1) / c.plan.block > kMostGroups) return BDSSM_ERR_SHAPE;
     (void)hipGetLastError();
     if (s->dtype == BDSSM_BF16) launch_conv<uint16_t>(c, st);
