@@ -104,14 +104,14 @@ __device__ __forceinline__ int conv_len(const ConvArgs<T> &a, int64_t b) {
 
 // The row's first chunk writes its last state: it alone has read the first one, which
 // may lie in the same place.
-template <typename T, int kW, int kN>
+template <typename T, int kW, int kN, bool kWhole>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     constexpr int kAhead = 6;   // tokens read at a time: a multiple of W - 1, so that no input moves
     const int64_t job = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (job >= a.jobs) return;
     const int lane = (int)(job % a.lanes), chunk = (int)(job / a.lanes % a.chunks);
     const int64_t b = job / a.lanes / a.chunks;
-    const int c0 = lane * kN, n_ch = a.ch - c0, n = conv_len(a, b);
+    const int c0 = lane * kN, n_ch = kWhole ? kN : a.ch - c0, n = conv_len(a, b);
     const int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
     const int stop = t1 < n ? t1 : n;   // of the tokens that are read
     const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 // registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
 // but at a row's ends (chunks are multiples of 6).  The parameters' sums of a workgroup's chunks join in LDS in
 // a fixed order and go to `parts`.
-template <typename T, int kW, int kN>
+template <typename T, int kW, int kN, bool kWhole>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
     constexpr int kAhead = kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
     static_assert(kAhead >= kW - 1 && 6 % kAhead == 0, "a chunk is whole groups; what its first one completes lies in front of it");
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
     const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
     const int lane = group * a.row_lanes + (int)(threadIdx.x & (a.row_lanes - 1));
     const int per = 256 / a.row_lanes;                        // chunks of the workgroup at a time
-    const int c0 = lane * kN, n_ch = a.ch - c0;
+    const int c0 = lane * kN, n_ch = kWhole ? kN : a.ch - c0;
     float dw[kN][kW], db[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
@@ -215,8 +215,9 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         for (int j = 0; j < kW; ++j) dw[e][j] = 0.f;
     }
     float wt[kN][kW], bs[kN];
-    if (n_ch > 0) conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
-    for (int64_t row = (int64_t)part * per + threadIdx.x / a.row_lanes; n_ch > 0 && row < a.rows; row += (int64_t)a.n_parts * per) {
+    const bool there = lane < a.lanes;
+    if (there) conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
+    for (int64_t row = (int64_t)part * per + threadIdx.x / a.row_lanes; there && row < a.rows; row += (int64_t)a.n_parts * per) {
         const int chunk = (int)(row % a.chunks);
         const int64_t b = row / a.chunks;
         const int n = conv_len(a, b), t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;

@@ -31,15 +31,27 @@ ConvArgs<T> conv_args(const ConvCall &c) {
     return a;
 }
 
+// calls f with the convolution's width, and whether its channels fill their lanes
+template <typename F>
+void with_width(const ConvCall &c, F &&f) {
+    const auto filled = [&](auto width) {
+        if (c.ch % kConvLane == 0) f(width, std::true_type{});
+        else f(width, std::false_type{});
+    };
+    if (c.width == 4) filled(std::integral_constant<int, 4>{});
+    else if (c.width == 3) filled(std::integral_constant<int, 3>{});
+    else filled(std::integral_constant<int, 2>{});
+}
+
 template <>
 void launch_conv<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     using T = BDSSM_TIN;
     constexpr int kN = kConvLane;
     const ConvArgs<T> a = conv_args<T>(c);
     const dim3 g((unsigned)((c.plan.jobs + c.plan.block - 1) / c.plan.block)), t(c.plan.block);
-    if (c.width == 4) hipLaunchKernelGGL((conv_kernel<T, 4, kN>), g, t, 0, st, a);
-    else if (c.width == 3) hipLaunchKernelGGL((conv_kernel<T, 3, kN>), g, t, 0, st, a);
-    else hipLaunchKernelGGL((conv_kernel<T, 2, kN>), g, t, 0, st, a);
+    with_width(c, [&](auto width, auto whole) {
+        hipLaunchKernelGGL((conv_kernel<T, decltype(width)::value, kN, decltype(whole)::value>), g, t, 0, st, a);
+    });
 }
 
 template <>
@@ -60,9 +72,9 @@ void launch_conv_bwd<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     a.n_parts = c.plan.n_parts;
     const dim3 g((unsigned)(c.plan.groups * c.plan.n_parts)), t(256);
     if (c.plan.n_parts > 0) {
-        if (c.width == 4) hipLaunchKernelGGL((conv_bwd_kernel<T, 4, kN>), g, t, 0, st, a);
-        else if (c.width == 3) hipLaunchKernelGGL((conv_bwd_kernel<T, 3, kN>), g, t, 0, st, a);
-        else hipLaunchKernelGGL((conv_bwd_kernel<T, 2, kN>), g, t, 0, st, a);
+        with_width(c, [&](auto width, auto whole) {
+            hipLaunchKernelGGL((conv_bwd_kernel<T, decltype(width)::value, kN, decltype(whole)::value>), g, t, 0, st, a);
+        });
     }
     const int64_t cols = (int64_t)(c.width + 1) * c.ch;
     hipLaunchKernelGGL((parts_sum_kernel<16>), dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, st, c.parts, c.plan.n_parts, c.width, 1,
