@@ -56,7 +56,7 @@ constexpr int kOld = 1 << 30;   // at least as far; stays below 2^31 over a row
 
 // The W - 1 inputs in front of token t0 (hist[0] the oldest) and their age.
 template <typename T, int kW, int kN>
-__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int t0, int c0, int n_ch, Vals<T, kN> (&hist)[kW - 1]) {
+__device__ __forceinline__ int conv_history(const ConvArgs<T> &a, const uint8_t *starts, int64_t b, int t0, int c0, int n_ch, Vals<T, kN> (&hist)[kW - 1]) {
     const T *ub = a.u + b * a.batch_ld + c0;
 #pragma unroll
     for (int j = 0; j < kW - 1; ++j) {
@@ -66,11 +66,11 @@ __device__ __forceinline__ int conv_history(const ConvArgs<T> &a, int64_t b, int
         else hist[j].zero();
     }
     int age = kOld;   // of token t0 - 1
-    if (a.starts != nullptr) {
+    if (starts != nullptr) {
 #pragma unroll
         for (int j = 0; j < kW - 1; ++j) {
             const int t = t0 - (kW - 1) + j;
-            if (t >= 0) age = age_after(a.starts + b * a.T_tokens, t, age);
+            if (t >= 0) age = age_after(starts, t, age);
         }
     }
     return age;
@@ -104,23 +104,23 @@ __device__ __forceinline__ int conv_len(const ConvArgs<T> &a, int64_t b) {
 
 // The row's first chunk writes its last state: it alone has read the first one, which
 // may lie in the same place.
-template <typename T, int kW, int kN, bool kWhole>
+template <typename T, int kW, int kN, bool kPlain>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     constexpr int kAhead = 6;   // tokens read at a time: a multiple of W - 1, so that no input moves
     const int64_t job = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (job >= a.jobs) return;
     const int lane = (int)(job % a.lanes), chunk = (int)(job / a.lanes % a.chunks);
     const int64_t b = job / a.lanes / a.chunks;
-    const int c0 = lane * kN, n_ch = kWhole ? kN : a.ch - c0, n = conv_len(a, b);
+    const int c0 = lane * kN, n_ch = kPlain ? kN : a.ch - c0, n = conv_len(a, b);
     const int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
     const int stop = t1 < n ? t1 : n;   // of the tokens that are read
-    const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+    const uint8_t *starts = kPlain || a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
     Vals<T, kN> hist[kW - 1];
     int age = kOld;
-    if (a.y != nullptr && t0 < stop) age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
+    if (a.y != nullptr && t0 < stop) age = conv_history<T, kW, kN>(a, starts, b, t0, c0, n_ch, hist);
     if (chunk == 0 && a.c_final != nullptr) {
         Vals<T, kN> last[kW - 1];
-        const int old = conv_history<T, kW, kN>(a, b, n, c0, n_ch, last);   // of token n - 1
+        const int old = conv_history<T, kW, kN>(a, starts, b, n, c0, n_ch, last);   // of token n - 1
 #pragma unroll
         for (int j = 0; j < kW - 1; ++j) {
             if (kW - 2 - j > old) last[j].zero();   // a document started behind it
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
                 for (int j = 0; j < kW - 1; ++j) p[e] = fmaf(wt[e][j], hist[j].at(e), p[e]);
                 p[e] = fmaf(wt[e][kW - 1], x.at(e), p[e]);
             }
-            if (a.silu) {
+            if (kPlain || a.silu) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e) p[e] *= sigmoid(p[e]);
             }
@@ -198,15 +198,15 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 // registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
 // but at a row's ends (chunks are multiples of 6).  The parameters' sums of a workgroup's chunks join in LDS in
 // a fixed order and go to `parts`.
-template <typename T, int kW, int kN, bool kWhole>
+template <typename T, int kW, int kN, bool kPlain>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
-    constexpr int kAhead = kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
+    constexpr int kAhead = kPlain ? 6 : kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
     static_assert(kAhead >= kW - 1 && 6 % kAhead == 0, "a chunk is whole groups; what its first one completes lies in front of it");
     __shared__ float sums[256 * kSums];
     const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
     const int lane = group * a.row_lanes + (int)(threadIdx.x & (a.row_lanes - 1));
     const int per = 256 / a.row_lanes;                        // chunks of the workgroup at a time
-    const int c0 = lane * kN, n_ch = kWhole ? kN : a.ch - c0;
+    const int c0 = lane * kN, n_ch = kPlain ? kN : a.ch - c0;
     float dw[kN][kW], db[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
@@ -223,13 +223,13 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         const int n = conv_len(a, b), t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
         float open[kW - 1][kN];                               // open[d - 1]: du of token t - d
         Vals<T, kN> hist[kW - 1];
-        int age = conv_history<T, kW, kN>(a, b, t0, c0, n_ch, hist);
+        const uint8_t *starts = kPlain || a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+        int age = conv_history<T, kW, kN>(a, starts, b, t0, c0, n_ch, hist);
 #pragma unroll
         for (int d = 0; d < kW - 1; ++d)
 #pragma unroll
             for (int e = 0; e < kN; ++e) open[d][e] = 0.f;
         const T *ub = a.u + b * a.batch_ld + c0, *dyb = a.dy + b * a.T_tokens * a.ch + c0;
-        const uint8_t *starts = a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
         T *dub = a.du + b * a.du_batch_ld + c0;
         // dp of token s, and what it adds to; own: the token is one of the chunk's
         const auto token = [&](int s, const Vals<T, kN> &x, const Vals<T, kN> &g, bool own, float (&dp)[kN]) {
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 dp[e] = g.at(e);
-                if (a.silu) {
+                if (kPlain || a.silu) {
                     float p = bs[e];
 #pragma unroll
                     for (int j = 0; j < kW - 1; ++j) p = fmaf(wt[e][j], hist[j].at(e), p);
