@@ -50,7 +50,7 @@ __device__ __forceinline__ float sigmoid(float p) {
 
 // How many tokens behind the last document's start a token is, as far as taps care.
 __device__ __forceinline__ int age_after(const uint8_t *starts, int t, int age) {
-    return starts != nullptr && starts[t] ? 0 : age + 1;
+    return starts[t] ? 0 : age + 1;
 }
 constexpr int kOld = 1 << 30;   // at least as far; stays below 2^31 over a row
 
@@ -104,7 +104,7 @@ __device__ __forceinline__ int conv_len(const ConvArgs<T> &a, int64_t b) {
 
 // The row's first chunk writes its last state: it alone has read the first one, which
 // may lie in the same place.
-template <typename T, int kW, int kN, bool kPlain>
+template <typename T, int kW, int kN, bool kPlain, bool kStarts>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     constexpr int kAhead = 6;   // tokens read at a time: a multiple of W - 1, so that no input moves
     const int64_t job = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
     const int c0 = lane * kN, n_ch = kPlain ? kN : a.ch - c0, n = conv_len(a, b);
     const int t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
     const int stop = t1 < n ? t1 : n;   // of the tokens that are read
-    const uint8_t *starts = kPlain || a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+    const uint8_t *starts = kStarts ? a.starts + b * a.T_tokens : nullptr;
     Vals<T, kN> hist[kW - 1];
     int age = kOld;
     if (a.y != nullptr && t0 < stop) age = conv_history<T, kW, kN>(a, starts, b, t0, c0, n_ch, hist);
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
         conv_weights<kW, kN>(a.w, a.bias, c0, n_ch, wt, bs);
         const T *ub = a.u + b * a.batch_ld + c0;
         const auto token = [&](int t, const Vals<T, kN> &x) {
-            if (starts != nullptr) {
+            if (kStarts) {
                 age = age_after(starts, t, age);
 #pragma unroll
                 for (int j = 0; j < kW - 1; ++j)
@@ -198,9 +198,9 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 // registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
 // but at a row's ends (chunks are multiples of 6).  The parameters' sums of a workgroup's chunks join in LDS in
 // a fixed order and go to `parts`.
-template <typename T, int kW, int kN, bool kPlain>
+template <typename T, int kW, int kN, bool kPlain, bool kStarts>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
-    constexpr int kAhead = kPlain ? 6 : kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
+    constexpr int kAhead = kPlain && !kStarts ? 6 : kW == 4 ? 3 : 2, kSums = kN * (kW + 1);
     static_assert(kAhead >= kW - 1 && 6 % kAhead == 0, "a chunk is whole groups; what its first one completes lies in front of it");
     __shared__ float sums[256 * kSums];
     const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         const int n = conv_len(a, b), t0 = chunk * a.chunk, t1 = a.T_tokens - t0 < a.chunk ? a.T_tokens : t0 + a.chunk;
         float open[kW - 1][kN];                               // open[d - 1]: du of token t - d
         Vals<T, kN> hist[kW - 1];
-        const uint8_t *starts = kPlain || a.starts == nullptr ? nullptr : a.starts + b * a.T_tokens;
+        const uint8_t *starts = kStarts ? a.starts + b * a.T_tokens : nullptr;
         int age = conv_history<T, kW, kN>(a, starts, b, t0, c0, n_ch, hist);
 #pragma unroll
         for (int d = 0; d < kW - 1; ++d)
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
         T *dub = a.du + b * a.du_batch_ld + c0;
         // dp of token s, and what it adds to; own: the token is one of the chunk's
         const auto token = [&](int s, const Vals<T, kN> &x, const Vals<T, kN> &g, bool own, float (&dp)[kN]) {
-            if (starts != nullptr) {
+            if (kStarts) {
                 age = age_after(starts, s, age);
 #pragma unroll
                 for (int j = 0; j < kW - 1; ++j)
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
             }
 #pragma unroll
             for (int d = 1; d < kW; ++d)
-                if (starts == nullptr || d <= age) {
+                if (!kStarts || d <= age) {
 #pragma unroll
                     for (int e = 0; e < kN; ++e) open[d - 1][e] = fmaf(wt[e][kW - 1 - d], dp[e], open[d - 1][e]);
                 }

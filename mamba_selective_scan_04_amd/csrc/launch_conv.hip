@@ -31,12 +31,18 @@ ConvArgs<T> conv_args(const ConvCall &c) {
     return a;
 }
 
-// calls f with the convolution's width, and whether it is a plain one (kPlain)
+// calls f with the convolution's width, whether it is a plain one and has starts
 template <typename F>
 void with_width(const ConvCall &c, F &&f) {
     const auto kind = [&](auto width) {
-        if (c.ch % kConvLane == 0 && c.starts == nullptr && c.silu) f(width, std::true_type{});
-        else f(width, std::false_type{});
+        const bool plain = c.ch % kConvLane == 0 && c.silu;
+        if (c.starts == nullptr) {
+            if (plain) f(width, std::true_type{}, std::false_type{});
+            else f(width, std::false_type{}, std::false_type{});
+        } else {
+            if (plain) f(width, std::true_type{}, std::true_type{});
+            else f(width, std::false_type{}, std::true_type{});
+        }
     };
     if (c.width == 4) kind(std::integral_constant<int, 4>{});
     else if (c.width == 3) kind(std::integral_constant<int, 3>{});
@@ -49,8 +55,8 @@ void launch_conv<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     constexpr int kN = kConvLane;
     const ConvArgs<T> a = conv_args<T>(c);
     const dim3 g((unsigned)((c.plan.jobs + c.plan.block - 1) / c.plan.block)), t(c.plan.block);
-    with_width(c, [&](auto width, auto plain) {
-        hipLaunchKernelGGL((conv_kernel<T, decltype(width)::value, kN, decltype(plain)::value>), g, t, 0, st, a);
+    with_width(c, [&](auto width, auto plain, auto starts) {
+        hipLaunchKernelGGL((conv_kernel<T, decltype(width)::value, kN, decltype(plain)::value, decltype(starts)::value>), g, t, 0, st, a);
     });
 }
 
@@ -72,8 +78,8 @@ void launch_conv_bwd<BDSSM_TIN>(const ConvCall &c, hipStream_t st) {
     a.n_parts = c.plan.n_parts;
     const dim3 g((unsigned)(c.plan.groups * c.plan.n_parts)), t(256);
     if (c.plan.n_parts > 0) {
-        with_width(c, [&](auto width, auto plain) {
-            hipLaunchKernelGGL((conv_bwd_kernel<T, decltype(width)::value, kN, decltype(plain)::value>), g, t, 0, st, a);
+        with_width(c, [&](auto width, auto plain, auto starts) {
+            hipLaunchKernelGGL((conv_bwd_kernel<T, decltype(width)::value, kN, decltype(plain)::value, decltype(starts)::value>), g, t, 0, st, a);
         });
     }
     const int64_t cols = (int64_t)(c.width + 1) * c.ch;
