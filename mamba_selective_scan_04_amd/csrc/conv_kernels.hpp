@@ -10,9 +10,12 @@
 // Memory is the bound: 2 W + 4 operations a value against 4 bytes (bf16).  A lane
 // takes four neighbouring channels and a chunk of consecutive tokens, keeping the last
 // W - 1 inputs in registers, so that each input is read once but for the W - 1 in
-// front of a chunk.  (Eight channels of bf16, 16 bytes a load, need 165 registers
-// instead of 100, and so fewer waves: 65,536 tokens of 2,048 channels 207 us instead
-// of 124.)
+// front of a chunk.  65,536 tokens of 2,048 channels in bf16, half of a projection: 104
+// us (5.2 TB/s read and written; a copy of 2 GiB runs at 4.9); 8 rows of 4,096 tokens of
+// 1,536: 42 us.  Eight channels of bf16, 16 bytes a load: 109 and 42 us, 6.8 instead of
+// 6.0 for 64 rows of 16 tokens.  kPlain: every lane has its kN channels and y = silu(p);
+// kStarts: there may be starts of documents.  Both are asked nowhere else: as
+// conditions in the kernel, at each token, load and store, they cost the first 116 us.
 #pragma once
 
 #include "layer_common.hpp"
@@ -196,8 +199,11 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 // Gradients.  A lane sweeps its chunk and the W - 1 tokens behind it forward in
 // time, the inputs' last W - 1 values and the W - 1 unfinished sums of du in
 // registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
-// but at a row's ends (chunks are multiples of 6).  The parameters' sums of a workgroup's chunks join in LDS in
-// a fixed order and go to `parts`.
+// but at a row's ends (chunks are multiples of 6).  The parameters' sums of a
+// workgroup's chunks join in LDS in a fixed order and go to `parts`.  Bound by memory
+// and the vector units (59% of their slots): 8 rows of 4,096 tokens of 1,536 channels in
+// bf16 68 us (4.5 TB/s; 84 with three tokens at a time, 105 with documents, whose
+// conditions leave registers for three).
 template <typename T, int kW, int kN, bool kPlain, bool kStarts>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
     constexpr int kAhead = kPlain && !kStarts ? 6 : kW == 4 ? 3 : 2, kSums = kN * (kW + 1);

@@ -37,7 +37,10 @@ struct Row {
     static constexpr int kThreads = kThreads_, kV = kV_, kVecs = kVecs_;
 };
 
-// calls f with the threads and vectors of a row of ch channels, at most kNormHeld
+// calls f with the threads and vectors of a row of ch channels, at most kNormHeld.
+// Up to 1,024 channels a wave in vectors of four, whose lanes are all in use at 256,
+// 512, 768 and 1,024 (in vectors of eight, a quarter idle at 768: 32,768 rows of 768 50
+// and 84 us instead of 36 and 34; 65,536 rows of 1,024 to e4m3 188 instead of 160).
 template <typename F>
 void with_row(int ch, F &&f) {
     if (ch <= 256) f(Row<64, 4, 1>{});

@@ -49,19 +49,19 @@ int64_t power_from(int64_t x, int64_t low, int64_t high) {   // the least power 
     return p;
 }
 
-// Tokens of a lane: so many that about 16 waves a CU share the work, but 4 to 66 (each
-// chunk reads the W - 1 tokens in front of its own again).  Microseconds by the least
-// and the most of them:
-//   64 rows of 16 tokens, 2,048 channels, bf16   2: 6.0   4: 5.8   6: 7.1   12: 9.1
-//   2 rows of 2,041, 1,021 channels, fp32        2: 11.8   4: 10.8   6: 11.4   12: 14.0
-//   1 row of 65,536, 2,048 channels, bf16        12: 128   24: 116   48: 118   66: 116
-//   8 rows of 4,096, 1,536 channels, bf16        12: 48   24: 45   48: 43   66: 42
+// Tokens of a lane: so many that about 16 waves a CU share the work, but 4 to 24 (each
+// chunk reads the W - 1 tokens in front of its own again, from L2 or beyond).
+// Microseconds by the least of them, and by the most:
+//   64 rows of 16 tokens, 2,048 channels, bf16   6: 5.6   4: 6.0   12: 6.7
+//   2 rows of 2,041, 1,021 channels, fp32        4: 11.2   6: 12.0   12: 14.6
+//   1 row of 65,536, 2,048 channels, bf16        12: 111   24: 104   48: 108   66: 106
+//   8 rows of 4,096, 1,536 channels, bf16        12: 43.6   24: 42.0   48: 44.3   66: 44.0
 // One chunk where only the state is wanted.
 ConvPlan conv_plan(const bdssm_conv_shape *s, int64_t T, bool state_only) {
     ConvPlan p{};
     p.lanes = (int)((s->channels + kConvLane - 1) / kConvLane);
     const int64_t most = kCus * 16 * 64, work = s->batch * T * p.lanes;
-    p.chunk = (int)(state_only ? (T > 0 ? T : 1) : within((work + most - 1) / most, 4, 66));
+    p.chunk = (int)(state_only ? (T > 0 ? T : 1) : within((work + most - 1) / most, 4, 24));
     p.chunks = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;
     p.jobs = s->batch * p.chunks * p.lanes;
     p.block = p.jobs < 256 * 256 ? 64 : 256;   // few lanes: spread over the CUs
@@ -147,7 +147,8 @@ int check_norm(const bdssm_norm_shape *s) {
     return BDSSM_OK;
 }
 
-// Workgroups: rows go round them, so that each has its weights once.
+// Workgroups: rows go round them, so that each reads the weights once; for rows of up to
+// 4,096 channels four waves a SIMD backward, eight forward, whose registers are fewer.
 int norm_groups(const bdssm_norm_shape *s, bool bwd) {
     const int64_t at_once = s->channels <= 1024 ? 4 : 1, most = bwd ? 1024 : 2048;
     const int64_t n = (s->rows + at_once - 1) / at_once;

@@ -209,3 +209,17 @@ def test_empty(dev):
         none = torch.zeros(0, 4, 6, dtype=dtype, device=dev)
         g = m.conv_scan_bwd(none, c["w"], none, bias=c["bias"])
         assert (g["dw"] == 0).all() and (g["dbias"] == 0).all() and m.conv_scan(none, c["w"])[0].shape == none.shape
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [2, 3, 4])
+@pytest.mark.parametrize("starts", [False, True])
+def test_whole_lanes_and_parts_of_lanes(dev, dtype, width, starts):
+    """Channels that fill their lanes and that do not, with and without documents, at lengths around chunks' ends.  (The
+    kernels of the two may round a product and a sum together or apart, so each is held to the formula.)"""
+    for T in (4, 6, 7, 23, 24, 25, 48, 53):
+        c = conv_inputs(3, T, 24, width, dtype, seed=14 + T, device=dev, lens=[T, T // 2, 1], starts=[(0, T // 2), (1, 0), (0, T - 1)] if starts else None)
+        check_all(c)
+        check_all({n: (x if n in ("lens", "starts") or x is None else x[:23].contiguous() if n in ("w", "bias") else x[..., :23].contiguous())
+                   for n, x in c.items()})

@@ -227,3 +227,25 @@ def test_evict_leaves_strange_rows_alone(dev):
     a = table.to(dev), torch.tensor([160, 33], dtype=torch.int32, device=dev), mass.to(dev), 16, 3
     got = m.kv_evict(*a, **outs)
     assert all(x is y for x, y in zip(got, outs.values())) and all(torch.equal(x, y) for x, y in zip(got, m.kv_evict(*a)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pages", [320, 321, 8192, 8193, 20480, 20481])
+@pytest.mark.parametrize("kind", ["spread", "narrow", "special", "negative"])
+def test_evict_layouts(dev, pages, kind):
+    """Each layout of a row over threads at its ends; weights of one exponent (more than one wave takes), of both
+    infinities and NaN, all below 0."""
+    gen = torch.Generator().manual_seed(pages + 1)
+    table = torch.stack([torch.randperm(pages, generator=gen) for _ in range(3)]).to(torch.int32)
+    mass = (torch.randn(3, pages, generator=gen) * 4).exp()
+    if kind == "narrow":
+        mass = 1 + torch.rand(3, pages, generator=gen).clamp(max=0.999)
+    if kind == "special":
+        r = torch.rand(3, pages, generator=gen)
+        mass[r < 0.2], mass[(r >= 0.2) & (r < 0.4)], mass[(r >= 0.4) & (r < 0.5)] = float("inf"), float("nan"), float("-inf")
+    if kind == "negative":
+        mass = -mass
+    ctx = torch.tensor([pages * 16, pages * 16 - 7, pages * 8], dtype=torch.int32)
+    for budget in (0, 1, pages // 10, pages // 2, pages * 3 // 5, pages * 9 // 10, pages - 1, pages):
+        check_evict(dev, table, ctx, mass, 16, budget, 0, 0)
+    check_evict(dev, table, ctx, mass, 16, pages // 2, 5, 64)
