@@ -679,6 +679,7 @@ int bdssm_conv_step(const bdssm_conv_shape *shape, int64_t T, const void *c_cach
  *   dc_init   NULL, or [batch, W-1, channels] stream dtype (with c_init NULL,
  *             the gradient at zero).
  *   ws        ws_bytes >= bdssm_conv_workspace_bytes(shape, T).
+ * At most 64 (2^22 - 1) / (width + 1) channels (53 million at width 4).
  * Sums are taken in a fixed order: results are bitwise reproducible.
  */
 int bdssm_conv_scan_bwd(const bdssm_conv_shape *shape, int64_t T, const void *u, const float *w,

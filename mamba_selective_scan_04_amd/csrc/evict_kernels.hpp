@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void kv_weights_kernel(WeightArgs<T> a) {
                 }
             }
             for (int r0 = 0; r0 < rows; r0 += 16) {
-                                const float less = now.less * kLog2e;
+                const float less = now.less * kLog2e;
                 Frag<kIn> Q[kSteps];
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) Q[s] = Fragments<T>::frag(now.raw[s]);

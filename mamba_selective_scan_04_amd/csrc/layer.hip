@@ -41,6 +41,13 @@ int check_conv(const bdssm_conv_shape *s, int64_t T) {
     return extent(s, T, s->u_stride, s->u_batch_stride, &n) ? BDSSM_OK : BDSSM_ERR_SHAPE;
 }
 
+// The gradients' parts are summed by workgroups of 1,024 threads, one for 64 columns.
+int check_conv_bwd(const bdssm_conv_shape *s, int64_t T) {
+    const int rc = check_conv(s, T);
+    if (rc) return rc;
+    return ((s->width + 1) * s->channels + 63) / 64 > kMostGroups / 4 ? BDSSM_ERR_SHAPE : BDSSM_OK;
+}
+
 int64_t within(int64_t x, int64_t low, int64_t high) { return x < low ? low : x > high ? high : x; }
 
 int64_t power_from(int64_t x, int64_t low, int64_t high) {   // the least power of two from x on, within low .. high
@@ -211,7 +218,7 @@ int bdssm_conv_scan_bwd(const bdssm_conv_shape *s, int64_t T, const void *u, con
                         const int32_t *lens, const uint8_t *starts, const void *c_init, const void *dy, const void *dc_final, void *du,
                         int64_t du_stride, int64_t du_batch_stride, float *dw, float *dbias, void *dc_init, void *ws, size_t ws_bytes,
                         hipStream_t st) {
-    const int rc = check_conv(s, T);
+    const int rc = check_conv_bwd(s, T);
     if (rc) return rc;
     int64_t nu, ndu;
     (void)extent(s, T, s->u_stride, s->u_batch_stride, &nu);
@@ -248,7 +255,7 @@ int bdssm_conv_scan_bwd(const bdssm_conv_shape *s, int64_t T, const void *u, con
 }
 
 size_t bdssm_conv_workspace_bytes(const bdssm_conv_shape *s, int64_t T) {
-    if (check_conv(s, T) != BDSSM_OK) return (size_t)-1;
+    if (check_conv_bwd(s, T) != BDSSM_OK) return (size_t)-1;
     return conv_workspace(s, conv_bwd_plan(s, T));
 }
 

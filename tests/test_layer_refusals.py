@@ -105,6 +105,19 @@ def test_conv_strides():
     assert scan_bwd(ld=63) == scan_bwd(batch_ld=639) == scan_bwd(ld=-1) == SHAPE
 
 
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_conv_gradients_widest(width):
+    """The sum of the gradients' parts: 1,024 threads for 64 of (width + 1) * channels
+    columns, and a grid's threads are counted in 32 bits."""
+    most = 64 * ((1 << 22) - 1) // (width + 1)
+    room = lambda ch: m.load().bdssm_conv_workspace_bytes(ctypes.byref(conv(batch=1, ch=ch, width=width, T=1)), 1)  # noqa: E731
+    assert room(most) == (width + 1) * most * 4
+    assert room(most + 1) == ctypes.c_size_t(-1).value
+    s = conv(batch=1, ch=most + 1, width=width, T=1)
+    assert scan_bwd(s, 1, ld=most + 1, batch_ld=most + 1) == SHAPE
+    assert scan(s, 1, y=None, c_final=None) == 0   # forward there is no such sum
+
+
 @pytest.mark.parametrize("T", [-1, 1 << 30, 1 << 40, (1 << 63) - 1])
 def test_conv_lengths(T):
     s = conv(batch=1)
