@@ -74,7 +74,8 @@ struct Vals<uint16_t, kN> {
 // [n_parts][taps + with_bias][ch], into dw [ch][taps] and dbias [ch] (null: not
 // wanted).  A workgroup takes 64 columns, its waves the parts' ranges, joined in
 // order: the sums do not depend on how the workgroups ran.  Bound by latency (of
-// each wave's n_parts / kWaves loads, eight under way at a time).
+// each wave's n_parts / kWaves loads, eight under way at a time): 1,024 parts of 768
+// columns 5.8 us (16 under way 6.2, 32 21.8), 126 of 7,680 5.3 (5.4, 5.2).
 template <int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void parts_sum_kernel(const float *parts, int n_parts, int taps, int with_bias, int ch, float *dw,
                                                                 float *dbias) {
