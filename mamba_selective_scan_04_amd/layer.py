@@ -68,16 +68,6 @@ def _conv(u, w, bias, lens, starts):
     return ConvShape(batch, ch, w.shape[1], *_strides(u, "u"), _dtype_code(u)), T
 
 
-def _room_like(ws, like, name, *args):
-    """_room, a new workspace made like a tensor at hand (1 us less a call)."""
-    if ws is not None:
-        return _room(ws, name, *args, like.device)
-    n = getattr(load(), name)(*args)
-    if n == 0 or n == ctypes.c_size_t(-1).value:   # none; or a shape that the call refuses
-        return None, 0
-    return like.new_empty((n,), dtype=torch.uint8), n
-
-
 def _conv_state(s):
     return (s.batch, s.width - 1, s.channels)
 
@@ -141,7 +131,7 @@ def conv_scan_bwd(u, w, dy, bias=None, silu=True, lens=None, starts=None, c_init
     dbias = None if bias is None else torch.empty_like(bias)
     dc = u.new_empty(_conv_state(s)) if want_dc_init else None
     stream = _stream(u.get_device(), w, bias, lens, starts, c_init, dy, dc_final, du, ws)
-    ws, room = _room_like(ws, u, "bdssm_conv_workspace_bytes", ctypes.byref(s), T)
+    ws, room = _room(ws, "bdssm_conv_workspace_bytes", ctypes.byref(s), T, u.device)
     rc = load().bdssm_conv_scan_bwd(ctypes.byref(s), T, _p(u), _p(w), _p(bias), 1 if silu else 0, _p(lens), _p(starts),
                                     _p(c_init), _p(dy), _p(dc_final), _p(du), *ld, _p(dw), _p(dbias), _p(dc), _p(ws), room,
                                     stream)
@@ -222,7 +212,7 @@ def rms_norm_bwd(h, w, rstd, dy, dh=None, ws=None):
     dx, dw = torch.empty_like(dy), torch.empty_like(w)
     dres = dx if h.dtype is dy.dtype else torch.empty_like(h)
     stream = _stream(dy.get_device(), h, w, rstd, dh, ws)
-    ws, room = _room_like(ws, dy, "bdssm_norm_workspace_bytes", ctypes.byref(s))
+    ws, room = _room(ws, "bdssm_norm_workspace_bytes", ctypes.byref(s), dy.device)
     rc = load().bdssm_rms_norm_bwd(ctypes.byref(s), _p(h), _p(w), _p(rstd), _p(dy), _p(dh), _p(dx),
                                    None if dres is dx else _p(dres), _p(dw), _p(ws), room, stream)
     _raise("bdssm_rms_norm_bwd", rc)
