@@ -276,13 +276,15 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
             for (int j = 0; j + 1 < kW - 1; ++j) hist[j] = hist[j + 1];
             hist[kW - 2] = x;
         };
-        const auto shift = [&](const float (&dp)[kN]) {
+        // there: the token is one of the row's.  Of padding nothing is formed, not even
+        // weights times 0, which an infinite weight would make a NaN
+        const auto shift = [&](bool there, const float (&dp)[kN]) {
 #pragma unroll
             for (int d = kW - 2; d > 0; --d)
 #pragma unroll
                 for (int e = 0; e < kN; ++e) open[d][e] = open[d - 1][e];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) open[0][e] = wt[e][kW - 1] * dp[e];
+            for (int e = 0; e < kN; ++e) open[0][e] = there ? wt[e][kW - 1] * dp[e] : 0.f;
         };
         const int inside = t1 < n ? t1 : n, end = t1 + kW - 1;
         int t = t0;
@@ -306,7 +308,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
                         out.put(open[kW - 2]);
                         out.store(dub + (int64_t)(t + i - (kW - 1)) * a.du_ld, n_ch);
                     }
-                    shift(dp);
+                    shift(true, dp);
                 }
                 t += kAhead;
                 continue;
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
                 if (state) out.store(a.dc_init + (b * (kW - 1) + at + kW - 1) * a.ch + c0, n_ch);
                 else out.store(dub + (int64_t)at * a.du_ld, n_ch);
             }
-            shift(dp);
+            shift(t < n, dp);
             ++t;
         }
     }
