@@ -586,6 +586,7 @@ int bdssm_kv_attn_step_ex(const bdssm_kv_shape *shape, int64_t L, int64_t Lq, co
  *   out   [batch, max_pages] fp32; may be mass (in place).  A position of the
  *         table behind the context, or that holds no page, keeps mass.
  * Values are not read.  Sums are taken in a fixed order.
+ * Limits: max_pages * page_len at most 2^30 - 128.
  */
 int bdssm_kv_attn_weights(const bdssm_kv_shape *shape, int64_t Lq, const void *q, const float *lse,
                           const void *k_cache, const float *k_scale, const int32_t *page_table,
@@ -605,7 +606,11 @@ int bdssm_kv_attn_weights(const bdssm_kv_shape *shape, int64_t Lq, const void *q
  *   ctx_out [batch] out: the tokens that are left in the context.
  * The cache itself is not touched: keys keep what position they were given.
  * Pages that rows share must not be evicted (the next commit would write them).
- * Limits: sink + recent <= budget; max_pages at most 2^18; page_len as above.
+ * A position that holds no page counts as any other and leaves by its mass (0, if
+ * it never got any); a commit that comes to it then writes nothing, until the
+ * caller has put a page there.
+ * Limits: batch at most 32767; sink + recent <= budget; max_pages at most 2^18;
+ * page_len as above.
  */
 int bdssm_kv_evict(int64_t batch, int64_t max_pages, int64_t page_len, int64_t budget, int64_t sink,
                    int64_t recent, const int32_t *page_table, const int32_t *ctx_lens,
@@ -627,7 +632,8 @@ int bdssm_kv_evict(int64_t batch, int64_t max_pages, int64_t page_len, int64_t b
  *           (values below 0 count as 0, above T as T): whatever they hold, y
  *           and gradients are 0 there and the state is as if they were not.
  *   starts  NULL, or [batch, T] uint8: nonzero where a document starts.  No tap
- *           reaches in front of it (as the delta rule's g of -inf).
+ *           reaches in front of it (as the delta rule's g of -inf): what lies
+ *           there counts as 0.
  *   state   [batch, W-1, channels] stream dtype: the inputs of the last W-1
  *           tokens, the newest last, 0 in front of a document's start.
  * The two-stream training form, every block from the clean stream's state, is

@@ -11,11 +11,17 @@
 // takes four neighbouring channels and a chunk of consecutive tokens, keeping the last
 // W - 1 inputs in registers, so that each input is read once but for the W - 1 in
 // front of a chunk.  65,536 tokens of 2,048 channels in bf16, half of a projection: 104
-// us (5.2 TB/s read and written; a copy of 2 GiB runs at 4.9); 8 rows of 4,096 tokens of
-// 1,536: 42 us.  Eight channels of bf16, 16 bytes a load: 109 and 42 us, 6.8 instead of
-// 6.0 for 64 rows of 16 tokens.  kPlain: every lane has its kN channels and y = silu(p);
-// kStarts: there may be starts of documents.  Both are asked nowhere else: as
-// conditions in the kernel, at each token, load and store, they cost the first 116 us.
+// us a call (5.2 TB/s read and written; copies run at 4.9 to 5.2); 8 rows of 4,096 tokens
+// of 1,536: 40 to 42 us.  Eight channels of bf16, 16 bytes a load: 109 and 42 us, 6.8
+// instead of 6.0 for 64 rows of 16 tokens.  kPlain: every lane has its kN channels and
+// y = silu(p); kStarts: there may be starts of documents.  Without kPlain, where all
+// lanes are whole and only silu is asked for at run time, the first takes 106 us and the
+// second 40; with 1,535 channels instead of 1,536, whose last lane's wave goes the whole
+// lanes' way and the values' one by one for every token, 73.
+// With kStarts the second takes 60 us: a token's byte of `starts` is loaded behind the
+// store of the token in front of it, which for all that the compiler knows may have
+// written it, and the wait for the byte is one for everything under way, the store and
+// the tokens read ahead among it (waves wait for 68% of the time, without documents 39%).
 #pragma once
 
 #include "layer_common.hpp"
@@ -201,9 +207,11 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs<T> a) {
 // registers; du_s is whole once dp_{s+W-1} is there.  Tokens go kAhead at a time
 // but at a row's ends (chunks are multiples of 6).  The parameters' sums of a
 // workgroup's chunks join in LDS in a fixed order and go to `parts`.  Bound by memory
-// and the vector units (59% of their slots): 8 rows of 4,096 tokens of 1,536 channels in
-// bf16 68 us (4.5 TB/s; 84 with three tokens at a time, 105 with documents, whose
-// conditions leave registers for three).
+// and the vector units (57% of their slots): 8 rows of 4,096 tokens of 1,536 channels in
+// bf16 66 to 71 us (4.3 to 4.6 TB/s; 84 with three tokens at a time).  With documents 92
+// to 94: three tokens at a time, by registers, and for each the wait for its byte of
+// `starts`, as above (waves wait for 60% of the time, without documents 39%).  1,535
+// channels, whose last lane's wave walks both ways: 205.
 template <typename T, int kW, int kN, bool kPlain, bool kStarts>
 __global__ __launch_bounds__(256, 3) void conv_bwd_kernel(ConvArgs<T> a) {
     constexpr int kAhead = kPlain && !kStarts ? 6 : kW == 4 ? 3 : 2, kSums = kN * (kW + 1);

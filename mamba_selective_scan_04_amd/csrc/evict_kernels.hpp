@@ -21,7 +21,7 @@ namespace bdssm_dev {
 // tiles join in LDS in a fixed order.
 //
 // Bound by memory (the keys' codes, half of what the attention reads) where query rows
-// are few: 64 rows of up to 8,192 int8 tokens of 4 heads of 64, 3 query rows, 19 us (4.3
+// are few: 64 rows of up to 8,192 int8 tokens of 4 heads of 64, 3 query rows, 19 us (4.4
 // TB/s).  65,536 e4m3 tokens of 4 heads of 128 and 64 query rows: 16 us (2.1 TB/s), start
 // and latency of a short kernel: its waves, two a SIMD, wait for 54% of the time, for
 // the table, then the codes, then each tile of queries.
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void kv_weights_kernel(WeightArgs<T> a) {
     int ctx = d.ctx[b] < 0 ? 0 : d.ctx[b];
     const int most = d.n_pages > 0 ? d.max_pages * d.page_len : 0;
     ctx = ctx < most ? ctx : most;
-    const int key0 = (int)blockIdx.x * kWeightKeys + wave % kShares * (kKeyTiles * 16);   // at most 2^31 - 128 + 64
+    const int key0 = (int)blockIdx.x * kWeightKeys + wave % kShares * (kKeyTiles * 16);   // below 2^30 + 64: the host's limit of a row's positions
     const int shift = 31 - __builtin_clz(d.page_len);
     const int32_t *table = d.table + (int64_t)b * d.max_pages;
     float sum[kKeyTiles];

@@ -7,12 +7,13 @@
 // up to 1,024 channels), so that it is read once; a workgroup goes over several rows
 // with the weights kept, the next row's loads on their way while one is worked on.
 // 65,536 rows of 1,024 channels, bf16 with an fp32 residual, to e4m3: 160 us (4.6 TB/s
-// read and written; a copy of 2 GiB runs at 4.9).  32,768 rows of 768, all bf16: 36 us
-// and 34 for the gradients (5.6 and 5.9 TB/s, partly out of the last-level cache).
+// read and written; copies run at 4.9 to 5.2).  32,768 rows of 768, all bf16: 36 to 38
+// us and 34 to 36 for the gradients (5.3 to 5.9 TB/s, partly out of the last-level cache).
 //
-// Sums of squares are taken in 64 bits: they then round to the same 32-bit r however
-// a row is laid out over lanes, and so do the outputs: codes beside a border do not
-// depend on the layout, as they would with r's last bit.
+// Sums of squares are taken in 64 bits: another order of the lanes moves them by some
+// 2^-52 of themselves, so that all but always they round to the same 32-bit r however a
+// row is laid out (in about one row of 2^27 r's 64-bit value lies that near a border),
+// and outputs, codes beside a border among them, come out the same.
 #pragma once
 
 #include "kv_kernels.hpp"
